@@ -15,6 +15,7 @@ include/lce.h; this package is the thin Python binding.
     y = lce.mlp_forward(x, Wg, Wu, Wd)          # sequence-tiled gated MLP
     dx, dWg, dWu, dWd = lce.mlp_backward(x, Wg, Wu, Wd, dy)
     y = lce.sequence_tiled_mlp(x, Wg, Wu, Wd)   # the same, autograd-aware
+    w, experts = lce.route_experts(logits, top_k)   # router, autograd-aware
     from chunked_lm_head_gemm_gb300 import sharded   # rows split over ranks
     loss, lse, dH, dW = sharded.forward_backward(h, W, labels, group)
     from chunked_lm_head_gemm_gb300 import vocab_parallel as vp  # head split
@@ -23,17 +24,19 @@ include/lce.h; this package is the thin Python binding.
                                group)
 """
 from ._binding import (IGNORE_INDEX, LCEError, LinearCrossEntropy,
-                       SequenceTiledMLP, alloc_workspace, backward, count_valid,
+                       RouteExperts, SequenceTiledMLP, alloc_workspace, backward, count_valid,
                        default_chunk_rows, forward, forward_backward,
                        get_error, library_path, linear_cross_entropy, load,
                        mlp_backward, mlp_forward, mlp_workspace_size,
-                       profile_start, profile_stop, scale_gradients,
+                       profile_start, profile_stop, route_backward,
+                       route_experts, route_forward, scale_gradients,
                        sequence_tiled_mlp, workspace_size)
 
-__all__ = ["IGNORE_INDEX", "LCEError", "LinearCrossEntropy", "SequenceTiledMLP",
-           "alloc_workspace",
+__all__ = ["IGNORE_INDEX", "LCEError", "LinearCrossEntropy", "RouteExperts",
+           "SequenceTiledMLP", "alloc_workspace",
            "backward", "count_valid", "default_chunk_rows", "forward",
            "forward_backward", "get_error", "library_path",
            "linear_cross_entropy", "load", "mlp_backward", "mlp_forward",
            "mlp_workspace_size", "profile_start", "profile_stop",
+           "route_backward", "route_experts", "route_forward",
            "scale_gradients", "sequence_tiled_mlp", "workspace_size"]

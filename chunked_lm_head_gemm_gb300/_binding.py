@@ -25,9 +25,12 @@ LCE_ERR_WORKSPACE = 3
 LCE_ERR_LABEL_RANGE = 4
 LCE_ERR_TIMEOUT = 5
 LCE_ERR_CUDA = 6
+LCE_ERR_EXPERT_RANGE = 7
 
 LCE_BF16 = 0
 LCE_F32 = 1
+
+SCORING = {"softmax": 0, "sigmoid": 1}
 
 IGNORE_INDEX = -100
 
@@ -45,15 +48,24 @@ EXPORTED = ("lce_workspace_size", "lce_default_chunk_rows", "lce_forward",
             "lce_forward_ex", "lce_backward_ex", "lce_forward_backward_ex",
             "lce_shard_sums", "lce_combine_shards", "lce_forward_slice_ex",
             "lce_combine_slices_ex", "lce_backward_slice_ex",
-            "lce_forward_slice_exp_ex", "lce_backward_slice_exp_ex")
+            "lce_forward_slice_exp_ex", "lce_backward_slice_exp_ex",
+            "lce_route_forward", "lce_route_backward")
 
-KERNEL_KINDS = 22
+KERNEL_KINDS = 33
 
 
 class LossOpts(ctypes.Structure):
     """lce_loss_opts: label smoothing in [0, 1] and the z-loss coefficient."""
     _fields_ = [("label_smoothing", ctypes.c_float),
                 ("z_loss", ctypes.c_float)]
+
+
+class RouteOpts(ctypes.Structure):
+    """lce_route_opts: how router logits become experts and weights."""
+    _fields_ = [("scoring", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class KernelStat(ctypes.Structure):
@@ -182,6 +194,12 @@ def load(build_if_missing: bool = False):
         lib.lce_mlp_backward.argtypes = [p, p, p, p, p, i64, i64, i64, i64, p,
                                          p, p, p, p, sz, p]
         lib.lce_mlp_backward.restype = i32
+        ropts = ctypes.POINTER(RouteOpts)
+        lib.lce_route_forward.argtypes = [p, i32, p, i64, i64, ropts, p, p, p]
+        lib.lce_route_forward.restype = i32
+        lib.lce_route_backward.argtypes = [p, i32, p, p, i64, i64, ropts, p,
+                                           p]
+        lib.lce_route_backward.restype = i32
         lib.lce_set_cta_pair.argtypes = [i32]
         lib.lce_set_cta_pair.restype = i32
         lib.lce_get_cta_pair.argtypes = []
@@ -743,6 +761,85 @@ def mlp_backward(x, Wg, Wu, Wd, dy, chunk_rows: int = 0, workspace=None,
     return dx, dWg, dWu, dWd
 
 
+def _route_opts(scoring, top_k, n_group, topk_group, group_top, renormalize,
+                scale):
+    if scoring not in SCORING:
+        raise ValueError(f"scoring must be one of {sorted(SCORING)}, got "
+                         f"{scoring!r}")
+    return RouteOpts(SCORING[scoring], top_k, n_group, topk_group, group_top,
+                     int(bool(renormalize)), scale)
+
+
+def _check_logits(logits):
+    if not logits.is_cuda or logits.dim() != 2 or not logits.is_contiguous():
+        raise ValueError("logits must be a contiguous CUDA [L,E] tensor")
+    return _dtype_code(logits)
+
+
+def route_forward(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
+                  bias=None, n_group: int = 1, topk_group: int = 1,
+                  group_top: int = 1, renormalize: bool = True,
+                  scale: float = 1.0, weights_out=None, experts_out=None):
+    """Routes each row of router logits [L,E] (bf16 or fp32) to top_k
+    experts: returns (weights [L,top_k] of logits' dtype, experts [L,top_k]
+    int32). bias: float32 [E] added to the scores for the selection alone;
+    n_group / topk_group / group_top: group-limited selection
+    (lce_route_forward)."""
+    lib = load()
+    code = _check_logits(logits)
+    L, E = logits.shape
+    dev = logits.device
+    opts = _route_opts(scoring, top_k, n_group, topk_group, group_top,
+                       renormalize, scale)
+    if bias is not None and not (bias.is_cuda and bias.shape == (E,) and
+                                 bias.dtype == torch.float32 and
+                                 bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous CUDA float32 [E] tensor")
+    k = max(int(top_k), 0)
+    weights = weights_out if weights_out is not None else torch.empty(
+        L, k, dtype=logits.dtype, device=dev)
+    experts = experts_out if experts_out is not None else torch.empty(
+        L, k, dtype=torch.int32, device=dev)
+    st = lib.lce_route_forward(logits.data_ptr(), code, _ptr(bias), L, E,
+                               ctypes.byref(opts), weights.data_ptr(),
+                               experts.data_ptr(), _stream_ptr(dev))
+    _check(st, "lce_route_forward")
+    return weights, experts
+
+
+def route_backward(logits: torch.Tensor, experts: torch.Tensor,
+                   dweights: torch.Tensor, scoring: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0,
+                   dlogits_out=None) -> torch.Tensor:
+    """dlogits [L,E] (logits' dtype) of route_forward from dweights
+    [L,top_k], the selection being constant (lce_route_backward)."""
+    lib = load()
+    code = _check_logits(logits)
+    L, E = logits.shape
+    dev = logits.device
+    _check_experts(experts, L)
+    k = experts.shape[1]
+    if not (dweights.is_cuda and dweights.shape == (L, k) and
+            dweights.dtype == logits.dtype and dweights.is_contiguous()):
+        raise ValueError("dweights must be a contiguous CUDA [L,top_k] tensor "
+                         "of logits' dtype")
+    opts = _route_opts(scoring, k, 1, 1, 1, renormalize, scale)
+    out = dlogits_out if dlogits_out is not None else torch.empty_like(logits)
+    st = lib.lce_route_backward(logits.data_ptr(), code, experts.data_ptr(),
+                                dweights.data_ptr(), L, E, ctypes.byref(opts),
+                                out.data_ptr(), _stream_ptr(dev))
+    _check(st, "lce_route_backward")
+    return out
+
+
+def _check_experts(experts, L):
+    if not (experts.is_cuda and experts.dtype == torch.int32 and
+            experts.dim() == 2 and experts.shape[0] == L and
+            experts.is_contiguous()):
+        raise ValueError("experts must be a contiguous CUDA int32 [L,top_k] "
+                         "tensor")
+
+
 def set_cta_pair(enable: bool):
     """Run the contractions on CTA pairs (cta_group::2) or single CTAs."""
     _check(load().lce_set_cta_pair(1 if enable else 0), "lce_set_cta_pair")
@@ -858,6 +955,41 @@ class SequenceTiledMLP(torch.autograd.Function):
                 for t, w, n in ((dWg, Wg, need[1]), (dWu, Wu, need[2]),
                                 (dWd, Wd, need[3]))]
         return (dx, cast[0], cast[1], cast[2], None)
+
+
+class RouteExperts(torch.autograd.Function):
+    """route_forward under autograd: the weights carry gradient to the
+    logits, the selection (experts) does not. bias steers the selection
+    alone and gets none."""
+
+    @staticmethod
+    def forward(ctx, logits, top_k, scoring="softmax", bias=None, n_group=1,
+                topk_group=1, group_top=1, renormalize=True, scale=1.0):
+        weights, experts = route_forward(logits, top_k, scoring, bias, n_group,
+                                         topk_group, group_top, renormalize,
+                                         scale)
+        ctx.opts = (scoring, renormalize, scale)
+        ctx.save_for_backward(logits, experts)
+        ctx.mark_non_differentiable(experts)
+        return weights, experts
+
+    @staticmethod
+    def backward(ctx, dweights, _):
+        logits, experts = ctx.saved_tensors
+        dlogits = None
+        if ctx.needs_input_grad[0]:
+            dlogits = route_backward(logits, experts,
+                                     dweights.to(logits.dtype).contiguous(),
+                                     *ctx.opts)
+        return (dlogits,) + (None,) * 8
+
+
+def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None,
+                  n_group: int = 1, topk_group: int = 1, group_top: int = 1,
+                  renormalize: bool = True, scale: float = 1.0):
+    """(weights, experts) of router logits, with autograd (route_forward)."""
+    return RouteExperts.apply(logits, top_k, scoring, bias, n_group,
+                              topk_group, group_top, renormalize, scale)
 
 
 def sequence_tiled_mlp(x, Wg, Wu, Wd, chunk_rows: int = 0):

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/lce.h"
+#include "lce_host.h"
 #include "lce_internal.h"
 
 namespace lce {
@@ -30,11 +31,15 @@ constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;  // 2 s per wait
 
 thread_local char t_last_cuda_error[256] = "";
 
+}  // namespace
+
 lce_status cuda_fail(cudaError_t e, const char* where) {
   std::snprintf(t_last_cuda_error, sizeof t_last_cuda_error, "%s: %s", where,
                 cudaGetErrorString(e));
   return LCE_ERR_CUDA;
 }
+
+namespace {
 
 // ---- optional per-kernel timing (lce_profile_start / lce_profile_stop) ----
 // When on, every kernel this thread launches is bracketed by two CUDA events
@@ -45,7 +50,10 @@ const char* const kKindNames[LCE_KERNEL_KINDS] = {
     "test_gemm",    "wait_probe",   "gemm_fused",    "grad_from_exp",
     "scale_grads",  "mlp_gate_up",  "mlp_down",      "mlp_da",
     "mlp_dx",       "mlp_dWd",      "mlp_dWgu",      "slice_stats",
-    "combine_slices", "shard_combine"};
+    "combine_slices", "shard_combine",
+    "route",        "route_bwd",    "experts_plan",  "experts_up",
+    "experts_down", "experts_combine", "experts_dgu", "experts_dx",
+    "experts_dWd",  "experts_dWgu", "experts_token"};
 
 struct ProfRec {
   int kind;
@@ -69,30 +77,21 @@ struct Profiler {
 };
 thread_local Profiler t_prof;
 
-// Brackets one launch: construct before, call done(flops) after.
-struct ProfScope {
-  int kind;
-  cudaStream_t s;
-  cudaEvent_t e0 = nullptr;
-  ProfScope(int k, cudaStream_t st) : kind(k), s(st) {
-    if (t_prof.on && (e0 = t_prof.take()) != nullptr) cudaEventRecord(e0, s);
-  }
-  void done(double flops) {
-    if (!e0) return;
-    cudaEvent_t e1 = t_prof.take();
-    if (!e1) return;
-    cudaEventRecord(e1, s);
-    t_prof.recs.push_back({kind, e0, e1, flops});
-  }
-};
+}  // namespace
 
-struct DeviceInfo {
-  bool ready = false;
-  bool supported = false;
-  int num_sms = 0;
-  int pair_slots = 0;       // co-resident CTA pairs of the pair kernels
-  unsigned* err = nullptr;  // device address of g_error_word
-};
+ProfScope::ProfScope(int k, cudaStream_t st) : kind(k), s(st) {
+  if (t_prof.on && (e0 = t_prof.take()) != nullptr) cudaEventRecord(e0, s);
+}
+
+void ProfScope::done(double flops) {
+  if (!e0) return;
+  cudaEvent_t e1 = t_prof.take();
+  if (!e1) return;
+  cudaEventRecord(e1, s);
+  t_prof.recs.push_back({kind, e0, e1, flops});
+}
+
+namespace {
 
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[kMaxDevices];
@@ -122,6 +121,8 @@ lce_status ensure_context() {
   if (e == cudaSuccess) e = cudaSetDevice(dev);
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, "cudaSetDevice");
 }
+
+}  // namespace
 
 lce_status device_info(DeviceInfo** out) {
   const lce_status cs = ensure_context();
@@ -159,6 +160,8 @@ lce_status device_info(DeviceInfo** out) {
   return LCE_OK;
 }
 
+namespace {
+
 // Contractions on single CTAs (128 x 256 tiles) or on CTA pairs
 // (256 x 256 tiles, tcgen05 cta_group::2). LCE_CTA_PAIR=0/1 in the
 // environment or lce_set_cta_pair() choose; the default is kDefaultPair.
@@ -175,6 +178,8 @@ bool use_pair() {
   return v != 0;
 }
 
+}  // namespace
+
 uint64_t wait_timeout_ns() {
   static uint64_t v = [] {
     const char* s = std::getenv("LCE_WAIT_TIMEOUT_MS");
@@ -186,6 +191,8 @@ uint64_t wait_timeout_ns() {
   }();
   return v;
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -202,6 +209,45 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   return fn;
 }
 
+}  // namespace
+
+lce_status make_tmap_nd(CUtensorMap* tm, CUtensorMapDataType type, int rank,
+                        const void* base, const uint64_t* dims,
+                        const uint64_t* strides, const uint32_t* box,
+                        CUtensorMapSwizzle swz) {
+  auto enc = tmap_encoder();
+  if (!enc) {
+    std::snprintf(t_last_cuda_error, sizeof t_last_cuda_error,
+                  "cuTensorMapEncodeTiled not available");
+    return LCE_ERR_CUDA;
+  }
+  cuuint64_t d[3] = {1, 1, 1}, st[2] = {0, 0};
+  cuuint32_t bx[3] = {1, 1, 1}, estr[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  CUresult r = enc(tm, type, static_cast<cuuint32_t>(rank),
+                   const_cast<void*>(base), d, st, bx, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    std::snprintf(t_last_cuda_error, sizeof t_last_cuda_error,
+                  "cuTensorMapEncodeTiled failed (%d): dims %llu x %llu x "
+                  "%llu, stride %llu",
+                  static_cast<int>(r), static_cast<unsigned long long>(d[0]),
+                  static_cast<unsigned long long>(d[1]),
+                  static_cast<unsigned long long>(d[2]),
+                  static_cast<unsigned long long>(st[0]));
+    return LCE_ERR_CUDA;
+  }
+  return LCE_OK;
+}
+
+namespace {
+
 // 2-D bf16 tensor map: `inner` contiguous elements per row, `outer` rows,
 // rows `row_bytes` apart; boxes of box_inner x box_outer with 128-byte
 // swizzle (box_inner = 64 elements = one swizzle row). Out-of-range
@@ -210,31 +256,10 @@ lce_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner,
                      uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                      uint32_t box_outer,
                      CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-  auto enc = tmap_encoder();
-  if (!enc) {
-    std::snprintf(t_last_cuda_error, sizeof t_last_cuda_error,
-                  "cuTensorMapEncodeTiled not available");
-    return LCE_ERR_CUDA;
-  }
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {row_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    std::snprintf(t_last_cuda_error, sizeof t_last_cuda_error,
-                  "cuTensorMapEncodeTiled failed (%d): dims %llu x %llu, "
-                  "stride %llu",
-                  static_cast<int>(r), static_cast<unsigned long long>(inner),
-                  static_cast<unsigned long long>(outer),
-                  static_cast<unsigned long long>(row_bytes));
-    return LCE_ERR_CUDA;
-  }
-  return LCE_OK;
+  const uint64_t dims[2] = {inner, outer};
+  const uint32_t box[2] = {box_inner, box_outer};
+  return make_tmap_nd(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims,
+                      &row_bytes, box, swz);
 }
 
 // Tensor maps of the two operand layouts the contractions read.
@@ -290,9 +315,6 @@ bool wave_sync_on() {
   }
   return v != 0;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 // Column-tile runs per row block for the contractions that sweep the whole
 // vocabulary (forward logits and their backward recompute). Enough runs that
@@ -1815,6 +1837,7 @@ lce_status lce_get_error(void* stream) {
   }
   if (word & ERRBIT_TIMEOUT) return LCE_ERR_TIMEOUT;
   if (word & ERRBIT_LABEL_RANGE) return LCE_ERR_LABEL_RANGE;
+  if (word & ERRBIT_EXPERT_RANGE) return LCE_ERR_EXPERT_RANGE;
   return LCE_OK;
 }
 
@@ -1827,6 +1850,7 @@ const char* lce_status_string(lce_status s) {
     case LCE_ERR_LABEL_RANGE: return "LCE_ERR_LABEL_RANGE";
     case LCE_ERR_TIMEOUT: return "LCE_ERR_TIMEOUT";
     case LCE_ERR_CUDA: return "LCE_ERR_CUDA";
+    case LCE_ERR_EXPERT_RANGE: return "LCE_ERR_EXPERT_RANGE";
   }
   return "LCE_ERR_UNKNOWN";
 }

@@ -34,6 +34,7 @@ constexpr int COMBINE_ROWS = 256;
 // Device error bits, OR-ed into the library's error word.
 constexpr unsigned ERRBIT_LABEL_RANGE = 1u << 4;
 constexpr unsigned ERRBIT_TIMEOUT = 1u << 5;
+constexpr unsigned ERRBIT_EXPERT_RANGE = 1u << 6;
 
 // Work decomposition of one contraction D[M,N] = A[M,K] B[K,N].
 // A unit is (row block m_blk, a run of n_count consecutive column tiles

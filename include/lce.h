@@ -67,7 +67,9 @@ typedef enum {
   LCE_ERR_LABEL_RANGE = 4, /* a label outside [0, V) that is not ignore_index
                               (that row was treated as ignored) */
   LCE_ERR_TIMEOUT = 5,     /* a bounded wait inside a kernel expired */
-  LCE_ERR_CUDA = 6         /* a CUDA runtime call failed */
+  LCE_ERR_CUDA = 6,        /* a CUDA runtime call failed */
+  LCE_ERR_EXPERT_RANGE = 7 /* an expert index outside [0, E) that is not -1
+                              (that slot was treated as dropped) */
 } lce_status;
 
 typedef enum {
@@ -523,6 +525,68 @@ lce_status lce_mlp_backward(const void* x, const void* Wg, const void* Wu,
                             void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Routing of tokens to experts, for a sparse (mixture-of-experts) MLP. No
+ * counterpart on the pages beyond their measured runs of a sparse model
+ * (TRL PR #6845, table "Measured"). For every row z of router logits:
+ *   score   s_j = softmax(z)_j or sigmoid(z_j)
+ *   key     t_j = s_j + bias_j; without a bias the order of the scores is
+ *           that of the logits, and t_j = z_j. -inf where z_j is -inf
+ *           or NaN (a masked expert), or where t_j is NaN.
+ *   groups  with n_group > 1 the experts form n_group runs of E / n_group;
+ *           a group's rank is the sum of its group_top largest keys (with
+ *           group_top = 2 always formed from s_j + bias_j, bias 0 without
+ *           one); the topk_group largest groups are kept.
+ *   experts the top_k largest keys among the kept groups, in falling order.
+ *           Every tie goes to the lowest index.
+ *   weights w_k = scale * s_{e_k}, or with renormalize
+ *           scale * s_{e_k} / sum_k s_{e_k} (0 where that sum is 0).
+ * A row whose logits are all -inf has scores and weights 0. Scores are
+ * computed in fp32; two keys closer than its error bound are compared in
+ * fp64, so the selection is that of exact arithmetic.
+ *   logits   device [L][E] of dt (LCE_BF16 or LCE_F32)
+ *   bias     device [E] float32 or NULL
+ *   weights  device [L][top_k] of dt out
+ *   experts  device [L][top_k] int32 out
+ * 1 <= E <= 1024, 1 <= top_k <= 32, n_group <= 32 a divisor of E, top_k <=
+ * topk_group * (E / n_group), group_top 1 or 2 (not above E / n_group),
+ * scale finite. L = 0 does nothing.
+ */
+typedef enum { LCE_SOFTMAX = 0, LCE_SIGMOID = 1 } lce_scoring;
+typedef struct {
+  int32_t scoring;     /* lce_scoring */
+  int32_t top_k;
+  int32_t n_group;     /* 1: no groups */
+  int32_t topk_group;
+  int32_t group_top;
+  int32_t renormalize; /* 0 or 1 */
+  float scale;
+} lce_route_opts;
+
+lce_status lce_route_forward(const void* logits, lce_dtype dt,
+                             const float* bias, int64_t L, int64_t E,
+                             const lce_route_opts* opts, void* weights,
+                             int32_t* experts, void* stream);
+
+/*
+ * The routing's gradient, the selection being constant: dlogits (device
+ * [L][E] of dt out, every element written) from dweights (device [L][top_k]
+ * of dt) and the forward's logits and experts. With u = scale * dweights, q
+ * the renormalised scores and S their sum:
+ *   renormalised softmax  dz_{e_k} = q_k (u_k - sum u q), else 0
+ *   plain softmax         dz_j = s_j (sum_{e_k = j} u_k - sum_k u_k s_{e_k})
+ *   sigmoid               dz_{e_k} = s (1 - s) ds_k, ds_k = u_k or
+ *                         (u_k - sum u q) / S when renormalised
+ * Of opts only scoring, top_k, renormalize and scale are used. Rows with S =
+ * 0 have gradient 0. An index outside [0, E) raises LCE_ERR_EXPERT_RANGE and
+ * is left out.
+ */
+lce_status lce_route_backward(const void* logits, lce_dtype dt,
+                              const int32_t* experts, const void* dweights,
+                              int64_t L, int64_t E,
+                              const lce_route_opts* opts, void* dlogits,
+                              void* stream);
+
+/*
  * Selects how the tensor-core contractions run, for the whole process:
  * enable = 1: on CTA pairs (a cluster of two SMs issues tcgen05.mma with
  * cta_group::2 on 256 x 256 tiles, each SM staging half of each operand);
@@ -559,7 +623,7 @@ int lce_get_wave_sync(void);
  * per tensor-core contraction, 0 for the other kernels). Host-side state
  * only; events are created on first use and reused.
  */
-#define LCE_KERNEL_KINDS 22
+#define LCE_KERNEL_KINDS 33
 enum {
   LCE_K_COUNT_VALID = 0,
   LCE_K_GEMM_LSE = 1,
@@ -582,7 +646,18 @@ enum {
   LCE_K_MLP_DWGU = 18,
   LCE_K_SLICE_STATS = 19,
   LCE_K_COMBINE_SLICES = 20,
-  LCE_K_SHARD_COMBINE = 21
+  LCE_K_SHARD_COMBINE = 21,
+  LCE_K_ROUTE = 22,
+  LCE_K_ROUTE_BWD = 23,
+  LCE_K_EXPERTS_PLAN = 24,
+  LCE_K_EXPERTS_UP = 25,
+  LCE_K_EXPERTS_DOWN = 26,
+  LCE_K_EXPERTS_COMBINE = 27,
+  LCE_K_EXPERTS_DGU = 28,
+  LCE_K_EXPERTS_DX = 29,
+  LCE_K_EXPERTS_DWD = 30,
+  LCE_K_EXPERTS_DWGU = 31,
+  LCE_K_EXPERTS_TOKEN = 32
 };
 
 typedef struct {

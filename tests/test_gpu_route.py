@@ -1,0 +1,221 @@
+"""Routing on the GPU against its float64 reference.
+
+Tolerances, fixed before the first run: the selection is exact. A score is
+within 2^-19 of its value (relative), so a renormalised weight is within
+3 * 2^-19, and is rounded once to its type (eps / 2). A gradient element is a
+product of a score and a difference of terms up to max |u|, each within a few
+2^-19: 16 * 2^-19 * score * max |u|, and one rounding."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import sparse_ref as ref
+from tests.gpu_util import require_gpu, to64
+
+pytestmark = pytest.mark.gpu
+
+SCORE = 2.0 ** -19
+
+
+def draw(L, E, dtype, seed, masked=0.0, spread=1.5):
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn(L, E, generator=g) * spread
+    if masked:
+        off = torch.rand(L, E, generator=g) < masked
+        z = z.masked_fill(off, -math.inf)
+    return z.to(dtype)
+
+
+def check(z, dev, top_k, bias=None, seed=0, **kw):
+    """Forward and backward of CPU logits z against the reference."""
+    import chunked_lm_head_gemm_gb300 as lce
+    zd = z.to(dev)
+    bd = None if bias is None else bias.to(dev)
+    w, e = lce.route_forward(zd, top_k, bias=bd, **kw)
+    rb = None if bias is None else bias.double().numpy()
+    rw, re_ = ref.route(to64(z), top_k, bias=rb, **kw)
+    assert np.array_equal(e.cpu().numpy(), re_)
+    half = torch.finfo(z.dtype).eps / 2
+    got = to64(w)
+    nan = np.isnan(rw)
+    assert np.array_equal(np.isnan(got), nan)
+    assert (np.abs(got - rw)[~nan] <=
+            (np.abs(rw) * (3 * SCORE + half) + 1e-37)[~nan]).all()
+    grad = {k: kw[k] for k in ("scoring", "renormalize", "scale") if k in kw}
+    dw = torch.randn(z.shape[0], top_k,
+                     generator=torch.Generator().manual_seed(seed + 99))
+    dw = dw.to(z.dtype)
+    dz = to64(lce.route_backward(zd, e, dw.to(dev), **grad))
+    assert lce.get_error() == 0
+    scoring = kw.get("scoring", "softmax")
+    scale = kw.get("scale", 1.0)
+    rz = ref.route_grad(to64(z), re_, to64(dw), scoring,
+                        kw.get("renormalize", True), scale)
+    for i in range(z.shape[0]):
+        if np.isnan(rz[i]).any():
+            continue
+        s = np.nan_to_num(ref.scores(to64(z[i]), scoring))
+        if kw.get("renormalize", True):
+            t = s[re_[i]].sum()
+            s = s / t if t else s
+        u = np.abs(scale * to64(dw[i])).max()
+        tol = 16 * SCORE * s * u + np.abs(rz[i]) * half + 1e-37
+        assert (np.abs(dz[i] - rz[i]) <= tol).all(), i
+
+
+SHAPES = [  # L, E, K, dtype, masked
+    (1, 1, 1, torch.float32, 0), (1, 128, 8, torch.bfloat16, 0),
+    (3, 5, 5, torch.float32, 0.3), (130, 60, 4, torch.bfloat16, 0.2),
+    (33, 127, 7, torch.float32, 0), (65, 128, 1, torch.bfloat16, 0),
+    (40, 250, 32, torch.float32, 0), (17, 256, 8, torch.bfloat16, 0.1),
+    (9, 511, 3, torch.float32, 0), (9, 512, 16, torch.bfloat16, 0),
+    (5, 1000, 10, torch.float32, 0.5), (6, 1024, 32, torch.bfloat16, 0)]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("L,E,K,dtype,masked", SHAPES)
+def test_shapes(L, E, K, dtype, masked, biased, scoring):
+    dev = require_gpu()
+    z = draw(L, E, dtype, seed=E + K, masked=masked)
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(1)) \
+        if biased else None
+    for renorm in (True, False):
+        check(z, dev, K, bias=bias, scoring=scoring, renormalize=renorm,
+              scale=2.5)
+
+
+GROUPS = [  # E, K, groups, kept, group_top
+    (64, 6, 8, 3, 1), (64, 6, 8, 3, 2), (256, 8, 8, 4, 2), (60, 4, 5, 2, 2),
+    (21, 2, 7, 1, 1), (96, 6, 32, 4, 2), (1024, 8, 16, 2, 2), (10, 3, 10, 4, 1),
+    (24, 8, 3, 3, 2), (250, 5, 2, 1, 2)]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("E,K,G,kept,top", GROUPS)
+def test_groups(E, K, G, kept, top, biased, scoring):
+    dev = require_gpu()
+    z = draw(37, E, torch.float32, seed=E, masked=0.15)
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(2)) \
+        if biased else None
+    check(z, dev, K, bias=bias, scoring=scoring, n_group=G, topk_group=kept,
+          group_top=top)
+
+
+@pytest.mark.parametrize("groups", [dict(), dict(n_group=4, topk_group=2,
+                                                 group_top=2)],
+                         ids=["flat", "groups"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_keys_closer_than_fp32(scoring, groups):
+    """The bias makes every key of a row 1 up to the bias's own rounding, so
+    the order is decided by differences near 2^-25 that fp32 scores cannot
+    see; and once more with whole rows of equal inputs (exact ties)."""
+    dev = require_gpu()
+    E = 64
+    z = draw(1, E, torch.float32, seed=5)
+    bias = torch.from_numpy(1.0 - ref.scores(to64(z[0]), scoring)).float()
+    z = z.expand(50, E).contiguous()
+    check(z, dev, 8, bias=bias, scoring=scoring, **groups)
+    check(torch.zeros(3, E), dev, 8, bias=torch.zeros(E), scoring=scoring,
+          **groups)
+    z = draw(200, E, torch.bfloat16, seed=6, spread=0.05)  # many equal logits
+    check(z, dev, 8, bias=torch.zeros(E), scoring=scoring, **groups)
+    check(z, dev, 8, scoring=scoring, **groups)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_rows_that_are_masked_or_not_finite(scoring, renorm):
+    dev = require_gpu()
+    E, inf, nan = 12, math.inf, math.nan
+    z = draw(8, E, torch.float32, seed=7)
+    z[0] = -inf                          # nothing left
+    z[1, 1:] = -inf                      # one expert left
+    z[2] = torch.finfo(torch.float32).min
+    z[3, 4] = nan
+    z[4, :6] = -inf
+    z[5] = -200.0                        # sigmoid scores underflow
+    z[6] = 300.0
+    z[7, 0], z[7, 1] = -0.0, 0.0
+    kw = dict(scoring=scoring, renormalize=renorm)
+    check(z, dev, 4, **kw)
+    bias = torch.zeros(E)
+    bias[3], bias[5], bias[6] = -inf, inf, inf
+    check(z, dev, 4, bias=bias, **kw)
+    check(z, dev, 4, bias=bias, n_group=3, topk_group=2, group_top=2, **kw)
+    check(z, dev, 4, n_group=3, topk_group=2, group_top=2, **kw)
+
+
+def test_addresses_and_streams():
+    """Rows off 16-byte addresses, another stream, and repeated calls give
+    the bits of the aligned call; strided logits are refused."""
+    dev = require_gpu()
+    import chunked_lm_head_gemm_gb300 as lce
+    z = draw(300, 64, torch.bfloat16, seed=8).to(dev)
+    w, e = lce.route_forward(z, 6)
+    dz = lce.route_backward(z, e, w)
+    flat = torch.empty(300 * 64 + 1, dtype=z.dtype, device=dev)
+    zz = flat[1:].view(300, 64)
+    zz.copy_(z)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        w2, e2 = lce.route_forward(zz, 6)
+        dz2 = lce.route_backward(zz, e2, w2)
+    side.synchronize()
+    assert torch.equal(w, w2) and torch.equal(e, e2) and torch.equal(dz, dz2)
+    with pytest.raises(ValueError, match="contiguous"):
+        lce.route_forward(z.t(), 6)
+    with pytest.raises(lce.LCEError):
+        lce.route_forward(z, 65)
+    assert lce.get_error() == 0
+
+
+def test_empty_and_bad_indices():
+    dev = require_gpu()
+    import chunked_lm_head_gemm_gb300 as lce
+    from chunked_lm_head_gemm_gb300 import _binding as B
+    w, e = lce.route_forward(torch.empty(0, 16, device=dev), 2)
+    assert w.shape == (0, 2) and e.shape == (0, 2)
+    z = draw(4, 16, torch.float32, seed=9).to(dev)
+    e = torch.tensor([[1, 2], [16, 3], [4, 5], [-7, 6]], dtype=torch.int32,
+                     device=dev)
+    dw = torch.ones(4, 2, device=dev)
+    dz = lce.route_backward(z, e, dw, scoring="sigmoid", renormalize=False)
+    assert lce.get_error() == B.LCE_ERR_EXPERT_RANGE
+    assert lce.get_error() == 0
+    s = ref.scores(to64(z), "sigmoid")
+    want = np.zeros((4, 16))
+    for i, j in ((0, 1), (0, 2), (1, 3), (2, 4), (2, 5), (3, 6)):
+        want[i, j] = s[i, j] * (1 - s[i, j])
+    assert np.allclose(to64(dz), want, rtol=1e-5, atol=0)
+
+
+def test_autograd_and_graph():
+    """route_experts under autograd equals the explicit calls; a captured
+    forward and backward replays with new logits."""
+    dev = require_gpu()
+    import chunked_lm_head_gemm_gb300 as lce
+    z = draw(64, 32, torch.float32, seed=10).to(dev)
+    leaf = z.clone().requires_grad_(True)
+    w, e = lce.route_experts(leaf, 4, "sigmoid", scale=2.0)
+    dw = torch.randn_like(w)
+    w.backward(dw)
+    want = lce.route_backward(z, e, dw, "sigmoid", scale=2.0)
+    assert torch.equal(leaf.grad, want) and not e.requires_grad
+    zs = z.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w2, e2 = lce.route_forward(zs, 4, "sigmoid", scale=2.0)
+        dz2 = lce.route_backward(zs, e2, dw, "sigmoid", scale=2.0)
+    z3 = draw(64, 32, torch.float32, seed=11).to(dev)
+    zs.copy_(z3)
+    g.replay()
+    w3, e3 = lce.route_forward(z3, 4, "sigmoid", scale=2.0)
+    assert torch.equal(w2, w3) and torch.equal(e2, e3)
+    assert torch.equal(dz2, lce.route_backward(z3, e3, dw, "sigmoid",
+                                               scale=2.0))
+    assert lce.get_error() == 0
