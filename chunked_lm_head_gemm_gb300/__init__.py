@@ -16,6 +16,7 @@ include/lce.h; this package is the thin Python binding.
     dx, dWg, dWu, dWd = lce.mlp_backward(x, Wg, Wu, Wd, dy)
     y = lce.sequence_tiled_mlp(x, Wg, Wu, Wd)   # the same, autograd-aware
     w, experts = lce.route_experts(logits, top_k)   # router, autograd-aware
+    y = lce.experts_mlp(x, Wg, Wu, Wd, w, experts)  # experts, autograd-aware
     from chunked_lm_head_gemm_gb300 import sharded   # rows split over ranks
     loss, lse, dH, dW = sharded.forward_backward(h, W, labels, group)
     from chunked_lm_head_gemm_gb300 import vocab_parallel as vp  # head split
@@ -23,18 +24,22 @@ include/lce.h; this package is the thin Python binding.
     dH, dW_slice = vp.backward(h, W[v0:v0 + Vs], labels, lse, dloss, v0, V,
                                group)
 """
-from ._binding import (IGNORE_INDEX, LCEError, LinearCrossEntropy,
-                       RouteExperts, SequenceTiledMLP, alloc_workspace, backward, count_valid,
-                       default_chunk_rows, forward, forward_backward,
+from ._binding import (ExpertsMLP, IGNORE_INDEX, LCEError, LinearCrossEntropy,
+                       RouteExperts, SequenceTiledMLP, alloc_workspace,
+                       backward, count_valid, default_chunk_rows,
+                       experts_backward, experts_forward, experts_mlp,
+                       experts_workspace_size, forward, forward_backward,
                        get_error, library_path, linear_cross_entropy, load,
                        mlp_backward, mlp_forward, mlp_workspace_size,
                        profile_start, profile_stop, route_backward,
                        route_experts, route_forward, scale_gradients,
                        sequence_tiled_mlp, workspace_size)
 
-__all__ = ["IGNORE_INDEX", "LCEError", "LinearCrossEntropy", "RouteExperts",
-           "SequenceTiledMLP", "alloc_workspace",
-           "backward", "count_valid", "default_chunk_rows", "forward",
+__all__ = ["ExpertsMLP", "IGNORE_INDEX", "LCEError", "LinearCrossEntropy",
+           "RouteExperts", "SequenceTiledMLP", "alloc_workspace",
+           "backward", "count_valid", "default_chunk_rows",
+           "experts_backward", "experts_forward", "experts_mlp",
+           "experts_workspace_size", "forward",
            "forward_backward", "get_error", "library_path",
            "linear_cross_entropy", "load", "mlp_backward", "mlp_forward",
            "mlp_workspace_size", "profile_start", "profile_stop",

@@ -49,7 +49,9 @@ EXPORTED = ("lce_workspace_size", "lce_default_chunk_rows", "lce_forward",
             "lce_shard_sums", "lce_combine_shards", "lce_forward_slice_ex",
             "lce_combine_slices_ex", "lce_backward_slice_ex",
             "lce_forward_slice_exp_ex", "lce_backward_slice_exp_ex",
-            "lce_route_forward", "lce_route_backward")
+            "lce_route_forward", "lce_route_backward",
+            "lce_experts_workspace_size", "lce_experts_forward",
+            "lce_experts_backward")
 
 KERNEL_KINDS = 33
 
@@ -200,6 +202,16 @@ def load(build_if_missing: bool = False):
         lib.lce_route_backward.argtypes = [p, i32, p, p, i64, i64, ropts, p,
                                            p]
         lib.lce_route_backward.restype = i32
+        lib.lce_experts_workspace_size.argtypes = [i64, i64, i64, i64, i64,
+                                                   i32]
+        lib.lce_experts_workspace_size.restype = sz
+        lib.lce_experts_forward.argtypes = [p, p, p, p, p, i32, p, i64, i64,
+                                            i64, i64, i64, p, p, sz, p]
+        lib.lce_experts_forward.restype = i32
+        lib.lce_experts_backward.argtypes = [p, p, p, p, p, i32, p, p, i64,
+                                             i64, i64, i64, i64, i32, p, p, p,
+                                             p, p, p, sz, p]
+        lib.lce_experts_backward.restype = i32
         lib.lce_set_cta_pair.argtypes = [i32]
         lib.lce_set_cta_pair.restype = i32
         lib.lce_get_cta_pair.argtypes = []
@@ -840,6 +852,93 @@ def _check_experts(experts, L):
                          "tensor")
 
 
+def _check_experts_mlp(x, Wg, Wu, Wd, weights, experts):
+    if not all(t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous()
+               for t in (x, Wg, Wu, Wd)):
+        raise ValueError("x, Wg, Wu, Wd must be contiguous bf16 CUDA tensors")
+    if x.dim() != 2 or Wg.dim() != 3:
+        raise ValueError("expected x [L,H], Wg and Wu [E,I,H], Wd [E,H,I]")
+    L, H = x.shape
+    E, I = Wg.shape[:2]
+    if Wg.shape != (E, I, H) or Wu.shape != (E, I, H) or Wd.shape != (E, H, I):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, Wg "
+                         f"{tuple(Wg.shape)}, Wu {tuple(Wu.shape)}, Wd "
+                         f"{tuple(Wd.shape)}")
+    _check_experts(experts, L)
+    if not (weights.is_cuda and weights.shape == experts.shape and
+            weights.is_contiguous()):
+        raise ValueError("weights must be a contiguous CUDA tensor of "
+                         "experts' shape")
+    return L, H, I, E, experts.shape[1], _dtype_code(weights)
+
+
+def experts_workspace_size(L: int, H: int, I: int, E: int, top_k: int,
+                           backward: bool = False) -> int:
+    n = load().lce_experts_workspace_size(L, H, I, E, top_k, int(backward))
+    if n == 0:
+        raise ValueError(f"invalid experts sizes L={L} H={H} I={I} E={E} "
+                         f"top_k={top_k}")
+    return n
+
+
+def experts_forward(x, Wg, Wu, Wd, weights, experts, workspace=None,
+                    y_out=None):
+    """y_t = sum_k weights[t,k] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)), e =
+    experts[t,k] (-1: dropped): x bf16 [L,H], Wg and Wu bf16 [E,I,H], Wd bf16
+    [E,H,I], weights [L,top_k] (bf16 or fp32), experts int32 [L,top_k]."""
+    lib = load()
+    L, H, I, E, K, code = _check_experts_mlp(x, Wg, Wu, Wd, weights, experts)
+    if workspace is None:
+        workspace = torch.empty(experts_workspace_size(L, H, I, E, K),
+                                dtype=torch.uint8, device=x.device)
+    y = y_out if y_out is not None else torch.empty_like(x)
+    st = lib.lce_experts_forward(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
+                                 Wd.data_ptr(), weights.data_ptr(), code,
+                                 experts.data_ptr(), L, H, I, E, K,
+                                 y.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel(), _stream_ptr(x.device))
+    _check(st, "lce_experts_forward")
+    return y
+
+
+def experts_backward(x, Wg, Wu, Wd, weights, experts, dy, workspace=None,
+                     grad_dtype=torch.float32, compute_dx: bool = True,
+                     compute_dWgu: bool = True, compute_dWd: bool = True,
+                     compute_dweights: bool = True):
+    """Returns (dx bf16 [L,H], dWg, dWu, dWd of grad_dtype (fp32 or bf16) in
+    the weights' shapes, dweights of weights' dtype) for upstream gradient dy,
+    recomputing the intermediates. compute_* = False skips that gradient
+    (returned as None)."""
+    lib = load()
+    L, H, I, E, K, code = _check_experts_mlp(x, Wg, Wu, Wd, weights, experts)
+    if not (dy.is_cuda and dy.dtype == torch.bfloat16 and dy.is_contiguous()
+            and dy.shape == (L, H)):
+        raise ValueError("dy must be a contiguous bf16 CUDA [L,H] tensor")
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("grad_dtype must be float32 or bfloat16")
+    if workspace is None:
+        workspace = torch.empty(experts_workspace_size(L, H, I, E, K, True),
+                                dtype=torch.uint8, device=x.device)
+    dx = dWg = dWu = dWd = dw = None
+    if compute_dx:
+        dx = torch.empty_like(x)
+    if compute_dWgu:
+        dWg = torch.empty_like(Wg, dtype=grad_dtype)
+        dWu = torch.empty_like(Wu, dtype=grad_dtype)
+    if compute_dWd:
+        dWd = torch.empty_like(Wd, dtype=grad_dtype)
+    if compute_dweights:
+        dw = torch.empty_like(weights)
+    st = lib.lce_experts_backward(
+        x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
+        weights.data_ptr(), code, experts.data_ptr(), dy.data_ptr(), L, H, I,
+        E, K, LCE_F32 if grad_dtype == torch.float32 else LCE_BF16, _ptr(dx),
+        _ptr(dWg), _ptr(dWu), _ptr(dWd), _ptr(dw), workspace.data_ptr(),
+        workspace.numel(), _stream_ptr(x.device))
+    _check(st, "lce_experts_backward")
+    return dx, dWg, dWu, dWd, dw
+
+
 def set_cta_pair(enable: bool):
     """Run the contractions on CTA pairs (cta_group::2) or single CTAs."""
     _check(load().lce_set_cta_pair(1 if enable else 0), "lce_set_cta_pair")
@@ -990,6 +1089,36 @@ def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None,
     """(weights, experts) of router logits, with autograd (route_forward)."""
     return RouteExperts.apply(logits, top_k, scoring, bias, n_group,
                               topk_group, group_top, renormalize, scale)
+
+
+class ExpertsMLP(torch.autograd.Function):
+    """experts_forward under autograd: forward keeps only its inputs,
+    backward recomputes the activations and returns dx, the weight gradients
+    in bf16 (the weights' type) and dweights, computing only those autograd
+    asks for. dy is made a contiguous bf16 tensor first."""
+
+    @staticmethod
+    def forward(ctx, x, Wg, Wu, Wd, weights, experts):
+        ctx.save_for_backward(x, Wg, Wu, Wd, weights, experts)
+        return experts_forward(x, Wg, Wu, Wd, weights, experts)
+
+    @staticmethod
+    def backward(ctx, dy):
+        need = ctx.needs_input_grad
+        if not any(need[:5]):
+            return (None,) * 6
+        dy = dy.to(torch.bfloat16).contiguous()
+        dx, dWg, dWu, dWd, dw = experts_backward(
+            *ctx.saved_tensors, dy, grad_dtype=torch.bfloat16,
+            compute_dx=need[0], compute_dWgu=need[1] or need[2],
+            compute_dWd=need[3], compute_dweights=need[4])
+        return (dx, dWg if need[1] else None, dWu if need[2] else None, dWd,
+                dw, None)
+
+
+def experts_mlp(x, Wg, Wu, Wd, weights, experts):
+    """The experts' gated MLP (experts_forward) with autograd."""
+    return ExpertsMLP.apply(x, Wg, Wu, Wd, weights, experts)
 
 
 def sequence_tiled_mlp(x, Wg, Wu, Wd, chunk_rows: int = 0):

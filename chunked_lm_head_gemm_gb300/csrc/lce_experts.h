@@ -1,0 +1,86 @@
+// Internal declarations of the experts' gated MLP: the plan that groups the
+// slots (token, choice) by expert, and the launch wrappers of its kernels.
+//
+// Rows: the slots of an expert, in slot order, form one segment of rows;
+// segments start at multiples of SEG_ROWS and are padded to one with rows
+// that hold no slot (token = L, which every gathering load reads as zero).
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/lce.h"
+
+namespace lce {
+
+constexpr int SEG_ROWS = 64;     // one K block of the weight gradients
+constexpr int MAX_EXPERTS = 1024;
+constexpr int PLAN_CHUNK = 2048; // slots of one counting block
+constexpr int PLAN_SMALL = 8192; // up to here one block makes the plan
+
+struct PlanHead {
+  int tiles;  // row tiles of at most 128 rows
+  int rows;   // padded rows
+};
+
+// A row tile: `rows` (64 or 128, padded) rows from row0 of one expert.
+struct RowTile {
+  int expert, row0, rows, pad;
+};
+
+// The plan, in device memory.
+struct Plan {
+  PlanHead* head;
+  RowTile* tile;  // [max_tiles]
+  int2* seg;      // [E]: first row, padded rows
+  int* token;     // [max_rows]: token of a row, L for a padding row
+  int* slot;      // [max_rows]: slot of a row, -1 for a padding row
+  int* row;       // [n]: row of a slot, -1 where it is dropped
+  int* count;     // [E]: slots of an expert
+  int* hist;      // [E][chunks]: slots of an expert in a chunk, then before it
+};
+
+// Queues the plan of `n` slots (experts[n], `K` to a token). Deterministic:
+// integer counts and positions that follow slot order.
+cudaError_t launch_plan(const int32_t* experts, int64_t n, int K, int64_t L,
+                        int E, const Plan& p, unsigned* err, cudaStream_t s);
+
+// out[t][:] = sum_k w[t][k] rows[row(t, k)][:] in bf16, k in order, dropped
+// slots left out (w NULL: weights 1).
+cudaError_t launch_combine(const float* rows, const int* row, const void* w,
+                           lce_dtype wdt, int64_t L, int K, int64_t H,
+                           void* out, cudaStream_t s);
+
+// dweights[slot] = sum over the column tiles of part[tile][row], in order.
+cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,
+                            const int* row, int64_t n, lce_dtype wdt,
+                            void* dweights, cudaStream_t s);
+
+// ---- grouped contractions ----------------------------------------------------
+struct ExpertsArgs {
+  Plan plan;
+  int64_t L, H, I;
+  int E;
+  uint64_t timeout_ns;
+  unsigned* err;
+  int grid;
+  // operand maps by use; each kernel takes the ones it names
+  const void *x, *dy, *Wg, *Wu, *Wd;
+  uint16_t *a, *dg, *du;   // [max_rows][I]
+  int64_t max_rows;
+  float* rows_out;         // [max_rows][H] fp32 (DOWN, DX)
+  const void* w;           // routing weights of the slots
+  lce_dtype wdt;
+  float* part;             // [ceil(I / 128)][max_rows] of da . a
+  void *dW, *dW2;          // weight gradients
+  lce_dtype gdt;
+};
+
+lce_status launch_experts_up(const ExpertsArgs& a, cudaStream_t s);
+lce_status launch_experts_down(const ExpertsArgs& a, cudaStream_t s);
+lce_status launch_experts_dgu(const ExpertsArgs& a, cudaStream_t s);
+lce_status launch_experts_dx(const ExpertsArgs& a, cudaStream_t s);
+lce_status launch_experts_dwd(const ExpertsArgs& a, cudaStream_t s);
+lce_status launch_experts_dwgu(const ExpertsArgs& a, cudaStream_t s);
+
+}  // namespace lce

@@ -1,0 +1,775 @@
+// Grouped tensor-core contractions of the experts' gated MLP. Rows are the
+// padded segments of the plan (lce_experts.h); an expert's rows meet only
+// its own weights. One persistent kernel template, six uses:
+//   UP    a = silu(g) u, g | u = x[token] (Wg_e | Wu_e)^T           K = H
+//   DOWN  rows = a Wd_e^T                                           K = I
+//   DGU   da' = dy[token] Wd_e beside g and u again, all three in tensor
+//         memory at once; the epilogue forms da = w da', dg, du, w a and
+//         the row's share of dw = da' . a without rounding g, u or da'
+//   DX    rows = [dg | du] [Wg_e ; Wu_e]                            K = 2 I
+//   DWD   dWd_e = dy[token]^T (w a)                       K = rows of e
+//   DWGU  dWg_e, dWu_e = dg^T x[token], du^T x[token]     K = rows of e
+// The token rows of x and dy are never copied: the producer gathers them
+// straight into the swizzled stage, four rows to one TMA instruction, one
+// instruction to a lane.
+//
+// Work: units are 128 x 256 output tiles (UP and DGU 128 x 128 of a, whose
+// accumulator columns are g | u), walked in a static stride by one CTA per
+// SM with the roles of k_gemm: producer warp, MMA lane, four epilogue warps.
+// A unit's accumulation is split into parts, each with its own columns,
+// number of buffers and K loop.
+#include "lce_device.cuh"
+#include "lce_experts.h"
+#include "lce_host.h"
+
+namespace lce {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+
+struct Maps {
+  CUtensorMap a0, a1;       // A operands
+  CUtensorMap b0, b1, b2;   // B operands
+  CUtensorMap s0, s1, s2;   // store maps (32 x 32 boxes)
+};
+
+struct Geom {
+  const PlanHead* head;
+  const RowTile* tile;
+  const int2* seg;
+  const int* token;
+  const int* slot;
+  int H, I, E, L;
+  int kb_h, kb_i;   // 64-wide K blocks of H and I
+  int num_n;        // column tiles of a row tile; or of an expert's gradient
+  int num_m;        // row tiles of an expert's gradient
+  uint64_t timeout_ns;
+};
+
+struct Unit {
+  int e;        // expert
+  int row0;     // first row (row tiles) or first K row (weight gradients)
+  int rows;     // padded rows: of the tile, or the K extent
+  int m, n;     // tile of the output
+};
+
+// ---- loads -------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
+                                            int c0, int c1, int c2,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_"
+      "tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// Four rows of 64 elements from column c0 (a multiple of 64) to dst, 128
+// bytes each, in the stage's 128-byte swizzle; rows past the map read as 0.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm,
+                                            int c0, int4 r, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::"
+      "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(r.x), "r"(r.y),
+      "r"(r.z), "r"(r.w), "r"(bar)
+      : "memory");
+}
+
+// Rows [row0, row0 + rows) of the plan, K-major: lane q takes rows 4q...
+__device__ __forceinline__ void gather_rows(uint32_t sa, const CUtensorMap* tm,
+                                            const Geom& g, int row0, int rows,
+                                            int c0, uint32_t bar, int lane) {
+  if (4 * lane < rows) {
+    const int4 t = __ldg(reinterpret_cast<const int4*>(g.token + row0) + lane);
+    tma_gather4(sa + lane * 512, tm, c0, t, bar);
+  }
+}
+
+// 64 rows of the plan as the K index of an MN-major operand, `boxes` boxes
+// of 64 columns from c0.
+__device__ __forceinline__ void gather_cols(uint32_t sa, const CUtensorMap* tm,
+                                            const Geom& g, int row0, int boxes,
+                                            int c0, uint32_t bar, int lane) {
+  const int q = lane & 15;
+  const int4 t = __ldg(reinterpret_cast<const int4*>(g.token + row0) + q);
+  for (int j = lane >> 4; j < boxes; j += 2)
+    tma_gather4(sa + j * 8192 + q * 512, tm, c0 + 64 * j, t, bar);
+}
+
+// ---- the uses ----------------------------------------------------------------
+struct RowUnits {
+  __device__ static int units(const Geom& g) {
+    return __ldg(&g.head->tiles) * g.num_n;
+  }
+  __device__ static Unit unit(const Geom& g, int u) {
+    const int t = u / g.num_n;
+    const int4 r = __ldg(reinterpret_cast<const int4*>(g.tile) + t);
+    return Unit{r.x, r.y, r.z, t, u - t * g.num_n};
+  }
+};
+struct GradUnits {
+  __device__ static int units(const Geom& g) { return g.E * g.num_m * g.num_n; }
+  __device__ static Unit unit(const Geom& g, int u) {
+    const int per = g.num_m * g.num_n;
+    const int e = u / per, r = u - e * per;
+    const int2 s = __ldg(g.seg + e);
+    return Unit{e, s.x, s.y, r / g.num_n, r % g.num_n};
+  }
+};
+
+template <int N_, int COL_, int BUFS_, bool A_MN_, bool B_MN_>
+struct Part {
+  static constexpr int N = N_, COL = COL_, BUFS = BUFS_;
+  static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
+};
+
+struct OpUp : RowUnits {
+  static constexpr int PARTS = 1;
+  using P0 = Part<256, 0, 2, false, false>;
+  using P1 = P0;
+  template <int P>
+  __device__ static int blocks(const Geom& g, const Unit&) { return g.kb_h; }
+  template <int P>
+  __device__ static uint32_t bytes(const Unit& u) {
+    return u.rows * 128u + 32768u;
+  }
+  template <int P>
+  __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
+                              int lane) {
+    gather_rows(sa, &m.a0, g, u.row0, u.rows, kb * BK, bar, lane);
+    if (lane == 0) {
+      tma_load_3d(sb, &m.b0, kb * BK, u.n * 128, u.e, bar);
+      tma_load_3d(sb + 16384, &m.b1, kb * BK, u.n * 128, u.e, bar);
+    }
+  }
+};
+
+struct OpDown : RowUnits {
+  static constexpr int PARTS = 1;
+  using P0 = Part<256, 0, 2, false, false>;
+  using P1 = P0;
+  template <int P>
+  __device__ static int blocks(const Geom& g, const Unit&) { return g.kb_i; }
+  template <int P>
+  __device__ static uint32_t bytes(const Unit& u) {
+    return u.rows * 128u + 32768u;
+  }
+  template <int P>
+  __device__ static void load(const Maps& m, const Geom&, const Unit& u,
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
+                              int lane) {
+    if (lane == 0) {
+      tma_load_2d(sa, &m.a0, kb * BK, u.row0, bar);
+      if (u.rows > 64) tma_load_2d(sa + 8192, &m.a0, kb * BK, u.row0 + 64, bar);
+      tma_load_3d(sb, &m.b0, kb * BK, u.n * 256, u.e, bar);
+    }
+  }
+};
+
+struct OpDx : RowUnits {
+  static constexpr int PARTS = 1;
+  using P0 = Part<256, 0, 2, false, true>;
+  using P1 = P0;
+  template <int P>
+  __device__ static int blocks(const Geom& g, const Unit&) {
+    return 2 * g.kb_i;
+  }
+  template <int P>
+  __device__ static uint32_t bytes(const Unit& u) {
+    return u.rows * 128u + 32768u;
+  }
+  template <int P>
+  __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
+                              int lane) {
+    if (lane != 0) return;
+    const bool second = kb >= g.kb_i;  // du and Wu after dg and Wg
+    const CUtensorMap* ta = second ? &m.a1 : &m.a0;
+    const CUtensorMap* tb = second ? &m.b1 : &m.b0;
+    const int k0 = (second ? kb - g.kb_i : kb) * BK;
+    tma_load_2d(sa, ta, k0, u.row0, bar);
+    if (u.rows > 64) tma_load_2d(sa + 8192, ta, k0, u.row0 + 64, bar);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      tma_load_3d(sb + j * 8192, tb, u.n * 256 + 64 * j, k0, u.e, bar);
+  }
+};
+
+// da' first (two buffers of 128 columns), then g | u (one of 256): while the
+// epilogue reads a tile, the next tile's da' is already being accumulated.
+struct OpDgu : RowUnits {
+  static constexpr int PARTS = 2;
+  using P0 = Part<128, 256, 2, false, true>;
+  using P1 = Part<256, 0, 1, false, false>;
+  template <int P>
+  __device__ static int blocks(const Geom& g, const Unit&) { return g.kb_h; }
+  template <int P>
+  __device__ static uint32_t bytes(const Unit& u) {
+    return u.rows * 128u + (P == 0 ? 16384u : 32768u);
+  }
+  template <int P>
+  __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
+                              int lane) {
+    if (P == 0) {
+      gather_rows(sa, &m.a1, g, u.row0, u.rows, kb * BK, bar, lane);
+      if (lane == 0) {
+        tma_load_3d(sb, &m.b2, u.n * 128, kb * BK, u.e, bar);
+        tma_load_3d(sb + 8192, &m.b2, u.n * 128 + 64, kb * BK, u.e, bar);
+      }
+    } else {
+      OpUp::load<0>(m, g, u, kb, sa, sb, bar, lane);
+    }
+  }
+};
+
+struct OpDwd : GradUnits {
+  static constexpr int PARTS = 1;
+  using P0 = Part<256, 0, 2, true, true>;
+  using P1 = P0;
+  template <int P>
+  __device__ static int blocks(const Geom&, const Unit& u) {
+    return u.rows / SEG_ROWS;
+  }
+  template <int P>
+  __device__ static uint32_t bytes(const Unit&) { return STAGE_BYTES; }
+  template <int P>
+  __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
+                              int lane) {
+    const int k0 = u.row0 + kb * BK;
+    gather_cols(sa, &m.a0, g, k0, 2, u.m * BM, bar, lane);
+    if (lane == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        tma_load_2d(sb + j * 8192, &m.b0, u.n * BN + 64 * j, k0, bar);
+    }
+  }
+};
+
+struct OpDwgu : GradUnits {
+  static constexpr int PARTS = 1;
+  using P0 = Part<256, 0, 2, true, true>;
+  using P1 = P0;
+  template <int P>
+  __device__ static int blocks(const Geom&, const Unit& u) {
+    return u.rows / SEG_ROWS;
+  }
+  template <int P>
+  __device__ static uint32_t bytes(const Unit&) { return STAGE_BYTES; }
+  template <int P>
+  __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
+                              int lane) {
+    const int k0 = u.row0 + kb * BK;
+    const int half = g.num_m >> 1;  // dWg's row tiles, then dWu's
+    const bool second = u.m >= half;
+    const int m0 = (second ? u.m - half : u.m) * BM;
+    if (lane == 0) {
+      const CUtensorMap* ta = second ? &m.a1 : &m.a0;
+      tma_load_2d(sa, ta, m0, k0, bar);
+      tma_load_2d(sa + 8192, ta, m0 + 64, k0, bar);
+    }
+    gather_cols(sb, &m.b0, g, k0, 4, u.n * BN, bar, lane);
+  }
+};
+
+// ---- epilogues ---------------------------------------------------------------
+// Each runs on a warp's 32 rows of a finished unit; taddr is the warp's lane
+// quarter of tensor memory.
+
+// a = silu(g) u in bf16.
+struct EpiUp : EpiBase {
+  struct Params {
+    int unused;
+  };
+  __device__ __forceinline__ void tile(const Params&, const Maps& m,
+                                       const Geom& g, const Unit& u,
+                                       uint32_t taddr, int r, int i) {
+    const int wr = r & ~31;
+    if (wr >= u.rows) return;
+    const uint32_t t0 = taddr + (i & 1) * 256;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      const int j0 = u.n * 128 + c * 32;
+      if (j0 >= g.I) break;
+      float gv[32], uv[32];
+      tmem_ld32(t0 + c * 32, gv);
+      tmem_ld32(t0 + 128 + c * 32, uv);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) uv[k] *= gv[k] * sigmoid_fast(gv[k]);
+      store_box(uv, j0, u.row0 + wr, &m.s0);
+    }
+  }
+};
+
+// fp32 rows of H columns.
+struct EpiRows : EpiBase {
+  struct Params {
+    float* out;
+  };
+  __device__ __forceinline__ void tile(const Params& p, const Maps&,
+                                       const Geom& g, const Unit& u,
+                                       uint32_t taddr, int r, int i) {
+    if ((r & ~31) >= u.rows) return;
+    float* row = p.out + static_cast<int64_t>(u.row0 + r) * g.H;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      const int j0 = u.n * 256 + c * 32;
+      if (j0 >= g.H) break;
+      float v[32];
+      tmem_ld32(taddr + (i & 1) * 256 + c * 32, v);
+      float4* d = reinterpret_cast<float4*>(row + j0);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (j0 + 4 * q < g.H)  // H % 8 == 0
+          d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2],
+                             v[4 * q + 3]);
+    }
+  }
+};
+
+// dg, du, w a and the row's part of da' . a (this tile's columns).
+struct EpiDgu : EpiBase {
+  struct Params {
+    const void* w;
+    int w_f32;
+    float* part;
+    int64_t stride;
+  };
+  __device__ __forceinline__ void tile(const Params& p, const Maps& m,
+                                       const Geom& g, const Unit& u,
+                                       uint32_t taddr, int r, int i) {
+    const int wr = r & ~31;
+    if (wr >= u.rows) return;
+    const int slot = __ldg(g.slot + u.row0 + r);
+    float w = 0.f;
+    if (slot >= 0)
+      w = p.w_f32 ? __ldg(static_cast<const float*>(p.w) + slot)
+                  : static_cast<float>(
+                        static_cast<const __nv_bfloat16*>(p.w)[slot]);
+    const uint32_t tda = taddr + 256 + (i & 1) * 128;
+    float dot = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      const int j0 = u.n * 128 + c * 32;
+      if (j0 >= g.I) break;
+      float gv[32], uv[32], da[32];
+      tmem_ld32(taddr + c * 32, gv);
+      tmem_ld32(taddr + 128 + c * 32, uv);
+      tmem_ld32(tda + c * 32, da);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float s = sigmoid_fast(gv[k]);
+        const float sil = gv[k] * s;     // silu(g)
+        const float a = sil * uv[k];
+        dot = fmaf(da[k], a, dot);
+        const float d = w * da[k];
+        // silu'(g) = s (1 + g (1 - s))
+        const float dg = d * uv[k] * s * (1.f + gv[k] * (1.f - s));
+        gv[k] = dg;
+        da[k] = d * sil;                 // du
+        uv[k] = w * a;
+      }
+      store_box(gv, j0, u.row0 + wr, &m.s0);
+      store_box(da, j0, u.row0 + wr, &m.s1);
+      store_box(uv, j0, u.row0 + wr, &m.s2);
+    }
+    p.part[u.n * p.stride + u.row0 + r] = dot;
+  }
+};
+
+// An expert's weight gradient, bf16 or fp32, zero where it has no rows.
+struct EpiGrad2 : EpiBase {
+  struct Params {
+    void *out, *out2;  // [E][rows][cols]; out2: the second half of the tiles
+    int f32;
+    int rows, cols;    // of one expert's gradient
+  };
+  __device__ __forceinline__ void tile(const Params& p, const Maps&,
+                                       const Geom& g, const Unit& u,
+                                       uint32_t taddr, int r, int i) {
+    void* base = p.out;
+    int m = u.m;
+    if (p.out2 != nullptr && m >= (g.num_m >> 1)) {
+      base = p.out2;
+      m -= g.num_m >> 1;
+    }
+    const int row = m * BM + r;
+    const int64_t at =
+        (static_cast<int64_t>(u.e) * p.rows + row) * p.cols;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      const int j0 = u.n * BN + c * 32;
+      if (j0 >= p.cols) break;
+      float v[32];
+      if (u.rows > 0) {
+        tmem_ld32(taddr + (i & 1) * 256 + c * 32, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+      }
+      if (row >= p.rows) continue;
+      if (p.f32) {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + at +
+                                              j0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (j0 + 4 * q < p.cols)  // cols % 8 == 0
+            d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2],
+                               v[4 * q + 3]);
+      } else {
+        uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at +
+                                            j0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (j0 + 8 * q < p.cols)
+            d[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                              pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                              pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                              pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+      }
+    }
+  }
+};
+
+// ---- roles -------------------------------------------------------------------
+// Barriers: full / empty per stage; tfull[2]: a unit's accumulators are
+// ready (by unit parity); tempty[part][2]: a part's buffer may be overwritten.
+struct Bars {
+  uint32_t base;
+  __device__ uint32_t full(int s) const { return base + 8u * s; }
+  __device__ uint32_t empty(int s) const { return base + 8u * (STAGES + s); }
+  __device__ uint32_t tfull(int b) const {
+    return base + 8u * (2 * STAGES + b);
+  }
+  __device__ uint32_t tempty(int part, int b) const {
+    return base + 8u * (2 * STAGES + 2 + 2 * part + b);
+  }
+  __device__ uint32_t drain() const { return base + 8u * (2 * STAGES + 6); }
+};
+constexpr int NUM_BARS = 2 * STAGES + 7;
+
+struct Ring {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <class Op, int P>
+__device__ __forceinline__ bool produce(const Maps& m, const Geom& g,
+                                        const Unit& u, uint32_t sa,
+                                        uint32_t sb, const Bars& bars,
+                                        Ring& ring, uint32_t& issued,
+                                        const WaitCtx& ctx, int lane) {
+  const int n = Op::template blocks<P>(g, u);
+  for (int kb = 0; kb < n; ++kb) {
+    const bool got =
+        mbar_wait(bars.empty(ring.stage), ring.phase ^ 1u, ctx, true);
+    if (!__all_sync(FULL, got)) return false;
+    const uint32_t fb = bars.full(ring.stage);
+    if (lane == 0) mbar_arrive_expect_tx(fb, Op::template bytes<P>(u));
+    __syncwarp();
+    Op::template load<P>(m, g, u, kb, sa + ring.stage * A_STAGE_BYTES,
+                         sb + ring.stage * B_STAGE_BYTES, fb, lane);
+    __syncwarp();
+    ++issued;
+    ring.next();
+  }
+  return true;
+}
+
+template <bool A_MN, bool B_MN, int N>
+__device__ __forceinline__ constexpr uint32_t idesc_n() {
+  return (1u << 4) | (1u << 7) | (1u << 10) |
+         (static_cast<uint32_t>(A_MN) << 15) |
+         (static_cast<uint32_t>(B_MN) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(BM >> 4) << 24);
+}
+
+template <class Op, int P, class PT>
+__device__ __forceinline__ bool multiply(const Geom& g, const Unit& u, int i,
+                                         uint32_t sa, uint32_t sb,
+                                         const Bars& bars, Ring& ring,
+                                         uint32_t tmem, const WaitCtx& ctx) {
+  constexpr uint32_t IDESC = idesc_n<PT::A_MN, PT::B_MN, PT::N>();
+  constexpr uint32_t MN_LBO = 64 * BK * 2;
+  const int buf = PT::BUFS == 2 ? (i & 1) : 0;
+  const uint32_t turn = PT::BUFS == 2 ? (i >> 1) : i;
+  if (!mbar_wait(bars.tempty(P, buf), (turn & 1u) ^ 1u, ctx, true))
+    return false;
+  tc_fence_after();
+  const uint32_t d = tmem + PT::COL + buf * PT::N;
+  const int n = Op::template blocks<P>(g, u);
+  for (int kb = 0; kb < n; ++kb) {
+    if (!mbar_wait(bars.full(ring.stage), ring.phase, ctx, true)) return false;
+    tc_fence_after();
+    const uint32_t a = sa + ring.stage * A_STAGE_BYTES;
+    const uint32_t b = sb + ring.stage * B_STAGE_BYTES;
+#pragma unroll
+    for (int k = 0; k < BK / 16; ++k) {
+      const uint64_t ad = PT::A_MN ? sdesc_sw128(a + k * 2048, MN_LBO, 1024)
+                                   : sdesc_sw128(a + k * 32, 16, 1024);
+      const uint64_t bd = PT::B_MN ? sdesc_sw128(b + k * 2048, MN_LBO, 1024)
+                                   : sdesc_sw128(b + k * 32, 16, 1024);
+      tc_mma(d, ad, bd, IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+    }
+    tc_commit(bars.empty(ring.stage));
+    ring.next();
+  }
+  return true;
+}
+
+template <class Op, class Epi>
+__global__ void __launch_bounds__(GEMM_THREADS, 1)
+    k_experts(const __grid_constant__ Maps maps, const Geom g,
+              const typename Epi::Params p, unsigned* err) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t sa = base, sb = base + STAGES * A_STAGE_BYTES;
+  const Bars bars{base + STAGES * STAGE_BYTES};
+  uint8_t* misc = smem_raw + (bars.base - raw) + 8 * NUM_BARS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile uint32_t* abort_flag =
+      reinterpret_cast<volatile uint32_t*>(misc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bars.full(s), 1);
+      mbar_init(bars.empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bars.tfull(b), 1);
+      for (int q = 0; q < 2; ++q) mbar_init(bars.tempty(q, b), 128);
+    }
+    mbar_init(bars.drain(), 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx ctx{abort_flag, err, g.timeout_ns};
+  const int units = Op::units(g);
+
+  if (warp == 0) {
+    Ring ring;
+    uint32_t issued = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const Unit t = Op::unit(g, u);
+      ok = produce<Op, 0>(maps, g, t, sa, sb, bars, ring, issued, ctx, lane);
+      if (Op::PARTS == 2 && ok)
+        ok = produce<Op, Op::PARTS - 1>(maps, g, t, sa, sb, bars, ring, issued,
+                                        ctx, lane);
+    }
+    // every copy issued must have landed before the CTA may exit
+    for (int s = 0; s < STAGES; ++s) {
+      const uint32_t cnt = issued / STAGES +
+                           (static_cast<uint32_t>(s) < issued % STAGES ? 1u : 0u);
+      if (cnt) mbar_wait(bars.full(s), (cnt - 1u) & 1u, ctx, false);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      Ring ring;
+      bool ok = true;
+      int i = 0;  // units this CTA has accumulated
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++i) {
+        const Unit t = Op::unit(g, u);
+        ok = multiply<Op, 0, typename Op::P0>(g, t, i, sa, sb, bars, ring,
+                                              tmem, ctx);
+        if (Op::PARTS == 2 && ok)
+          ok = multiply<Op, Op::PARTS - 1, typename Op::P1>(
+              g, t, i, sa, sb, bars, ring, tmem, ctx);
+        if (ok) tc_commit(bars.tfull(i & 1));
+      }
+      tc_commit(bars.drain());
+      mbar_wait(bars.drain(), 0, ctx, false);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    const int r = q * 32 + lane;
+    Epi epi;
+    epi.stage = base + STAGES * STAGE_BYTES + 1024 +
+                static_cast<uint32_t>(q) * 2u * EPI_BUF_BYTES;
+    int i = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+      const Unit t = Op::unit(g, u);
+      const bool got = mbar_wait(bars.tfull(i & 1), (i >> 1) & 1, ctx, true);
+      if (!__all_sync(FULL, got)) break;
+      tc_fence_after();
+      epi.tile(p, maps, g, t, tmem + (static_cast<uint32_t>(q * 32) << 16), r,
+               i);
+      tc_fence_before();
+      mbar_arrive(bars.tempty(0, Op::P0::BUFS == 2 ? (i & 1) : 0));
+      if (Op::PARTS == 2)
+        mbar_arrive(bars.tempty(1, Op::P1::BUFS == 2 ? (i & 1) : 0));
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// ---- host side ---------------------------------------------------------------
+constexpr CUtensorMapDataType BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+constexpr CUtensorMapSwizzle SW128 = CU_TENSOR_MAP_SWIZZLE_128B;
+
+// [rows][cols] bf16, boxes of box_c x box_r.
+lce_status map2(CUtensorMap* m, const void* p, int64_t cols, int64_t rows,
+                uint32_t box_c, uint32_t box_r,
+                CUtensorMapSwizzle swz = SW128) {
+  const uint64_t d[2] = {static_cast<uint64_t>(cols),
+                         static_cast<uint64_t>(rows)};
+  const uint64_t st[1] = {static_cast<uint64_t>(cols) * 2};
+  const uint32_t b[2] = {box_c, box_r};
+  return make_tmap_nd(m, BF, 2, p, d, st, b, swz);
+}
+// [E][rows][cols] bf16, boxes inside one expert.
+lce_status map3(CUtensorMap* m, const void* p, int64_t cols, int64_t rows,
+                int64_t E, uint32_t box_c, uint32_t box_r) {
+  const uint64_t d[3] = {static_cast<uint64_t>(cols),
+                         static_cast<uint64_t>(rows),
+                         static_cast<uint64_t>(E)};
+  const uint64_t st[2] = {static_cast<uint64_t>(cols) * 2,
+                          static_cast<uint64_t>(cols) * rows * 2};
+  const uint32_t b[3] = {box_c, box_r, 1};
+  return make_tmap_nd(m, BF, 3, p, d, st, b, SW128);
+}
+lce_status store_map(CUtensorMap* m, const void* p, int64_t cols,
+                     int64_t rows) {
+  return map2(m, p, cols, rows, EPI_BOX, EPI_BOX, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+Geom geom(const ExpertsArgs& a) {
+  Geom g{};
+  g.head = a.plan.head;
+  g.tile = a.plan.tile;
+  g.seg = a.plan.seg;
+  g.token = a.plan.token;
+  g.slot = a.plan.slot;
+  g.H = static_cast<int>(a.H);
+  g.I = static_cast<int>(a.I);
+  g.E = a.E;
+  g.L = static_cast<int>(a.L);
+  g.kb_h = static_cast<int>(ceil_div(a.H, BK));
+  g.kb_i = static_cast<int>(ceil_div(a.I, BK));
+  g.timeout_ns = a.timeout_ns;
+  return g;
+}
+
+template <class Op, class Epi>
+lce_status launch(const char* what, const Maps& m, const Geom& g,
+                  const typename Epi::Params& p, const ExpertsArgs& a,
+                  cudaStream_t s) {
+  auto kern = k_experts<Op, Epi>;
+  cudaError_t e = cudaFuncSetAttribute(
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM_BYTES);
+  if (e == cudaSuccess) {
+    kern<<<a.grid, GEMM_THREADS, GEMM_SMEM_BYTES, s>>>(m, g, p, a.err);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? LCE_OK : cuda_fail(e, what);
+}
+
+#define LCE_TRY(call)                       \
+  do {                                      \
+    const lce_status st_ = (call);          \
+    if (st_ != LCE_OK) return st_;          \
+  } while (0)
+
+}  // namespace
+
+lce_status launch_experts_up(const ExpertsArgs& a, cudaStream_t s) {
+  Maps m{};
+  LCE_TRY(map2(&m.a0, a.x, a.H, a.L, BK, 1));
+  LCE_TRY(map3(&m.b0, a.Wg, a.H, a.I, a.E, BK, 128));
+  LCE_TRY(map3(&m.b1, a.Wu, a.H, a.I, a.E, BK, 128));
+  LCE_TRY(store_map(&m.s0, a.a, a.I, a.max_rows));
+  Geom g = geom(a);
+  g.num_n = static_cast<int>(ceil_div(a.I, 128));
+  return launch<OpUp, EpiUp>("experts_up", m, g, {0}, a, s);
+}
+
+lce_status launch_experts_down(const ExpertsArgs& a, cudaStream_t s) {
+  Maps m{};
+  LCE_TRY(map2(&m.a0, a.a, a.I, a.max_rows, BK, 64));
+  LCE_TRY(map3(&m.b0, a.Wd, a.I, a.H, a.E, BK, 256));
+  Geom g = geom(a);
+  g.num_n = static_cast<int>(ceil_div(a.H, 256));
+  return launch<OpDown, EpiRows>("experts_down", m, g, {a.rows_out}, a, s);
+}
+
+lce_status launch_experts_dgu(const ExpertsArgs& a, cudaStream_t s) {
+  Maps m{};
+  LCE_TRY(map2(&m.a0, a.x, a.H, a.L, BK, 1));
+  LCE_TRY(map2(&m.a1, a.dy, a.H, a.L, BK, 1));
+  LCE_TRY(map3(&m.b0, a.Wg, a.H, a.I, a.E, BK, 128));
+  LCE_TRY(map3(&m.b1, a.Wu, a.H, a.I, a.E, BK, 128));
+  LCE_TRY(map3(&m.b2, a.Wd, a.I, a.H, a.E, 64, BK));
+  LCE_TRY(store_map(&m.s0, a.dg, a.I, a.max_rows));
+  LCE_TRY(store_map(&m.s1, a.du, a.I, a.max_rows));
+  LCE_TRY(store_map(&m.s2, a.a, a.I, a.max_rows));
+  Geom g = geom(a);
+  g.num_n = static_cast<int>(ceil_div(a.I, 128));
+  return launch<OpDgu, EpiDgu>(
+      "experts_dgu", m, g, {a.w, a.wdt == LCE_F32, a.part, a.max_rows}, a, s);
+}
+
+lce_status launch_experts_dx(const ExpertsArgs& a, cudaStream_t s) {
+  Maps m{};
+  LCE_TRY(map2(&m.a0, a.dg, a.I, a.max_rows, BK, 64));
+  LCE_TRY(map2(&m.a1, a.du, a.I, a.max_rows, BK, 64));
+  LCE_TRY(map3(&m.b0, a.Wg, a.H, a.I, a.E, 64, BK));
+  LCE_TRY(map3(&m.b1, a.Wu, a.H, a.I, a.E, 64, BK));
+  Geom g = geom(a);
+  g.num_n = static_cast<int>(ceil_div(a.H, 256));
+  return launch<OpDx, EpiRows>("experts_dx", m, g, {a.rows_out}, a, s);
+}
+
+lce_status launch_experts_dwd(const ExpertsArgs& a, cudaStream_t s) {
+  Maps m{};
+  LCE_TRY(map2(&m.a0, a.dy, a.H, a.L, BK, 1));
+  LCE_TRY(map2(&m.b0, a.a, a.I, a.max_rows, 64, BK));
+  Geom g = geom(a);
+  g.num_m = static_cast<int>(ceil_div(a.H, BM));
+  g.num_n = static_cast<int>(ceil_div(a.I, BN));
+  return launch<OpDwd, EpiGrad2>(
+      "experts_dWd", m, g,
+      {a.dW, nullptr, a.gdt == LCE_F32, g.H, g.I}, a, s);
+}
+
+lce_status launch_experts_dwgu(const ExpertsArgs& a, cudaStream_t s) {
+  Maps m{};
+  LCE_TRY(map2(&m.a0, a.dg, a.I, a.max_rows, 64, BK));
+  LCE_TRY(map2(&m.a1, a.du, a.I, a.max_rows, 64, BK));
+  LCE_TRY(map2(&m.b0, a.x, a.H, a.L, BK, 1));
+  Geom g = geom(a);
+  g.num_m = 2 * static_cast<int>(ceil_div(a.I, BM));
+  g.num_n = static_cast<int>(ceil_div(a.H, BN));
+  return launch<OpDwgu, EpiGrad2>(
+      "experts_dWgu", m, g, {a.dW, a.dW2, a.gdt == LCE_F32, g.I, g.H}, a, s);
+}
+
+}  // namespace lce

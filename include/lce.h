@@ -587,6 +587,56 @@ lce_status lce_route_backward(const void* logits, lce_dtype dt,
                               void* stream);
 
 /*
+ * The experts' gated MLP: lce_mlp_forward once per expert, each token
+ * through its own top_k of the E experts (weights and experts from
+ * lce_route_forward, or any others). For token t with slots (t, k), e =
+ * experts[t][k], w = weights[t][k]:
+ *   y_t = sum_k w Wd_e (silu(Wg_e x_t) * (Wu_e x_t))
+ * and, given dy, with a the product in the brackets and da' = Wd_e^T dy_t:
+ *   dweights[t][k] = da' . a            da = w da'
+ *   dg = da u silu'(g), du = da silu(g)  dx_t = sum_k Wg_e^T dg + Wu_e^T du
+ *   dWg_e = sum dg x_t^T, dWu_e = sum du x_t^T, dWd_e = sum dy_t (w a)^T
+ * over the slots of e (0 for an expert without slots).
+ *   x        device bf16 [L][H]
+ *   Wg, Wu   device bf16 [E][I][H];  Wd device bf16 [E][H][I]
+ *   weights  device [L][top_k] of weights_dt (LCE_BF16 or LCE_F32)
+ *   experts  device int32 [L][top_k]; -1 drops the slot (it adds nothing,
+ *            its dweights is 0); any other index outside [0, E) does too
+ *            and raises LCE_ERR_EXPERT_RANGE
+ *   y        device bf16 [L][H] out
+ *   dy       device bf16 [L][H]
+ *   dx       device bf16 [L][H] out
+ *   dWg, dWu, dWd  device out, shaped as the weights, of grad_dt (LCE_BF16
+ *            or LCE_F32), overwritten
+ *   dweights device [L][top_k] of weights_dt out
+ *   dx, dWd, dweights and the pair (dWg, dWu) may each be NULL, and that
+ *   gradient is not computed; not all of them, and dWg, dWu both or neither.
+ *   ws       lce_experts_workspace_size(..., backward = 0 or 1) bytes, 256-
+ *            byte aligned; contents before and after are of no account
+ * H % 8 == 0, I % 8 == 0, 1 <= E <= 1024, 1 <= top_k <= 32, L top_k <= 2^30.
+ * L = 0: nothing to do forward, zero weight gradients backward.
+ * Accumulation is fp32; a (and dg, du, w a) are rounded to bf16 between the
+ * contractions, the sum over a token's slots is rounded once. Results do not
+ * depend on the order of execution (no floating-point atomics).
+ */
+size_t lce_experts_workspace_size(int64_t L, int64_t H, int64_t I, int64_t E,
+                                  int64_t top_k, int backward);
+lce_status lce_experts_forward(const void* x, const void* Wg, const void* Wu,
+                               const void* Wd, const void* weights,
+                               lce_dtype weights_dt, const int32_t* experts,
+                               int64_t L, int64_t H, int64_t I, int64_t E,
+                               int64_t top_k, void* y, void* ws,
+                               size_t ws_bytes, void* stream);
+lce_status lce_experts_backward(const void* x, const void* Wg, const void* Wu,
+                                const void* Wd, const void* weights,
+                                lce_dtype weights_dt, const int32_t* experts,
+                                const void* dy, int64_t L, int64_t H,
+                                int64_t I, int64_t E, int64_t top_k,
+                                lce_dtype grad_dt, void* dx, void* dWg,
+                                void* dWu, void* dWd, void* dweights, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/*
  * Selects how the tensor-core contractions run, for the whole process:
  * enable = 1: on CTA pairs (a cluster of two SMs issues tcgen05.mma with
  * cta_group::2 on 256 x 256 tiles, each SM staging half of each operand);
