@@ -3,7 +3,7 @@
 //
 // Rows: the slots of an expert, in slot order, form one segment of rows;
 // segments start at multiples of SEG_ROWS and are padded to one with rows
-// that hold no slot (token = L, which every gathering load reads as zero).
+// that hold no slot (token = -1) and are zero.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -33,7 +33,7 @@ struct Plan {
   PlanHead* head;
   RowTile* tile;  // [max_tiles]
   int2* seg;      // [E]: first row, padded rows
-  int* token;     // [max_rows]: token of a row, L for a padding row
+  int* token;     // [max_rows]: token of a row, -1 for a padding row
   int* slot;      // [max_rows]: slot of a row, -1 for a padding row
   int* row;       // [n]: row of a slot, -1 where it is dropped
   int* count;     // [E]: slots of an expert
@@ -42,8 +42,14 @@ struct Plan {
 
 // Queues the plan of `n` slots (experts[n], `K` to a token). Deterministic:
 // integer counts and positions that follow slot order.
-cudaError_t launch_plan(const int32_t* experts, int64_t n, int K, int64_t L,
-                        int E, const Plan& p, unsigned* err, cudaStream_t s);
+cudaError_t launch_plan(const int32_t* experts, int64_t n, int K, int E,
+                        const Plan& p, unsigned* err, cudaStream_t s);
+
+// out[r][:] = x[token of row r][:] (0 in padding rows) for the plan's rows,
+// bf16 of H columns; with y also out_y from y.
+cudaError_t launch_gather(const Plan& p, int64_t max_rows, int64_t H,
+                          const void* x, uint16_t* out, const void* y,
+                          uint16_t* out_y, cudaStream_t s);
 
 // out[t][:] = sum_k w[t][k] rows[row(t, k)][:] in bf16, k in order, dropped
 // slots left out (w NULL: weights 1).
@@ -59,13 +65,14 @@ cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,
 // ---- grouped contractions ----------------------------------------------------
 struct ExpertsArgs {
   Plan plan;
-  int64_t L, H, I;
+  int64_t H, I;
   int E;
   uint64_t timeout_ns;
   unsigned* err;
   int grid;
   // operand maps by use; each kernel takes the ones it names
-  const void *x, *dy, *Wg, *Wu, *Wd;
+  const void *Wg, *Wu, *Wd;
+  uint16_t *xr, *dyr;      // [max_rows][H]: token rows in plan order
   uint16_t *a, *dg, *du;   // [max_rows][I]
   int64_t max_rows;
   float* rows_out;         // [max_rows][H] fp32 (DOWN, DX)

@@ -34,7 +34,7 @@ int64_t max_tiles(const Sizes& z) {
 
 struct Layout {
   size_t head, tile, seg, token, slot, row, count, hist;
-  size_t a, dg, du, rows, part, total;
+  size_t xr, dyr, a, dg, du, rows, part, total;
 };
 
 Layout layout(const Sizes& z, bool backward) {
@@ -54,8 +54,10 @@ Layout layout(const Sizes& z, bool backward) {
   w.row = take(n * 4);
   w.count = take(z.E * 4);
   w.hist = take(z.E * ceil_div(n, PLAN_CHUNK) * 4);
+  w.xr = take(P * z.H * 2);
   w.a = take(P * z.I * 2);
   if (backward) {
+    w.dyr = take(P * z.H * 2);
     w.dg = take(P * z.I * 2);
     w.du = take(P * z.I * 2);
     w.part = take(P * ceil_div(z.I, 128) * 4);
@@ -91,13 +93,14 @@ ExpertsArgs arguments(const Sizes& z, const Layout& w, uint8_t* ws,
   a.plan.row = reinterpret_cast<int*>(ws + w.row);
   a.plan.count = reinterpret_cast<int*>(ws + w.count);
   a.plan.hist = reinterpret_cast<int*>(ws + w.hist);
-  a.L = z.L;
   a.H = z.H;
   a.I = z.I;
   a.E = static_cast<int>(z.E);
   a.timeout_ns = wait_timeout_ns();
   a.err = dev.err;
   a.grid = dev.num_sms;
+  a.xr = reinterpret_cast<uint16_t*>(ws + w.xr);
+  a.dyr = reinterpret_cast<uint16_t*>(ws + w.dyr);
   a.a = reinterpret_cast<uint16_t*>(ws + w.a);
   a.dg = reinterpret_cast<uint16_t*>(ws + w.dg);
   a.du = reinterpret_cast<uint16_t*>(ws + w.du);
@@ -125,12 +128,18 @@ lce_status timed(int kind, double flops, cudaStream_t s, F&& f) {
   return st;
 }
 
-lce_status make_plan(const Sizes& z, const int32_t* experts,
-                     const ExpertsArgs& a, cudaStream_t s) {
-  return timed(LCE_K_EXPERTS_PLAN, 0, s, [&] {
-    return cuda_try(launch_plan(experts, z.L * z.K, static_cast<int>(z.K), z.L,
+// The plan, and the token rows of x (and dy) in its order.
+lce_status make_plan(const Sizes& z, const int32_t* experts, const void* x,
+                     const void* dy, const ExpertsArgs& a, cudaStream_t s) {
+  LCE_TRY(timed(LCE_K_EXPERTS_PLAN, 0, s, [&] {
+    return cuda_try(launch_plan(experts, z.L * z.K, static_cast<int>(z.K),
                                 a.E, a.plan, a.err, s),
                     "experts_plan");
+  }));
+  return timed(LCE_K_EXPERTS_GATHER, 0, s, [&] {
+    return cuda_try(launch_gather(a.plan, a.max_rows, z.H, x, a.xr, dy, a.dyr,
+                                  s),
+                    "experts_gather");
   });
 }
 
@@ -164,12 +173,11 @@ lce_status lce_experts_forward(const void* x, const void* Wg, const void* Wu,
   LCE_TRY(device_info(&dev));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ExpertsArgs a = arguments(z, w, static_cast<uint8_t*>(ws), *dev);
-  a.x = x;
   a.Wg = Wg;
   a.Wu = Wu;
   a.Wd = Wd;
   const double slot_flops = 2.0 * L * top_k * H * I;
-  LCE_TRY(make_plan(z, experts, a, s));
+  LCE_TRY(make_plan(z, experts, x, nullptr, a, s));
   LCE_TRY(timed(LCE_K_EXPERTS_UP, 2 * slot_flops, s,
                 [&] { return launch_experts_up(a, s); }));
   LCE_TRY(timed(LCE_K_EXPERTS_DOWN, slot_flops, s,
@@ -211,8 +219,6 @@ lce_status lce_experts_backward(const void* x, const void* Wg, const void* Wu,
     return LCE_OK;
   }
   ExpertsArgs a = arguments(z, w, static_cast<uint8_t*>(ws), *dev);
-  a.x = x;
-  a.dy = dy;
   a.Wg = Wg;
   a.Wu = Wu;
   a.Wd = Wd;
@@ -221,7 +227,7 @@ lce_status lce_experts_backward(const void* x, const void* Wg, const void* Wu,
   a.gdt = grad_dt;
   const double slot_flops = 2.0 * L * top_k * H * I;
   const int K = static_cast<int>(top_k);
-  LCE_TRY(make_plan(z, experts, a, s));
+  LCE_TRY(make_plan(z, experts, x, dy, a, s));
   LCE_TRY(timed(LCE_K_EXPERTS_DGU, 3 * slot_flops, s,
                 [&] { return launch_experts_dgu(a, s); }));
   if (dweights)

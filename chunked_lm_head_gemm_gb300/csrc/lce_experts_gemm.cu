@@ -9,9 +9,12 @@
 //   DX    rows = [dg | du] [Wg_e ; Wu_e]                            K = 2 I
 //   DWD   dWd_e = dy[token]^T (w a)                       K = rows of e
 //   DWGU  dWg_e, dWu_e = dg^T x[token], du^T x[token]     K = rows of e
-// The token rows of x and dy are never copied: the producer gathers them
-// straight into the swizzled stage, four rows to one TMA instruction, one
-// instruction to a lane.
+// x[token] and dy[token] are copies of the token rows in plan order, made
+// once for all contractions that read them. Gathering them into the stages by
+// TMA instead (four rows to an instruction, one instruction to a lane) needs
+// no copy but held every contraction to 37 ns an instruction per SM, 32 of
+// them a stage: UP ran at 540 and DWGU at 251 TFLOP/s (L = 32768, H = 2048,
+// I = 768, E = 128, top 8) where the tiled loads of DX reach 1295.
 //
 // Work: units are 128 x 256 output tiles (UP and DGU 128 x 128 of a, whose
 // accumulator columns are g | u), walked in a static stride by one CTA per
@@ -37,9 +40,8 @@ struct Geom {
   const PlanHead* head;
   const RowTile* tile;
   const int2* seg;
-  const int* token;
   const int* slot;
-  int H, I, E, L;
+  int H, I, E;
   int kb_h, kb_i;   // 64-wide K blocks of H and I
   int num_n;        // column tiles of a row tile; or of an expert's gradient
   int num_m;        // row tiles of an expert's gradient
@@ -64,37 +66,21 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
       : "memory");
 }
 
-// Four rows of 64 elements from column c0 (a multiple of 64) to dst, 128
-// bytes each, in the stage's 128-byte swizzle; rows past the map read as 0.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm,
-                                            int c0, int4 r, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::"
-      "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(r.x), "r"(r.y),
-      "r"(r.z), "r"(r.w), "r"(bar)
-      : "memory");
+// K-major A rows of a tile: 64 or 128 rows of 64 elements.
+__device__ __forceinline__ void load_rows(uint32_t sa, const CUtensorMap* tm,
+                                          const Unit& u, int c0, uint32_t bar) {
+  tma_load_2d(sa, tm, c0, u.row0, bar);
+  if (u.rows > 64) tma_load_2d(sa + 8192, tm, c0, u.row0 + 64, bar);
 }
 
-// Rows [row0, row0 + rows) of the plan, K-major: lane q takes rows 4q...
-__device__ __forceinline__ void gather_rows(uint32_t sa, const CUtensorMap* tm,
-                                            const Geom& g, int row0, int rows,
-                                            int c0, uint32_t bar, int lane) {
-  if (4 * lane < rows) {
-    const int4 t = __ldg(reinterpret_cast<const int4*>(g.token + row0) + lane);
-    tma_gather4(sa + lane * 512, tm, c0, t, bar);
-  }
-}
-
-// 64 rows of the plan as the K index of an MN-major operand, `boxes` boxes
-// of 64 columns from c0.
-__device__ __forceinline__ void gather_cols(uint32_t sa, const CUtensorMap* tm,
-                                            const Geom& g, int row0, int boxes,
-                                            int c0, uint32_t bar, int lane) {
-  const int q = lane & 15;
-  const int4 t = __ldg(reinterpret_cast<const int4*>(g.token + row0) + q);
-  for (int j = lane >> 4; j < boxes; j += 2)
-    tma_gather4(sa + j * 8192 + q * 512, tm, c0 + 64 * j, t, bar);
+// 64 rows from r0 as the K index of an MN-major operand: BOXES boxes of 64
+// columns from c0.
+template <int BOXES>
+__device__ __forceinline__ void load_cols(uint32_t dst, const CUtensorMap* tm,
+                                          int c0, int r0, uint32_t bar) {
+#pragma unroll
+  for (int j = 0; j < BOXES; ++j)
+    tma_load_2d(dst + j * 8192, tm, c0 + 64 * j, r0, bar);
 }
 
 // ---- the uses ----------------------------------------------------------------
@@ -136,13 +122,10 @@ struct OpUp : RowUnits {
   }
   template <int P>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
-                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
-                              int lane) {
-    gather_rows(sa, &m.a0, g, u.row0, u.rows, kb * BK, bar, lane);
-    if (lane == 0) {
-      tma_load_3d(sb, &m.b0, kb * BK, u.n * 128, u.e, bar);
-      tma_load_3d(sb + 16384, &m.b1, kb * BK, u.n * 128, u.e, bar);
-    }
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
+    load_rows(sa, &m.a0, u, kb * BK, bar);
+    tma_load_3d(sb, &m.b0, kb * BK, u.n * 128, u.e, bar);
+    tma_load_3d(sb + 16384, &m.b1, kb * BK, u.n * 128, u.e, bar);
   }
 };
 
@@ -158,13 +141,9 @@ struct OpDown : RowUnits {
   }
   template <int P>
   __device__ static void load(const Maps& m, const Geom&, const Unit& u,
-                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
-                              int lane) {
-    if (lane == 0) {
-      tma_load_2d(sa, &m.a0, kb * BK, u.row0, bar);
-      if (u.rows > 64) tma_load_2d(sa + 8192, &m.a0, kb * BK, u.row0 + 64, bar);
-      tma_load_3d(sb, &m.b0, kb * BK, u.n * 256, u.e, bar);
-    }
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
+    load_rows(sa, &m.a0, u, kb * BK, bar);
+    tma_load_3d(sb, &m.b0, kb * BK, u.n * 256, u.e, bar);
   }
 };
 
@@ -182,15 +161,12 @@ struct OpDx : RowUnits {
   }
   template <int P>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
-                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
-                              int lane) {
-    if (lane != 0) return;
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     const bool second = kb >= g.kb_i;  // du and Wu after dg and Wg
     const CUtensorMap* ta = second ? &m.a1 : &m.a0;
     const CUtensorMap* tb = second ? &m.b1 : &m.b0;
     const int k0 = (second ? kb - g.kb_i : kb) * BK;
-    tma_load_2d(sa, ta, k0, u.row0, bar);
-    if (u.rows > 64) tma_load_2d(sa + 8192, ta, k0, u.row0 + 64, bar);
+    load_rows(sa, ta, u, k0, bar);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       tma_load_3d(sb + j * 8192, tb, u.n * 256 + 64 * j, k0, u.e, bar);
@@ -211,16 +187,13 @@ struct OpDgu : RowUnits {
   }
   template <int P>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
-                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
-                              int lane) {
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     if (P == 0) {
-      gather_rows(sa, &m.a1, g, u.row0, u.rows, kb * BK, bar, lane);
-      if (lane == 0) {
-        tma_load_3d(sb, &m.b2, u.n * 128, kb * BK, u.e, bar);
-        tma_load_3d(sb + 8192, &m.b2, u.n * 128 + 64, kb * BK, u.e, bar);
-      }
+      load_rows(sa, &m.a1, u, kb * BK, bar);
+      tma_load_3d(sb, &m.b2, u.n * 128, kb * BK, u.e, bar);
+      tma_load_3d(sb + 8192, &m.b2, u.n * 128 + 64, kb * BK, u.e, bar);
     } else {
-      OpUp::load<0>(m, g, u, kb, sa, sb, bar, lane);
+      OpUp::load<0>(m, g, u, kb, sa, sb, bar);
     }
   }
 };
@@ -237,15 +210,10 @@ struct OpDwd : GradUnits {
   __device__ static uint32_t bytes(const Unit&) { return STAGE_BYTES; }
   template <int P>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
-                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
-                              int lane) {
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     const int k0 = u.row0 + kb * BK;
-    gather_cols(sa, &m.a0, g, k0, 2, u.m * BM, bar, lane);
-    if (lane == 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        tma_load_2d(sb + j * 8192, &m.b0, u.n * BN + 64 * j, k0, bar);
-    }
+    load_cols<2>(sa, &m.a0, u.m * BM, k0, bar);
+    load_cols<4>(sb, &m.b0, u.n * BN, k0, bar);
   }
 };
 
@@ -261,18 +229,13 @@ struct OpDwgu : GradUnits {
   __device__ static uint32_t bytes(const Unit&) { return STAGE_BYTES; }
   template <int P>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
-                              int kb, uint32_t sa, uint32_t sb, uint32_t bar,
-                              int lane) {
+                              int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     const int k0 = u.row0 + kb * BK;
     const int half = g.num_m >> 1;  // dWg's row tiles, then dWu's
     const bool second = u.m >= half;
     const int m0 = (second ? u.m - half : u.m) * BM;
-    if (lane == 0) {
-      const CUtensorMap* ta = second ? &m.a1 : &m.a0;
-      tma_load_2d(sa, ta, m0, k0, bar);
-      tma_load_2d(sa + 8192, ta, m0 + 64, k0, bar);
-    }
-    gather_cols(sb, &m.b0, g, k0, 4, u.n * BN, bar, lane);
+    load_cols<2>(sa, second ? &m.a1 : &m.a0, m0, k0, bar);
+    load_cols<4>(sb, &m.b0, u.n * BN, k0, bar);
   }
 };
 
@@ -467,18 +430,15 @@ __device__ __forceinline__ bool produce(const Maps& m, const Geom& g,
                                         const Unit& u, uint32_t sa,
                                         uint32_t sb, const Bars& bars,
                                         Ring& ring, uint32_t& issued,
-                                        const WaitCtx& ctx, int lane) {
+                                        const WaitCtx& ctx) {
   const int n = Op::template blocks<P>(g, u);
   for (int kb = 0; kb < n; ++kb) {
-    const bool got =
-        mbar_wait(bars.empty(ring.stage), ring.phase ^ 1u, ctx, true);
-    if (!__all_sync(FULL, got)) return false;
+    if (!mbar_wait(bars.empty(ring.stage), ring.phase ^ 1u, ctx, true))
+      return false;
     const uint32_t fb = bars.full(ring.stage);
-    if (lane == 0) mbar_arrive_expect_tx(fb, Op::template bytes<P>(u));
-    __syncwarp();
+    mbar_arrive_expect_tx(fb, Op::template bytes<P>(u));
     Op::template load<P>(m, g, u, kb, sa + ring.stage * A_STAGE_BYTES,
-                         sb + ring.stage * B_STAGE_BYTES, fb, lane);
-    __syncwarp();
+                         sb + ring.stage * B_STAGE_BYTES, fb);
     ++issued;
     ring.next();
   }
@@ -567,21 +527,24 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   const int units = Op::units(g);
 
   if (warp == 0) {
-    Ring ring;
-    uint32_t issued = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const Unit t = Op::unit(g, u);
-      ok = produce<Op, 0>(maps, g, t, sa, sb, bars, ring, issued, ctx, lane);
-      if (Op::PARTS == 2 && ok)
-        ok = produce<Op, Op::PARTS - 1>(maps, g, t, sa, sb, bars, ring, issued,
-                                        ctx, lane);
-    }
-    // every copy issued must have landed before the CTA may exit
-    for (int s = 0; s < STAGES; ++s) {
-      const uint32_t cnt = issued / STAGES +
-                           (static_cast<uint32_t>(s) < issued % STAGES ? 1u : 0u);
-      if (cnt) mbar_wait(bars.full(s), (cnt - 1u) & 1u, ctx, false);
+    if (lane == 0) {
+      Ring ring;
+      uint32_t issued = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Unit t = Op::unit(g, u);
+        ok = produce<Op, 0>(maps, g, t, sa, sb, bars, ring, issued, ctx);
+        if (Op::PARTS == 2 && ok)
+          ok = produce<Op, Op::PARTS - 1>(maps, g, t, sa, sb, bars, ring,
+                                          issued, ctx);
+      }
+      // every copy issued must have landed before the CTA may exit
+      for (int s = 0; s < STAGES; ++s) {
+        const uint32_t cnt =
+            issued / STAGES +
+            (static_cast<uint32_t>(s) < issued % STAGES ? 1u : 0u);
+        if (cnt) mbar_wait(bars.full(s), (cnt - 1u) & 1u, ctx, false);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -667,12 +630,10 @@ Geom geom(const ExpertsArgs& a) {
   g.head = a.plan.head;
   g.tile = a.plan.tile;
   g.seg = a.plan.seg;
-  g.token = a.plan.token;
   g.slot = a.plan.slot;
   g.H = static_cast<int>(a.H);
   g.I = static_cast<int>(a.I);
   g.E = a.E;
-  g.L = static_cast<int>(a.L);
   g.kb_h = static_cast<int>(ceil_div(a.H, BK));
   g.kb_i = static_cast<int>(ceil_div(a.I, BK));
   g.timeout_ns = a.timeout_ns;
@@ -703,7 +664,7 @@ lce_status launch(const char* what, const Maps& m, const Geom& g,
 
 lce_status launch_experts_up(const ExpertsArgs& a, cudaStream_t s) {
   Maps m{};
-  LCE_TRY(map2(&m.a0, a.x, a.H, a.L, BK, 1));
+  LCE_TRY(map2(&m.a0, a.xr, a.H, a.max_rows, BK, 64));
   LCE_TRY(map3(&m.b0, a.Wg, a.H, a.I, a.E, BK, 128));
   LCE_TRY(map3(&m.b1, a.Wu, a.H, a.I, a.E, BK, 128));
   LCE_TRY(store_map(&m.s0, a.a, a.I, a.max_rows));
@@ -723,8 +684,8 @@ lce_status launch_experts_down(const ExpertsArgs& a, cudaStream_t s) {
 
 lce_status launch_experts_dgu(const ExpertsArgs& a, cudaStream_t s) {
   Maps m{};
-  LCE_TRY(map2(&m.a0, a.x, a.H, a.L, BK, 1));
-  LCE_TRY(map2(&m.a1, a.dy, a.H, a.L, BK, 1));
+  LCE_TRY(map2(&m.a0, a.xr, a.H, a.max_rows, BK, 64));
+  LCE_TRY(map2(&m.a1, a.dyr, a.H, a.max_rows, BK, 64));
   LCE_TRY(map3(&m.b0, a.Wg, a.H, a.I, a.E, BK, 128));
   LCE_TRY(map3(&m.b1, a.Wu, a.H, a.I, a.E, BK, 128));
   LCE_TRY(map3(&m.b2, a.Wd, a.I, a.H, a.E, 64, BK));
@@ -750,7 +711,7 @@ lce_status launch_experts_dx(const ExpertsArgs& a, cudaStream_t s) {
 
 lce_status launch_experts_dwd(const ExpertsArgs& a, cudaStream_t s) {
   Maps m{};
-  LCE_TRY(map2(&m.a0, a.dy, a.H, a.L, BK, 1));
+  LCE_TRY(map2(&m.a0, a.dyr, a.H, a.max_rows, 64, BK));
   LCE_TRY(map2(&m.b0, a.a, a.I, a.max_rows, 64, BK));
   Geom g = geom(a);
   g.num_m = static_cast<int>(ceil_div(a.H, BM));
@@ -764,7 +725,7 @@ lce_status launch_experts_dwgu(const ExpertsArgs& a, cudaStream_t s) {
   Maps m{};
   LCE_TRY(map2(&m.a0, a.dg, a.I, a.max_rows, 64, BK));
   LCE_TRY(map2(&m.a1, a.du, a.I, a.max_rows, 64, BK));
-  LCE_TRY(map2(&m.b0, a.x, a.H, a.L, BK, 1));
+  LCE_TRY(map2(&m.b0, a.xr, a.H, a.max_rows, 64, BK));
   Geom g = geom(a);
   g.num_m = 2 * static_cast<int>(ceil_div(a.I, BM));
   g.num_n = static_cast<int>(ceil_div(a.H, BN));

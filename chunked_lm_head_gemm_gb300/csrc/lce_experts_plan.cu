@@ -58,7 +58,7 @@ __device__ __forceinline__ int tiles_of(int c) {
 
 // One block of MAX_EXPERTS threads: segments, tiles and padding rows from
 // the experts' counts. start[] (shared or global) gets each segment's row.
-__device__ __forceinline__ void lay_out(int c, int E, int L, const Plan& p,
+__device__ __forceinline__ void lay_out(int c, int E, const Plan& p,
                                         int* start) {
   __shared__ int warp_rows[32], warp_tiles[32];
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
@@ -91,7 +91,7 @@ __device__ __forceinline__ void lay_out(int c, int E, int L, const Plan& p,
     for (int q = 0; q < rows; q += BM)
       p.tile[at++] = RowTile{e, row0 + q, min(BM, rows - q), 0};
     for (int q = c; q < rows; ++q) {
-      p.token[row0 + q] = L;
+      p.token[row0 + q] = -1;
       p.slot[row0 + q] = -1;
     }
     if (e == E - 1) *p.head = PlanHead{t, r};
@@ -100,7 +100,7 @@ __device__ __forceinline__ void lay_out(int c, int E, int L, const Plan& p,
 
 // Few slots: the whole plan in one block (a launch instead of four).
 __global__ void __launch_bounds__(1024)
-    k_plan_small(const int32_t* experts, int n, int K, int L, int E, Plan p,
+    k_plan_small(const int32_t* experts, int n, int K, int E, Plan p,
                  unsigned* err) {
   extern __shared__ int plan_smem[];
   int* cnt = plan_smem;          // [warps][E]
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(1024)
       cnt[w * E + threadIdx.x] = total;
       total += c;
     }
-  lay_out(total, E, L, p, start);
+  lay_out(total, E, p, start);
   __syncthreads();
   walk_slots<true>(experts, n, i0, i1, E, K, cnt + warp * E, start, p, err);
 }
@@ -166,9 +166,9 @@ __global__ void __launch_bounds__(256) k_plan_scan(int E, int chunks, Plan p) {
 }
 
 // Step 3: segments and tiles.
-__global__ void __launch_bounds__(1024) k_plan_layout(int L, int E, Plan p) {
+__global__ void __launch_bounds__(1024) k_plan_layout(int E, Plan p) {
   __shared__ int start[MAX_EXPERTS];
-  lay_out(threadIdx.x < E ? p.count[threadIdx.x] : 0, E, L, p, start);
+  lay_out(threadIdx.x < E ? p.count[threadIdx.x] : 0, E, p, start);
 }
 
 // Step 4: every slot's row.
@@ -199,6 +199,30 @@ __global__ void __launch_bounds__(CHUNK_WARPS * 32)
   __syncthreads();
   walk_slots<true>(experts, n, i0, i1, E, K, cnt + warp * E, start, p,
                    nullptr);
+}
+
+// One warp per row, 16 bytes a lane, four loads in flight.
+__global__ void __launch_bounds__(256)
+    k_gather(const PlanHead* __restrict__ head, const int* __restrict__ token,
+             int64_t H, const uint4* __restrict__ x, uint4* __restrict__ out,
+             const uint4* __restrict__ y, uint4* __restrict__ out_y) {
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= head->rows) return;
+  const int t = token[r];
+  const int vecs = static_cast<int>(H / 8);
+  const uint4* src = blockIdx.y ? y : x;
+  uint4* dst = (blockIdx.y ? out_y : out) + static_cast<int64_t>(r) * vecs;
+  src += static_cast<int64_t>(t < 0 ? 0 : t) * vecs;
+  for (int i = threadIdx.x & 31; i < vecs; i += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      v[q] = t >= 0 && i + 32 * q < vecs ? __ldg(src + i + 32 * q)
+                                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i + 32 * q < vecs) dst[i + 32 * q] = v[q];
+  }
 }
 
 template <typename T>
@@ -255,29 +279,40 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
 
 }  // namespace
 
-cudaError_t launch_plan(const int32_t* experts, int64_t n, int K, int64_t L,
-                        int E, const Plan& p, unsigned* err, cudaStream_t s) {
+cudaError_t launch_plan(const int32_t* experts, int64_t n, int K, int E,
+                        const Plan& p, unsigned* err, cudaStream_t s) {
   cudaError_t e;
   if (n <= PLAN_SMALL) {
     const size_t smem = sizeof(int) * 33 * static_cast<size_t>(E);
     if ((e = allow_smem(reinterpret_cast<const void*>(k_plan_small), smem)) !=
         cudaSuccess)
       return e;
-    k_plan_small<<<1, 1024, smem, s>>>(experts, static_cast<int>(n), K,
-                                       static_cast<int>(L), E, p, err);
+    k_plan_small<<<1, 1024, smem, s>>>(experts, static_cast<int>(n), K, E,
+                                       p, err);
     return cudaGetLastError();
   }
   const int chunks = static_cast<int>(ceil_div(n, PLAN_CHUNK));
   k_plan_count<<<chunks, CHUNK_WARPS * 32, sizeof(int) * E, s>>>(
       experts, n, E, chunks, p, err);
   k_plan_scan<<<(E + 7) / 8, 256, 0, s>>>(E, chunks, p);
-  k_plan_layout<<<1, 1024, 0, s>>>(static_cast<int>(L), E, p);
+  k_plan_layout<<<1, 1024, 0, s>>>(E, p);
   const size_t smem = sizeof(int) * (CHUNK_WARPS + 1) * static_cast<size_t>(E);
   if ((e = allow_smem(reinterpret_cast<const void*>(k_plan_place), smem)) !=
       cudaSuccess)
     return e;
   k_plan_place<<<chunks, CHUNK_WARPS * 32, smem, s>>>(experts, n, K, E, chunks,
                                                       p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather(const Plan& p, int64_t max_rows, int64_t H,
+                          const void* x, uint16_t* out, const void* y,
+                          uint16_t* out_y, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(max_rows, 8)), y ? 2 : 1);
+  k_gather<<<grid, 256, 0, s>>>(
+      p.head, p.token, H, static_cast<const uint4*>(x),
+      reinterpret_cast<uint4*>(out), static_cast<const uint4*>(y),
+      reinterpret_cast<uint4*>(out_y));
   return cudaGetLastError();
 }
 
