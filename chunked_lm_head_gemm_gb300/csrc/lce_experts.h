@@ -52,10 +52,12 @@ cudaError_t launch_gather(const Plan& p, int64_t max_rows, int64_t H,
                           uint16_t* out_y, cudaStream_t s);
 
 // out[t][:] = sum_k w[t][k] rows[row(t, k)][:] in bf16, k in order, dropped
-// slots left out (w NULL: weights 1).
-cudaError_t launch_combine(const float* rows, const int* row, const void* w,
-                           lce_dtype wdt, int64_t L, int K, int64_t H,
-                           void* out, cudaStream_t s);
+// slots left out (w NULL: weights 1). rows: fp16 times the scale of each row
+// and 256-column tile.
+cudaError_t launch_combine(const uint16_t* rows, const float* scale,
+                           const int* row, const void* w, lce_dtype wdt,
+                           int64_t L, int K, int64_t H, void* out,
+                           cudaStream_t s);
 
 // dweights[slot] = sum over the column tiles of part[tile][row], in order.
 cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,
@@ -75,7 +77,8 @@ struct ExpertsArgs {
   uint16_t *xr, *dyr;      // [max_rows][H]: token rows in plan order
   uint16_t *a, *dg, *du;   // [max_rows][I]
   int64_t max_rows;
-  float* rows_out;         // [max_rows][H] fp32 (DOWN, DX)
+  uint16_t* rows_out;      // [max_rows][H] fp16 (DOWN, DX) ...
+  float* rows_scale;       // ... times [max_rows][ceil(H / 256)]
   const void* w;           // routing weights of the slots
   lce_dtype wdt;
   float* part;             // [ceil(I / 128)][max_rows] of da . a

@@ -34,7 +34,7 @@ int64_t max_tiles(const Sizes& z) {
 
 struct Layout {
   size_t head, tile, seg, token, slot, row, count, hist;
-  size_t xr, dyr, a, dg, du, rows, part, total;
+  size_t xr, dyr, a, dg, du, rows, scale, part, total;
 };
 
 Layout layout(const Sizes& z, bool backward) {
@@ -62,7 +62,8 @@ Layout layout(const Sizes& z, bool backward) {
     w.du = take(P * z.I * 2);
     w.part = take(P * ceil_div(z.I, 128) * 4);
   }
-  w.rows = take(P * z.H * 4);
+  w.rows = take(P * z.H * 2);
+  w.scale = take(P * ceil_div(z.H, 256) * 4);
   w.total = off;
   return w;
 }
@@ -105,7 +106,8 @@ ExpertsArgs arguments(const Sizes& z, const Layout& w, uint8_t* ws,
   a.dg = reinterpret_cast<uint16_t*>(ws + w.dg);
   a.du = reinterpret_cast<uint16_t*>(ws + w.du);
   a.part = reinterpret_cast<float*>(ws + w.part);
-  a.rows_out = reinterpret_cast<float*>(ws + w.rows);
+  a.rows_out = reinterpret_cast<uint16_t*>(ws + w.rows);
+  a.rows_scale = reinterpret_cast<float*>(ws + w.scale);
   a.max_rows = max_rows(z);
   return a;
 }
@@ -183,8 +185,9 @@ lce_status lce_experts_forward(const void* x, const void* Wg, const void* Wu,
   LCE_TRY(timed(LCE_K_EXPERTS_DOWN, slot_flops, s,
                 [&] { return launch_experts_down(a, s); }));
   return timed(LCE_K_EXPERTS_COMBINE, 0, s, [&] {
-    return cuda_try(launch_combine(a.rows_out, a.plan.row, weights, weights_dt,
-                                   L, static_cast<int>(top_k), H, y, s),
+    return cuda_try(launch_combine(a.rows_out, a.rows_scale, a.plan.row,
+                                   weights, weights_dt, L,
+                                   static_cast<int>(top_k), H, y, s),
                     "experts_combine");
   });
 }
@@ -242,8 +245,8 @@ lce_status lce_experts_backward(const void* x, const void* Wg, const void* Wu,
     LCE_TRY(timed(LCE_K_EXPERTS_DX, 2 * slot_flops, s,
                   [&] { return launch_experts_dx(a, s); }));
     LCE_TRY(timed(LCE_K_EXPERTS_COMBINE, 0, s, [&] {
-      return cuda_try(launch_combine(a.rows_out, a.plan.row, nullptr, LCE_F32,
-                                     L, K, H, dx, s),
+      return cuda_try(launch_combine(a.rows_out, a.rows_scale, a.plan.row,
+                                     nullptr, LCE_F32, L, K, H, dx, s),
                       "experts_combine");
     }));
   }

@@ -21,6 +21,8 @@
 // SM with the roles of k_gemm: producer warp, MMA lane, four epilogue warps.
 // A unit's accumulation is split into parts, each with its own columns,
 // number of buffers and K loop.
+#include <cuda_fp16.h>
+
 #include "lce_device.cuh"
 #include "lce_experts.h"
 #include "lce_host.h"
@@ -268,28 +270,59 @@ struct EpiUp : EpiBase {
   }
 };
 
-// fp32 rows of H columns.
+// Rows of H columns for the sum over a token's slots, in fp16 under a power
+// of two for each row and 256-column tile: the largest finite value of the
+// piece lands in [2^14, 2^15), so a value is off by 2^-12 of itself at most
+// (2^-25 of the piece's largest below that), an eighth of a bf16 rounding, at
+// half the bytes of fp32. Infinities and NaN stay what they are. Against fp32
+// rows stored straight from registers: DOWN 1149 -> DOWN_US us, DX 1303 ->
+// DX_US us, the two sums 694 -> SUM_US us (L = 32768, H = 2048, I = 768, E =
+// 128, top 8).
 struct EpiRows : EpiBase {
   struct Params {
-    float* out;
+    float* scale;  // [max_rows][num_n]
   };
-  __device__ __forceinline__ void tile(const Params& p, const Maps&,
+  __device__ __forceinline__ void tile(const Params& p, const Maps& m,
                                        const Geom& g, const Unit& u,
                                        uint32_t taddr, int r, int i) {
-    if ((r & ~31) >= u.rows) return;
-    float* row = p.out + static_cast<int64_t>(u.row0 + r) * g.H;
+    const int wr = r & ~31;
+    if (wr >= u.rows) return;
+    te = &m.s0;
+    const uint32_t t0 = taddr + (i & 1) * 256;
+    float mx = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-      const int j0 = u.n * 256 + c * 32;
-      if (j0 >= g.H) break;
-      float v[32];
-      tmem_ld32(taddr + (i & 1) * 256 + c * 32, v);
-      float4* d = reinterpret_cast<float4*>(row + j0);
+    for (int c = 0; c < 4; ++c) {
+      if (u.n * 256 + c * 64 >= g.H) break;
+      float v[64];  // columns past H are zero
+      tmem_ld64(t0 + c * 64, v);
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (j0 + 4 * q < g.H)  // H % 8 == 0
-          d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2],
-                             v[4 * q + 3]);
+      for (int k = 0; k < 64; ++k) {
+        const float x = fabsf(v[k]);
+        if (x <= 3.4028235e38f) mx = fmaxf(mx, x);
+      }
+    }
+    // 2^(exponent - 14), kept normal; 1 for a piece of zeros
+    const int e = static_cast<int>(__float_as_uint(mx) >> 23);  // mx >= 0
+    const int se = mx == 0.f ? 127 : max(e - 14, 1);
+    const float scale = __uint_as_float(static_cast<uint32_t>(se) << 23);
+    const float inv = __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
+    p.scale[static_cast<int64_t>(u.row0 + r) * g.num_n + u.n] = scale;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      const int j0 = u.n * 256 + c * 64;
+      if (j0 >= g.H) break;
+      float v[64];
+      tmem_ld64(t0 + c * 64, v);
+      uint32_t w0[16], w1[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const __half2 a = __floats2half2_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
+        const __half2 b =
+            __floats2half2_rn(v[32 + 2 * k] * inv, v[33 + 2 * k] * inv);
+        w0[k] = *reinterpret_cast<const uint32_t*>(&a);
+        w1[k] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      store_box_pair(w0, w1, j0, u.row0 + wr, j0 + 32 < g.H);
     }
   }
 };
@@ -678,8 +711,9 @@ lce_status launch_experts_down(const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(map2(&m.a0, a.a, a.I, a.max_rows, BK, 64));
   LCE_TRY(map3(&m.b0, a.Wd, a.I, a.H, a.E, BK, 256));
   Geom g = geom(a);
+  LCE_TRY(store_map(&m.s0, a.rows_out, a.H, a.max_rows));
   g.num_n = static_cast<int>(ceil_div(a.H, 256));
-  return launch<OpDown, EpiRows>("experts_down", m, g, {a.rows_out}, a, s);
+  return launch<OpDown, EpiRows>("experts_down", m, g, {a.rows_scale}, a, s);
 }
 
 lce_status launch_experts_dgu(const ExpertsArgs& a, cudaStream_t s) {
@@ -705,8 +739,9 @@ lce_status launch_experts_dx(const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(map3(&m.b0, a.Wg, a.H, a.I, a.E, 64, BK));
   LCE_TRY(map3(&m.b1, a.Wu, a.H, a.I, a.E, 64, BK));
   Geom g = geom(a);
+  LCE_TRY(store_map(&m.s0, a.rows_out, a.H, a.max_rows));
   g.num_n = static_cast<int>(ceil_div(a.H, 256));
-  return launch<OpDx, EpiRows>("experts_dx", m, g, {a.rows_out}, a, s);
+  return launch<OpDx, EpiRows>("experts_dx", m, g, {a.rows_scale}, a, s);
 }
 
 lce_status launch_experts_dwd(const ExpertsArgs& a, cudaStream_t s) {

@@ -1,5 +1,7 @@
 // The experts' gated MLP around its contractions: the plan that groups slots
 // by expert (a stable counting sort), and the sums over a token's slots.
+#include <cuda_fp16.h>
+
 #include "lce_device.cuh"
 #include "lce_experts.h"
 #include "lce_host.h"
@@ -230,31 +232,53 @@ __device__ __forceinline__ float weight_at(const void* w, int64_t i) {
   return static_cast<float>(static_cast<const T*>(w)[i]);
 }
 
-// Four columns of a token per thread; a token's rows are added in the order
-// of its slots.
+// Eight columns of a token per thread; a token's rows are added in fp32 in
+// the order of its slots, eight loads in flight. Bound by the rows' bytes.
 template <typename T, bool WEIGHTED>
 __global__ void __launch_bounds__(256)
-    k_combine(const float* __restrict__ rows, const int* __restrict__ row,
+    k_combine(const uint16_t* __restrict__ rows,
+              const float* __restrict__ scale, const int* __restrict__ row,
               const void* __restrict__ w, int64_t L, int K, int64_t H,
               uint16_t* __restrict__ out) {
-  const int64_t quads = H / 4;
+  const int64_t oct = H / 8, tiles = (H + 255) / 256;
   const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (i >= L * quads) return;
-  const int64_t t = i / quads, h = (i - t * quads) * 4;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < K; ++k) {
-    const int r = row[t * K + k];
-    if (r < 0) continue;
-    const float c = WEIGHTED ? weight_at<T>(w, t * K + k) : 1.f;
-    const float4 v = *reinterpret_cast<const float4*>(
-        rows + static_cast<int64_t>(r) * H + h);
-    acc[0] = fmaf(c, v.x, acc[0]);
-    acc[1] = fmaf(c, v.y, acc[1]);
-    acc[2] = fmaf(c, v.z, acc[2]);
-    acc[3] = fmaf(c, v.w, acc[3]);
+  if (i >= L * oct) return;
+  const int64_t t = i / oct, h = (i - t * oct) * 8;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < K; k0 += 8) {
+    uint4 v[8];
+    float c[8];
+    bool live[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int64_t at = t * K + k0 + q;
+      const int r = k0 + q < K ? row[at] : -1;
+      live[q] = r >= 0;
+      v[q] = make_uint4(0, 0, 0, 0);
+      c[q] = 0.f;
+      if (live[q]) {
+        v[q] = __ldg(reinterpret_cast<const uint4*>(
+            rows + static_cast<int64_t>(r) * H + h));
+        c[q] = scale[r * tiles + (h >> 8)];
+        if (WEIGHTED) c[q] *= weight_at<T>(w, at);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (!live[q]) continue;
+      const uint32_t x[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f =
+            __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+        acc[2 * j] = fmaf(c[q], f.x, acc[2 * j]);
+        acc[2 * j + 1] = fmaf(c[q], f.y, acc[2 * j + 1]);
+      }
+    }
   }
-  *reinterpret_cast<uint2*>(out + t * H + h) = make_uint2(
-      pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+  *reinterpret_cast<uint4*>(out + t * H + h) =
+      make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                 pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
 }
 
 template <typename T>
@@ -316,18 +340,21 @@ cudaError_t launch_gather(const Plan& p, int64_t max_rows, int64_t H,
   return cudaGetLastError();
 }
 
-cudaError_t launch_combine(const float* rows, const int* row, const void* w,
-                           lce_dtype wdt, int64_t L, int K, int64_t H,
-                           void* out, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(ceil_div(L * (H / 4), 256));
+cudaError_t launch_combine(const uint16_t* rows, const float* scale,
+                           const int* row, const void* w, lce_dtype wdt,
+                           int64_t L, int K, int64_t H, void* out,
+                           cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(ceil_div(L * (H / 8), 256));
   uint16_t* o = static_cast<uint16_t*>(out);
   if (!w)
-    k_combine<float, false><<<grid, 256, 0, s>>>(rows, row, w, L, K, H, o);
+    k_combine<float, false>
+        <<<grid, 256, 0, s>>>(rows, scale, row, w, L, K, H, o);
   else if (wdt == LCE_F32)
-    k_combine<float, true><<<grid, 256, 0, s>>>(rows, row, w, L, K, H, o);
+    k_combine<float, true>
+        <<<grid, 256, 0, s>>>(rows, scale, row, w, L, K, H, o);
   else
     k_combine<__nv_bfloat16, true>
-        <<<grid, 256, 0, s>>>(rows, row, w, L, K, H, o);
+        <<<grid, 256, 0, s>>>(rows, scale, row, w, L, K, H, o);
   return cudaGetLastError();
 }
 
