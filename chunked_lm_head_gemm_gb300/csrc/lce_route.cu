@@ -3,11 +3,16 @@
 // and the weights stay in registers; a row is read once and only its top_k
 // weights and indices are written.
 //
-// Bound: the logits' bytes forward (67 MB at L = 65536, E = 256 in fp32), the
-// gradient's bytes backward. The selection's rounds are what a row costs in
-// instructions, so each round is two warp-wide integer reductions (largest
-// ordered key, then lowest index among the lanes that hold it) on keys kept
-// as order-preserving integers.
+// Bound: the logits' bytes (67 MB at L = 65536, E = 256 in fp32), but the
+// instructions of the selection come first. So the selection does not search
+// the row top_k times: the n-th largest of the 32 lanes' maxima is a lower
+// bound of the row's n-th largest key, and the few keys that reach it (about
+// n + 2 of 256) are packed one to a lane and ranked against each other at
+// once. Scores of a whole row are computed only where its keys or its sum
+// need them, with the fast exponential; the chosen ones again, exactly.
+// Against top_k rounds of two warp-wide reductions over the whole row: L =
+// 32768, E = 128, top 8 of bf16 39 -> 31 us; L = 65536, E = 256 in 8 groups
+// with a bias 223 -> 121 us.
 #include <math.h>
 
 #include <type_traits>
@@ -23,18 +28,6 @@ constexpr int ROUTE_WARPS = 4;  // rows per block
 constexpr int MAX_E = 1024;
 constexpr int MAX_K = 32;
 constexpr int MAX_GROUPS = 32;
-
-struct RouteArgs {
-  const void* logits;
-  const float* bias;
-  int64_t L;
-  int E, K, groups, topk_group, group_top;
-  int scoring, renorm;
-  float scale;
-  int buf;  // shared-memory elements of one warp (group ranks), or 0
-  void* weights;
-  int32_t* experts;
-};
 
 // fp32 as an unsigned integer of the same order (-0 as +0); every number,
 // the infinities included, lies above 0, which marks "out of the running".
@@ -112,33 +105,45 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane,
   }
 }
 
-// Scores of the row in place of its logits. Softmax: exp(z - max) / sum, 0
-// everywhere when no logit is above -inf; NaN logits reach the sum and with
-// it every score. Error of a score, relative: below 2^-19 (expf 2 ulp twice,
-// the rounding of z - max times at most ln of the score's reciprocal, a sum
-// of at most 1024 terms, one division).
+// The row's maximum for the softmax (0 for a row without a finite logit).
 template <int PER>
-__device__ __forceinline__ void scores(float (&z)[PER], int scoring) {
-  if (scoring == LCE_SIGMOID) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) z[i] = 1.f / (1.f + expf(-z[i]));
-    return;
-  }
+__device__ __forceinline__ float row_max(const float (&z)[PER]) {
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < PER; ++i) m = fmaxf(m, z[i]);
   m = warp_max(m);
-  if (m == -INFINITY) m = 0.f;
+  return m == -INFINITY ? 0.f : m;
+}
+
+// Scores of the row in place of its logits, by ex2.approx. Softmax: exp(z -
+// max) / sum, 0 everywhere when no logit is above -inf; NaN logits reach the
+// sum and with it every score. Returns the sum (1 for an empty row; sigmoid:
+// 1). With e the error of ex2.approx, 2^-22, and that of its argument,
+// 1.5 * 2^-24 of it: a sigmoid score is off by at most s (1 - s) (e + 1.5 *
+// 2^-24 |z|) + 2^-22 + 2^-24 < 2^-21; a softmax score, whose terms lose 2.5 *
+// 2^-24 d to an argument -d and whose sum of at most 1024 adds 36 * 2^-24, by
+// at most 2^-17 of itself (d < 17) or 2^-24 (beyond, where it is tiny).
+template <int PER>
+__device__ __forceinline__ float scores(float (&z)[PER], int scoring,
+                                        float m) {
+  if (scoring == LCE_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      z[i] = __fdividef(1.f, 1.f + ex2(-z[i] * LOG2E));
+    return 1.f;
+  }
   float t = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    z[i] = expf(z[i] - m);
+    z[i] = ex2((z[i] - m) * LOG2E);
     t += z[i];
   }
   t = warp_sum(t);
   if (t == 0.f) t = 1.f;
+  const float r = 1.f / t;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) z[i] /= t;
+  for (int i = 0; i < PER; ++i) z[i] *= r;
+  return t;
 }
 
 // Sigmoid scores of chosen logits so low that their fp32 sum loses its
@@ -151,10 +156,13 @@ __device__ __noinline__ double sigmoid64(float z, double* sum) {
   return p;
 }
 
-// Bound of the error of an fp32 key against exact arithmetic: the score's
-// (scores are at most 1) and the bias addition's rounding.
-__device__ __forceinline__ float key_error(float v) {
-  return 0x1p-19f + 0x1p-23f * fabsf(v);
+// Bound of the error of an fp32 key v with bias b: the score's (scores())
+// and the rounding of the addition.
+__device__ __forceinline__ float key_error(float v, float b, int scoring) {
+  const float s = scoring == LCE_SIGMOID
+                      ? 0x1p-21f
+                      : 0x1p-17f * fabsf(v - b) + 0x1p-24f;
+  return s + 0x1p-23f * fabsf(v);
 }
 
 // Group ranks from per-element values: the values go through shared memory
@@ -163,24 +171,44 @@ __device__ __forceinline__ float key_error(float v) {
 // the rank of group g, -inf where the sum is not a number (inf - inf).
 struct GroupGeom {
   int per, lpg, stride;
-  __host__ __device__ __forceinline__ GroupGeom(int E, int groups) {
+  unsigned recip;  // ceil(2^20 / per): j / per = j recip >> 20 for j < 1024
+  GroupGeom() = default;
+  GroupGeom(int E, int groups) {
     per = E / groups;
+    recip = ((1u << 20) + per - 1) / per;
     int p = 1;
     while (p < groups) p *= 2;
     lpg = 32 / p;
     stride = per + (lpg - per % 32 + 32) % 32;
   }
+  __device__ __forceinline__ int group(int j) const {
+    return static_cast<int>(static_cast<unsigned>(j) * recip >> 20);
+  }
+};
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  int64_t L;
+  int E, K, groups, topk_group, group_top;
+  int scoring, renorm;
+  float scale;
+  GroupGeom gg;
+  void* weights;
+  int32_t* experts;
 };
 
 template <typename F, int PER, int V>
-__device__ __forceinline__ F group_rank(const F (&v)[PER], F* buf, int E,
-                                        int groups, int top, int lane) {
-  const GroupGeom gg(E, groups);
+__device__ __forceinline__ F group_rank(const F (&v)[PER], F* buf,
+                                        const RouteArgs& a_, int top,
+                                        int lane) {
+  const GroupGeom& gg = a_.gg;
+  const int E = a_.E, groups = a_.groups;
   const F lowest = static_cast<F>(-INFINITY);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int j = element<V>(i, lane);
-    if (j < E) buf[(j / gg.per) * gg.stride + j % gg.per] = v[i];
+    if (j < E) buf[j + gg.group(j) * (gg.stride - gg.per)] = v[i];
   }
   __syncwarp();
   const int g = lane / gg.lpg, sub = lane % gg.lpg;
@@ -223,8 +251,8 @@ __device__ __forceinline__ uint32_t keep_groups(F rank, int groups, int take,
 }
 
 // ---------------------------------------------------------------------------
-// the row in 64 bits: taken when two fp32 keys that decide something lie
-// within their error bounds
+// the whole row in 64 bits: taken when two group ranks lie within their error
+// bounds, or when more than 32 keys with a bias reach the threshold
 // ---------------------------------------------------------------------------
 template <typename T, int PER, int V>
 __device__ __noinline__ int select_exact(const RouteArgs& a, const T* row,
@@ -262,10 +290,8 @@ __device__ __noinline__ int select_exact(const RouteArgs& a, const T* row,
     if (j >= a.E || !(z32[i] > -INFINITY) || isnan(v[i])) v[i] = -INFINITY;
   }
   uint32_t kept = FULL;
-  const int per = a.E / a.groups;
   if (a.groups > 1) {
-    const double rank =
-        group_rank<double, PER, V>(v, buf, a.E, a.groups, a.group_top, lane);
+    const double rank = group_rank<double, PER, V>(v, buf, a, a.group_top, lane);
     kept = keep_groups(rank, a.groups, a.topk_group, lane);
   }
   if (key_is_logit)
@@ -276,7 +302,8 @@ __device__ __noinline__ int select_exact(const RouteArgs& a, const T* row,
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int j = element<V>(i, lane);
-    if (j < a.E && (a.groups == 1 || (kept >> (j / per) & 1u))) open |= 1u << i;
+    if (j < a.E && (a.groups == 1 || (kept >> a.gg.group(j) & 1u)))
+      open |= 1u << i;
   }
   int mine = 0;
   for (int k = 0; k < a.K; ++k) {
@@ -308,16 +335,90 @@ __device__ __noinline__ int select_exact(const RouteArgs& a, const T* row,
   return mine;
 }
 
-// The value at element j of the row (j the same in every lane).
-template <int PER, int V>
-__device__ __forceinline__ float gather_slot(const float (&v)[PER], int j) {
-  const int slot = (j / (32 * V)) * V + j % V;
-  float r = 0.f;
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (i == slot) r = v[i];
-  return __shfl_sync(FULL, r, (j / V) % 32);
+// The candidates' order in 64 bits, where neighbours lie within their fp32
+// errors: one exact key a lane, compared as ordered integers (the fp64 pipe
+// is 64 times slower than fp32's, so it sees one exponential and one division
+// a lane, not the whole row; a softmax needs the row's sum in fp64 too).
+// Returns lane k's k-th candidate.
+template <typename T, int PER, int V>
+__device__ __noinline__ int rank_exact(const RouteArgs& a, const T* row,
+                                       bool live, int j, float z, float b,
+                                       int lane, uint2* list) {
+  double p;
+  if (a.scoring == LCE_SIGMOID) {
+    p = 1.0 / (1.0 + exp(-static_cast<double>(z)));
+  } else {
+    float zs[PER];
+    load_row<T, PER, V>(row, a.E, lane, zs);
+    const float m = row_max<PER>(zs);
+    double t = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < PER; ++i)
+      t += exp(static_cast<double>(zs[i]) - static_cast<double>(m));
+    t = warp_sum(t);
+    p = exp(static_cast<double>(z) - static_cast<double>(m)) / t;
+  }
+  double v = p + static_cast<double>(b);
+  if (!(z > -INFINITY) || isnan(v)) v = -INFINITY;
+  const long long bits = __double_as_longlong(v + 0.0);
+  const unsigned long long key =
+      live ? (bits < 0 ? ~static_cast<unsigned long long>(bits)
+                       : static_cast<unsigned long long>(bits) | 1ull << 63)
+           : 0ull;
+  __syncwarp();
+  list[lane] = make_uint2(static_cast<unsigned>(key >> 32),
+                          static_cast<unsigned>(key));
+  list[32 + lane] = make_uint2(static_cast<unsigned>(j), 0u);
+  __syncwarp();
+  int rank = 0;
+  for (int q = 0; q < 32; ++q) {
+    const uint2 o = list[q];
+    const unsigned long long ok =
+        static_cast<unsigned long long>(o.x) << 32 | o.y;
+    const int oj = static_cast<int>(list[32 + q].x);
+    if (ok > key || (ok == key && oj < j && ok != 0ull)) ++rank;
+  }
+  __syncwarp();
+  if (live) list[rank] = make_uint2(static_cast<unsigned>(j), 0u);
+  __syncwarp();
+  return static_cast<int>(list[lane].x);
 }
+
+// top_k rounds over the whole row, each the largest key and the lowest index
+// that has it: for exact keys of which more than 32 reach the threshold.
+template <int PER, int V>
+__device__ __forceinline__ int select_rounds(const uint32_t (&keys)[PER], int K,
+                                          int lane) {
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = keys[i];
+  int mine = 0;
+  for (int k = 0; k < K; ++k) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(FULL, best);
+    unsigned j = FULL;
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i)
+      if (key[i] == top) j = static_cast<unsigned>(element<V>(i, lane));
+    j = __reduce_min_sync(FULL, j);
+    if (lane == k) mine = static_cast<int>(j);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (static_cast<unsigned>(element<V>(i, lane)) == j) key[i] = 0u;
+  }
+  return mine;
+}
+
+// The chosen score of one lane from its logit, to fp32 accuracy.
+__device__ __forceinline__ float one_score(float z, int scoring, float m,
+                                           float t) {
+  return scoring == LCE_SIGMOID ? 1.f / (1.f + expf(-z)) : expf(z - m) / t;
+}
+
+// smem of a warp: two lists of 32 (key, element), then the group ranks.
+constexpr int LIST_BYTES = 2 * 32 * 8;
 
 template <typename T, int PER, int V>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32)
@@ -326,124 +427,180 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = blockIdx.x * static_cast<int64_t>(ROUTE_WARPS) + warp;
   if (row >= a.L) return;
-  double* buf = route_smem + warp * a.buf;
+  const int buf_len = a.groups > 1 ? a.groups * a.gg.stride : 0;
+  double* mine_smem = route_smem + warp * (LIST_BYTES / 8 + buf_len);
+  uint2* list = reinterpret_cast<uint2*>(mine_smem);
+  double* buf = mine_smem + LIST_BYTES / 8;
   const T* zr = static_cast<const T*>(a.logits) + row * a.E;
   float z[PER];
   load_row<T, PER, V>(zr, a.E, lane, z);
-  float s[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) s[i] = z[i];
-  scores<PER>(s, a.scoring);
 
-  const bool key_is_logit = a.bias == nullptr;
-  const int per = a.E / a.groups;
+  const bool biased = a.bias != nullptr;
+  const bool rank_scores = a.groups > 1 && a.group_top == 2;
+  const bool softmax = a.scoring == LCE_SOFTMAX;
+  // a softmax renormalised over the chosen needs neither maximum nor sum
+  const bool whole = biased || rank_scores || (softmax && !a.renorm);
+  float m = 0.f, t = 1.f;
   float v[PER];  // keys
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int j = element<V>(i, lane);
-    const bool live = j < a.E && z[i] > -INFINITY;
-    v[i] = -INFINITY;
-    if (live) {
-      const float t = key_is_logit ? z[i] : s[i] + a.bias[j];
-      if (!isnan(t)) v[i] = t;
+  for (int i = 0; i < PER; ++i) v[i] = z[i];
+  if (whole) {
+    if (softmax) m = row_max<PER>(z);
+    t = scores<PER>(v, a.scoring, m);
+  }
+  if (biased) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int j = element<V>(i, lane);
+      if (j < a.E) v[i] += a.bias[j];
     }
   }
   bool unsure = false;
   uint32_t kept = FULL;
   if (a.groups > 1) {
-    float rank;
-    const bool exact = key_is_logit && a.group_top == 1;
-    if (key_is_logit && a.group_top == 2) {
-      float u[PER];
+    // masked experts, and keys that are no numbers, rank lowest
 #pragma unroll
-      for (int i = 0; i < PER; ++i) u[i] = z[i] > -INFINITY ? s[i] : -INFINITY;
-      rank = group_rank<float, PER, V>(u, reinterpret_cast<float*>(buf), a.E,
-                                       a.groups, 2, lane);
-    } else {
-      rank = group_rank<float, PER, V>(v, reinterpret_cast<float*>(buf), a.E,
-                                       a.groups, a.group_top, lane);
+    for (int i = 0; i < PER; ++i)
+      if (!(z[i] > -INFINITY) || isnan(v[i])) v[i] = -INFINITY;
+    const bool exact = !biased && !rank_scores;
+    if (exact) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        v[i] = z[i] > -INFINITY ? z[i] : -INFINITY;
     }
+    const float rank = group_rank<float, PER, V>(
+        v, reinterpret_cast<float*>(buf), a, a.group_top, lane);
     kept = keep_groups(rank, a.groups, a.topk_group, lane);
-    if (!exact && a.topk_group < a.groups) {
+    if (!exact) {
       const bool in = kept >> lane & 1u;
-      // the lowest kept rank against the highest one left out
+      // the lowest kept rank against the highest one left out; of the
+      // softmax scores in a rank none is above the row's largest, 1 / t
       const float lo = -warp_max(lane < a.groups && in ? -rank : -INFINITY);
       const float hi = warp_max(lane < a.groups && !in ? rank : -INFINITY);
-      if (hi > -INFINITY)
-        unsure = !(lo - hi > 2.f * (key_error(lo) + key_error(hi)));
+      const float top = softmax ? 1.f / t : 0.f;
+      float big = 0.f;  // the largest key's size: what additions round by
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (v[i] > -INFINITY) big = fmaxf(big, fabsf(v[i]));
+      big = warp_max(big);
+      const float err = key_error(top, 0.f, a.scoring) + 0x1p-22f * big;
+      if (hi > -INFINITY) unsure = !(lo - hi > 4.f * err);
     }
   }
-  uint32_t key[PER];
+  uint32_t key[PER], largest = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int j = element<V>(i, lane);
-    const bool in = j < a.E && (a.groups == 1 || (kept >> (j / per) & 1u));
-    key[i] = in ? ordered(v[i]) : 0u;
+    const bool in = j < a.E && (a.groups == 1 || (kept >> a.gg.group(j) & 1u));
+    const float x = biased ? v[i] : z[i];
+    const bool live = z[i] > -INFINITY && !isnan(x);
+    key[i] = in ? ordered(live ? x : -INFINITY) : 0u;
+    largest = max(largest, key[i]);
   }
 
-  int mine = 0;          // lane k: the k-th expert
-  uint32_t last = 0;     // the previous round's key, its logit and its bias
-  float last_z = 0.f, last_b = 0.f;
-  const int open = a.groups == 1 ? a.E : a.topk_group * per;
-  // With a bias the rounds go on past top_k until a key clearly below the
-  // last one shows that nothing left out could belong in.
-  for (int k = 0; k < open && !unsure; ++k) {
-    if (k >= a.K && key_is_logit) break;
-    uint32_t best = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    const uint32_t top = __reduce_max_sync(FULL, best);
-    const int j = static_cast<int>(__reduce_min_sync(
-        FULL, best == top ? static_cast<unsigned>(element<V>(at, lane))
-                          : FULL));
-    if (!key_is_logit) {
-      const float jz = gather_slot<PER, V>(z, j), jb = a.bias[j];
-      if (k > 0) {
-        const float hi = from_ordered(last), lo = from_ordered(top);
-        const bool apart =
-            lo == -INFINITY || hi - lo > key_error(hi) + key_error(lo);
-        if (apart && k >= a.K) break;
-        // equal inputs have equal keys, whatever the rounding
-        if (!apart && !(jz == last_z && jb == last_b)) unsure = true;
-      }
-      last = top;
-      last_z = jz;
-      last_b = jb;
+  // threshold: the want-th largest of the lanes' maxima; every key if fewer
+  // lanes than that are in the running
+  const int open = a.groups == 1 ? a.E : a.topk_group * a.gg.per;
+  const int want = min(open, a.K + (biased ? 1 : 0));
+  uint32_t floor_key = 1u;
+  {
+    uint32_t cur = largest;
+    for (int k = 0; k < want; ++k) {
+      floor_key = __reduce_max_sync(FULL, cur);
+      const unsigned who = __ballot_sync(FULL, cur == floor_key);
+      if (lane == __ffs(who) - 1) cur = 0u;
     }
-    if (lane == k) mine = j;
+    if (biased && floor_key > 0u) {
+      // down by what both sides of the border may be off, so that nothing
+      // below it can belong to the chosen in exact arithmetic
+      const float x = from_ordered(floor_key);
+      const float s_max = softmax ? 1.f / t : 1.f;
+      const float err = key_error(s_max, 0.f, a.scoring) +
+                        0x1p-23f * (fabsf(x) + s_max);
+      if (x > -INFINITY) floor_key = ordered(x - 4.f * err);
+    }
+    floor_key = max(floor_key, 1u);
+  }
+  int found = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (element<V>(i, lane) == j) key[i] = 0u;
+  for (int i = 0; i < PER; ++i) {
+    const bool take = key[i] >= floor_key;
+    const unsigned who = __ballot_sync(FULL, take);
+    const int at = found + __popc(who & ((1u << lane) - 1u));
+    if (take && at < 32)
+      list[at] = make_uint2(key[i], static_cast<unsigned>(element<V>(i, lane)));
+    found += __popc(who);
+  }
+  int mine = 0;  // lane k: the k-th expert
+  if (found > 32) {
+    if (biased)
+      unsure = true;
+    else if (!unsure)
+      mine = select_rounds<PER, V>(key, a.K, lane);
+  } else if (!unsure) {
+    __syncwarp();
+    const uint2 own = lane < found ? list[lane] : make_uint2(0u, 0u);
+    int rank = 0;
+    for (int q = 0; q < found; ++q) {
+      const uint2 o = list[q];
+      if (o.x > own.x || (o.x == own.x && o.y < own.y)) ++rank;
+    }
+    if (lane < found) list[32 + rank] = own;
+    __syncwarp();
+    const uint2 at = list[32 + (lane < found ? lane : 0)];
+    mine = static_cast<int>(at.y);
+    if (biased) {
+      // neighbours in the order: apart beyond their errors, or the same
+      // inputs (equal keys, whatever the rounding)
+      const float x = from_ordered(at.x), jz = load1(zr + mine),
+                  jb = a.bias[mine];
+      const float err = key_error(x, jb, a.scoring);
+      const float nx = __shfl_down_sync(FULL, x, 1),
+                  nz = __shfl_down_sync(FULL, jz, 1),
+                  nb = __shfl_down_sync(FULL, jb, 1),
+                  ne = __shfl_down_sync(FULL, err, 1);
+      const bool pair = lane + 1 < found;
+      const bool apart = pair && (nx == -INFINITY || x - nx > err + ne);
+      const bool same = pair && nz == jz && nb == jb;
+      const unsigned apart_of = __ballot_sync(FULL, apart);
+      const unsigned fine = __ballot_sync(FULL, apart || same);
+      // the first clear step at or past the last chosen key
+      const unsigned past = apart_of >> (a.K - 1) << (a.K - 1);
+      const int end = past ? __ffs(past) - 1 : found - 1;
+      const unsigned before = end >= 31 ? 0x7fffffffu : (1u << end) - 1u;
+      if ((fine & before) != before)  // the same for the whole warp
+        mine = rank_exact<T, PER, V>(a, zr, lane < found, mine, jz, jb, lane,
+                                     list);
+    }
   }
   if (unsure)  // the same for the whole warp
     mine = select_exact<T, PER, V>(a, zr, buf, lane);
 
-  float w = 0.f;
-  for (int k = 0; k < a.K; ++k) {
-    const int j = __shfl_sync(FULL, mine, k);
-    const float x = gather_slot<PER, V>(s, j);
-    if (lane == k) w = x;
-  }
   const bool out = lane < a.K;
+  const float zk = out ? load1(zr + mine) : -INFINITY;
+  float w;
   if (a.renorm) {
-    const float t = warp_sum(out ? w : 0.f);
-    if (t < TINY_SUM && a.scoring == LCE_SIGMOID) {  // the same for the warp
-      float zk = -INFINITY;
-      for (int k = 0; k < a.K; ++k) {
-        const float x = gather_slot<PER, V>(z, __shfl_sync(FULL, mine, k));
-        if (lane == k) zk = x;
-      }
-      double t64;
-      const double p = sigmoid64(zk, &t64);
-      w = t64 == 0.0 ? 0.f : static_cast<float>(p / t64);
+    if (softmax) {
+      m = warp_max(zk);
+      if (m == -INFINITY) m = 0.f;
+      w = out ? expf(zk - m) : 0.f;
+      bool nan = false;  // a NaN anywhere in the row reaches every weight
+#pragma unroll
+      for (int i = 0; i < PER; ++i) nan |= isnan(z[i]);
+      if (__any_sync(FULL, nan)) w = NAN;
     } else {
-      w = t == 0.f ? 0.f : w / t;
+      w = out ? one_score(zk, LCE_SIGMOID, 0.f, 1.f) : 0.f;
     }
+    const float sum = warp_sum(w);
+    if (sum < TINY_SUM && !softmax) {  // the same for the warp
+      double sum64;
+      const double p = sigmoid64(zk, &sum64);
+      w = sum64 == 0.0 ? 0.f : static_cast<float>(p / sum64);
+    } else {
+      w = sum == 0.f ? 0.f : w / sum;
+    }
+  } else {
+    w = out ? one_score(zk, a.scoring, m, t) : 0.f;
   }
   w *= a.scale;
   if (out) {
@@ -495,12 +652,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32)
   float fill[PER];
   if (WHOLE) {
     load_row<T, PER, V>(zr, a.E, lane, fill);
-    scores<PER>(fill, LCE_SOFTMAX);
-    for (int k = 0; k < a.K; ++k) {
-      const int jk = __shfl_sync(FULL, j, k);
-      const float x = gather_slot<PER, V>(fill, jk < 0 ? 0 : jk);
-      if (lane == k && j >= 0) p = x;
-    }
+    const float m = row_max<PER>(fill);
+    const float t = scores<PER>(fill, LCE_SOFTMAX, m);
+    if (j >= 0) p = one_score(load1(zr + j), LCE_SOFTMAX, m, t);
     const float dot = warp_sum(u * p);
     d = p * u;  // the element's own share; -p dot once per element, below
 #pragma unroll
@@ -570,7 +724,10 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 
 template <typename T, int PER, int V>
 cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s) {
-  const size_t smem = sizeof(double) * ROUTE_WARPS * a.buf;
+  const size_t smem =
+      ROUTE_WARPS * (LIST_BYTES + (a.groups > 1 ? sizeof(double) * a.groups *
+                                                      a.gg.stride
+                                                : 0));
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(
         k_route<T, PER, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -677,7 +834,7 @@ lce_status lce_route_forward(const void* logits, lce_dtype dt,
   a.scoring = o.scoring;
   a.renorm = o.renormalize;
   a.scale = o.scale;
-  if (a.groups > 1) a.buf = a.groups * GroupGeom(a.E, a.groups).stride;
+  a.gg = GroupGeom(a.E, a.groups);
   a.weights = weights;
   a.experts = experts;
   ProfScope ps(LCE_K_ROUTE, s);
