@@ -8,6 +8,7 @@ built or the device is not sm_103, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -237,7 +238,13 @@ def _check(status: int, where: str):
 
 
 def _stream_ptr(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The device's current stream (device None: the current device's)."""
+    if isinstance(device, str):
+        device = torch.device(device)
+    index = getattr(device, "index", device)
+    if index is None:
+        index = torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -773,13 +780,15 @@ def mlp_backward(x, Wg, Wu, Wd, dy, chunk_rows: int = 0, workspace=None,
     return dx, dWg, dWu, dWd
 
 
+@functools.lru_cache(maxsize=256)
 def _route_opts(scoring, top_k, n_group, topk_group, group_top, renormalize,
                 scale):
     if scoring not in SCORING:
         raise ValueError(f"scoring must be one of {sorted(SCORING)}, got "
                          f"{scoring!r}")
-    return RouteOpts(SCORING[scoring], top_k, n_group, topk_group, group_top,
-                     int(bool(renormalize)), scale)
+    return ctypes.pointer(RouteOpts(SCORING[scoring], top_k, n_group,
+                                    topk_group, group_top,
+                                    int(bool(renormalize)), scale))
 
 
 def _check_logits(logits):
@@ -813,7 +822,7 @@ def route_forward(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
     experts = experts_out if experts_out is not None else torch.empty(
         L, k, dtype=torch.int32, device=dev)
     st = lib.lce_route_forward(logits.data_ptr(), code, _ptr(bias), L, E,
-                               ctypes.byref(opts), weights.data_ptr(),
+                               opts, weights.data_ptr(),
                                experts.data_ptr(), _stream_ptr(dev))
     _check(st, "lce_route_forward")
     return weights, experts
@@ -838,7 +847,7 @@ def route_backward(logits: torch.Tensor, experts: torch.Tensor,
     opts = _route_opts(scoring, k, 1, 1, 1, renormalize, scale)
     out = dlogits_out if dlogits_out is not None else torch.empty_like(logits)
     st = lib.lce_route_backward(logits.data_ptr(), code, experts.data_ptr(),
-                                dweights.data_ptr(), L, E, ctypes.byref(opts),
+                                dweights.data_ptr(), L, E, opts,
                                 out.data_ptr(), _stream_ptr(dev))
     _check(st, "lce_route_backward")
     return out

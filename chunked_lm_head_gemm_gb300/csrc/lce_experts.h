@@ -3,7 +3,7 @@
 //
 // Rows: the slots of an expert, in slot order, form one segment of rows;
 // segments start at multiples of SEG_ROWS and are padded to one with rows
-// that hold no slot (token = -1) and are zero.
+// that hold no slot.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -13,10 +13,20 @@
 
 namespace lce {
 
+// Programmatic dependent launch (launch_early): every kernel of a call but its
+// first begins early, waits here before its first access to global memory,
+// and lets the next one begin. What the kernels before it wrote is read by
+// plain loads, never by the read-only path, whose loads the compiler may move
+// up past the wait.
+__device__ __forceinline__ void begin_early() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 constexpr int SEG_ROWS = 64;     // one K block of the weight gradients
 constexpr int MAX_EXPERTS = 1024;
 constexpr int PLAN_CHUNK = 2048; // slots of one counting block
-constexpr int PLAN_SMALL = 8192; // up to here one block makes the plan
+constexpr int PLAN_SMALL = 4096; // up to here one block makes the plan
 
 struct PlanHead {
   int tiles;  // row tiles of at most 128 rows
@@ -33,23 +43,23 @@ struct Plan {
   PlanHead* head;
   RowTile* tile;  // [max_tiles]
   int2* seg;      // [E]: first row, padded rows
-  int* token;     // [max_rows]: token of a row, -1 for a padding row
   int* slot;      // [max_rows]: slot of a row, -1 for a padding row
   int* row;       // [n]: row of a slot, -1 where it is dropped
-  int* count;     // [E]: slots of an expert
   int* hist;      // [E][chunks]: slots of an expert in a chunk, then before it
 };
 
-// Queues the plan of `n` slots (experts[n], `K` to a token). Deterministic:
+// Queues the plan of the slots experts[n]. Deterministic:
 // integer counts and positions that follow slot order.
-cudaError_t launch_plan(const int32_t* experts, int64_t n, int K, int E,
+cudaError_t launch_plan(const int32_t* experts, int64_t n, int E,
                         const Plan& p, unsigned* err, cudaStream_t s);
 
-// out[r][:] = x[token of row r][:] (0 in padding rows) for the plan's rows,
-// bf16 of H columns; with y also out_y from y.
-cudaError_t launch_gather(const Plan& p, int64_t max_rows, int64_t H,
+// out[row of (t, k)][:] = x[t][:] for every slot of the plan, bf16 of H
+// columns; with y also out_y from y. With `zero` the padding rows become 0:
+// the weight gradients sum over them; elsewhere what they hold reaches no
+// result.
+cudaError_t launch_gather(const Plan& p, int64_t L, int K, int E, int64_t H,
                           const void* x, uint16_t* out, const void* y,
-                          uint16_t* out_y, cudaStream_t s);
+                          uint16_t* out_y, bool zero, cudaStream_t s);
 
 // out[t][:] = sum_k w[t][k] rows[row(t, k)][:] in bf16, k in order, dropped
 // slots left out (w NULL: weights 1). rows: fp16 times the scale of each row
@@ -58,6 +68,13 @@ cudaError_t launch_combine(const uint16_t* rows, const float* scale,
                            const int* row, const void* w, lce_dtype wdt,
                            int64_t L, int K, int64_t H, void* out,
                            cudaStream_t s);
+
+// The forward of few slots without a plan (a: fp32 [L K][I] scratch).
+cudaError_t launch_token(const void* x, const void* Wg, const void* Wu,
+                         const void* Wd, const void* weights, lce_dtype wdt,
+                         const int32_t* experts, int64_t L, int K, int64_t H,
+                         int64_t I, int E, float* a, void* y, unsigned* err,
+                         cudaStream_t s);
 
 // dweights[slot] = sum over the column tiles of part[tile][row], in order.
 cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,

@@ -13,6 +13,10 @@ struct Sizes {
   int64_t L, H, I, E, K;
 };
 
+// Up to this many slots the forward reads weights slot by slot on the CUDA
+// cores (launch_token) instead of planning tiles for the tensor cores.
+constexpr int64_t TOKEN_SLOTS = 32;
+
 bool sizes_ok(const Sizes& z) {
   if (z.L < 0 || z.E < 1 || z.E > MAX_EXPERTS || z.K < 1 || z.K > 32)
     return false;
@@ -33,7 +37,7 @@ int64_t max_tiles(const Sizes& z) {
 }
 
 struct Layout {
-  size_t head, tile, seg, token, slot, row, count, hist;
+  size_t head, tile, seg, slot, row, hist;
   size_t xr, dyr, a, dg, du, rows, scale, part, total;
 };
 
@@ -49,10 +53,8 @@ Layout layout(const Sizes& z, bool backward) {
   w.head = take(sizeof(PlanHead));
   w.tile = take(max_tiles(z) * static_cast<int64_t>(sizeof(RowTile)));
   w.seg = take(z.E * 8);
-  w.token = take(P * 4);
   w.slot = take(P * 4);
   w.row = take(n * 4);
-  w.count = take(z.E * 4);
   w.hist = take(z.E * ceil_div(n, PLAN_CHUNK) * 4);
   w.xr = take(P * z.H * 2);
   w.a = take(P * z.I * 2);
@@ -89,10 +91,8 @@ ExpertsArgs arguments(const Sizes& z, const Layout& w, uint8_t* ws,
   a.plan.head = reinterpret_cast<PlanHead*>(ws + w.head);
   a.plan.tile = reinterpret_cast<RowTile*>(ws + w.tile);
   a.plan.seg = reinterpret_cast<int2*>(ws + w.seg);
-  a.plan.token = reinterpret_cast<int*>(ws + w.token);
   a.plan.slot = reinterpret_cast<int*>(ws + w.slot);
   a.plan.row = reinterpret_cast<int*>(ws + w.row);
-  a.plan.count = reinterpret_cast<int*>(ws + w.count);
   a.plan.hist = reinterpret_cast<int*>(ws + w.hist);
   a.H = z.H;
   a.I = z.I;
@@ -134,13 +134,12 @@ lce_status timed(int kind, double flops, cudaStream_t s, F&& f) {
 lce_status make_plan(const Sizes& z, const int32_t* experts, const void* x,
                      const void* dy, const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(timed(LCE_K_EXPERTS_PLAN, 0, s, [&] {
-    return cuda_try(launch_plan(experts, z.L * z.K, static_cast<int>(z.K),
-                                a.E, a.plan, a.err, s),
+    return cuda_try(launch_plan(experts, z.L * z.K, a.E, a.plan, a.err, s),
                     "experts_plan");
   }));
   return timed(LCE_K_EXPERTS_GATHER, 0, s, [&] {
-    return cuda_try(launch_gather(a.plan, a.max_rows, z.H, x, a.xr, dy, a.dyr,
-                                  s),
+    return cuda_try(launch_gather(a.plan, z.L, static_cast<int>(z.K), a.E, z.H,
+                                  x, a.xr, dy, a.dyr, dy != nullptr, s),
                     "experts_gather");
   });
 }
@@ -179,6 +178,14 @@ lce_status lce_experts_forward(const void* x, const void* Wg, const void* Wu,
   a.Wu = Wu;
   a.Wd = Wd;
   const double slot_flops = 2.0 * L * top_k * H * I;
+  if (L * top_k <= TOKEN_SLOTS)
+    return timed(LCE_K_EXPERTS_TOKEN, 3 * slot_flops, s, [&] {
+      return cuda_try(
+          launch_token(x, Wg, Wu, Wd, weights, weights_dt, experts, L,
+                       static_cast<int>(top_k), H, I, a.E,
+                       reinterpret_cast<float*>(a.a), y, a.err, s),
+          "experts_token");
+    });
   LCE_TRY(make_plan(z, experts, x, nullptr, a, s));
   LCE_TRY(timed(LCE_K_EXPERTS_UP, 2 * slot_flops, s,
                 [&] { return launch_experts_up(a, s); }));

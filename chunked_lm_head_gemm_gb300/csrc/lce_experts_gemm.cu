@@ -88,11 +88,11 @@ __device__ __forceinline__ void load_cols(uint32_t dst, const CUtensorMap* tm,
 // ---- the uses ----------------------------------------------------------------
 struct RowUnits {
   __device__ static int units(const Geom& g) {
-    return __ldg(&g.head->tiles) * g.num_n;
+    return g.head->tiles * g.num_n;
   }
   __device__ static Unit unit(const Geom& g, int u) {
     const int t = u / g.num_n;
-    const int4 r = __ldg(reinterpret_cast<const int4*>(g.tile) + t);
+    const int4 r = reinterpret_cast<const int4*>(g.tile)[t];
     return Unit{r.x, r.y, r.z, t, u - t * g.num_n};
   }
 };
@@ -101,7 +101,7 @@ struct GradUnits {
   __device__ static Unit unit(const Geom& g, int u) {
     const int per = g.num_m * g.num_n;
     const int e = u / per, r = u - e * per;
-    const int2 s = __ldg(g.seg + e);
+    const int2 s = g.seg[e];
     return Unit{e, s.x, s.y, r / g.num_n, r % g.num_n};
   }
 };
@@ -340,7 +340,7 @@ struct EpiDgu : EpiBase {
                                        uint32_t taddr, int r, int i) {
     const int wr = r & ~31;
     if (wr >= u.rows) return;
-    const int slot = __ldg(g.slot + u.row0 + r);
+    const int slot = g.slot[u.row0 + r];
     float w = 0.f;
     if (slot >= 0)
       w = p.w_f32 ? __ldg(static_cast<const float*>(p.w) + slot)
@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx ctx{abort_flag, err, g.timeout_ns};
+  begin_early();  // all above touches no global memory
   const int units = Op::units(g);
 
   if (warp == 0) {
@@ -681,8 +682,8 @@ lce_status launch(const char* what, const Maps& m, const Geom& g,
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM_BYTES);
   if (e == cudaSuccess) {
-    kern<<<a.grid, GEMM_THREADS, GEMM_SMEM_BYTES, s>>>(m, g, p, a.err);
-    e = cudaGetLastError();
+    e = launch_early(kern, a.grid, GEMM_THREADS, GEMM_SMEM_BYTES, s, m, g, p,
+                     a.err);
   }
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, what);
 }

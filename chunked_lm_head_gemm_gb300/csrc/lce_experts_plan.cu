@@ -22,31 +22,54 @@ __device__ __forceinline__ int expert_of(const int32_t* experts, int64_t n,
   return -1;
 }
 
-// One warp over the slots [i0, i1), 32 at a time: cnt[e] grows by the slots
-// of e. With PLACE, cnt[e] holds the position of the warp's next slot of e
-// in its segment, and every slot gets its row.
-template <bool PLACE>
-__device__ __forceinline__ void walk_slots(const int32_t* experts, int64_t n,
-                                           int64_t i0, int64_t i1, int E,
-                                           int K, int* cnt, const int* start,
-                                           const Plan& p, unsigned* err) {
+// A warp's slots, ITEMS to a lane: slot i0 + 32 q + lane in e[q], -1 where it
+// is dropped or past the end. All loads are in flight at once.
+template <int ITEMS>
+__device__ __forceinline__ void load_slots(const int32_t* experts, int64_t n,
+                                           int64_t i0, int E, int (&e)[ITEMS],
+                                           unsigned* err) {
   const int lane = threadIdx.x & 31;
-  for (int64_t i = i0 + lane; i - lane < i1; i += 32) {
-    const int e = expert_of(experts, i < i1 ? n : 0, i, E, PLACE ? nullptr : err);
-    const unsigned same = __match_any_sync(FULL, e);
+#pragma unroll
+  for (int q = 0; q < ITEMS; ++q)
+    e[q] = expert_of(experts, n, i0 + 32 * q + lane, E, err);
+}
+
+// Counts a warp's slots into cnt[expert].
+template <int ITEMS>
+__device__ __forceinline__ void count_slots(const int (&e)[ITEMS], int* cnt) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < ITEMS; ++q) {
+    const unsigned same = __match_any_sync(FULL, e[q]);
+    if (e[q] >= 0 && (same & ((1u << lane) - 1u)) == 0u)
+      cnt[e[q]] += __popc(same);
+    __syncwarp();
+  }
+}
+
+// Gives a warp's slots their rows, in slot order; cnt[e] holds the position
+// in its segment of the warp's next slot of e.
+template <int ITEMS>
+__device__ __forceinline__ void place_slots(const int (&e)[ITEMS], int64_t n,
+                                            int64_t i0, int* cnt,
+                                            const int* start, const Plan& p) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < ITEMS; ++q) {
+    const int64_t i = i0 + 32 * q + lane;
+    const unsigned same = __match_any_sync(FULL, e[q]);
     const int before = __popc(same & ((1u << lane) - 1u));
-    if (e >= 0) {
-      if (PLACE) {
-        const int r = start[e] + cnt[e] + before;
-        p.token[r] = static_cast<int>(i / K);
-        p.slot[r] = static_cast<int>(i);
-        p.row[i] = r;
-      }
-    } else if (PLACE && i < i1) {
+    int at = 0;
+    if (e[q] >= 0) at = cnt[e[q]];
+    __syncwarp();
+    if (e[q] >= 0) {
+      const int r = start[e[q]] + at + before;
+      p.slot[r] = static_cast<int>(i);
+      p.row[i] = r;
+      if (before == 0) cnt[e[q]] = at + __popc(same);
+    } else if (i < n) {
       p.row[i] = -1;
     }
-    __syncwarp();
-    if (e >= 0 && before == 0) cnt[e] += __popc(same);
     __syncwarp();
   }
 }
@@ -58,10 +81,11 @@ __device__ __forceinline__ int tiles_of(int c) {
   return (padded(c) + BM - 1) / BM;
 }
 
-// One block of MAX_EXPERTS threads: segments, tiles and padding rows from
-// the experts' counts. start[] (shared or global) gets each segment's row.
+// One block of 1024 threads: segments, tiles and padding rows from the
+// experts' counts (c: thread e's expert). start[] (shared, E + 1 entries) gets
+// each segment's row, cnt[] (shared) the counts.
 __device__ __forceinline__ void lay_out(int c, int E, const Plan& p,
-                                        int* start) {
+                                        int* start, int* cnt) {
   __shared__ int warp_rows[32], warp_tiles[32];
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   if (e >= E) c = 0;
@@ -86,45 +110,52 @@ __device__ __forceinline__ void lay_out(int c, int E, const Plan& p,
   }
   if (e < E) {
     const int row0 = r - rows;
-    int at = t - tiles;
     start[e] = row0;
+    cnt[e] = c;
     p.seg[e] = make_int2(row0, rows);
-    p.count[e] = c;
+    int at = t - tiles;
     for (int q = 0; q < rows; q += BM)
       p.tile[at++] = RowTile{e, row0 + q, min(BM, rows - q), 0};
-    for (int q = c; q < rows; ++q) {
-      p.token[row0 + q] = -1;
-      p.slot[row0 + q] = -1;
-    }
     if (e == E - 1) *p.head = PlanHead{t, r};
+  }
+  __syncthreads();
+  // padding rows: a warp to an expert, so that the stores are contiguous
+  for (int x = warp; x < E; x += 32) {
+    const int n = cnt[x];
+    for (int q = n + lane; q < padded(n); q += 32) p.slot[start[x] + q] = -1;
   }
 }
 
-// Few slots: the whole plan in one block (a launch instead of four).
+// Few slots: the whole plan in one block (a launch instead of four). Each of
+// `workers` warps takes 32 ITEMS slots.
+template <int ITEMS>
 __global__ void __launch_bounds__(1024)
-    k_plan_small(const int32_t* experts, int n, int K, int E, Plan p,
+    k_plan_small(const int32_t* experts, int n, int E, Plan p,
                  unsigned* err) {
   extern __shared__ int plan_smem[];
-  int* cnt = plan_smem;          // [warps][E]
-  const int warps = blockDim.x >> 5;
-  int* start = cnt + warps * E;  // [E]
+  const int workers = (n + 32 * ITEMS - 1) / (32 * ITEMS);
+  int* cnt = plan_smem;            // [workers][E]
+  int* start = cnt + workers * E;  // [E]
+  int* totals = start + E;         // [E]
   const int warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < warps * E; i += blockDim.x) cnt[i] = 0;
+  const int i0 = warp * 32 * ITEMS;
+  int e[ITEMS];
+  if (warp < workers) load_slots<ITEMS>(experts, n, i0, E, e, err);
+  for (int i = threadIdx.x; i < workers * E; i += blockDim.x) cnt[i] = 0;
   __syncthreads();
-  const int per = ((n + warps - 1) / warps + 31) / 32 * 32;
-  const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
-  walk_slots<false>(experts, n, i0, i1, E, K, cnt + warp * E, nullptr, p, err);
+  if (warp < workers) count_slots<ITEMS>(e, cnt + warp * E);
   __syncthreads();
   int total = 0;
   if (threadIdx.x < E)
-    for (int w = 0; w < warps; ++w) {
+    for (int w = 0; w < workers; ++w) {
       const int c = cnt[w * E + threadIdx.x];
       cnt[w * E + threadIdx.x] = total;
       total += c;
     }
-  lay_out(total, E, p, start);
+  lay_out(total, E, p, start, totals);
   __syncthreads();
-  walk_slots<true>(experts, n, i0, i1, E, K, cnt + warp * E, start, p, err);
+  if (warp < workers)
+    place_slots<ITEMS>(e, n, i0, cnt + warp * E, start, p);
 }
 
 constexpr int CHUNK_WARPS = 8;
@@ -146,48 +177,59 @@ __global__ void __launch_bounds__(CHUNK_WARPS * 32)
     p.hist[static_cast<int64_t>(e) * chunks + blockIdx.x] = plan_smem[e];
 }
 
-// Step 2: one warp per expert turns the chunk counts into the counts before.
-__global__ void __launch_bounds__(256) k_plan_scan(int E, int chunks, Plan p) {
-  const int e = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+// Step 2, one block: the chunk counts become the counts before the chunk
+// (a warp to an expert), then segments, tiles and padding.
+__global__ void __launch_bounds__(1024) k_plan_layout(int E, int chunks,
+                                                      Plan p) {
+  __shared__ int start[MAX_EXPERTS], cnt[MAX_EXPERTS];
+  begin_early();
   const int lane = threadIdx.x & 31;
-  if (e >= E) return;
-  int* h = p.hist + static_cast<int64_t>(e) * chunks;
-  int before = 0;
-  for (int c0 = 0; c0 < chunks; c0 += 32) {
-    const int c = c0 + lane < chunks ? h[c0 + lane] : 0;
-    int r = c;
+  for (int e = threadIdx.x >> 5; e < E; e += 32) {
+    int* h = p.hist + static_cast<int64_t>(e) * chunks;
+    int before = 0;
+    for (int c0 = 0; c0 < chunks; c0 += 128) {
+      int c[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(FULL, r, o);
-      if (lane >= o) r += a;
+      for (int q = 0; q < 4; ++q) {
+        const int at = c0 + 32 * q + lane;
+        c[q] = at < chunks ? h[at] : 0;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        int r = c[q];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int a = __shfl_up_sync(FULL, r, o);
+          if (lane >= o) r += a;
+        }
+        const int at = c0 + 32 * q + lane;
+        if (at < chunks) h[at] = before + r - c[q];
+        before += __shfl_sync(FULL, r, 31);
+      }
     }
-    if (c0 + lane < chunks) h[c0 + lane] = before + r - c;
-    before += __shfl_sync(FULL, r, 31);
+    if (lane == 0) cnt[e] = before;
   }
-  if (lane == 0) p.count[e] = before;
+  __syncthreads();
+  const int c = threadIdx.x < E ? cnt[threadIdx.x] : 0;
+  lay_out(c, E, p, start, cnt);
 }
 
-// Step 3: segments and tiles.
-__global__ void __launch_bounds__(1024) k_plan_layout(int E, Plan p) {
-  __shared__ int start[MAX_EXPERTS];
-  lay_out(threadIdx.x < E ? p.count[threadIdx.x] : 0, E, p, start);
-}
-
-// Step 4: every slot's row.
+// Step 3: every slot's row.
 __global__ void __launch_bounds__(CHUNK_WARPS * 32)
-    k_plan_place(const int32_t* experts, int64_t n, int K, int E, int chunks,
-                 Plan p) {
+    k_plan_place(const int32_t* experts, int64_t n, int E, int chunks, Plan p) {
   extern __shared__ int plan_smem[];
   int* cnt = plan_smem;                // [CHUNK_WARPS][E]
   int* start = cnt + CHUNK_WARPS * E;  // [E]
   const int warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < CHUNK_WARPS * E; i += blockDim.x) cnt[i] = 0;
+  constexpr int ITEMS = PLAN_CHUNK / CHUNK_WARPS / 32;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * PLAN_CHUNK +
+                     warp * (32 * ITEMS);
+  int mine[ITEMS];
+  load_slots<ITEMS>(experts, n, i0, E, mine, nullptr);
   __syncthreads();
-  constexpr int PER = PLAN_CHUNK / CHUNK_WARPS;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * PLAN_CHUNK;
-  const int64_t i0 = min(n, c0 + warp * PER), i1 = min(n, i0 + PER);
-  walk_slots<false>(experts, n, i0, i1, E, K, cnt + warp * E, nullptr, p,
-                    nullptr);
+  begin_early();
+  count_slots<ITEMS>(mine, cnt + warp * E);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int before = p.hist[static_cast<int64_t>(e) * chunks + blockIdx.x];
@@ -199,31 +241,42 @@ __global__ void __launch_bounds__(CHUNK_WARPS * 32)
     start[e] = p.seg[e].x;
   }
   __syncthreads();
-  walk_slots<true>(experts, n, i0, i1, E, K, cnt + warp * E, start, p,
-                   nullptr);
+  place_slots<ITEMS>(mine, n, i0, cnt + warp * E, start, p);
 }
 
-// One warp per row, 16 bytes a lane, four loads in flight.
+// Eight columns of a token per thread (threads x: columns, y: tokens): read
+// once, written to each of the token's rows. The blocks past the tokens' zero
+// an expert's padding rows each. Bound by the rows' bytes.
 __global__ void __launch_bounds__(256)
-    k_gather(const PlanHead* __restrict__ head, const int* __restrict__ token,
-             int64_t H, const uint4* __restrict__ x, uint4* __restrict__ out,
+    k_gather(Plan p, int64_t L, int K, int vecs, unsigned token_blocks,
+             const uint4* __restrict__ x, uint4* __restrict__ out,
              const uint4* __restrict__ y, uint4* __restrict__ out_y) {
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= head->rows) return;
-  const int t = token[r];
-  const int vecs = static_cast<int>(H / 8);
-  const uint4* src = blockIdx.y ? y : x;
-  uint4* dst = (blockIdx.y ? out_y : out) + static_cast<int64_t>(r) * vecs;
-  src += static_cast<int64_t>(t < 0 ? 0 : t) * vecs;
-  for (int i = threadIdx.x & 31; i < vecs; i += 128) {
-    uint4 v[4];
+  begin_early();
+  const uint4* src = blockIdx.z ? y : x;
+  uint4* dst = blockIdx.z ? out_y : out;
+  const int c = blockIdx.y * blockDim.x + threadIdx.x;
+  if (c >= vecs) return;
+  if (blockIdx.x >= token_blocks) {
+    const int2 seg = p.seg[blockIdx.x - token_blocks];
+    const int first = max(0, seg.y - SEG_ROWS);
+    for (int q = first + threadIdx.y; q < seg.y; q += blockDim.y)
+      if (p.slot[seg.x + q] < 0)
+        dst[static_cast<int64_t>(seg.x + q) * vecs + c] =
+            make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int64_t t =
+      blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y;
+  if (t >= L) return;
+  const uint4 v = __ldg(src + t * vecs + c);
+  const int* row = p.row + t * K;
+  for (int k0 = 0; k0 < K; k0 += 8) {
+    int r[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      v[q] = t >= 0 && i + 32 * q < vecs ? __ldg(src + i + 32 * q)
-                                         : make_uint4(0, 0, 0, 0);
+    for (int q = 0; q < 8; ++q) r[q] = k0 + q < K ? row[k0 + q] : -1;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (i + 32 * q < vecs) dst[i + 32 * q] = v[q];
+    for (int q = 0; q < 8; ++q)
+      if (r[q] >= 0) dst[static_cast<int64_t>(r[q]) * vecs + c] = v;
   }
 }
 
@@ -232,40 +285,41 @@ __device__ __forceinline__ float weight_at(const void* w, int64_t i) {
   return static_cast<float>(static_cast<const T*>(w)[i]);
 }
 
-// Eight columns of a token per thread; a token's rows are added in fp32 in
-// the order of its slots, eight loads in flight. Bound by the rows' bytes.
-template <typename T, bool WEIGHTED>
+// Eight columns of a token per thread (threads x: columns, y: tokens); a
+// token's rows are added in fp32 in the order of its slots, KB loads in
+// flight. Bound by the rows' bytes.
+template <typename T, bool WEIGHTED, int KB>
 __global__ void __launch_bounds__(256)
-    k_combine(const uint16_t* __restrict__ rows,
-              const float* __restrict__ scale, const int* __restrict__ row,
-              const void* __restrict__ w, int64_t L, int K, int64_t H,
-              uint16_t* __restrict__ out) {
-  const int64_t oct = H / 8, tiles = (H + 255) / 256;
-  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (i >= L * oct) return;
-  const int64_t t = i / oct, h = (i - t * oct) * 8;
+    k_combine(const uint16_t* rows, const float* scale, const int* row,
+              const void* w, int64_t L, int K, int H, uint16_t* out) {
+  begin_early();
+  const int64_t t =
+      blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y;
+  const int h = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+  if (t >= L || h >= H) return;
+  const int tiles = (H + 255) / 256;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < K; k0 += 8) {
-    uint4 v[8];
-    float c[8];
-    bool live[8];
+  for (int k0 = 0; k0 < K; k0 += KB) {
+    int r[KB];
+    uint4 v[KB];
+    float c[KB];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int64_t at = t * K + k0 + q;
-      const int r = k0 + q < K ? row[at] : -1;
-      live[q] = r >= 0;
+    for (int q = 0; q < KB; ++q)
+      r[q] = k0 + q < K ? row[t * K + k0 + q] : -1;
+#pragma unroll
+    for (int q = 0; q < KB; ++q) {
       v[q] = make_uint4(0, 0, 0, 0);
       c[q] = 0.f;
-      if (live[q]) {
-        v[q] = __ldg(reinterpret_cast<const uint4*>(
-            rows + static_cast<int64_t>(r) * H + h));
-        c[q] = scale[r * tiles + (h >> 8)];
-        if (WEIGHTED) c[q] *= weight_at<T>(w, at);
+      if (r[q] >= 0) {
+        v[q] = *reinterpret_cast<const uint4*>(
+            rows + static_cast<int64_t>(r[q]) * H + h);
+        c[q] = scale[static_cast<int64_t>(r[q]) * tiles + (h >> 8)];
+        if (WEIGHTED) c[q] *= weight_at<T>(w, t * K + k0 + q);
       }
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (!live[q]) continue;
+    for (int q = 0; q < KB; ++q) {
+      if (r[q] < 0) continue;
       const uint32_t x[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -281,10 +335,153 @@ __global__ void __launch_bounds__(256)
                  pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
 }
 
+// ---------------------------------------------------------------------------
+// single tokens: few slots, no plan and no tensor cores. What bounds them is
+// reading the chosen experts' weights once; every warp keeps 16 loads of 16
+// bytes a lane in flight.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    s = fmaf(__uint_as_float(x[j] << 16), __uint_as_float(y[j] << 16), s);
+    s = fmaf(__uint_as_float(x[j] & 0xffff0000u),
+             __uint_as_float(y[j] & 0xffff0000u), s);
+  }
+  return s;
+}
+
+__device__ __forceinline__ uint4 load_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+constexpr int TOKEN_WARPS = 8;
+
+// a[slot][i] = silu(Wg_e[i] . x_t) (Wu_e[i] . x_t) in fp32, one warp per
+// (slot, i). The call's first kernel: it begins when earlier work has ended,
+// and lets k_token_down begin once each of its blocks runs.
+__global__ void __launch_bounds__(TOKEN_WARPS * 32, 4)
+    k_token_up(const uint4* __restrict__ x, const uint4* __restrict__ Wg,
+               const uint4* __restrict__ Wu, const int32_t* __restrict__ experts,
+               int n, int K, int H, int I, int E, float* __restrict__ a,
+               unsigned* err) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int i = blockIdx.x * TOKEN_WARPS + (threadIdx.x >> 5);
+  const int slot = blockIdx.y;
+  const int e = expert_of(experts, n, slot, E,
+                          blockIdx.x == 0 && threadIdx.x == 0 ? err : nullptr);
+  if (e < 0 || i >= I) return;
+  const int vecs = H / 8;
+  const int64_t at = (static_cast<int64_t>(e) * I + i) * vecs;
+  const uint4* xr = x + static_cast<int64_t>(slot / K) * vecs;
+  float g = 0.f, u = 0.f;
+  for (int c = lane; c < vecs; c += 128) {
+    uint4 vg[4], vu[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool in = c + 32 * q < vecs;
+      vg[q] = in ? load_stream(Wg + at + c + 32 * q) : make_uint4(0, 0, 0, 0);
+      vu[q] = in ? load_stream(Wu + at + c + 32 * q) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (c + 32 * q >= vecs) break;
+      const uint4 xv = __ldg(xr + c + 32 * q);
+      g += dot8(vg[q], xv);
+      u += dot8(vu[q], xv);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    g += __shfl_xor_sync(FULL, g, o);
+    u += __shfl_xor_sync(FULL, u, o);
+  }
+  if (lane == 0)
+    a[static_cast<int64_t>(slot) * I + i] = g * sigmoid_fast(g) * u;
+}
+
+// y[t][h] = sum_k w_k Wd_e[h] . a[t, k], one warp per (t, h). The first 16
+// weight loads of a lane are on their way before k_token_up is waited for.
+template <typename T>
+__global__ void __launch_bounds__(TOKEN_WARPS * 32)
+    k_token_down(const float* a, const uint4* __restrict__ Wd,
+                 const int32_t* __restrict__ experts,
+                 const void* __restrict__ weights, int n, int K, int H, int I,
+                 int E, uint16_t* __restrict__ y) {
+  __shared__ int chosen[32];
+  __shared__ float weight[32];
+  const int lane = threadIdx.x & 31;
+  const int h = blockIdx.x * TOKEN_WARPS + (threadIdx.x >> 5);
+  const int t = blockIdx.y;
+  if (threadIdx.x < K) {
+    const int e = expert_of(experts, n, t * K + threadIdx.x, E, nullptr);
+    chosen[threadIdx.x] = e;
+    weight[threadIdx.x] = e >= 0 ? weight_at<T>(weights, t * K + threadIdx.x)
+                                 : 0.f;
+  }
+  __syncthreads();
+  const int vecs = I / 8;
+  const int cols = h < H ? vecs : 0;
+  float acc = 0.f;
+  bool waited = false;
+  for (int k0 = 0; k0 < K; k0 += 4)
+    for (int c0 = lane; c0 - lane < vecs; c0 += 128) {
+      uint4 v[4][4];  // four slots by four columns
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = k0 + k < K ? chosen[k0 + k] : -1;
+        const uint4* wr =
+            Wd + (static_cast<int64_t>(e < 0 ? 0 : e) * H + h) * vecs;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[k][q] = e >= 0 && c0 + 32 * q < cols ? load_stream(wr + c0 + 32 * q)
+                                                 : make_uint4(0, 0, 0, 0);
+      }
+      if (!waited) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k >= K || chosen[k0 + k] < 0) continue;
+        const float* ar = a + static_cast<int64_t>(t * K + k0 + k) * I;
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (c0 + 32 * q >= cols) break;
+          const float4* ap =
+              reinterpret_cast<const float4*>(ar + (c0 + 32 * q) * 8);
+          const float4 lo = ap[0], hi = ap[1];
+          const uint4 w4 = v[k][q];
+          s = fmaf(__uint_as_float(w4.x << 16), lo.x, s);
+          s = fmaf(__uint_as_float(w4.x & 0xffff0000u), lo.y, s);
+          s = fmaf(__uint_as_float(w4.y << 16), lo.z, s);
+          s = fmaf(__uint_as_float(w4.y & 0xffff0000u), lo.w, s);
+          s = fmaf(__uint_as_float(w4.z << 16), hi.x, s);
+          s = fmaf(__uint_as_float(w4.z & 0xffff0000u), hi.y, s);
+          s = fmaf(__uint_as_float(w4.w << 16), hi.z, s);
+          s = fmaf(__uint_as_float(w4.w & 0xffff0000u), hi.w, s);
+        }
+        acc = fmaf(weight[k0 + k], s, acc);
+      }
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(FULL, acc, o);
+  if (h < H && lane == 0)
+    y[static_cast<int64_t>(t) * H + h] = to_bf16_bits(acc);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256)
-    k_dweights(const float* __restrict__ part, int64_t stride, int tiles,
-               const int* __restrict__ row, int64_t n, T* __restrict__ out) {
+    k_dweights(const float* part, int64_t stride, int tiles, const int* row,
+               int64_t n, T* out) {
+  begin_early();
   const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
   if (i >= n) return;
   const int r = row[i];
@@ -303,59 +500,109 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
 
 }  // namespace
 
-cudaError_t launch_plan(const int32_t* experts, int64_t n, int K, int E,
+cudaError_t launch_plan(const int32_t* experts, int64_t n, int E,
                         const Plan& p, unsigned* err, cudaStream_t s) {
   cudaError_t e;
-  if (n <= PLAN_SMALL) {
-    const size_t smem = sizeof(int) * 33 * static_cast<size_t>(E);
-    if ((e = allow_smem(reinterpret_cast<const void*>(k_plan_small), smem)) !=
+  // slots of a lane: one while 32 warps suffice
+  const int few = n <= 1024 ? 1 : PLAN_SMALL / 1024;
+  const size_t small_smem =
+      sizeof(int) * (ceil_div(n, 32 * few) + 2) * static_cast<size_t>(E);
+  if (n <= PLAN_SMALL && small_smem <= 200 * 1024) {
+    auto kern = few == 1 ? k_plan_small<1> : k_plan_small<PLAN_SMALL / 1024>;
+    if ((e = allow_smem(reinterpret_cast<const void*>(kern), small_smem)) !=
         cudaSuccess)
       return e;
-    k_plan_small<<<1, 1024, smem, s>>>(experts, static_cast<int>(n), K, E,
-                                       p, err);
+    kern<<<1, 1024, small_smem, s>>>(experts, static_cast<int>(n), E, p, err);
     return cudaGetLastError();
   }
   const int chunks = static_cast<int>(ceil_div(n, PLAN_CHUNK));
   k_plan_count<<<chunks, CHUNK_WARPS * 32, sizeof(int) * E, s>>>(
       experts, n, E, chunks, p, err);
-  k_plan_scan<<<(E + 7) / 8, 256, 0, s>>>(E, chunks, p);
-  k_plan_layout<<<1, 1024, 0, s>>>(E, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_early(k_plan_layout, 1, 1024, 0, s, E, chunks, p)) !=
+      cudaSuccess)
+    return e;
   const size_t smem = sizeof(int) * (CHUNK_WARPS + 1) * static_cast<size_t>(E);
   if ((e = allow_smem(reinterpret_cast<const void*>(k_plan_place), smem)) !=
       cudaSuccess)
     return e;
-  k_plan_place<<<chunks, CHUNK_WARPS * 32, smem, s>>>(experts, n, K, E, chunks,
-                                                      p);
-  return cudaGetLastError();
+  return launch_early(k_plan_place, chunks, CHUNK_WARPS * 32, smem, s, experts,
+                      n, E, chunks, p);
 }
 
-cudaError_t launch_gather(const Plan& p, int64_t max_rows, int64_t H,
-                          const void* x, uint16_t* out, const void* y,
-                          uint16_t* out_y, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(max_rows, 8)), y ? 2 : 1);
-  k_gather<<<grid, 256, 0, s>>>(
-      p.head, p.token, H, static_cast<const uint4*>(x),
-      reinterpret_cast<uint4*>(out), static_cast<const uint4*>(y),
-      reinterpret_cast<uint4*>(out_y));
-  return cudaGetLastError();
+namespace {
+// Threads over the columns (x, in eights) and tokens (y) of a row kernel.
+dim3 row_block(int64_t H) {
+  unsigned bx = 32;
+  while (bx < 256 && bx * 8 < H) bx *= 2;
+  return dim3(bx, 256 / bx);
 }
+}  // namespace
+
+cudaError_t launch_gather(const Plan& p, int64_t L, int K, int E, int64_t H,
+                          const void* x, uint16_t* out, const void* y,
+                          uint16_t* out_y, bool zero, cudaStream_t s) {
+  const dim3 block = row_block(H);
+  const unsigned tokens = static_cast<unsigned>(ceil_div(L, block.y));
+  const dim3 grid(tokens + (zero ? E : 0),
+                  static_cast<unsigned>(ceil_div(H, block.x * 8)), y ? 2 : 1);
+  return launch_early(k_gather, grid, block, 0, s, p, L, K,
+                      static_cast<int>(H / 8), tokens,
+                      static_cast<const uint4*>(x),
+                      reinterpret_cast<uint4*>(out),
+                      static_cast<const uint4*>(y),
+                      reinterpret_cast<uint4*>(out_y));
+}
+
+namespace {
+template <typename T, bool WEIGHTED>
+cudaError_t launch_combine_t(const uint16_t* rows, const float* scale,
+                             const int* row, const void* w, int64_t L, int K,
+                             int64_t H, uint16_t* out, cudaStream_t s) {
+  const dim3 block = row_block(H);
+  const dim3 grid(static_cast<unsigned>(ceil_div(L, block.y)),
+                  static_cast<unsigned>(ceil_div(H, block.x * 8)));
+  auto kern = K <= 2   ? k_combine<T, WEIGHTED, 2>
+              : K <= 4 ? k_combine<T, WEIGHTED, 4>
+                       : k_combine<T, WEIGHTED, 8>;
+  return launch_early(kern, grid, block, 0, s, rows, scale, row, w, L, K,
+                      static_cast<int>(H), out);
+}
+}  // namespace
 
 cudaError_t launch_combine(const uint16_t* rows, const float* scale,
                            const int* row, const void* w, lce_dtype wdt,
                            int64_t L, int K, int64_t H, void* out,
                            cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(ceil_div(L * (H / 8), 256));
   uint16_t* o = static_cast<uint16_t*>(out);
   if (!w)
-    k_combine<float, false>
-        <<<grid, 256, 0, s>>>(rows, scale, row, w, L, K, H, o);
-  else if (wdt == LCE_F32)
-    k_combine<float, true>
-        <<<grid, 256, 0, s>>>(rows, scale, row, w, L, K, H, o);
-  else
-    k_combine<__nv_bfloat16, true>
-        <<<grid, 256, 0, s>>>(rows, scale, row, w, L, K, H, o);
-  return cudaGetLastError();
+    return launch_combine_t<float, false>(rows, scale, row, w, L, K, H, o, s);
+  if (wdt == LCE_F32)
+    return launch_combine_t<float, true>(rows, scale, row, w, L, K, H, o, s);
+  return launch_combine_t<__nv_bfloat16, true>(rows, scale, row, w, L, K, H, o,
+                                               s);
+}
+
+cudaError_t launch_token(const void* x, const void* Wg, const void* Wu,
+                         const void* Wd, const void* weights, lce_dtype wdt,
+                         const int32_t* experts, int64_t L, int K, int64_t H,
+                         int64_t I, int E, float* a, void* y, unsigned* err,
+                         cudaStream_t s) {
+  const int n = static_cast<int>(L) * K;
+  const int h = static_cast<int>(H), i = static_cast<int>(I);
+  k_token_up<<<dim3(static_cast<unsigned>(ceil_div(I, TOKEN_WARPS)), n),
+               TOKEN_WARPS * 32, 0, s>>>(
+      static_cast<const uint4*>(x), static_cast<const uint4*>(Wg),
+      static_cast<const uint4*>(Wu), experts, n, K, h, i, E, a, err);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  auto kern = wdt == LCE_F32 ? k_token_down<float> : k_token_down<__nv_bfloat16>;
+  return launch_early(
+      kern,
+      dim3(static_cast<unsigned>(ceil_div(H, TOKEN_WARPS)),
+           static_cast<unsigned>(L)),
+      TOKEN_WARPS * 32, 0, s, a, static_cast<const uint4*>(Wd), experts,
+      weights, n, K, h, i, E, static_cast<uint16_t*>(y));
 }
 
 cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,
@@ -363,12 +610,10 @@ cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,
                             void* dweights, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(ceil_div(n, 256));
   if (wdt == LCE_F32)
-    k_dweights<float><<<grid, 256, 0, s>>>(part, stride, tiles, row, n,
-                                           static_cast<float*>(dweights));
-  else
-    k_dweights<__nv_bfloat16><<<grid, 256, 0, s>>>(
-        part, stride, tiles, row, n, static_cast<__nv_bfloat16*>(dweights));
-  return cudaGetLastError();
+    return launch_early(k_dweights<float>, grid, 256, 0, s, part, stride,
+                        tiles, row, n, static_cast<float*>(dweights));
+  return launch_early(k_dweights<__nv_bfloat16>, grid, 256, 0, s, part, stride,
+                      tiles, row, n, static_cast<__nv_bfloat16*>(dweights));
 }
 
 }  // namespace lce

@@ -52,4 +52,23 @@ inline bool aligned_to(const void* p, uintptr_t n) {
   return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
+// Launches a kernel that may begin while the kernel before it on the stream
+// still runs (programmatic dependent launch): it has to execute
+// griddepcontrol.wait before it touches what earlier kernels read or write.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block,
+                         size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 }  // namespace lce
