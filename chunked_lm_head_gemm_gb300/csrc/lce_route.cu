@@ -10,9 +10,9 @@
 // n + 2 of 256) are packed one to a lane and ranked against each other at
 // once. Scores of a whole row are computed only where its keys or its sum
 // need them, with the fast exponential; the chosen ones again, exactly.
-// Against top_k rounds of two warp-wide reductions over the whole row: L =
-// 32768, E = 128, top 8 of bf16 39 -> 31 us; L = 65536, E = 256 in 8 groups
-// with a bias 223 -> 121 us.
+// Against top_k rounds of two warp-wide reductions over the whole row, both a
+// warp to a row: L = 32768, E = 128, top 8 of bf16 39 -> 31 us; L = 65536, E =
+// 256 in 8 groups with a bias 223 -> 121 us.
 #include <math.h>
 
 #include <type_traits>
@@ -194,6 +194,7 @@ struct RouteArgs {
   int scoring, renorm;
   float scale;
   GroupGeom gg;
+  int warp_smem;  // shared memory of one warp, in doubles
   void* weights;
   int32_t* experts;
 };
@@ -420,17 +421,12 @@ __device__ __forceinline__ float one_score(float z, int scoring, float m,
 // smem of a warp: two lists of 32 (key, element), then the group ranks.
 constexpr int LIST_BYTES = 2 * 32 * 8;
 
+// One row by a whole warp.
 template <typename T, int PER, int V>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32)
-    k_route(const RouteArgs a) {
-  extern __shared__ double route_smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x * static_cast<int64_t>(ROUTE_WARPS) + warp;
-  if (row >= a.L) return;
-  const int buf_len = a.groups > 1 ? a.groups * a.gg.stride : 0;
-  double* mine_smem = route_smem + warp * (LIST_BYTES / 8 + buf_len);
-  uint2* list = reinterpret_cast<uint2*>(mine_smem);
-  double* buf = mine_smem + LIST_BYTES / 8;
+__device__ __forceinline__ void route_row(const RouteArgs& a, int64_t row,
+                                          int lane, double* smem) {
+  uint2* list = reinterpret_cast<uint2*>(smem);
+  double* buf = smem + LIST_BYTES / 8;
   const T* zr = static_cast<const T*>(a.logits) + row * a.E;
   float z[PER];
   load_row<T, PER, V>(zr, a.E, lane, z);
@@ -532,6 +528,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32)
     found += __popc(who);
   }
   int mine = 0;  // lane k: the k-th expert
+  if (found < want) unsure = true;  // an infinite bias has no finite border
   if (found > 32) {
     if (biased)
       unsure = true;
@@ -609,6 +606,436 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32)
   }
 }
 
+template <typename T, int PER, int V>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32)
+    k_route(const RouteArgs a) {
+  extern __shared__ double route_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x * static_cast<int64_t>(ROUTE_WARPS) + warp;
+  if (row >= a.L) return;
+  route_row<T, PER, V>(a, row, lane, route_smem + warp * a.warp_smem);
+}
+
+// ---------------------------------------------------------------------------
+// many rows: four to a warp, eight lanes to a row. The steps are those of
+// route_row, but the warp-wide reductions become three shuffles for four rows,
+// and the kept groups alone are searched. The keys lie in shared memory
+// (element j of a row belongs to lane j % 8; the row stride is 8 mod 32, so
+// the 32 lanes hit 32 banks). Rows with a NaN, with more than 32
+// candidates, or with softmax keys that fp32 does not settle go through
+// route_row afterwards; sigmoid keys are settled in place in fp64, for a row
+// that goes through route_row keeps its warp 20 us longer. Against a
+// warp to a row: L = 32768, E = 128, top 8 of fp32 26 -> 14 us, E = 256 in 8
+// groups with a bias 60 -> 31 us.
+// ---------------------------------------------------------------------------
+constexpr int MANY_LANES = 8;               // lanes of a row
+constexpr int MANY_ROWS = 32 / MANY_LANES;  // rows of a warp
+constexpr int MANY_MAXIMA = 32 / MANY_LANES;
+constexpr int MANY_K = 8;
+constexpr int MANY_LIST = 32;
+
+// Shared memory of a warp: keys, candidates, sorted candidates, group ranks
+// and kept groups.
+__host__ __device__ __forceinline__ int many_stride(int E) {
+  if (E < 2 * MANY_LIST) E = 2 * MANY_LIST;  // or the candidates' exact keys
+  return E + (MANY_LANES - E % 32 + 32) % 32;
+}
+__host__ __device__ __forceinline__ int many_bytes(int E, int groups) {
+  return MANY_ROWS *
+         (many_stride(E) * 4 + MANY_LIST * 8 + (MANY_K + 2) * 8 + 2 * groups * 4);
+}
+
+// Reductions over a row's lanes, in each of them.
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = 1; o < MANY_LANES; o <<= 1)
+    v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+  return v;
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < MANY_LANES; o <<= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+__device__ __forceinline__ unsigned lanes_ballot(bool p, int lane) {
+  return __ballot_sync(FULL, p) >> (lane & ~(MANY_LANES - 1)) &
+         ((1u << MANY_LANES) - 1u);
+}
+
+template <typename T, int PER, int V>
+__device__ __noinline__ void route_row_again(const RouteArgs& a, int64_t row,
+                                             int lane, double* smem) {
+  route_row<T, PER, V>(a, row, lane, smem);
+}
+
+template <typename T, int PER, int V>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32, PER <= 8 ? 8 : 4)
+    k_route_many(const RouteArgs a) {
+  extern __shared__ double route_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row0 =
+      (blockIdx.x * static_cast<int64_t>(ROUTE_WARPS) + warp) * MANY_ROWS;
+  if (row0 >= a.L) return;
+  double* smem = route_smem + warp * a.warp_smem;
+  const int E = a.E, stride = many_stride(E);
+  float* keys = reinterpret_cast<float*>(smem);
+  uint2* lists = reinterpret_cast<uint2*>(keys + MANY_ROWS * stride);
+  uint2* sorted = lists + MANY_ROWS * MANY_LIST;
+  float* ranks = reinterpret_cast<float*>(sorted + MANY_ROWS * (MANY_K + 2));
+  int* kept_list = reinterpret_cast<int*>(ranks + MANY_ROWS * a.groups);
+
+  const bool biased = a.bias != nullptr;
+  const bool softmax = a.scoring == LCE_SOFTMAX;
+  const bool rank_scores = a.groups > 1 && a.group_top == 2;
+  const bool whole = biased || rank_scores || (softmax && !a.renorm);
+
+  // ---- the rows' logits, or their keys where those need no other element ----
+  const int rows =
+      a.L - row0 < MANY_ROWS ? static_cast<int>(a.L - row0) : MANY_ROWS;
+  const T* base = static_cast<const T*>(a.logits) + row0 * E;
+  const bool keys_now = biased && !softmax;
+  float bias[PER];
+  if (keys_now) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int j = element<V>(i, lane);
+      bias[i] = j < E ? a.bias[j] : 0.f;
+    }
+  }
+  unsigned nan_rows = 0;
+  float big = 0.f;  // the largest key's size
+#pragma unroll
+  for (int r = 0; r < MANY_ROWS; ++r) {
+    float z[PER];
+    // rows past the last repeat it: they are computed and not written
+    load_row<T, PER, V>(base + static_cast<int64_t>(min(r, rows - 1)) * E, E,
+                        lane, z);
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) nan |= isnan(z[i]);
+    if (__any_sync(FULL, nan)) nan_rows |= 1u << r;
+    if (keys_now) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float x =
+            __fdividef(1.f, 1.f + ex2(-z[i] * LOG2E)) + bias[i];
+        z[i] = z[i] > -INFINITY && !isnan(x) ? x : -INFINITY;
+        if (z[i] > -INFINITY) big = fmaxf(big, fabsf(z[i]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; i += V) {
+      const int j = element<V>(i, lane);
+      if (j >= E) continue;
+      if (V == 4)
+        *reinterpret_cast<float4*>(keys + r * stride + j) =
+            make_float4(z[i], z[i + (V > 1 ? 1 : 0)], z[i + (V > 2 ? 2 : 0)],
+                        z[i + (V > 3 ? 3 : 0)]);
+      else
+        keys[r * stride + j] = z[i];
+    }
+  }
+  if (keys_now) big = warp_max(big);
+  __syncwarp();
+
+  const int r = lane / MANY_LANES, s = lane % MANY_LANES;
+  float* key = keys + r * stride;
+  bool slow = nan_rows >> r & 1u;
+
+  // ---- softmax maximum and sum -----------------------------------------------
+  float m = 0.f, t = 1.f;
+  if (softmax && whole) {
+    m = -INFINITY;
+    for (int j = s; j < E; j += MANY_LANES) m = fmaxf(m, key[j]);
+    m = lanes_max(m);
+    if (m == -INFINITY) m = 0.f;
+    if (m == INFINITY) slow = true;
+    t = 0.f;
+    for (int j = s; j < E; j += MANY_LANES) t += ex2((key[j] - m) * LOG2E);
+    t = lanes_sum(t);
+    if (t == 0.f) t = 1.f;
+  }
+  const float rt = 1.f / t;
+  auto score = [&](float z) {
+    return softmax ? ex2((z - m) * LOG2E) * rt
+                   : __fdividef(1.f, 1.f + ex2(-z * LOG2E));
+  };
+  if (biased && softmax) {
+    for (int j = s; j < E; j += MANY_LANES) {
+      const float k = key[j];
+      float v = score(k) + a.bias[j];
+      if (!(k > -INFINITY) || isnan(v)) v = -INFINITY;
+      key[j] = v;
+      if (v > -INFINITY) big = fmaxf(big, fabsf(v));
+    }
+    big = lanes_max(big);
+  }
+
+  // ---- groups ------------------------------------------------------------------
+  const float s_max = softmax ? rt : 1.f;
+  if (a.groups > 1) {
+    const int per = a.gg.per;
+    const bool by_score = rank_scores && !biased;
+    for (int g = 0; g < a.groups; ++g) {
+      float x = -INFINITY, y = -INFINITY;  // two largest
+#pragma unroll 4
+      for (int j = s; j < per; j += MANY_LANES) {
+        float v = key[g * per + j];
+        if (by_score && v > -INFINITY) v = score(v);
+        y = fmaxf(y, fminf(x, v));
+        x = fmaxf(x, v);
+      }
+#pragma unroll
+      for (int o = 1; o < MANY_LANES; o <<= 1) {
+        const float ox = __shfl_xor_sync(FULL, x, o),
+                    oy = __shfl_xor_sync(FULL, y, o);
+        y = fmaxf(fmaxf(y, oy), fminf(x, ox));
+        x = fmaxf(x, ox);
+      }
+      float rank = a.group_top == 2 ? x + y : x;
+      if (isnan(rank)) rank = -INFINITY;
+      if (s == 0) ranks[r * a.groups + g] = rank;
+    }
+    __syncwarp();
+    float lo = INFINITY, hi = -INFINITY;
+    for (int g = s; g < a.groups; g += MANY_LANES) {
+      const float mine = ranks[r * a.groups + g];
+      int above = 0;
+      for (int q = 0; q < a.groups; ++q) {
+        const float o = ranks[r * a.groups + q];
+        if (o > mine || (o == mine && q < g)) ++above;
+      }
+      if (above < a.topk_group) {
+        kept_list[r * a.groups + above] = g;
+        lo = fminf(lo, mine);
+      } else {
+        hi = fmaxf(hi, mine);
+      }
+    }
+    lo = -lanes_max(-lo);
+    hi = lanes_max(hi);
+    if (biased || rank_scores) {
+      const float size = biased ? big : s_max;
+      const float err = key_error(s_max, 0.f, a.scoring) + 0x1p-22f * size;
+      const bool close = hi > -INFINITY && !(lo - hi > 4.f * err);
+      if (softmax) {
+        slow |= close;
+      } else if (__any_sync(FULL, close)) {
+        // ranks in 64 bits, a lane to a group: the exact values of the keys
+        // that may be among its group_top largest
+        double* exact = reinterpret_cast<double*>(lists + r * MANY_LIST);
+        const T* zr = base + static_cast<int64_t>(min(r, rows - 1)) * E;
+        for (int g0 = 0; g0 < a.groups; g0 += MANY_LANES) {
+          const int g = g0 + s;
+          float x = -INFINITY, y = -INFINITY;
+          for (int j = 0; g < a.groups && j < per; ++j) {
+            float v = key[g * per + j];
+            if (by_score && v > -INFINITY) v = score(v);
+            y = fmaxf(y, fminf(x, v));
+            x = fmaxf(x, v);
+          }
+          const float from = (a.group_top == 2 ? y : x) - 4.f * err;
+          int pick[4] = {0, 0, 0, 0}, n = 0;  // collected first: the lanes'
+          for (int j = 0; g < a.groups && j < per; ++j) {  // exponentials run
+            float v = key[g * per + j];                    // side by side
+            if (!(v > -INFINITY)) continue;  // masked
+            if (by_score) v = score(v);
+            if (!(v >= from)) continue;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (c == n) pick[c] = g * per + j;
+            ++n;
+          }
+          if (n > 4) slow = true;
+          double x64 = -INFINITY, y64 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (!__any_sync(FULL, c < n)) break;
+            double e =
+                1.0 / (1.0 + exp(-static_cast<double>(load1(zr + pick[c]))));
+            if (biased) e += static_cast<double>(a.bias[pick[c]]);
+            if (c < n) {
+              y64 = fmax(y64, fmin(x64, e));
+              x64 = fmax(x64, e);
+            }
+          }
+          double rank = a.group_top == 2 ? x64 + y64 : x64;
+          if (isnan(rank)) rank = -INFINITY;
+          if (g < a.groups) exact[g] = rank;
+        }
+        __syncwarp();
+        for (int g = s; g < a.groups; g += MANY_LANES) {
+          const double mine = exact[g];
+          int above = 0;
+          for (int q = 0; q < a.groups; ++q) {
+            const double o = exact[q];
+            if (o > mine || (o == mine && q < g)) ++above;
+          }
+          if (above < a.topk_group) kept_list[r * a.groups + above] = g;
+        }
+      }
+    }
+    __syncwarp();
+  }
+  const int runs = a.groups > 1 ? a.topk_group : 1;
+  const int per = a.groups > 1 ? a.gg.per : E;
+
+  // ---- threshold: the want-th largest of 32 maxima of the row -----------------
+  const int want = min(runs * per, a.K + (biased ? 1 : 0));
+  float mx[MANY_MAXIMA];
+#pragma unroll
+  for (int q = 0; q < MANY_MAXIMA; ++q) mx[q] = -INFINITY;
+  for (int x = 0; x < runs; ++x) {
+    const float* run = key + (a.groups > 1 ? kept_list[r * a.groups + x] * per
+                                           : 0);
+    for (int i = s; i < per; i += 32) {
+#pragma unroll
+      for (int q = 0; q < MANY_MAXIMA; ++q)
+        if (i + MANY_LANES * q < per)
+          mx[q] = fmaxf(mx[q], run[i + MANY_LANES * q]);
+    }
+  }
+  // each lane's maxima in falling order
+  static_assert(MANY_MAXIMA == 4, "network of four");
+  auto order = [&](int x, int y) {
+    const float hi = fmaxf(mx[x], mx[y]), lo = fminf(mx[x], mx[y]);
+    mx[x] = hi;
+    mx[y] = lo;
+  };
+  order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+  float floor_key = -INFINITY;  // -inf: every key is a candidate
+  for (int k = 0; k < want; ++k) {
+    floor_key = lanes_max(mx[0]);
+    const unsigned who = lanes_ballot(mx[0] == floor_key, lane);
+    if (s == __ffs(who) - 1) {
+#pragma unroll
+      for (int q = 0; q + 1 < MANY_MAXIMA; ++q) mx[q] = mx[q + 1];
+      mx[MANY_MAXIMA - 1] = -INFINITY;
+    }
+  }
+  if (biased && floor_key > -INFINITY) {
+    const float err = key_error(s_max, 0.f, a.scoring) +
+                      0x1p-23f * (fabsf(floor_key) + s_max);
+    floor_key -= 4.f * err;
+  }
+
+  // ---- candidates, packed by row ------------------------------------------------
+  uint2* list = lists + r * MANY_LIST;
+  int found = 0;
+  for (int x = 0; x < runs; ++x) {
+    const int j0 = a.groups > 1 ? kept_list[r * a.groups + x] * per : 0;
+#pragma unroll 4
+    for (int i = 0; i < per; i += MANY_LANES) {
+      const int j = i + s;
+      const float k = j < per ? key[j0 + j] : 0.f;
+      const bool take = j < per && k >= floor_key;
+      const unsigned who = lanes_ballot(take, lane);
+      const int at = found + __popc(who & ((1u << s) - 1u));
+      if (take && at < MANY_LIST)
+        list[at] =
+            make_uint2(__float_as_uint(k), static_cast<unsigned>(j0 + j));
+      found += __popc(who);
+    }
+  }
+  if (found > MANY_LIST || found < want) slow = true;
+  __syncwarp();
+  // ---- their order ---------------------------------------------------------------
+  uint2* fall = sorted + r * (MANY_K + 2);
+  const int count = min(found, MANY_LIST);
+  for (int c = s; c < count; c += MANY_LANES) {
+    const uint2 own = list[c];
+    const float v = __uint_as_float(own.x);
+    int rank = 0;
+#pragma unroll 4
+    for (int q = 0; q < count; ++q) {
+      const uint2 o = list[q];
+      const float ov = __uint_as_float(o.x);
+      if (ov > v || (ov == v && o.y < own.y)) ++rank;
+    }
+    if (rank <= MANY_K) fall[rank] = own;
+  }
+  __syncwarp();
+  const int64_t row = row0 + r;
+  const bool in = r < rows;
+  const T* zr = base + static_cast<int64_t>(in ? r : rows - 1) * E;
+  if (biased) {
+    // neighbours apart beyond their errors, or the same inputs; the last
+    // chosen one apart from the next
+    bool close = false;
+    for (int k = s; k < a.K && k + 1 < count; k += MANY_LANES) {
+      const uint2 p = fall[k], q = fall[k + 1];
+      const float x = __uint_as_float(p.x), y = __uint_as_float(q.x);
+      if (y == -INFINITY) continue;
+      const float bx = a.bias[p.y], by = a.bias[q.y];
+      const bool apart = x - y > key_error(x, bx, a.scoring) +
+                                     key_error(y, by, a.scoring);
+      if (!apart && (k + 1 == a.K || bx != by ||
+                     load1(zr + p.y) != load1(zr + q.y)))
+        close = true;
+    }
+    if (softmax) {
+      slow |= close;  // the exact scores need the row's sum
+    } else if (__any_sync(FULL, close)) {
+      // the order in 64 bits: exact keys of the candidates as ordered
+      // integers, in the place of the row's fp32 keys
+      unsigned long long* exact = reinterpret_cast<unsigned long long*>(key);
+      for (int c = s; c < count; c += MANY_LANES) {
+        const unsigned j = list[c].y;
+        const float z = load1(zr + j);
+        double v = 1.0 / (1.0 + exp(-static_cast<double>(z))) +
+                   static_cast<double>(a.bias[j]);
+        if (!(z > -INFINITY) || isnan(v)) v = -INFINITY;
+        const long long bits = __double_as_longlong(v + 0.0);
+        exact[c] = static_cast<unsigned long long>(bits) ^
+                   (static_cast<unsigned long long>(bits >> 63) | 1ull << 63);
+      }
+      __syncwarp();
+      for (int c = s; c < count; c += MANY_LANES) {
+        const unsigned long long own = exact[c];
+        const unsigned j = list[c].y;
+        int rank = 0;
+#pragma unroll 4
+        for (int q = 0; q < count; ++q) {
+          const unsigned long long o = exact[q];
+          if (o > own || (o == own && list[q].y < j)) ++rank;
+        }
+        if (rank <= MANY_K) fall[rank] = list[c];
+      }
+      __syncwarp();
+    }
+  }
+  slow = lanes_ballot(slow, lane) != 0u;
+
+  // ---- weights: lane s has choice s ----------------------------------------------
+  static_assert(MANY_K <= MANY_LANES, "a lane to a choice");
+  const bool out = s < a.K && !slow;
+  const int chosen = out ? static_cast<int>(fall[s].y) : 0;
+  const float zk = out ? load1(zr + chosen) : -INFINITY;
+  if (a.renorm && softmax) {
+    m = lanes_max(zk);
+    if (m == -INFINITY) m = 0.f;
+    t = 1.f;
+  }
+  float w = s < a.K ? one_score(zk, a.scoring, m, t) : 0.f;
+  if (a.renorm) {
+    const float sum = lanes_sum(w);
+    if (!softmax && sum < TINY_SUM) slow = true;  // the same for the row
+    w = sum == 0.f ? 0.f : w / sum;
+  }
+  if (in && !slow && s < a.K) {
+    store1(static_cast<T*>(a.weights) + row * a.K + s, w * a.scale);
+    a.experts[row * a.K + s] = chosen;
+  }
+  unsigned again = __ballot_sync(FULL, slow && in && s == 0);
+  __syncwarp();
+  while (again) {
+    const int q = (__ffs(again) - 1) / MANY_LANES;
+    again &= again - 1u;
+    route_row_again<T, PER, V>(a, row0 + q, lane, smem);
+    __syncwarp();
+  }
+}
+
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
@@ -623,129 +1050,180 @@ struct RouteBwdArgs {
   unsigned* err;
 };
 
-// One warp per row. Only the plain softmax needs the whole row again (its
-// gradient is nonzero everywhere); the other forms read the chosen logits
-// alone and write zeros elsewhere. The row is written first, the chosen
-// elements after it by the same warp.
-template <typename T, int PER, int V, bool WHOLE>
+// Sums over the LANES lanes of a row.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float row_top(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1)
+    v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+  return v;
+}
+
+// The choices of a row sit in LANES lanes (8 when top_k <= 8: four rows to a
+// warp). Only the plain softmax needs the whole row again (its gradient is
+// nonzero everywhere; one row to a warp); the other forms read the chosen
+// logits alone and write zeros elsewhere, so they are bound by dlogits'
+// bytes. The rows are written first, the chosen elements after them by the
+// same warp. Four rows to a warp against one: L = 32768, E = 128, top 8 of
+// bf16 26.6 -> 7.9 us, L = 65536, E = 256, fp32 27.4 -> 16.7 us.
+template <typename T, int PER, int V, int LANES, bool WHOLE>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32)
     k_route_bwd(const RouteBwdArgs a) {
+  constexpr int ROWS = 32 / LANES;
+  static_assert(!WHOLE || ROWS == 1, "one row to a warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x * static_cast<int64_t>(ROUTE_WARPS) + warp;
-  if (row >= a.L) return;
+  const int64_t row0 =
+      (blockIdx.x * static_cast<int64_t>(ROUTE_WARPS) + warp) * ROWS;
+  if (row0 >= a.L) return;
+  const int64_t row = row0 + lane / LANES;
+  const int k = lane % LANES;
   const T* zr = static_cast<const T*>(a.logits) + row * a.E;
   T* dr = static_cast<T*>(a.dlogits) + row * a.E;
 
   int j = -1;
   float u = 0.f;
-  if (lane < a.K) {
-    j = a.experts[row * a.K + lane];
+  if (k < a.K && row < a.L) {
+    j = a.experts[row * a.K + k];
     if (j < 0 || j >= a.E) {
       atomicOr(a.err, ERRBIT_EXPERT_RANGE);
       j = -1;
     } else {
-      u = a.scale *
-          load1(static_cast<const T*>(a.dweights) + row * a.K + lane);
+      u = a.scale * load1(static_cast<const T*>(a.dweights) + row * a.K + k);
     }
   }
-  float p = 0.f, d = 0.f;
-  float fill[PER];
+  const float z = j >= 0 ? load1(zr + j) : -INFINITY;
+  float p = 0.f, d = 0.f, dot = 0.f;
   if (WHOLE) {
+    float fill[PER];
     load_row<T, PER, V>(zr, a.E, lane, fill);
     const float m = row_max<PER>(fill);
     const float t = scores<PER>(fill, LCE_SOFTMAX, m);
-    if (j >= 0) p = one_score(load1(zr + j), LCE_SOFTMAX, m, t);
-    const float dot = warp_sum(u * p);
-    d = p * u;  // the element's own share; -p dot once per element, below
+    if (j >= 0) p = one_score(z, LCE_SOFTMAX, m, t);
+    dot = row_sum<LANES>(u * p);
+    d = p * u;  // an element's own shares; -p dot once per element
 #pragma unroll
-    for (int i = 0; i < PER; ++i) fill[i] *= -dot;
+    for (int i = 0; i < PER; i += V) {
+      const int e = element<V>(i, lane);
+      if (e >= a.E) continue;
+      if (V == 4) {
+        float q[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) q[x] = -fill[i + x] * dot;
+        store4(dr + e, q);
+      } else {
+        store1(dr + e, -fill[i] * dot);
+      }
+    }
   } else {
-    const float z = j >= 0 ? load1(zr + j) : -INFINITY;
+    // the warp's rows are contiguous: zeros, 16 bytes a lane where aligned
+    const int64_t left = a.L - row0;
+    const int n = static_cast<int>(left < ROWS ? left : ROWS) * a.E;
+    T* d0 = static_cast<T*>(a.dlogits) + row0 * a.E;
+    constexpr int W = V == 4 ? 16 / sizeof(T) : 1;
+    if (V == 4 && n % W == 0 && (reinterpret_cast<uintptr_t>(d0) & 15u) == 0) {
+      for (int e = lane; e < n / W; e += 32)
+        reinterpret_cast<uint4*>(d0)[e] = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int e = lane; e < n; e += 32) store1(d0 + e, 0.f);
+    }
     if (a.scoring == LCE_SOFTMAX) {  // renormalised: a softmax of the chosen
-      float m = warp_max(z);
+      float m = row_top<LANES>(z);
       if (m == -INFINITY) m = 0.f;
       p = j >= 0 ? expf(z - m) : 0.f;
-      float t = warp_sum(p);
+      float t = row_sum<LANES>(p);
       if (t == 0.f) t = 1.f;
       const float q = p / t;
-      const float dot = warp_sum(u * q);
-      d = q * (u - dot);
+      const float all = row_sum<LANES>(u * q);
+      d = q * (u - all);
     } else {
       p = j >= 0 ? 1.f / (1.f + expf(-z)) : 0.f;
       const float slope = j >= 0 ? p / (1.f + expf(z)) : 0.f;  // p (1 - p)
       if (a.renorm) {
-        const float t = warp_sum(p);
+        const float t = row_sum<LANES>(p);
         float q = t == 0.f ? 0.f : p / t;
         float gain = t == 0.f ? 0.f : slope / t;
-        if (t < TINY_SUM) {
-          double t64;
-          const double p64 = sigmoid64(z, &t64);
-          q = t64 == 0.0 ? 0.f : static_cast<float>(p64 / t64);
-          gain = q;  // p (1 - p) / t with 1 - p = 1
+        if (__any_sync(FULL, t < TINY_SUM)) {
+          const double p64 = 1.0 / (1.0 + exp(-static_cast<double>(z)));
+          double t64 = p64;
+#pragma unroll
+          for (int o = LANES / 2; o > 0; o >>= 1)
+            t64 += __shfl_xor_sync(FULL, t64, o);
+          if (t < TINY_SUM) {
+            q = t64 == 0.0 ? 0.f : static_cast<float>(p64 / t64);
+            gain = q;  // p (1 - p) / t with 1 - p = 1
+          }
         }
-        const float dot = warp_sum(u * q);
-        d = gain * (u - dot);
+        const float all = row_sum<LANES>(u * q);
+        d = gain * (u - all);
       } else {
         d = slope * u;
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < PER; i += V) {
-    const int e = element<V>(i, lane);
-    if (e >= a.E) continue;
-    if (V == 4) {
-      float q[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) q[k] = WHOLE ? fill[i + k] : 0.f;
-      store4(dr + e, q);
-    } else {
-      store1(dr + e, WHOLE ? fill[i] : 0.f);
+  // shares of an index given more than once in a row add up in the first
+  // lane that has it, in the order of the choices
+  const unsigned mates =
+      (LANES == 32 ? FULL : ((1u << LANES) - 1u) << (lane & ~(LANES - 1)));
+  const unsigned same = __match_any_sync(FULL, j) & mates;
+  const bool first = j >= 0 && (same & ((1u << lane) - 1u)) == 0u;
+  float sum = d;
+  if (__any_sync(FULL, j >= 0 && (same & (same - 1u)) != 0u)) {
+    sum = 0.f;
+    for (int q = 0; q < LANES; ++q) {
+      const int from = (lane & ~(LANES - 1)) + q;
+      const float dq = __shfl_sync(FULL, d, from);
+      if (same >> from & 1u) sum += dq;
     }
   }
-  // shares of an index given more than once add up in the first lane of it
-  float sum = 0.f;
-  bool first = j >= 0;
-  for (int k = 0; k < a.K; ++k) {
-    const int jk = __shfl_sync(FULL, j, k);
-    const float dk = __shfl_sync(FULL, d, k);
-    if (jk == j) {
-      sum += dk;
-      if (k < lane) first = false;
-    }
-  }
-  if (WHOLE) {
-    const float dot = warp_sum(u * p);
-    sum -= p * dot;
-  }
-  __syncwarp();  // the row's stores come before the chosen elements'
+  if (WHOLE) sum -= p * dot;
+  __syncwarp();  // the rows' stores come before the chosen elements'
   if (first) store1(dr + j, sum);
 }
 
+// Four rows to a warp from MANY_MIN rows on: at E = 128 (fp32, top 8) L = 2048
+// takes 4.7 us a warp to a row and 5.1 us four to a warp, L = 4096 5.8 and 5.1.
+constexpr int64_t MANY_MIN = 3000;
+constexpr int MANY_MAX_E = 512;  // shared memory of the keys
+
 template <typename T, int PER, int V>
-cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s) {
-  const size_t smem =
-      ROUTE_WARPS * (LIST_BYTES + (a.groups > 1 ? sizeof(double) * a.groups *
-                                                      a.gg.stride
-                                                : 0));
+cudaError_t launch_route_t(const RouteArgs& args, cudaStream_t s) {
+  RouteArgs a = args;
+  const bool many =
+      a.L >= MANY_MIN && a.K <= MANY_K && a.E <= MANY_MAX_E;
+  int bytes = LIST_BYTES + (a.groups > 1 ? 8 * a.groups * a.gg.stride : 0);
+  if (many && many_bytes(a.E, a.groups) > bytes)
+    bytes = many_bytes(a.E, a.groups);
+  a.warp_smem = (bytes + 15) / 16 * 2;
+  const size_t smem = sizeof(double) * ROUTE_WARPS * a.warp_smem;
+  auto kern = many ? k_route_many<T, PER, V> : k_route<T, PER, V>;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(
-        k_route<T, PER, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
         static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const unsigned grid = static_cast<unsigned>(ceil_div(a.L, ROUTE_WARPS));
-  k_route<T, PER, V><<<grid, ROUTE_WARPS * 32, smem, s>>>(a);
+  const unsigned grid = static_cast<unsigned>(
+      ceil_div(a.L, ROUTE_WARPS * (many ? MANY_ROWS : 1)));
+  kern<<<grid, ROUTE_WARPS * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T, int PER, int V>
 cudaError_t launch_route_bwd_t(const RouteBwdArgs& a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(ceil_div(a.L, ROUTE_WARPS));
-  if (a.scoring == LCE_SOFTMAX && !a.renorm)
-    k_route_bwd<T, PER, V, true><<<grid, ROUTE_WARPS * 32, 0, s>>>(a);
-  else
-    k_route_bwd<T, PER, V, false><<<grid, ROUTE_WARPS * 32, 0, s>>>(a);
+  const bool whole = a.scoring == LCE_SOFTMAX && !a.renorm;
+  const bool four = !whole && a.K <= 8;
+  auto kern = whole  ? k_route_bwd<T, PER, V, 32, true>
+              : four ? k_route_bwd<T, PER, V, 8, false>
+                     : k_route_bwd<T, PER, V, 32, false>;
+  const unsigned grid = static_cast<unsigned>(
+      ceil_div(a.L, ROUTE_WARPS * (four ? 4 : 1)));
+  kern<<<grid, ROUTE_WARPS * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
 

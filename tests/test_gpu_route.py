@@ -219,3 +219,63 @@ def test_autograd_and_graph():
     assert torch.equal(dz2, lce.route_backward(z3, e3, dw, "sigmoid",
                                                scale=2.0))
     assert lce.get_error() == 0
+
+
+MANY = [  # E, K, dtype, kwargs, biased
+    (128, 8, torch.bfloat16, dict(), False),
+    (128, 8, torch.bfloat16, dict(renormalize=False), True),
+    (60, 4, torch.float32, dict(scoring="sigmoid"), True),
+    (61, 5, torch.bfloat16, dict(scoring="sigmoid", renormalize=False), False),
+    (3, 3, torch.float32, dict(), True), (1, 1, torch.float32, dict(), False),
+    (512, 8, torch.float32, dict(), True), (511, 1, torch.bfloat16, {}, False),
+    (256, 8, torch.float32, dict(scoring="sigmoid", n_group=8, topk_group=4,
+                                 group_top=2), True),
+    (256, 6, torch.bfloat16, dict(n_group=8, topk_group=3, group_top=1), False),
+    (96, 6, torch.float32, dict(n_group=32, topk_group=5, group_top=2), False),
+    (105, 7, torch.float32, dict(n_group=7, topk_group=2, group_top=2), True),
+    (250, 8, torch.bfloat16, dict(scoring="sigmoid", n_group=2, topk_group=1,
+                                  group_top=2), False)]
+
+
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+@pytest.mark.parametrize("E,K,dtype,kw,biased", MANY)
+def test_many_rows_like_few(E, K, dtype, kw, biased, masked):
+    """4099 rows in one call (eight rows to a warp) choose the experts that
+    calls on 700 of them choose (a warp to a row, tested above against the
+    reference), with the same weights up to the two computations' scores;
+    rows that are masked, infinite, NaN or all equal among them."""
+    dev = require_gpu()
+    import chunked_lm_head_gemm_gb300 as lce
+    L, inf = 4099, math.inf
+    z = draw(L, E, dtype, seed=E + 1, masked=masked)
+    z[5] = -inf
+    z[6, : E // 2] = -inf
+    z[7, 0] = inf
+    z[8, E - 1] = math.nan
+    z[9] = 0.25
+    z[10] = -200.0
+    z[4098] = torch.finfo(dtype).min
+    z[4000:4090] = z[4000:4090].round()  # many ties
+    z = z.to(dev)
+    biases = [None]
+    if biased:
+        g = torch.Generator().manual_seed(4)
+        b = 0.1 * torch.randn(E, generator=g)
+        c = b.clone()
+        c[0], c[E // 2] = inf, -inf
+        flat = 1.0 - torch.from_numpy(ref.scores(
+            to64(z[11].cpu()), kw.get("scoring", "softmax"))).float()
+        biases = [b.to(dev), torch.zeros(E, device=dev), c.to(dev),
+                  torch.nan_to_num(flat).to(dev)]
+        z[12:40] = z[11]
+    for bias in biases:
+        w, e = lce.route_forward(z, K, bias=bias, **kw)
+        for i in range(0, L, 700):
+            part = z[i:i + 700].contiguous()
+            w2, e2 = lce.route_forward(part, K, bias=bias, **kw)
+            assert torch.equal(e[i:i + 700], e2)
+            a, b = to64(w[i:i + 700]), to64(w2)
+            assert np.array_equal(np.isnan(a), np.isnan(b))
+            tol = np.abs(b) * (6 * SCORE + torch.finfo(dtype).eps) + 1e-37
+            assert (np.nan_to_num(np.abs(a - b)) <= np.nan_to_num(tol)).all()
+    assert lce.get_error() == 0
