@@ -33,7 +33,8 @@ struct PlanHead {
   int rows;   // padded rows
 };
 
-// A row tile: `rows` (64 or 128, padded) rows from row0 of one expert.
+// A row tile: `rows` padded rows (at most 128, or 256 on CTA pairs) from row0
+// of one expert.
 struct RowTile {
   int expert, row0, rows, pad;
 };
@@ -48,9 +49,9 @@ struct Plan {
   int* hist;      // [E][chunks]: slots of an expert in a chunk, then before it
 };
 
-// Queues the plan of the slots experts[n]. Deterministic:
+// Queues the plan of the slots experts[n], in row tiles of tile_m. Deterministic:
 // integer counts and positions that follow slot order.
-cudaError_t launch_plan(const int32_t* experts, int64_t n, int E,
+cudaError_t launch_plan(const int32_t* experts, int64_t n, int E, int tile_m,
                         const Plan& p, unsigned* err, cudaStream_t s);
 
 // out[row of (t, k)][:] = x[t][:] for every slot of the plan, bf16 of H
@@ -89,6 +90,7 @@ struct ExpertsArgs {
   uint64_t timeout_ns;
   unsigned* err;
   int grid;
+  bool pair;               // contractions on CTA pairs, row tiles of 256
   // operand maps by use; each kernel takes the ones it names
   const void *Wg, *Wu, *Wd;
   uint16_t *xr, *dyr;      // [max_rows][H]: token rows in plan order

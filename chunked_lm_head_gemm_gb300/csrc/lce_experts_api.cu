@@ -17,6 +17,9 @@ struct Sizes {
 // cores (launch_token) instead of planning tiles for the tensor cores.
 constexpr int64_t TOKEN_SLOTS = 32;
 
+// Rows an expert has on average from which the contractions run on CTA pairs.
+constexpr int64_t PAIR_ROWS = 512;
+
 bool sizes_ok(const Sizes& z) {
   if (z.L < 0 || z.E < 1 || z.E > MAX_EXPERTS || z.K < 1 || z.K > 32)
     return false;
@@ -99,7 +102,9 @@ ExpertsArgs arguments(const Sizes& z, const Layout& w, uint8_t* ws,
   a.E = static_cast<int>(z.E);
   a.timeout_ns = wait_timeout_ns();
   a.err = dev.err;
-  a.grid = dev.num_sms;
+  a.pair = lce_get_cta_pair() != 0 && dev.pair_slots > 0 &&
+           z.L * z.K >= PAIR_ROWS * z.E;
+  a.grid = a.pair ? 2 * dev.pair_slots : dev.num_sms;
   a.xr = reinterpret_cast<uint16_t*>(ws + w.xr);
   a.dyr = reinterpret_cast<uint16_t*>(ws + w.dyr);
   a.a = reinterpret_cast<uint16_t*>(ws + w.a);
@@ -134,7 +139,8 @@ lce_status timed(int kind, double flops, cudaStream_t s, F&& f) {
 lce_status make_plan(const Sizes& z, const int32_t* experts, const void* x,
                      const void* dy, const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(timed(LCE_K_EXPERTS_PLAN, 0, s, [&] {
-    return cuda_try(launch_plan(experts, z.L * z.K, a.E, a.plan, a.err, s),
+    return cuda_try(launch_plan(experts, z.L * z.K, a.E, a.pair ? 2 * BM : BM,
+                                a.plan, a.err, s),
                     "experts_plan");
   }));
   return timed(LCE_K_EXPERTS_GATHER, 0, s, [&] {

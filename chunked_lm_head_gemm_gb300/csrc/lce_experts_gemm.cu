@@ -18,8 +18,8 @@
 //
 // Work: units are 128 x 256 output tiles (UP and DGU 128 x 128 of a, whose
 // accumulator columns are g | u), walked in a static stride by one CTA per
-// SM with the roles of k_gemm: producer warp, MMA lane, four epilogue warps.
-// A unit's accumulation is split into parts, each with its own columns,
+// SM with the roles of k_gemm: producer warp, MMA lane, four epilogue warps;
+// or 256 x 256 tiles by CTA pairs (PAIR). A unit's accumulation is split into parts, each with its own columns,
 // number of buffers and K loop.
 #include <cuda_fp16.h>
 
@@ -47,42 +47,75 @@ struct Geom {
   int kb_h, kb_i;   // 64-wide K blocks of H and I
   int num_n;        // column tiles of a row tile; or of an expert's gradient
   int num_m;        // row tiles of an expert's gradient
+  int tile_m;       // output rows of a unit: 128, or 256 of a CTA pair
+  int rank;         // of this CTA in its pair (set by the kernel)
   uint64_t timeout_ns;
 };
 
 struct Unit {
   int e;        // expert
   int row0;     // first row (row tiles) or first K row (weight gradients)
-  int rows;     // padded rows: of the tile, or the K extent
+  int rows;     // padded rows of this CTA's part of the tile, or the K extent
+  int both;     // row tiles: padded rows of the whole tile
   int m, n;     // tile of the output
 };
 
 // ---- loads -------------------------------------------------------------------
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
-                                            int c0, int c1, int c2,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_"
-      "tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-      : "memory");
+// PAIR: on CTA pairs (cta_group::2, tiles of 256 rows). Each CTA stages its
+// 128 rows of A and its half of B's columns; completion is counted on the
+// leader's barrier (bar: its cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* tm,
+                                        int c0, int c1, uint32_t bar) {
+  if (PAIR)
+    tma_load_2d_pair(dst, tm, c0, c1, bar);
+  else
+    tma_load_2d(dst, tm, c0, c1, bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* tm,
+                                        int c0, int c1, int c2, uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile."
+        "mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::"
+        "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(bar)
+        : "memory");
 }
 
-// K-major A rows of a tile: 64 or 128 rows of 64 elements.
+// K-major A rows of this CTA's part of a tile: 0, 64 or 128 rows.
+template <bool PAIR>
 __device__ __forceinline__ void load_rows(uint32_t sa, const CUtensorMap* tm,
                                           const Unit& u, int c0, uint32_t bar) {
-  tma_load_2d(sa, tm, c0, u.row0, bar);
-  if (u.rows > 64) tma_load_2d(sa + 8192, tm, c0, u.row0 + 64, bar);
+  if (u.rows > 0) load_2d<PAIR>(sa, tm, c0, u.row0, bar);
+  if (u.rows > 64) load_2d<PAIR>(sa + 8192, tm, c0, u.row0 + 64, bar);
 }
 
 // 64 rows from r0 as the K index of an MN-major operand: BOXES boxes of 64
 // columns from c0.
-template <int BOXES>
+template <bool PAIR, int BOXES>
 __device__ __forceinline__ void load_cols(uint32_t dst, const CUtensorMap* tm,
                                           int c0, int r0, uint32_t bar) {
 #pragma unroll
   for (int j = 0; j < BOXES; ++j)
-    tma_load_2d(dst + j * 8192, tm, c0 + 64 * j, r0, bar);
+    load_2d<PAIR>(dst + j * 8192, tm, c0 + 64 * j, r0, bar);
+}
+template <bool PAIR, int BOXES>
+__device__ __forceinline__ void load_cols_of(uint32_t dst,
+                                             const CUtensorMap* tm, int c0,
+                                             int r0, int e, uint32_t bar) {
+#pragma unroll
+  for (int j = 0; j < BOXES; ++j)
+    load_3d<PAIR>(dst + j * 8192, tm, c0 + 64 * j, r0, e, bar);
 }
 
 // ---- the uses ----------------------------------------------------------------
@@ -93,7 +126,12 @@ struct RowUnits {
   __device__ static Unit unit(const Geom& g, int u) {
     const int t = u / g.num_n;
     const int4 r = reinterpret_cast<const int4*>(g.tile)[t];
-    return Unit{r.x, r.y, r.z, t, u - t * g.num_n};
+    return Unit{r.x,
+                r.y + g.rank * BM,
+                min(max(r.z - g.rank * BM, 0), BM),
+                r.z,
+                t,
+                u - t * g.num_n};
   }
 };
 struct GradUnits {
@@ -102,7 +140,7 @@ struct GradUnits {
     const int per = g.num_m * g.num_n;
     const int e = u / per, r = u - e * per;
     const int2 s = g.seg[e];
-    return Unit{e, s.x, s.y, r / g.num_n, r % g.num_n};
+    return Unit{e, s.x, s.y, 0, r / g.num_n, r % g.num_n};
   }
 };
 
@@ -112,6 +150,8 @@ struct Part {
   static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
 };
 
+// blocks: K blocks of a part; bytes: what a K block's loads of all CTAs of the
+// unit bring; load: this CTA's loads of one K block.
 struct OpUp : RowUnits {
   static constexpr int PARTS = 1;
   using P0 = Part<256, 0, 2, false, false>;
@@ -119,15 +159,19 @@ struct OpUp : RowUnits {
   template <int P>
   __device__ static int blocks(const Geom& g, const Unit&) { return g.kb_h; }
   template <int P>
-  __device__ static uint32_t bytes(const Unit& u) {
-    return u.rows * 128u + 32768u;
+  __device__ static uint32_t bytes(const Geom&, const Unit& u) {
+    return u.both * 128u + 32768u;
   }
-  template <int P>
+  template <int P, bool PAIR>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
                               int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
-    load_rows(sa, &m.a0, u, kb * BK, bar);
-    tma_load_3d(sb, &m.b0, kb * BK, u.n * 128, u.e, bar);
-    tma_load_3d(sb + 16384, &m.b1, kb * BK, u.n * 128, u.e, bar);
+    load_rows<PAIR>(sa, &m.a0, u, kb * BK, bar);
+    if (PAIR) {  // the leader stages Wg's rows, its peer Wu's
+      load_3d<PAIR>(sb, g.rank ? &m.b1 : &m.b0, kb * BK, u.n * 128, u.e, bar);
+    } else {
+      load_3d<PAIR>(sb, &m.b0, kb * BK, u.n * 128, u.e, bar);
+      load_3d<PAIR>(sb + 16384, &m.b1, kb * BK, u.n * 128, u.e, bar);
+    }
   }
 };
 
@@ -138,14 +182,15 @@ struct OpDown : RowUnits {
   template <int P>
   __device__ static int blocks(const Geom& g, const Unit&) { return g.kb_i; }
   template <int P>
-  __device__ static uint32_t bytes(const Unit& u) {
-    return u.rows * 128u + 32768u;
+  __device__ static uint32_t bytes(const Geom&, const Unit& u) {
+    return u.both * 128u + 32768u;
   }
-  template <int P>
-  __device__ static void load(const Maps& m, const Geom&, const Unit& u,
+  template <int P, bool PAIR>
+  __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
                               int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
-    load_rows(sa, &m.a0, u, kb * BK, bar);
-    tma_load_3d(sb, &m.b0, kb * BK, u.n * 256, u.e, bar);
+    load_rows<PAIR>(sa, &m.a0, u, kb * BK, bar);
+    // boxes of 256 rows of Wd_e, of 128 on a pair
+    load_3d<PAIR>(sb, &m.b0, kb * BK, u.n * 256 + g.rank * 128, u.e, bar);
   }
 };
 
@@ -158,20 +203,17 @@ struct OpDx : RowUnits {
     return 2 * g.kb_i;
   }
   template <int P>
-  __device__ static uint32_t bytes(const Unit& u) {
-    return u.rows * 128u + 32768u;
+  __device__ static uint32_t bytes(const Geom&, const Unit& u) {
+    return u.both * 128u + 32768u;
   }
-  template <int P>
+  template <int P, bool PAIR>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
                               int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     const bool second = kb >= g.kb_i;  // du and Wu after dg and Wg
-    const CUtensorMap* ta = second ? &m.a1 : &m.a0;
-    const CUtensorMap* tb = second ? &m.b1 : &m.b0;
     const int k0 = (second ? kb - g.kb_i : kb) * BK;
-    load_rows(sa, ta, u, k0, bar);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      tma_load_3d(sb + j * 8192, tb, u.n * 256 + 64 * j, k0, u.e, bar);
+    load_rows<PAIR>(sa, second ? &m.a1 : &m.a0, u, k0, bar);
+    load_cols_of<PAIR, PAIR ? 2 : 4>(sb, second ? &m.b1 : &m.b0,
+                                     u.n * 256 + g.rank * 128, k0, u.e, bar);
   }
 };
 
@@ -184,18 +226,18 @@ struct OpDgu : RowUnits {
   template <int P>
   __device__ static int blocks(const Geom& g, const Unit&) { return g.kb_h; }
   template <int P>
-  __device__ static uint32_t bytes(const Unit& u) {
-    return u.rows * 128u + (P == 0 ? 16384u : 32768u);
+  __device__ static uint32_t bytes(const Geom&, const Unit& u) {
+    return u.both * 128u + (P == 0 ? 16384u : 32768u);
   }
-  template <int P>
+  template <int P, bool PAIR>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
                               int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     if (P == 0) {
-      load_rows(sa, &m.a1, u, kb * BK, bar);
-      tma_load_3d(sb, &m.b2, u.n * 128, kb * BK, u.e, bar);
-      tma_load_3d(sb + 8192, &m.b2, u.n * 128 + 64, kb * BK, u.e, bar);
+      load_rows<PAIR>(sa, &m.a1, u, kb * BK, bar);
+      load_cols_of<PAIR, PAIR ? 1 : 2>(sb, &m.b2, u.n * 128 + g.rank * 64,
+                                       kb * BK, u.e, bar);
     } else {
-      OpUp::load<0>(m, g, u, kb, sa, sb, bar);
+      OpUp::load<0, PAIR>(m, g, u, kb, sa, sb, bar);
     }
   }
 };
@@ -209,13 +251,15 @@ struct OpDwd : GradUnits {
     return u.rows / SEG_ROWS;
   }
   template <int P>
-  __device__ static uint32_t bytes(const Unit&) { return STAGE_BYTES; }
-  template <int P>
+  __device__ static uint32_t bytes(const Geom& g, const Unit&) {
+    return g.tile_m * 128u + 32768u;
+  }
+  template <int P, bool PAIR>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
                               int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     const int k0 = u.row0 + kb * BK;
-    load_cols<2>(sa, &m.a0, u.m * BM, k0, bar);
-    load_cols<4>(sb, &m.b0, u.n * BN, k0, bar);
+    load_cols<PAIR, 2>(sa, &m.a0, u.m * g.tile_m + g.rank * BM, k0, bar);
+    load_cols<PAIR, PAIR ? 2 : 4>(sb, &m.b0, u.n * BN + g.rank * 128, k0, bar);
   }
 };
 
@@ -228,16 +272,18 @@ struct OpDwgu : GradUnits {
     return u.rows / SEG_ROWS;
   }
   template <int P>
-  __device__ static uint32_t bytes(const Unit&) { return STAGE_BYTES; }
-  template <int P>
+  __device__ static uint32_t bytes(const Geom& g, const Unit&) {
+    return g.tile_m * 128u + 32768u;
+  }
+  template <int P, bool PAIR>
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
                               int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     const int k0 = u.row0 + kb * BK;
     const int half = g.num_m >> 1;  // dWg's row tiles, then dWu's
     const bool second = u.m >= half;
-    const int m0 = (second ? u.m - half : u.m) * BM;
-    load_cols<2>(sa, second ? &m.a1 : &m.a0, m0, k0, bar);
-    load_cols<4>(sb, &m.b0, u.n * BN, k0, bar);
+    const int m0 = (second ? u.m - half : u.m) * g.tile_m + g.rank * BM;
+    load_cols<PAIR, 2>(sa, second ? &m.a1 : &m.a0, m0, k0, bar);
+    load_cols<PAIR, PAIR ? 2 : 4>(sb, &m.b0, u.n * BN + g.rank * 128, k0, bar);
   }
 };
 
@@ -393,7 +439,7 @@ struct EpiGrad2 : EpiBase {
       base = p.out2;
       m -= g.num_m >> 1;
     }
-    const int row = m * BM + r;
+    const int row = m * g.tile_m + g.rank * BM + r;
     const int64_t at =
         (static_cast<int64_t>(u.e) * p.rows + row) * p.cols;
 #pragma unroll 1
@@ -432,67 +478,84 @@ struct EpiGrad2 : EpiBase {
 };
 
 // ---- roles -------------------------------------------------------------------
+// Ring of stages by form: one CTA stages 128 rows of A and 256 columns of B,
+// a CTA of a pair 128 and 128.
+template <bool PAIR>
+struct Form {
+  static constexpr int STAGES_ = PAIR ? STAGES2 : STAGES;
+  static constexpr int A_BYTES = A_STAGE_BYTES;
+  static constexpr int B_BYTES = PAIR ? B2_STAGE_BYTES : B_STAGE_BYTES;
+  static constexpr int RING_BYTES = STAGES_ * (A_BYTES + B_BYTES);
+  static constexpr int SMEM = 1024 + RING_BYTES + 1024 + EPI_STAGE_BYTES;
+};
+
 // Barriers: full / empty per stage; tfull[2]: a unit's accumulators are
 // ready (by unit parity); tempty[part][2]: a part's buffer may be overwritten.
+// On a pair, full and tempty live in the leader, empty and tfull in both.
+template <bool PAIR>
 struct Bars {
+  static constexpr int S = Form<PAIR>::STAGES_;
+  static constexpr int COUNT = 2 * S + 7;
   uint32_t base;
   __device__ uint32_t full(int s) const { return base + 8u * s; }
-  __device__ uint32_t empty(int s) const { return base + 8u * (STAGES + s); }
-  __device__ uint32_t tfull(int b) const {
-    return base + 8u * (2 * STAGES + b);
-  }
+  __device__ uint32_t empty(int s) const { return base + 8u * (S + s); }
+  __device__ uint32_t tfull(int b) const { return base + 8u * (2 * S + b); }
   __device__ uint32_t tempty(int part, int b) const {
-    return base + 8u * (2 * STAGES + 2 + 2 * part + b);
+    return base + 8u * (2 * S + 2 + 2 * part + b);
   }
-  __device__ uint32_t drain() const { return base + 8u * (2 * STAGES + 6); }
+  __device__ uint32_t drain() const { return base + 8u * (2 * S + 6); }
 };
-constexpr int NUM_BARS = 2 * STAGES + 7;
 
+template <bool PAIR>
 struct Ring {
   uint32_t stage = 0, phase = 0;
   __device__ __forceinline__ void next() {
-    if (++stage == STAGES) {
+    if (++stage == Form<PAIR>::STAGES_) {
       stage = 0;
       phase ^= 1u;
     }
   }
 };
 
-template <class Op, int P>
+template <class Op, int P, bool PAIR>
 __device__ __forceinline__ bool produce(const Maps& m, const Geom& g,
                                         const Unit& u, uint32_t sa,
-                                        uint32_t sb, const Bars& bars,
-                                        Ring& ring, uint32_t& issued,
+                                        uint32_t sb, const Bars<PAIR>& bars,
+                                        Ring<PAIR>& ring, uint32_t& issued,
                                         const WaitCtx& ctx) {
   const int n = Op::template blocks<P>(g, u);
   for (int kb = 0; kb < n; ++kb) {
     if (!mbar_wait(bars.empty(ring.stage), ring.phase ^ 1u, ctx, true))
       return false;
-    const uint32_t fb = bars.full(ring.stage);
-    mbar_arrive_expect_tx(fb, Op::template bytes<P>(u));
-    Op::template load<P>(m, g, u, kb, sa + ring.stage * A_STAGE_BYTES,
-                         sb + ring.stage * B_STAGE_BYTES, fb);
+    uint32_t fb = bars.full(ring.stage);
+    if (!PAIR || g.rank == 0)
+      mbar_arrive_expect_tx(fb, Op::template bytes<P>(g, u));
+    if (PAIR) fb = mapa_shared(fb, 0);
+    Op::template load<P, PAIR>(m, g, u, kb,
+                               sa + ring.stage * Form<PAIR>::A_BYTES,
+                               sb + ring.stage * Form<PAIR>::B_BYTES, fb);
     ++issued;
     ring.next();
   }
   return true;
 }
 
-template <bool A_MN, bool B_MN, int N>
+template <bool A_MN, bool B_MN, int N, bool PAIR>
 __device__ __forceinline__ constexpr uint32_t idesc_n() {
   return (1u << 4) | (1u << 7) | (1u << 10) |
          (static_cast<uint32_t>(A_MN) << 15) |
          (static_cast<uint32_t>(B_MN) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(BM >> 4) << 24);
+         (static_cast<uint32_t>((PAIR ? 2 * BM : BM) >> 4) << 24);
 }
 
-template <class Op, int P, class PT>
+template <class Op, int P, class PT, bool PAIR>
 __device__ __forceinline__ bool multiply(const Geom& g, const Unit& u, int i,
                                          uint32_t sa, uint32_t sb,
-                                         const Bars& bars, Ring& ring,
-                                         uint32_t tmem, const WaitCtx& ctx) {
-  constexpr uint32_t IDESC = idesc_n<PT::A_MN, PT::B_MN, PT::N>();
+                                         const Bars<PAIR>& bars,
+                                         Ring<PAIR>& ring, uint32_t tmem,
+                                         const WaitCtx& ctx) {
+  constexpr uint32_t IDESC = idesc_n<PT::A_MN, PT::B_MN, PT::N, PAIR>();
   constexpr uint32_t MN_LBO = 64 * BK * 2;
   const int buf = PT::BUFS == 2 ? (i & 1) : 0;
   const uint32_t turn = PT::BUFS == 2 ? (i >> 1) : i;
@@ -504,53 +567,70 @@ __device__ __forceinline__ bool multiply(const Geom& g, const Unit& u, int i,
   for (int kb = 0; kb < n; ++kb) {
     if (!mbar_wait(bars.full(ring.stage), ring.phase, ctx, true)) return false;
     tc_fence_after();
-    const uint32_t a = sa + ring.stage * A_STAGE_BYTES;
-    const uint32_t b = sb + ring.stage * B_STAGE_BYTES;
+    const uint32_t a = sa + ring.stage * Form<PAIR>::A_BYTES;
+    const uint32_t b = sb + ring.stage * Form<PAIR>::B_BYTES;
 #pragma unroll
     for (int k = 0; k < BK / 16; ++k) {
       const uint64_t ad = PT::A_MN ? sdesc_sw128(a + k * 2048, MN_LBO, 1024)
                                    : sdesc_sw128(a + k * 32, 16, 1024);
       const uint64_t bd = PT::B_MN ? sdesc_sw128(b + k * 2048, MN_LBO, 1024)
                                    : sdesc_sw128(b + k * 32, 16, 1024);
-      tc_mma(d, ad, bd, IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+      const uint32_t more = (kb > 0 || k > 0) ? 1u : 0u;
+      if (PAIR)
+        tc_mma_pair(d, ad, bd, IDESC, more);
+      else
+        tc_mma(d, ad, bd, IDESC, more);
     }
-    tc_commit(bars.empty(ring.stage));
+    if (PAIR)
+      tc_commit_pair_both(bars.empty(ring.stage));
+    else
+      tc_commit(bars.empty(ring.stage));
     ring.next();
   }
   return true;
 }
 
-template <class Op, class Epi>
+template <class Op, class Epi, bool PAIR>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
-    k_experts(const __grid_constant__ Maps maps, const Geom g,
+    k_experts(const __grid_constant__ Maps maps, Geom g,
               const typename Epi::Params p, unsigned* err) {
   extern __shared__ uint8_t smem_raw[];
+  using F = Form<PAIR>;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  const uint32_t sa = base, sb = base + STAGES * A_STAGE_BYTES;
-  const Bars bars{base + STAGES * STAGE_BYTES};
-  uint8_t* misc = smem_raw + (bars.base - raw) + 8 * NUM_BARS;
+  const uint32_t sa = base, sb = base + F::STAGES_ * F::A_BYTES;
+  const Bars<PAIR> bars{base + F::RING_BYTES};
+  uint8_t* misc = smem_raw + (bars.base - raw) + 8 * Bars<PAIR>::COUNT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile uint32_t* abort_flag =
       reinterpret_cast<volatile uint32_t*>(misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  g.rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < F::STAGES_; ++s) {
       mbar_init(bars.full(s), 1);
       mbar_init(bars.empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bars.tfull(b), 1);
-      for (int q = 0; q < 2; ++q) mbar_init(bars.tempty(q, b), 128);
+      // one arrival per epilogue warp
+      for (int q = 0; q < 2; ++q) mbar_init(bars.tempty(q, b), PAIR ? 8 : 4);
     }
     mbar_init(bars.drain(), 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
+  // both CTAs' barriers exist before either CTA signals the other's
+  if (PAIR) cluster_sync_all();
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -559,43 +639,55 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   const WaitCtx ctx{abort_flag, err, g.timeout_ns};
   begin_early();  // all above touches no global memory
   const int units = Op::units(g);
+  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int stride = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (warp == 0) {
     if (lane == 0) {
-      Ring ring;
+      Ring<PAIR> ring;
       uint32_t issued = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = first; ok && u < units; u += stride) {
         const Unit t = Op::unit(g, u);
-        ok = produce<Op, 0>(maps, g, t, sa, sb, bars, ring, issued, ctx);
+        ok = produce<Op, 0, PAIR>(maps, g, t, sa, sb, bars, ring, issued, ctx);
         if (Op::PARTS == 2 && ok)
-          ok = produce<Op, Op::PARTS - 1>(maps, g, t, sa, sb, bars, ring,
-                                          issued, ctx);
+          ok = produce<Op, Op::PARTS - 1, PAIR>(maps, g, t, sa, sb, bars, ring,
+                                                issued, ctx);
       }
-      // every copy issued must have landed before the CTA may exit
-      for (int s = 0; s < STAGES; ++s) {
-        const uint32_t cnt =
-            issued / STAGES +
-            (static_cast<uint32_t>(s) < issued % STAGES ? 1u : 0u);
-        if (cnt) mbar_wait(bars.full(s), (cnt - 1u) & 1u, ctx, false);
-      }
+      // every copy issued must have landed before the CTA may exit (the
+      // leader's full barriers count both CTAs' copies)
+      if (!PAIR || g.rank == 0)
+        for (int s = 0; s < F::STAGES_; ++s) {
+          const uint32_t cnt =
+              issued / F::STAGES_ +
+              (static_cast<uint32_t>(s) < issued % F::STAGES_ ? 1u : 0u);
+          if (cnt) mbar_wait(bars.full(s), (cnt - 1u) & 1u, ctx, false);
+        }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      Ring ring;
+    if (lane == 0 && g.rank == 0) {
+      Ring<PAIR> ring;
       bool ok = true;
-      int i = 0;  // units this CTA has accumulated
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++i) {
+      int i = 0;  // units accumulated so far
+      for (int u = first; ok && u < units; u += stride, ++i) {
         const Unit t = Op::unit(g, u);
-        ok = multiply<Op, 0, typename Op::P0>(g, t, i, sa, sb, bars, ring,
-                                              tmem, ctx);
+        ok = multiply<Op, 0, typename Op::P0, PAIR>(g, t, i, sa, sb, bars,
+                                                    ring, tmem, ctx);
         if (Op::PARTS == 2 && ok)
-          ok = multiply<Op, Op::PARTS - 1, typename Op::P1>(
+          ok = multiply<Op, Op::PARTS - 1, typename Op::P1, PAIR>(
               g, t, i, sa, sb, bars, ring, tmem, ctx);
-        if (ok) tc_commit(bars.tfull(i & 1));
+        if (ok) {
+          if (PAIR)
+            tc_commit_pair_both(bars.tfull(i & 1));
+          else
+            tc_commit(bars.tfull(i & 1));
+        }
       }
-      tc_commit(bars.drain());
+      if (PAIR)
+        tc_commit_pair_local(bars.drain());
+      else
+        tc_commit(bars.drain());
       mbar_wait(bars.drain(), 0, ctx, false);
     }
     __syncwarp();
@@ -603,10 +695,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const int q = warp & 3;
     const int r = q * 32 + lane;
     Epi epi;
-    epi.stage = base + STAGES * STAGE_BYTES + 1024 +
+    epi.stage = base + F::RING_BYTES + 1024 +
                 static_cast<uint32_t>(q) * 2u * EPI_BUF_BYTES;
     int i = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+    for (int u = first; u < units; u += stride, ++i) {
       const Unit t = Op::unit(g, u);
       const bool got = mbar_wait(bars.tfull(i & 1), (i >> 1) & 1, ctx, true);
       if (!__all_sync(FULL, got)) break;
@@ -614,18 +706,35 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       epi.tile(p, maps, g, t, tmem + (static_cast<uint32_t>(q * 32) << 16), r,
                i);
       tc_fence_before();
-      mbar_arrive(bars.tempty(0, Op::P0::BUFS == 2 ? (i & 1) : 0));
-      if (Op::PARTS == 2)
-        mbar_arrive(bars.tempty(1, Op::P1::BUFS == 2 ? (i & 1) : 0));
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t b0 =
+            bars.tempty(0, Op::P0::BUFS == 2 ? (i & 1) : 0);
+        const uint32_t b1 =
+            bars.tempty(1, Op::P1::BUFS == 2 ? (i & 1) : 0);
+        if (PAIR) {
+          mbar_arrive_cluster(mapa_shared(b0, 0));
+          if (Op::PARTS == 2) mbar_arrive_cluster(mapa_shared(b1, 0));
+        } else {
+          mbar_arrive(b0);
+          if (Op::PARTS == 2) mbar_arrive(b1);
+        }
+      }
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
+  // neither CTA frees its memory while the pair's MMAs or the peer's barrier
+  // traffic may still touch it
+  if (PAIR) cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    if (PAIR)
+      tmem_dealloc_pair(tmem, TMEM_COLS);
+    else
+      tmem_dealloc(tmem, TMEM_COLS);
   }
 }
 
@@ -670,6 +779,7 @@ Geom geom(const ExpertsArgs& a) {
   g.E = a.E;
   g.kb_h = static_cast<int>(ceil_div(a.H, BK));
   g.kb_i = static_cast<int>(ceil_div(a.I, BK));
+  g.tile_m = a.pair ? 2 * BM : BM;
   g.timeout_ns = a.timeout_ns;
   return g;
 }
@@ -678,13 +788,13 @@ template <class Op, class Epi>
 lce_status launch(const char* what, const Maps& m, const Geom& g,
                   const typename Epi::Params& p, const ExpertsArgs& a,
                   cudaStream_t s) {
-  auto kern = k_experts<Op, Epi>;
+  auto kern = a.pair ? k_experts<Op, Epi, true> : k_experts<Op, Epi, false>;
+  const int smem = a.pair ? Form<true>::SMEM : Form<false>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM_BYTES);
-  if (e == cudaSuccess) {
-    e = launch_early(kern, a.grid, GEMM_THREADS, GEMM_SMEM_BYTES, s, m, g, p,
-                     a.err);
-  }
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = launch_early_cluster(kern, a.grid, GEMM_THREADS, smem, s,
+                             a.pair ? 2 : 1, m, g, p, a.err);
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, what);
 }
 
@@ -710,7 +820,7 @@ lce_status launch_experts_up(const ExpertsArgs& a, cudaStream_t s) {
 lce_status launch_experts_down(const ExpertsArgs& a, cudaStream_t s) {
   Maps m{};
   LCE_TRY(map2(&m.a0, a.a, a.I, a.max_rows, BK, 64));
-  LCE_TRY(map3(&m.b0, a.Wd, a.I, a.H, a.E, BK, 256));
+  LCE_TRY(map3(&m.b0, a.Wd, a.I, a.H, a.E, BK, a.pair ? 128 : 256));
   Geom g = geom(a);
   LCE_TRY(store_map(&m.s0, a.rows_out, a.H, a.max_rows));
   g.num_n = static_cast<int>(ceil_div(a.H, 256));
@@ -750,7 +860,7 @@ lce_status launch_experts_dwd(const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(map2(&m.a0, a.dyr, a.H, a.max_rows, 64, BK));
   LCE_TRY(map2(&m.b0, a.a, a.I, a.max_rows, 64, BK));
   Geom g = geom(a);
-  g.num_m = static_cast<int>(ceil_div(a.H, BM));
+  g.num_m = static_cast<int>(ceil_div(a.H, g.tile_m));
   g.num_n = static_cast<int>(ceil_div(a.I, BN));
   return launch<OpDwd, EpiGrad2>(
       "experts_dWd", m, g,
@@ -763,7 +873,7 @@ lce_status launch_experts_dwgu(const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(map2(&m.a1, a.du, a.I, a.max_rows, 64, BK));
   LCE_TRY(map2(&m.b0, a.xr, a.H, a.max_rows, 64, BK));
   Geom g = geom(a);
-  g.num_m = 2 * static_cast<int>(ceil_div(a.I, BM));
+  g.num_m = 2 * static_cast<int>(ceil_div(a.I, g.tile_m));
   g.num_n = static_cast<int>(ceil_div(a.H, BN));
   return launch<OpDwgu, EpiGrad2>(
       "experts_dWgu", m, g, {a.dW, a.dW2, a.gdt == LCE_F32, g.I, g.H}, a, s);

@@ -77,19 +77,19 @@ __device__ __forceinline__ void place_slots(const int (&e)[ITEMS], int64_t n,
 __device__ __forceinline__ int padded(int c) {
   return (c + SEG_ROWS - 1) / SEG_ROWS * SEG_ROWS;
 }
-__device__ __forceinline__ int tiles_of(int c) {
-  return (padded(c) + BM - 1) / BM;
+__device__ __forceinline__ int tiles_of(int c, int tile_m) {
+  return (padded(c) + tile_m - 1) / tile_m;
 }
 
 // One block of 1024 threads: segments, tiles and padding rows from the
 // experts' counts (c: thread e's expert). start[] (shared, E + 1 entries) gets
 // each segment's row, cnt[] (shared) the counts.
-__device__ __forceinline__ void lay_out(int c, int E, const Plan& p,
-                                        int* start, int* cnt) {
+__device__ __forceinline__ void lay_out(int c, int E, int tile_m,
+                                        const Plan& p, int* start, int* cnt) {
   __shared__ int warp_rows[32], warp_tiles[32];
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   if (e >= E) c = 0;
-  const int rows = padded(c), tiles = tiles_of(c);
+  const int rows = padded(c), tiles = tiles_of(c, tile_m);
   int r = rows, t = tiles;  // inclusive scans over the experts
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -114,8 +114,8 @@ __device__ __forceinline__ void lay_out(int c, int E, const Plan& p,
     cnt[e] = c;
     p.seg[e] = make_int2(row0, rows);
     int at = t - tiles;
-    for (int q = 0; q < rows; q += BM)
-      p.tile[at++] = RowTile{e, row0 + q, min(BM, rows - q), 0};
+    for (int q = 0; q < rows; q += tile_m)
+      p.tile[at++] = RowTile{e, row0 + q, min(tile_m, rows - q), 0};
     if (e == E - 1) *p.head = PlanHead{t, r};
   }
   __syncthreads();
@@ -130,7 +130,7 @@ __device__ __forceinline__ void lay_out(int c, int E, const Plan& p,
 // `workers` warps takes 32 ITEMS slots.
 template <int ITEMS>
 __global__ void __launch_bounds__(1024)
-    k_plan_small(const int32_t* experts, int n, int E, Plan p,
+    k_plan_small(const int32_t* experts, int n, int E, int tile_m, Plan p,
                  unsigned* err) {
   extern __shared__ int plan_smem[];
   const int workers = (n + 32 * ITEMS - 1) / (32 * ITEMS);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(1024)
       cnt[w * E + threadIdx.x] = total;
       total += c;
     }
-  lay_out(total, E, p, start, totals);
+  lay_out(total, E, tile_m, p, start, totals);
   __syncthreads();
   if (warp < workers)
     place_slots<ITEMS>(e, n, i0, cnt + warp * E, start, p);
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(CHUNK_WARPS * 32)
 // Step 2, one block: the chunk counts become the counts before the chunk
 // (a warp to an expert), then segments, tiles and padding.
 __global__ void __launch_bounds__(1024) k_plan_layout(int E, int chunks,
-                                                      Plan p) {
+                                                      int tile_m, Plan p) {
   __shared__ int start[MAX_EXPERTS], cnt[MAX_EXPERTS];
   begin_early();
   const int lane = threadIdx.x & 31;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(1024) k_plan_layout(int E, int chunks,
   }
   __syncthreads();
   const int c = threadIdx.x < E ? cnt[threadIdx.x] : 0;
-  lay_out(c, E, p, start, cnt);
+  lay_out(c, E, tile_m, p, start, cnt);
 }
 
 // Step 3: every slot's row.
@@ -500,7 +500,7 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
 
 }  // namespace
 
-cudaError_t launch_plan(const int32_t* experts, int64_t n, int E,
+cudaError_t launch_plan(const int32_t* experts, int64_t n, int E, int tile_m,
                         const Plan& p, unsigned* err, cudaStream_t s) {
   cudaError_t e;
   // slots of a lane: one while 32 warps suffice
@@ -512,14 +512,15 @@ cudaError_t launch_plan(const int32_t* experts, int64_t n, int E,
     if ((e = allow_smem(reinterpret_cast<const void*>(kern), small_smem)) !=
         cudaSuccess)
       return e;
-    kern<<<1, 1024, small_smem, s>>>(experts, static_cast<int>(n), E, p, err);
+    kern<<<1, 1024, small_smem, s>>>(experts, static_cast<int>(n), E, tile_m,
+                                     p, err);
     return cudaGetLastError();
   }
   const int chunks = static_cast<int>(ceil_div(n, PLAN_CHUNK));
   k_plan_count<<<chunks, CHUNK_WARPS * 32, sizeof(int) * E, s>>>(
       experts, n, E, chunks, p, err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = launch_early(k_plan_layout, 1, 1024, 0, s, E, chunks, p)) !=
+  if ((e = launch_early(k_plan_layout, 1, 1024, 0, s, E, chunks, tile_m, p)) !=
       cudaSuccess)
     return e;
   const size_t smem = sizeof(int) * (CHUNK_WARPS + 1) * static_cast<size_t>(E);

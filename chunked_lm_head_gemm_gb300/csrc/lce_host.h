@@ -56,19 +56,29 @@ inline bool aligned_to(const void* p, uintptr_t n) {
 // still runs (programmatic dependent launch): it has to execute
 // griddepcontrol.wait before it touches what earlier kernels read or write.
 template <class... P, class... A>
-cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block,
-                         size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch_early_cluster(void (*kern)(P...), dim3 grid, dim3 block,
+                                 size_t smem, cudaStream_t s, unsigned cluster,
+                                 A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block,
+                         size_t smem, cudaStream_t s, A... args) {
+  return launch_early_cluster(kern, grid, block, smem, s, 1u, args...);
 }
 
 }  // namespace lce

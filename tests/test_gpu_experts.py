@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from tests import sparse_ref as ref
-from tests.gpu_util import rel_fro, require_gpu, to64
+from tests.gpu_util import PAIRS, cta_pair, rel_fro, require_gpu, to64
 
 pytestmark = pytest.mark.gpu
 
@@ -84,6 +84,22 @@ def test_shapes(L, H, I, E, K, wdt):
     dev = require_gpu()
     args, dy = draw(dev, L, H, I, E, K, seed=L + E, wdt=wdt)
     compare(run(args, dy, wdt), args, dy)
+    assert lce.get_error() == 0
+
+
+@pytest.mark.parametrize("pair", PAIRS, ids=lambda v: "pair" if v else "cta")
+@pytest.mark.parametrize("L,H,I,E,K", [
+    (600, 264, 328, 1, 1), (1100, 136, 72, 2, 1), (2600, 512, 768, 3, 2),
+    (4000, 1000, 424, 4, 2), (5000, 72, 8, 9, 4)])
+def test_many_rows_to_an_expert(L, H, I, E, K, pair):
+    """Enough rows that CTA pairs take the contractions, and the same on
+    single CTAs."""
+    import chunked_lm_head_gemm_gb300 as lce
+    dev = require_gpu()
+    args, dy = draw(dev, L, H, I, E, K, seed=L, drop=0.02)
+    with cta_pair(pair):
+        compare(run(args, dy, torch.bfloat16), args, dy)
+        compare(run(args, dy), args, dy)
     assert lce.get_error() == 0
 
 
