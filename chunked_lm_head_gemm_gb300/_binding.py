@@ -54,7 +54,7 @@ EXPORTED = ("lce_workspace_size", "lce_default_chunk_rows", "lce_forward",
             "lce_experts_workspace_size", "lce_experts_forward",
             "lce_experts_backward")
 
-KERNEL_KINDS = 34
+KERNEL_KINDS = 33
 
 
 class LossOpts(ctypes.Structure):

@@ -53,7 +53,7 @@ const char* const kKindNames[LCE_KERNEL_KINDS] = {
     "combine_slices", "shard_combine",
     "route",        "route_bwd",    "experts_plan",  "experts_up",
     "experts_down", "experts_combine", "experts_dgu", "experts_dx",
-    "experts_dWd",  "experts_dWgu", "experts_token", "experts_gather"};
+    "experts_grads", "experts_token", "experts_gather"};
 
 struct ProfRec {
   int kind;

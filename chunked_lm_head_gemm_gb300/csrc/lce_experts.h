@@ -64,7 +64,7 @@ cudaError_t launch_gather(const Plan& p, int64_t L, int K, int E, int64_t H,
 
 // out[t][:] = sum_k w[t][k] rows[row(t, k)][:] in bf16, k in order, dropped
 // slots left out (w NULL: weights 1). rows: fp16 times the scale of each row
-// and 256-column tile.
+// and 128 columns.
 cudaError_t launch_combine(const uint16_t* rows, const float* scale,
                            const int* row, const void* w, lce_dtype wdt,
                            int64_t L, int K, int64_t H, void* out,
@@ -77,8 +77,8 @@ cudaError_t launch_token(const void* x, const void* Wg, const void* Wu,
                          int64_t I, int E, float* a, void* y, unsigned* err,
                          cudaStream_t s);
 
-// dweights[slot] = sum over the column tiles of part[tile][row], in order.
-cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,
+// dweights[slot] = sum over the column pieces of part[piece][row], in order.
+cudaError_t launch_dweights(const float* part, int64_t stride, int pieces,
                             const int* row, int64_t n, lce_dtype wdt,
                             void* dweights, cudaStream_t s);
 
@@ -89,19 +89,20 @@ struct ExpertsArgs {
   int E;
   uint64_t timeout_ns;
   unsigned* err;
-  int grid;
-  bool pair;               // contractions on CTA pairs, row tiles of 256
+  int num_sms, pair_slots;
+  bool use_pairs;          // CTA pairs may be used (lce_set_cta_pair)
+  bool pair;               // row tiles of 256, contracted on CTA pairs
   // operand maps by use; each kernel takes the ones it names
   const void *Wg, *Wu, *Wd;
   uint16_t *xr, *dyr;      // [max_rows][H]: token rows in plan order
   uint16_t *a, *dg, *du;   // [max_rows][I]
   int64_t max_rows;
   uint16_t* rows_out;      // [max_rows][H] fp16 (DOWN, DX) ...
-  float* rows_scale;       // ... times [max_rows][ceil(H / 256)]
+  float* rows_scale;       // ... times [max_rows][2 ceil(H / 256)]
   const void* w;           // routing weights of the slots
   lce_dtype wdt;
-  float* part;             // [ceil(I / 128)][max_rows] of da . a
-  void *dW, *dW2;          // weight gradients
+  float* part;             // [2 ceil(I / 128)][max_rows] of da' . a
+  void *dWg, *dWu, *dWd;   // weight gradients, or NULL
   lce_dtype gdt;
 };
 
@@ -109,7 +110,6 @@ lce_status launch_experts_up(const ExpertsArgs& a, cudaStream_t s);
 lce_status launch_experts_down(const ExpertsArgs& a, cudaStream_t s);
 lce_status launch_experts_dgu(const ExpertsArgs& a, cudaStream_t s);
 lce_status launch_experts_dx(const ExpertsArgs& a, cudaStream_t s);
-lce_status launch_experts_dwd(const ExpertsArgs& a, cudaStream_t s);
-lce_status launch_experts_dwgu(const ExpertsArgs& a, cudaStream_t s);
+lce_status launch_experts_grads(const ExpertsArgs& a, cudaStream_t s);
 
 }  // namespace lce

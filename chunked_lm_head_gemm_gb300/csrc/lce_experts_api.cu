@@ -65,10 +65,10 @@ Layout layout(const Sizes& z, bool backward) {
     w.dyr = take(P * z.H * 2);
     w.dg = take(P * z.I * 2);
     w.du = take(P * z.I * 2);
-    w.part = take(P * ceil_div(z.I, 128) * 4);
+    w.part = take(P * 2 * ceil_div(z.I, 128) * 4);
   }
   w.rows = take(P * z.H * 2);
-  w.scale = take(P * ceil_div(z.H, 256) * 4);
+  w.scale = take(P * 2 * ceil_div(z.H, 256) * 4);
   w.total = off;
   return w;
 }
@@ -102,9 +102,10 @@ ExpertsArgs arguments(const Sizes& z, const Layout& w, uint8_t* ws,
   a.E = static_cast<int>(z.E);
   a.timeout_ns = wait_timeout_ns();
   a.err = dev.err;
-  a.pair = lce_get_cta_pair() != 0 && dev.pair_slots > 0 &&
-           z.L * z.K >= PAIR_ROWS * z.E;
-  a.grid = a.pair ? 2 * dev.pair_slots : dev.num_sms;
+  a.num_sms = dev.num_sms;
+  a.pair_slots = dev.pair_slots;
+  a.use_pairs = lce_get_cta_pair() != 0 && dev.pair_slots > 0;
+  a.pair = a.use_pairs && z.L * z.K >= PAIR_ROWS * z.E;
   a.xr = reinterpret_cast<uint16_t*>(ws + w.xr);
   a.dyr = reinterpret_cast<uint16_t*>(ws + w.dyr);
   a.a = reinterpret_cast<uint16_t*>(ws + w.a);
@@ -250,7 +251,7 @@ lce_status lce_experts_backward(const void* x, const void* Wg, const void* Wu,
     LCE_TRY(timed(LCE_K_EXPERTS_COMBINE, 0, s, [&] {
       return cuda_try(
           launch_dweights(a.part, a.max_rows,
-                          static_cast<int>(ceil_div(I, 128)), a.plan.row,
+                          2 * static_cast<int>(ceil_div(I, 128)), a.plan.row,
                           L * top_k, weights_dt, dweights, s),
           "experts_dweights");
     }));
@@ -263,16 +264,13 @@ lce_status lce_experts_backward(const void* x, const void* Wg, const void* Wu,
                       "experts_combine");
     }));
   }
-  if (dWd) {
-    a.dW = dWd;
-    LCE_TRY(timed(LCE_K_EXPERTS_DWD, slot_flops, s,
-                  [&] { return launch_experts_dwd(a, s); }));
-  }
-  if (dWg) {
-    a.dW = dWg;
-    a.dW2 = dWu;
-    LCE_TRY(timed(LCE_K_EXPERTS_DWGU, 2 * slot_flops, s,
-                  [&] { return launch_experts_dwgu(a, s); }));
+  if (dWd || dWg) {
+    a.dWg = dWg;
+    a.dWu = dWu;
+    a.dWd = dWd;
+    const double flops = (dWd ? 1.0 : 0.0) + (dWg ? 2.0 : 0.0);
+    LCE_TRY(timed(LCE_K_EXPERTS_GRADS, flops * slot_flops, s,
+                  [&] { return launch_experts_grads(a, s); }));
   }
   return LCE_OK;
 }

@@ -1,20 +1,20 @@
 // Grouped tensor-core contractions of the experts' gated MLP. Rows are the
 // padded segments of the plan (lce_experts.h); an expert's rows meet only
-// its own weights. One persistent kernel template, six uses:
+// its own weights. One persistent kernel template, five uses:
 //   UP    a = silu(g) u, g | u = x[token] (Wg_e | Wu_e)^T           K = H
 //   DOWN  rows = a Wd_e^T                                           K = I
 //   DGU   da' = dy[token] Wd_e beside g and u again, all three in tensor
 //         memory at once; the epilogue forms da = w da', dg, du, w a and
 //         the row's share of dw = da' . a without rounding g, u or da'
 //   DX    rows = [dg | du] [Wg_e ; Wu_e]                            K = 2 I
-//   DWD   dWd_e = dy[token]^T (w a)                       K = rows of e
-//   DWGU  dWg_e, dWu_e = dg^T x[token], du^T x[token]     K = rows of e
+//   GRAD  dWd_e = dy[token]^T (w a), dWg_e = dg^T x[token],
+//         dWu_e = du^T x[token]                           K = rows of e
 // x[token] and dy[token] are copies of the token rows in plan order, made
 // once for all contractions that read them. Gathering them into the stages by
 // TMA instead (four rows to an instruction, one instruction to a lane) needs
 // no copy but held every contraction to 37 ns an instruction per SM, 32 of
-// them a stage: UP ran at 540 and DWGU at 251 TFLOP/s (L = 32768, H = 2048,
-// I = 768, E = 128, top 8) where the tiled loads of DX reach 1295.
+// them a stage: UP ran at 540 TFLOP/s (L = 32768, H = 2048, I = 768, E = 128,
+// top 8), from copies at 1690.
 //
 // Work: units are 128 x 256 output tiles (UP and DGU 128 x 128 of a, whose
 // accumulator columns are g | u), walked in a static stride by one CTA per
@@ -45,8 +45,9 @@ struct Geom {
   const int* slot;
   int H, I, E;
   int kb_h, kb_i;   // 64-wide K blocks of H and I
-  int num_n;        // column tiles of a row tile; or of an expert's gradient
-  int num_m;        // row tiles of an expert's gradient
+  int num_n;        // column tiles of a row tile
+  int d_tiles, d_n;    // tiles of dWd_e (0: not wanted), and column tiles
+  int gu_tiles, gu_n;  // of dWg_e, and of dWu_e
   int tile_m;       // output rows of a unit: 128, or 256 of a CTA pair
   int rank;         // of this CTA in its pair (set by the kernel)
   uint64_t timeout_ns;
@@ -58,6 +59,7 @@ struct Unit {
   int rows;     // padded rows of this CTA's part of the tile, or the K extent
   int both;     // row tiles: padded rows of the whole tile
   int m, n;     // tile of the output
+  int which;    // weight gradients: 0 dWd, 1 dWg, 2 dWu
 };
 
 // ---- loads -------------------------------------------------------------------
@@ -131,16 +133,25 @@ struct RowUnits {
                 min(max(r.z - g.rank * BM, 0), BM),
                 r.z,
                 t,
-                u - t * g.num_n};
+                u - t * g.num_n,
+                0};
   }
 };
 struct GradUnits {
-  __device__ static int units(const Geom& g) { return g.E * g.num_m * g.num_n; }
+  __device__ static int units(const Geom& g) {
+    return g.E * (g.d_tiles + 2 * g.gu_tiles);
+  }
   __device__ static Unit unit(const Geom& g, int u) {
-    const int per = g.num_m * g.num_n;
-    const int e = u / per, r = u - e * per;
+    const int per = g.d_tiles + 2 * g.gu_tiles;
+    const int e = u / per;
+    int r = u - e * per;
     const int2 s = g.seg[e];
-    return Unit{e, s.x, s.y, 0, r / g.num_n, r % g.num_n};
+    if (r < g.d_tiles)
+      return Unit{e, s.x, s.y, 0, r / g.d_n, r % g.d_n, 0};
+    r -= g.d_tiles;
+    const int which = r >= g.gu_tiles ? 2 : 1;
+    if (which == 2) r -= g.gu_tiles;
+    return Unit{e, s.x, s.y, 0, r / g.gu_n, r % g.gu_n, which};
   }
 };
 
@@ -242,7 +253,9 @@ struct OpDgu : RowUnits {
   }
 };
 
-struct OpDwd : GradUnits {
+// The three weight gradients in one launch: units of an expert are the tiles
+// of dWd_e (A dy, B w a), then of dWg_e and dWu_e (A dg or du, B x).
+struct OpGrad : GradUnits {
   static constexpr int PARTS = 1;
   using P0 = Part<256, 0, 2, true, true>;
   using P1 = P0;
@@ -258,38 +271,19 @@ struct OpDwd : GradUnits {
   __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
                               int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
     const int k0 = u.row0 + kb * BK;
-    load_cols<PAIR, 2>(sa, &m.a0, u.m * g.tile_m + g.rank * BM, k0, bar);
-    load_cols<PAIR, PAIR ? 2 : 4>(sb, &m.b0, u.n * BN + g.rank * 128, k0, bar);
-  }
-};
-
-struct OpDwgu : GradUnits {
-  static constexpr int PARTS = 1;
-  using P0 = Part<256, 0, 2, true, true>;
-  using P1 = P0;
-  template <int P>
-  __device__ static int blocks(const Geom&, const Unit& u) {
-    return u.rows / SEG_ROWS;
-  }
-  template <int P>
-  __device__ static uint32_t bytes(const Geom& g, const Unit&) {
-    return g.tile_m * 128u + 32768u;
-  }
-  template <int P, bool PAIR>
-  __device__ static void load(const Maps& m, const Geom& g, const Unit& u,
-                              int kb, uint32_t sa, uint32_t sb, uint32_t bar) {
-    const int k0 = u.row0 + kb * BK;
-    const int half = g.num_m >> 1;  // dWg's row tiles, then dWu's
-    const bool second = u.m >= half;
-    const int m0 = (second ? u.m - half : u.m) * g.tile_m + g.rank * BM;
-    load_cols<PAIR, 2>(sa, second ? &m.a1 : &m.a0, m0, k0, bar);
-    load_cols<PAIR, PAIR ? 2 : 4>(sb, &m.b0, u.n * BN + g.rank * 128, k0, bar);
+    const CUtensorMap* ta = u.which == 0 ? &m.b0 : u.which == 1 ? &m.a0 : &m.a1;
+    const CUtensorMap* tb = u.which == 0 ? &m.b1 : &m.b2;
+    load_cols<PAIR, 2>(sa, ta, u.m * g.tile_m + g.rank * BM, k0, bar);
+    load_cols<PAIR, PAIR ? 2 : 4>(sb, tb, u.n * BN + g.rank * 128, k0, bar);
   }
 };
 
 // ---- epilogues ---------------------------------------------------------------
-// Each runs on a warp's 32 rows of a finished unit; taddr is the warp's lane
-// quarter of tensor memory.
+// Each runs on a warp's 32 rows and its half of the columns of a finished
+// unit (eight epilogue warps: two to each lane quarter of tensor memory;
+// taddr is the quarter). Four warps, one to a quarter, left DGU waiting: with
+// eight DGU 1906 -> DGU8 us, DOWN 596 -> DOWN8 us, DWD 600 -> DWD8 us (L =
+// 32768, H = 2048, I = 768, E = 128, top 8).
 
 // a = silu(g) u in bf16.
 struct EpiUp : EpiBase {
@@ -298,12 +292,13 @@ struct EpiUp : EpiBase {
   };
   __device__ __forceinline__ void tile(const Params&, const Maps& m,
                                        const Geom& g, const Unit& u,
-                                       uint32_t taddr, int r, int i) {
+                                       uint32_t taddr, int r, int half,
+                                       int i) {
     const int wr = r & ~31;
     if (wr >= u.rows) return;
     const uint32_t t0 = taddr + (i & 1) * 256;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 2 * half; c < 2 * half + 2; ++c) {
       const int j0 = u.n * 128 + c * 32;
       if (j0 >= g.I) break;
       float gv[32], uv[32];
@@ -317,7 +312,7 @@ struct EpiUp : EpiBase {
 };
 
 // Rows of H columns for the sum over a token's slots, in fp16 under a power
-// of two for each row and 256-column tile: the largest finite value of the
+// of two for each row and 128 columns: the largest finite value of the
 // piece lands in [2^14, 2^15), so a value is off by 2^-12 of itself at most
 // (2^-25 of the piece's largest below that), an eighth of a bf16 rounding, at
 // half the bytes of fp32. Infinities and NaN stay what they are. Against fp32
@@ -326,18 +321,19 @@ struct EpiUp : EpiBase {
 // 128, top 8).
 struct EpiRows : EpiBase {
   struct Params {
-    float* scale;  // [max_rows][num_n]
+    float* scale;  // [max_rows][2 num_n]
   };
   __device__ __forceinline__ void tile(const Params& p, const Maps& m,
                                        const Geom& g, const Unit& u,
-                                       uint32_t taddr, int r, int i) {
+                                       uint32_t taddr, int r, int half,
+                                       int i) {
     const int wr = r & ~31;
     if (wr >= u.rows) return;
     te = &m.s0;
     const uint32_t t0 = taddr + (i & 1) * 256;
     float mx = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 2 * half; c < 2 * half + 2; ++c) {
       if (u.n * 256 + c * 64 >= g.H) break;
       float v[64];  // columns past H are zero
       tmem_ld64(t0 + c * 64, v);
@@ -352,9 +348,10 @@ struct EpiRows : EpiBase {
     const int se = mx == 0.f ? 127 : max(e - 14, 1);
     const float scale = __uint_as_float(static_cast<uint32_t>(se) << 23);
     const float inv = __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
-    p.scale[static_cast<int64_t>(u.row0 + r) * g.num_n + u.n] = scale;
+    p.scale[static_cast<int64_t>(u.row0 + r) * (2 * g.num_n) + 2 * u.n + half] =
+        scale;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 2 * half; c < 2 * half + 2; ++c) {
       const int j0 = u.n * 256 + c * 64;
       if (j0 >= g.H) break;
       float v[64];
@@ -383,7 +380,8 @@ struct EpiDgu : EpiBase {
   };
   __device__ __forceinline__ void tile(const Params& p, const Maps& m,
                                        const Geom& g, const Unit& u,
-                                       uint32_t taddr, int r, int i) {
+                                       uint32_t taddr, int r, int half,
+                                       int i) {
     const int wr = r & ~31;
     if (wr >= u.rows) return;
     const int slot = g.slot[u.row0 + r];
@@ -395,7 +393,7 @@ struct EpiDgu : EpiBase {
     const uint32_t tda = taddr + 256 + (i & 1) * 128;
     float dot = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 2 * half; c < 2 * half + 2; ++c) {
       const int j0 = u.n * 128 + c * 32;
       if (j0 >= g.I) break;
       float gv[32], uv[32], da[32];
@@ -419,33 +417,29 @@ struct EpiDgu : EpiBase {
       store_box(da, j0, u.row0 + wr, &m.s1);
       store_box(uv, j0, u.row0 + wr, &m.s2);
     }
-    p.part[u.n * p.stride + u.row0 + r] = dot;
+    p.part[(2 * u.n + half) * p.stride + u.row0 + r] = dot;
   }
 };
 
 // An expert's weight gradient, bf16 or fp32, zero where it has no rows.
-struct EpiGrad2 : EpiBase {
+struct EpiWeights : EpiBase {
   struct Params {
-    void *out, *out2;  // [E][rows][cols]; out2: the second half of the tiles
+    void* out[3];  // dWd [E][H][I], dWg and dWu [E][I][H]
     int f32;
-    int rows, cols;    // of one expert's gradient
   };
   __device__ __forceinline__ void tile(const Params& p, const Maps&,
                                        const Geom& g, const Unit& u,
-                                       uint32_t taddr, int r, int i) {
-    void* base = p.out;
-    int m = u.m;
-    if (p.out2 != nullptr && m >= (g.num_m >> 1)) {
-      base = p.out2;
-      m -= g.num_m >> 1;
-    }
-    const int row = m * g.tile_m + g.rank * BM + r;
-    const int64_t at =
-        (static_cast<int64_t>(u.e) * p.rows + row) * p.cols;
+                                       uint32_t taddr, int r, int half,
+                                       int i) {
+    void* base = p.out[u.which];
+    const int rows = u.which == 0 ? g.H : g.I;
+    const int cols = u.which == 0 ? g.I : g.H;
+    const int row = u.m * g.tile_m + g.rank * BM + r;
+    const int64_t at = (static_cast<int64_t>(u.e) * rows + row) * cols;
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 4 * half; c < 4 * half + 4; ++c) {
       const int j0 = u.n * BN + c * 32;
-      if (j0 >= p.cols) break;
+      if (j0 >= cols) break;
       float v[32];
       if (u.rows > 0) {
         tmem_ld32(taddr + (i & 1) * 256 + c * 32, v);
@@ -453,13 +447,13 @@ struct EpiGrad2 : EpiBase {
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = 0.f;
       }
-      if (row >= p.rows) continue;
+      if (row >= rows) continue;
       if (p.f32) {
         float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + at +
                                               j0);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (j0 + 4 * q < p.cols)  // cols % 8 == 0
+          if (j0 + 4 * q < cols)  // cols % 8 == 0
             d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2],
                                v[4 * q + 3]);
       } else {
@@ -467,7 +461,7 @@ struct EpiGrad2 : EpiBase {
                                             j0);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (j0 + 8 * q < p.cols)
+          if (j0 + 8 * q < cols)
             d[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]),
                               pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                               pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
@@ -480,13 +474,17 @@ struct EpiGrad2 : EpiBase {
 // ---- roles -------------------------------------------------------------------
 // Ring of stages by form: one CTA stages 128 rows of A and 256 columns of B,
 // a CTA of a pair 128 and 128.
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+
 template <bool PAIR>
 struct Form {
   static constexpr int STAGES_ = PAIR ? STAGES2 : STAGES;
   static constexpr int A_BYTES = A_STAGE_BYTES;
   static constexpr int B_BYTES = PAIR ? B2_STAGE_BYTES : B_STAGE_BYTES;
   static constexpr int RING_BYTES = STAGES_ * (A_BYTES + B_BYTES);
-  static constexpr int SMEM = 1024 + RING_BYTES + 1024 + EPI_STAGE_BYTES;
+  static constexpr int SMEM =
+      1024 + RING_BYTES + 1024 + EPI_WARPS * 2 * EPI_BUF_BYTES;
 };
 
 // Barriers: full / empty per stage; tfull[2]: a unit's accumulators are
@@ -591,7 +589,7 @@ __device__ __forceinline__ bool multiply(const Geom& g, const Unit& u, int i,
 }
 
 template <class Op, class Epi, bool PAIR>
-__global__ void __launch_bounds__(GEMM_THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
     k_experts(const __grid_constant__ Maps maps, Geom g,
               const typename Epi::Params p, unsigned* err) {
   extern __shared__ uint8_t smem_raw[];
@@ -615,7 +613,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(bars.tfull(b), 1);
       // one arrival per epilogue warp
-      for (int q = 0; q < 2; ++q) mbar_init(bars.tempty(q, b), PAIR ? 8 : 4);
+      for (int q = 0; q < 2; ++q) mbar_init(bars.tempty(q, b), EPI_WARPS * (PAIR ? 2 : 1));
     }
     mbar_init(bars.drain(), 1);
     *abort_flag = 0u;
@@ -692,11 +690,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3;  // the lane quarter this warp may access
+    const int half = (warp - 2) >> 2;
     const int r = q * 32 + lane;
     Epi epi;
     epi.stage = base + F::RING_BYTES + 1024 +
-                static_cast<uint32_t>(q) * 2u * EPI_BUF_BYTES;
+                static_cast<uint32_t>(warp - 2) * 2u * EPI_BUF_BYTES;
     int i = 0;
     for (int u = first; u < units; u += stride, ++i) {
       const Unit t = Op::unit(g, u);
@@ -704,7 +703,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       if (!__all_sync(FULL, got)) break;
       tc_fence_after();
       epi.tile(p, maps, g, t, tmem + (static_cast<uint32_t>(q * 32) << 16), r,
-               i);
+               half, i);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -768,7 +767,7 @@ lce_status store_map(CUtensorMap* m, const void* p, int64_t cols,
   return map2(m, p, cols, rows, EPI_BOX, EPI_BOX, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-Geom geom(const ExpertsArgs& a) {
+Geom geom(const ExpertsArgs& a, bool pair) {
   Geom g{};
   g.head = a.plan.head;
   g.tile = a.plan.tile;
@@ -779,7 +778,7 @@ Geom geom(const ExpertsArgs& a) {
   g.E = a.E;
   g.kb_h = static_cast<int>(ceil_div(a.H, BK));
   g.kb_i = static_cast<int>(ceil_div(a.I, BK));
-  g.tile_m = a.pair ? 2 * BM : BM;
+  g.tile_m = BM * (pair ? 2 : 1);
   g.timeout_ns = a.timeout_ns;
   return g;
 }
@@ -788,13 +787,14 @@ template <class Op, class Epi>
 lce_status launch(const char* what, const Maps& m, const Geom& g,
                   const typename Epi::Params& p, const ExpertsArgs& a,
                   cudaStream_t s) {
-  auto kern = a.pair ? k_experts<Op, Epi, true> : k_experts<Op, Epi, false>;
-  const int smem = a.pair ? Form<true>::SMEM : Form<false>::SMEM;
+  const bool pair = g.tile_m > BM;
+  auto kern = pair ? k_experts<Op, Epi, true> : k_experts<Op, Epi, false>;
+  const int smem = pair ? Form<true>::SMEM : Form<false>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
-    e = launch_early_cluster(kern, a.grid, GEMM_THREADS, smem, s,
-                             a.pair ? 2 : 1, m, g, p, a.err);
+    e = launch_early_cluster(kern, pair ? 2 * a.pair_slots : a.num_sms,
+                             THREADS, smem, s, pair ? 2 : 1, m, g, p, a.err);
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, what);
 }
 
@@ -812,7 +812,7 @@ lce_status launch_experts_up(const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(map3(&m.b0, a.Wg, a.H, a.I, a.E, BK, 128));
   LCE_TRY(map3(&m.b1, a.Wu, a.H, a.I, a.E, BK, 128));
   LCE_TRY(store_map(&m.s0, a.a, a.I, a.max_rows));
-  Geom g = geom(a);
+  Geom g = geom(a, a.pair);
   g.num_n = static_cast<int>(ceil_div(a.I, 128));
   return launch<OpUp, EpiUp>("experts_up", m, g, {0}, a, s);
 }
@@ -821,7 +821,7 @@ lce_status launch_experts_down(const ExpertsArgs& a, cudaStream_t s) {
   Maps m{};
   LCE_TRY(map2(&m.a0, a.a, a.I, a.max_rows, BK, 64));
   LCE_TRY(map3(&m.b0, a.Wd, a.I, a.H, a.E, BK, a.pair ? 128 : 256));
-  Geom g = geom(a);
+  Geom g = geom(a, a.pair);
   LCE_TRY(store_map(&m.s0, a.rows_out, a.H, a.max_rows));
   g.num_n = static_cast<int>(ceil_div(a.H, 256));
   return launch<OpDown, EpiRows>("experts_down", m, g, {a.rows_scale}, a, s);
@@ -837,7 +837,7 @@ lce_status launch_experts_dgu(const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(store_map(&m.s0, a.dg, a.I, a.max_rows));
   LCE_TRY(store_map(&m.s1, a.du, a.I, a.max_rows));
   LCE_TRY(store_map(&m.s2, a.a, a.I, a.max_rows));
-  Geom g = geom(a);
+  Geom g = geom(a, a.pair);
   g.num_n = static_cast<int>(ceil_div(a.I, 128));
   return launch<OpDgu, EpiDgu>(
       "experts_dgu", m, g, {a.w, a.wdt == LCE_F32, a.part, a.max_rows}, a, s);
@@ -849,34 +849,29 @@ lce_status launch_experts_dx(const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(map2(&m.a1, a.du, a.I, a.max_rows, BK, 64));
   LCE_TRY(map3(&m.b0, a.Wg, a.H, a.I, a.E, 64, BK));
   LCE_TRY(map3(&m.b1, a.Wu, a.H, a.I, a.E, 64, BK));
-  Geom g = geom(a);
+  Geom g = geom(a, a.pair);
   LCE_TRY(store_map(&m.s0, a.rows_out, a.H, a.max_rows));
   g.num_n = static_cast<int>(ceil_div(a.H, 256));
   return launch<OpDx, EpiRows>("experts_dx", m, g, {a.rows_scale}, a, s);
 }
 
-lce_status launch_experts_dwd(const ExpertsArgs& a, cudaStream_t s) {
-  Maps m{};
-  LCE_TRY(map2(&m.a0, a.dyr, a.H, a.max_rows, 64, BK));
-  LCE_TRY(map2(&m.b0, a.a, a.I, a.max_rows, 64, BK));
-  Geom g = geom(a);
-  g.num_m = static_cast<int>(ceil_div(a.H, g.tile_m));
-  g.num_n = static_cast<int>(ceil_div(a.I, BN));
-  return launch<OpDwd, EpiGrad2>(
-      "experts_dWd", m, g,
-      {a.dW, nullptr, a.gdt == LCE_F32, g.H, g.I}, a, s);
-}
-
-lce_status launch_experts_dwgu(const ExpertsArgs& a, cudaStream_t s) {
+lce_status launch_experts_grads(const ExpertsArgs& a, cudaStream_t s) {
+  // 256-row tiles unless a gradient's rows fit one of 128
+  Geom g = geom(a, a.use_pairs && a.H > BM && a.I > BM);
+  const int h_m = static_cast<int>(ceil_div(a.H, g.tile_m));
+  const int i_m = static_cast<int>(ceil_div(a.I, g.tile_m));
+  g.d_n = static_cast<int>(ceil_div(a.I, BN));
+  g.gu_n = static_cast<int>(ceil_div(a.H, BN));
+  g.d_tiles = a.dWd ? h_m * g.d_n : 0;
+  g.gu_tiles = a.dWg ? i_m * g.gu_n : 0;
   Maps m{};
   LCE_TRY(map2(&m.a0, a.dg, a.I, a.max_rows, 64, BK));
   LCE_TRY(map2(&m.a1, a.du, a.I, a.max_rows, 64, BK));
-  LCE_TRY(map2(&m.b0, a.xr, a.H, a.max_rows, 64, BK));
-  Geom g = geom(a);
-  g.num_m = 2 * static_cast<int>(ceil_div(a.I, g.tile_m));
-  g.num_n = static_cast<int>(ceil_div(a.H, BN));
-  return launch<OpDwgu, EpiGrad2>(
-      "experts_dWgu", m, g, {a.dW, a.dW2, a.gdt == LCE_F32, g.I, g.H}, a, s);
+  LCE_TRY(map2(&m.b0, a.dyr, a.H, a.max_rows, 64, BK));
+  LCE_TRY(map2(&m.b1, a.a, a.I, a.max_rows, 64, BK));
+  LCE_TRY(map2(&m.b2, a.xr, a.H, a.max_rows, 64, BK));
+  return launch<OpGrad, EpiWeights>(
+      "experts_grads", m, g, {{a.dWd, a.dWg, a.dWu}, a.gdt == LCE_F32}, a, s);
 }
 
 }  // namespace lce

@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(256)
       blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y;
   const int h = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
   if (t >= L || h >= H) return;
-  const int tiles = (H + 255) / 256;
+  const int tiles = 2 * ((H + 255) / 256);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int k0 = 0; k0 < K; k0 += KB) {
     int r[KB];
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(256)
       if (r[q] >= 0) {
         v[q] = *reinterpret_cast<const uint4*>(
             rows + static_cast<int64_t>(r[q]) * H + h);
-        c[q] = scale[static_cast<int64_t>(r[q]) * tiles + (h >> 8)];
+        c[q] = scale[static_cast<int64_t>(r[q]) * tiles + (h >> 7)];
         if (WEIGHTED) c[q] *= weight_at<T>(w, t * K + k0 + q);
       }
     }

@@ -673,7 +673,7 @@ int lce_get_wave_sync(void);
  * per tensor-core contraction, 0 for the other kernels). Host-side state
  * only; events are created on first use and reused.
  */
-#define LCE_KERNEL_KINDS 34
+#define LCE_KERNEL_KINDS 33
 enum {
   LCE_K_COUNT_VALID = 0,
   LCE_K_GEMM_LSE = 1,
@@ -705,10 +705,9 @@ enum {
   LCE_K_EXPERTS_COMBINE = 27,
   LCE_K_EXPERTS_DGU = 28,
   LCE_K_EXPERTS_DX = 29,
-  LCE_K_EXPERTS_DWD = 30,
-  LCE_K_EXPERTS_DWGU = 31,
-  LCE_K_EXPERTS_TOKEN = 32,
-  LCE_K_EXPERTS_GATHER = 33
+  LCE_K_EXPERTS_GRADS = 30,
+  LCE_K_EXPERTS_TOKEN = 31,
+  LCE_K_EXPERTS_GATHER = 32
 };
 
 typedef struct {
