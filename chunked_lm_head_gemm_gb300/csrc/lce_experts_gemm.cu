@@ -329,18 +329,24 @@ struct EpiRows : EpiBase {
                                        int i) {
     const int wr = r & ~31;
     if (wr >= u.rows) return;
+    const int c0 = u.n * 256 + half * 128;
+    if (c0 >= g.H) return;
     te = &m.s0;
-    const uint32_t t0 = taddr + (i & 1) * 256;
+    const uint32_t t0 = taddr + (i & 1) * 256 + half * 128;
+    float v[2][64];  // columns past H are zero
+    tmem_ld64(t0, v[0]);
+    tmem_ld64(t0 + 64, v[1]);
     float mx = 0.f;
-#pragma unroll 1
-    for (int c = 2 * half; c < 2 * half + 2; ++c) {
-      if (u.n * 256 + c * 64 >= g.H) break;
-      float v[64];  // columns past H are zero
-      tmem_ld64(t0 + c * 64, v);
+#pragma unroll
+    for (int k = 0; k < 64; ++k)
+      mx = fmaxf(fmaxf(mx, fabsf(v[0][k])), fabsf(v[1][k]));
+    if (__any_sync(FULL, mx > 3.4028235e38f)) {  // infinities: the others' max
+      mx = 0.f;
 #pragma unroll
       for (int k = 0; k < 64; ++k) {
-        const float x = fabsf(v[k]);
+        const float x = fabsf(v[0][k]), y = fabsf(v[1][k]);
         if (x <= 3.4028235e38f) mx = fmaxf(mx, x);
+        if (y <= 3.4028235e38f) mx = fmaxf(mx, y);
       }
     }
     // 2^(exponent - 14), kept normal; 1 for a piece of zeros
@@ -350,20 +356,19 @@ struct EpiRows : EpiBase {
     const float inv = __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
     p.scale[static_cast<int64_t>(u.row0 + r) * (2 * g.num_n) + 2 * u.n + half] =
         scale;
-#pragma unroll 1
-    for (int c = 2 * half; c < 2 * half + 2; ++c) {
-      const int j0 = u.n * 256 + c * 64;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int j0 = c0 + c * 64;
       if (j0 >= g.H) break;
-      float v[64];
-      tmem_ld64(t0 + c * 64, v);
       uint32_t w0[16], w1[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const __half2 a = __floats2half2_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
-        const __half2 b =
-            __floats2half2_rn(v[32 + 2 * k] * inv, v[33 + 2 * k] * inv);
-        w0[k] = *reinterpret_cast<const uint32_t*>(&a);
-        w1[k] = *reinterpret_cast<const uint32_t*>(&b);
+        const __half2 x = __floats2half2_rn(v[c][2 * k] * inv,
+                                            v[c][2 * k + 1] * inv);
+        const __half2 y = __floats2half2_rn(v[c][32 + 2 * k] * inv,
+                                            v[c][33 + 2 * k] * inv);
+        w0[k] = *reinterpret_cast<const uint32_t*>(&x);
+        w1[k] = *reinterpret_cast<const uint32_t*>(&y);
       }
       store_box_pair(w0, w1, j0, u.row0 + wr, j0 + 32 < g.H);
     }
@@ -424,17 +429,51 @@ struct EpiDgu : EpiBase {
 // An expert's weight gradient, bf16 or fp32, zero where it has no rows.
 struct EpiWeights : EpiBase {
   struct Params {
-    void* out[3];  // dWd [E][H][I], dWg and dWu [E][I][H]
-    int f32;
+    float* out[3];  // fp32 gradients: dWd [E][H][I], dWg and dWu [E][I][H];
+                    // NULL: bf16, through the store maps
   };
-  __device__ __forceinline__ void tile(const Params& p, const Maps&,
+  // Box of this warp's 32 rows and 32 columns of expert e's gradient (as
+  // store_box; the map drops what lies past the expert's rows and columns).
+  __device__ __forceinline__ void store_box_of(const float (&v)[32],
+                                               const CUtensorMap* map, int j0,
+                                               int row0, int e) {
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t buf = stage + (nstored & 1u) * EPI_BUF_BYTES;
+    if (lane == 0 && nstored >= 2) bulk_wait_read1();
+    __syncwarp();
+    const uint32_t rowa = buf + lane * 64u;
+    const uint32_t sw = (lane >> 1) & 3u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      st_shared_v4(rowa + ((static_cast<uint32_t>(q) ^ sw) << 4),
+                   pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                   pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                   pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                   pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile(
+          "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, "
+          "%3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+          "r"(buf), "r"(j0), "r"(row0), "r"(e)
+          : "memory");
+      bulk_commit();
+    }
+    ++nstored;
+  }
+
+  __device__ __forceinline__ void tile(const Params& p, const Maps& m,
                                        const Geom& g, const Unit& u,
                                        uint32_t taddr, int r, int half,
                                        int i) {
-    void* base = p.out[u.which];
+    float* base = p.out[u.which];
+    const CUtensorMap* map =
+        u.which == 0 ? &m.s0 : u.which == 1 ? &m.s1 : &m.s2;
     const int rows = u.which == 0 ? g.H : g.I;
     const int cols = u.which == 0 ? g.I : g.H;
     const int row = u.m * g.tile_m + g.rank * BM + r;
+    if (row - (r & 31) >= rows) return;  // the same for the warp
     const int64_t at = (static_cast<int64_t>(u.e) * rows + row) * cols;
 #pragma unroll 1
     for (int c = 4 * half; c < 4 * half + 4; ++c) {
@@ -447,26 +486,17 @@ struct EpiWeights : EpiBase {
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = 0.f;
       }
-      if (row >= rows) continue;
-      if (p.f32) {
-        float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + at +
-                                              j0);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (j0 + 4 * q < cols)  // cols % 8 == 0
-            d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2],
-                               v[4 * q + 3]);
-      } else {
-        uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at +
-                                            j0);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (j0 + 8 * q < cols)
-            d[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]),
-                              pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                              pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
-                              pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+      if (base == nullptr) {
+        store_box_of(v, map, j0, row - (r & 31), u.e);
+        continue;
       }
+      if (row >= rows) continue;
+      float4* d = reinterpret_cast<float4*>(base + at + j0);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (j0 + 4 * q < cols)  // cols % 8 == 0
+          d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2],
+                             v[4 * q + 3]);
     }
   }
 };
@@ -753,14 +783,15 @@ lce_status map2(CUtensorMap* m, const void* p, int64_t cols, int64_t rows,
 }
 // [E][rows][cols] bf16, boxes inside one expert.
 lce_status map3(CUtensorMap* m, const void* p, int64_t cols, int64_t rows,
-                int64_t E, uint32_t box_c, uint32_t box_r) {
+                int64_t E, uint32_t box_c, uint32_t box_r,
+                CUtensorMapSwizzle swz = SW128) {
   const uint64_t d[3] = {static_cast<uint64_t>(cols),
                          static_cast<uint64_t>(rows),
                          static_cast<uint64_t>(E)};
   const uint64_t st[2] = {static_cast<uint64_t>(cols) * 2,
                           static_cast<uint64_t>(cols) * rows * 2};
   const uint32_t b[3] = {box_c, box_r, 1};
-  return make_tmap_nd(m, BF, 3, p, d, st, b, SW128);
+  return make_tmap_nd(m, BF, 3, p, d, st, b, swz);
 }
 lce_status store_map(CUtensorMap* m, const void* p, int64_t cols,
                      int64_t rows) {
@@ -870,8 +901,18 @@ lce_status launch_experts_grads(const ExpertsArgs& a, cudaStream_t s) {
   LCE_TRY(map2(&m.b0, a.dyr, a.H, a.max_rows, 64, BK));
   LCE_TRY(map2(&m.b1, a.a, a.I, a.max_rows, 64, BK));
   LCE_TRY(map2(&m.b2, a.xr, a.H, a.max_rows, 64, BK));
-  return launch<OpGrad, EpiWeights>(
-      "experts_grads", m, g, {{a.dWd, a.dWg, a.dWu}, a.gdt == LCE_F32}, a, s);
+  EpiWeights::Params p{};
+  if (a.gdt == LCE_F32) {
+    p.out[0] = static_cast<float*>(a.dWd);
+    p.out[1] = static_cast<float*>(a.dWg);
+    p.out[2] = static_cast<float*>(a.dWu);
+  } else {
+    constexpr CUtensorMapSwizzle SW64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    if (a.dWd) LCE_TRY(map3(&m.s0, a.dWd, a.I, a.H, a.E, 32, 32, SW64));
+    if (a.dWg) LCE_TRY(map3(&m.s1, a.dWg, a.H, a.I, a.E, 32, 32, SW64));
+    if (a.dWg) LCE_TRY(map3(&m.s2, a.dWu, a.H, a.I, a.E, 32, 32, SW64));
+  }
+  return launch<OpGrad, EpiWeights>("experts_grads", m, g, p, a, s);
 }
 
 }  // namespace lce
