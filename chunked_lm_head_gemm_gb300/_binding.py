@@ -92,6 +92,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False):
     """Open liblce.so and declare the C signatures. Raises if it is absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -816,11 +818,11 @@ def route_forward(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
                                  bias.dtype == torch.float32 and
                                  bias.is_contiguous()):
         raise ValueError("bias must be a contiguous CUDA float32 [E] tensor")
-    k = max(int(top_k), 0)
-    weights = weights_out if weights_out is not None else torch.empty(
-        L, k, dtype=logits.dtype, device=dev)
-    experts = experts_out if experts_out is not None else torch.empty(
-        L, k, dtype=torch.int32, device=dev)
+    shape = (L, max(top_k, 0))
+    weights = (weights_out if weights_out is not None
+               else logits.new_empty(shape))
+    experts = (experts_out if experts_out is not None
+               else torch.empty(shape, dtype=torch.int32, device=dev))
     st = lib.lce_route_forward(logits.data_ptr(), code, _ptr(bias), L, E,
                                opts, weights.data_ptr(),
                                experts.data_ptr(), _stream_ptr(dev))
@@ -854,33 +856,38 @@ def route_backward(logits: torch.Tensor, experts: torch.Tensor,
 
 
 def _check_experts(experts, L):
-    if not (experts.is_cuda and experts.dtype == torch.int32 and
-            experts.dim() == 2 and experts.shape[0] == L and
-            experts.is_contiguous()):
+    if (experts.dtype is not torch.int32 or not experts.is_cuda or
+            experts.dim() != 2 or experts.size(0) != L or
+            not experts.is_contiguous()):
         raise ValueError("experts must be a contiguous CUDA int32 [L,top_k] "
                          "tensor")
 
 
 def _check_experts_mlp(x, Wg, Wu, Wd, weights, experts):
-    if not all(t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous()
-               for t in (x, Wg, Wu, Wd)):
-        raise ValueError("x, Wg, Wu, Wd must be contiguous bf16 CUDA tensors")
+    for t in (x, Wg, Wu, Wd):
+        if (t.dtype is not torch.bfloat16 or not t.is_cuda or
+                not t.is_contiguous()):
+            raise ValueError("x, Wg, Wu, Wd must be contiguous bf16 CUDA "
+                             "tensors")
     if x.dim() != 2 or Wg.dim() != 3:
         raise ValueError("expected x [L,H], Wg and Wu [E,I,H], Wd [E,H,I]")
     L, H = x.shape
-    E, I = Wg.shape[:2]
-    if Wg.shape != (E, I, H) or Wu.shape != (E, I, H) or Wd.shape != (E, H, I):
+    shape = Wg.shape
+    E, I, Hw = shape
+    if Hw != H or Wu.shape != shape or Wd.shape != (E, H, I):
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, Wg "
                          f"{tuple(Wg.shape)}, Wu {tuple(Wu.shape)}, Wd "
                          f"{tuple(Wd.shape)}")
     _check_experts(experts, L)
-    if not (weights.is_cuda and weights.shape == experts.shape and
-            weights.is_contiguous()):
+    shape = experts.shape
+    if (weights.shape != shape or not weights.is_cuda or
+            not weights.is_contiguous()):
         raise ValueError("weights must be a contiguous CUDA tensor of "
                          "experts' shape")
-    return L, H, I, E, experts.shape[1], _dtype_code(weights)
+    return L, H, I, E, shape[1], _dtype_code(weights)
 
 
+@functools.lru_cache(maxsize=1024)
 def experts_workspace_size(L: int, H: int, I: int, E: int, top_k: int,
                            backward: bool = False) -> int:
     n = load().lce_experts_workspace_size(L, H, I, E, top_k, int(backward))
@@ -895,18 +902,19 @@ def experts_forward(x, Wg, Wu, Wd, weights, experts, workspace=None,
     """y_t = sum_k weights[t,k] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)), e =
     experts[t,k] (-1: dropped): x bf16 [L,H], Wg and Wu bf16 [E,I,H], Wd bf16
     [E,H,I], weights [L,top_k] (bf16 or fp32), experts int32 [L,top_k]."""
-    lib = load()
     L, H, I, E, K, code = _check_experts_mlp(x, Wg, Wu, Wd, weights, experts)
+    dev = x.device
     if workspace is None:
         workspace = torch.empty(experts_workspace_size(L, H, I, E, K),
-                                dtype=torch.uint8, device=x.device)
+                                dtype=torch.uint8, device=dev)
     y = y_out if y_out is not None else torch.empty_like(x)
-    st = lib.lce_experts_forward(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
-                                 Wd.data_ptr(), weights.data_ptr(), code,
-                                 experts.data_ptr(), L, H, I, E, K,
-                                 y.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel(), _stream_ptr(x.device))
-    _check(st, "lce_experts_forward")
+    st = load().lce_experts_forward(
+        x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
+        weights.data_ptr(), code, experts.data_ptr(), L, H, I, E, K,
+        y.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _stream_ptr(dev))
+    if st:
+        _check(st, "lce_experts_forward")
     return y
 
 

@@ -2,6 +2,7 @@
 // lce_experts_backward): argument checks, workspace carving and the launch
 // sequence.
 #include <algorithm>
+#include <cmath>
 
 #include "lce_experts.h"
 #include "lce_host.h"
@@ -13,9 +14,21 @@ struct Sizes {
   int64_t L, H, I, E, K;
 };
 
-// Up to this many slots the forward reads weights slot by slot on the CUDA
-// cores (launch_token) instead of planning tiles for the tensor cores.
-constexpr int64_t TOKEN_SLOTS = 32;
+// Whether the forward takes its slots one by one on the CUDA cores
+// (launch_token), each reading its expert's weights, instead of planning tiles
+// for the tensor cores, which read the weights of every expert hit once but
+// cost about 18 us of small launches. Both read at 5.6 to 5.9 TB/s, so the
+// border is where the weights read again are 100 MB: slots - (experts hit)
+// experts' weights, with the slots falling evenly. At H = 2048, I = 768, E =
+// 128 the two take 60 and 70 us for 32 slots, 112 and 92 us for 64; at I =
+// 4096, E = 8 they take 47 and 59 us for 4 slots, 80 and 77 us for 8. (At most
+// 64 slots: their fp32 activations fit the bf16 rows of a planned call.)
+bool takes_tokens(const Sizes& z) {
+  const double n = static_cast<double>(z.L) * z.K;
+  if (n > 64) return false;
+  const double hit = z.E * (1.0 - std::pow(1.0 - 1.0 / z.E, n));
+  return (n - hit) * 6.0 * z.H * z.I <= 100e6;
+}
 
 // Rows an expert has on average from which the contractions run on CTA pairs.
 constexpr int64_t PAIR_ROWS = 512;
@@ -185,7 +198,7 @@ lce_status lce_experts_forward(const void* x, const void* Wg, const void* Wu,
   a.Wu = Wu;
   a.Wd = Wd;
   const double slot_flops = 2.0 * L * top_k * H * I;
-  if (L * top_k <= TOKEN_SLOTS)
+  if (takes_tokens(z))
     return timed(LCE_K_EXPERTS_TOKEN, 3 * slot_flops, s, [&] {
       return cuda_try(
           launch_token(x, Wg, Wu, Wd, weights, weights_dt, experts, L,

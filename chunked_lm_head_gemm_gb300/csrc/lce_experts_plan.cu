@@ -337,8 +337,12 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------------------
 // single tokens: few slots, no plan and no tensor cores. What bounds them is
-// reading the chosen experts' weights once; every warp keeps 16 loads of 16
-// bytes a lane in flight.
+// reading the chosen experts' weights once: 75 MB, 11 us, for one token at H
+// = 2048, I = 768, top 8. So every warp of k_token_up is resident at once
+// (40 registers, two 16-byte loads of each matrix in flight a lane; with four
+// there are two waves of warps, 25 us against 22 for both kernels), and
+// k_token_down fetches its weights before k_token_up has ended. Fetching the
+// rows by bulk copies into shared memory took 26 us.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -351,6 +355,16 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
   }
   return s;
 }
+__device__ __forceinline__ float dot8(uint4 a, float4 lo, float4 hi) {
+  float s = __uint_as_float(a.x << 16) * lo.x;
+  s = fmaf(__uint_as_float(a.x & 0xffff0000u), lo.y, s);
+  s = fmaf(__uint_as_float(a.y << 16), lo.z, s);
+  s = fmaf(__uint_as_float(a.y & 0xffff0000u), lo.w, s);
+  s = fmaf(__uint_as_float(a.z << 16), hi.x, s);
+  s = fmaf(__uint_as_float(a.z & 0xffff0000u), hi.y, s);
+  s = fmaf(__uint_as_float(a.w << 16), hi.z, s);
+  return fmaf(__uint_as_float(a.w & 0xffff0000u), hi.w, s);
+}
 
 __device__ __forceinline__ uint4 load_stream(const uint4* p) {
   uint4 v;
@@ -360,12 +374,12 @@ __device__ __forceinline__ uint4 load_stream(const uint4* p) {
   return v;
 }
 
-constexpr int TOKEN_WARPS = 8;
+constexpr int TOKEN_WARPS = 4;
 
 // a[slot][i] = silu(Wg_e[i] . x_t) (Wu_e[i] . x_t) in fp32, one warp per
 // (slot, i). The call's first kernel: it begins when earlier work has ended,
 // and lets k_token_down begin once each of its blocks runs.
-__global__ void __launch_bounds__(TOKEN_WARPS * 32, 4)
+__global__ void __launch_bounds__(TOKEN_WARPS * 32, 12)
     k_token_up(const uint4* __restrict__ x, const uint4* __restrict__ Wg,
                const uint4* __restrict__ Wu, const int32_t* __restrict__ experts,
                int n, int K, int H, int I, int E, float* __restrict__ a,
@@ -381,20 +395,17 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 4)
   const int64_t at = (static_cast<int64_t>(e) * I + i) * vecs;
   const uint4* xr = x + static_cast<int64_t>(slot / K) * vecs;
   float g = 0.f, u = 0.f;
-  for (int c = lane; c < vecs; c += 128) {
-    uint4 vg[4], vu[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bool in = c + 32 * q < vecs;
-      vg[q] = in ? load_stream(Wg + at + c + 32 * q) : make_uint4(0, 0, 0, 0);
-      vu[q] = in ? load_stream(Wu + at + c + 32 * q) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (c + 32 * q >= vecs) break;
-      const uint4 xv = __ldg(xr + c + 32 * q);
-      g += dot8(vg[q], xv);
-      u += dot8(vu[q], xv);
+  for (int c = lane; c < vecs; c += 64) {
+    const bool two = c + 32 < vecs;
+    const int d = two ? c + 32 : c;
+    const uint4 g0 = load_stream(Wg + at + c), u0 = load_stream(Wu + at + c);
+    const uint4 g1 = load_stream(Wg + at + d), u1 = load_stream(Wu + at + d);
+    const uint4 x0 = __ldg(xr + c), x1 = __ldg(xr + d);
+    g += dot8(g0, x0);
+    u += dot8(u0, x0);
+    if (two) {
+      g += dot8(g1, x1);
+      u += dot8(u1, x1);
     }
   }
 #pragma unroll
@@ -406,75 +417,82 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 4)
     a[static_cast<int64_t>(slot) * I + i] = g * sigmoid_fast(g) * u;
 }
 
-// y[t][h] = sum_k w_k Wd_e[h] . a[t, k], one warp per (t, h). The first 16
-// weight loads of a lane are on their way before k_token_up is waited for.
+// y[t][h] = sum_k w_k Wd_e[h] . a[t, k]: TOKEN_SPLIT warps to an (t, h), each
+// with every TOKEN_SPLIT-th slot, two at a time; their first loads are on
+// their way before k_token_up is waited for. The warps' sums are added in
+// order.
+constexpr int TOKEN_SPLIT = 4;
+constexpr int TOKEN_HS = 2;  // (t, h) of a block
+
 template <typename T>
-__global__ void __launch_bounds__(TOKEN_WARPS * 32)
+__global__ void __launch_bounds__(TOKEN_SPLIT * TOKEN_HS * 32)
     k_token_down(const float* a, const uint4* __restrict__ Wd,
                  const int32_t* __restrict__ experts,
                  const void* __restrict__ weights, int n, int K, int H, int I,
                  int E, uint16_t* __restrict__ y) {
-  __shared__ int chosen[32];
-  __shared__ float weight[32];
-  const int lane = threadIdx.x & 31;
-  const int h = blockIdx.x * TOKEN_WARPS + (threadIdx.x >> 5);
+  __shared__ float part[TOKEN_HS][TOKEN_SPLIT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = warp % TOKEN_SPLIT;
+  const int h = blockIdx.x * TOKEN_HS + warp / TOKEN_SPLIT;
   const int t = blockIdx.y;
-  if (threadIdx.x < K) {
-    const int e = expert_of(experts, n, t * K + threadIdx.x, E, nullptr);
-    chosen[threadIdx.x] = e;
-    weight[threadIdx.x] = e >= 0 ? weight_at<T>(weights, t * K + threadIdx.x)
-                                 : 0.f;
-  }
-  __syncthreads();
   const int vecs = I / 8;
   const int cols = h < H ? vecs : 0;
   float acc = 0.f;
   bool waited = false;
-  for (int k0 = 0; k0 < K; k0 += 4)
-    for (int c0 = lane; c0 - lane < vecs; c0 += 128) {
-      uint4 v[4][4];  // four slots by four columns
+  for (int k0 = sub; k0 < K; k0 += 2 * TOKEN_SPLIT) {
+    int e[2];
+    float w[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int e = k0 + k < K ? chosen[k0 + k] : -1;
+    for (int k = 0; k < 2; ++k) {
+      const int kk = k0 + k * TOKEN_SPLIT;
+      e[k] = kk < K ? expert_of(experts, n, t * K + kk, E, nullptr) : -1;
+      w[k] = e[k] >= 0 ? weight_at<T>(weights, t * K + kk) : 0.f;
+    }
+    for (int c0 = lane; c0 - lane < vecs; c0 += 128) {
+      uint4 v[2][4];  // two slots by four columns
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
         const uint4* wr =
-            Wd + (static_cast<int64_t>(e < 0 ? 0 : e) * H + h) * vecs;
+            Wd + (static_cast<int64_t>(e[k] < 0 ? 0 : e[k]) * H + h) * vecs;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          v[k][q] = e >= 0 && c0 + 32 * q < cols ? load_stream(wr + c0 + 32 * q)
-                                                 : make_uint4(0, 0, 0, 0);
+          v[k][q] = e[k] >= 0 && c0 + 32 * q < cols
+                        ? load_stream(wr + c0 + 32 * q)
+                        : make_uint4(0, 0, 0, 0);
       }
       if (!waited) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         waited = true;
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k0 + k >= K || chosen[k0 + k] < 0) continue;
-        const float* ar = a + static_cast<int64_t>(t * K + k0 + k) * I;
+      for (int k = 0; k < 2; ++k) {
+        if (e[k] < 0) continue;
+        const float* ar =
+            a + static_cast<int64_t>(t * K + k0 + k * TOKEN_SPLIT) * I;
         float s = 0.f;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (c0 + 32 * q >= cols) break;
           const float4* ap =
               reinterpret_cast<const float4*>(ar + (c0 + 32 * q) * 8);
-          const float4 lo = ap[0], hi = ap[1];
-          const uint4 w4 = v[k][q];
-          s = fmaf(__uint_as_float(w4.x << 16), lo.x, s);
-          s = fmaf(__uint_as_float(w4.x & 0xffff0000u), lo.y, s);
-          s = fmaf(__uint_as_float(w4.y << 16), lo.z, s);
-          s = fmaf(__uint_as_float(w4.y & 0xffff0000u), lo.w, s);
-          s = fmaf(__uint_as_float(w4.z << 16), hi.x, s);
-          s = fmaf(__uint_as_float(w4.z & 0xffff0000u), hi.y, s);
-          s = fmaf(__uint_as_float(w4.w << 16), hi.z, s);
-          s = fmaf(__uint_as_float(w4.w & 0xffff0000u), hi.w, s);
+          s += dot8(v[k][q], ap[0], ap[1]);
         }
-        acc = fmaf(weight[k0 + k], s, acc);
+        acc = fmaf(w[k], s, acc);
       }
     }
+  }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(FULL, acc, o);
-  if (h < H && lane == 0)
-    y[static_cast<int64_t>(t) * H + h] = to_bf16_bits(acc);
+  if (lane == 0) part[warp / TOKEN_SPLIT][sub] = acc;
+  __syncthreads();
+  if (threadIdx.x < TOKEN_HS) {
+    const int out = blockIdx.x * TOKEN_HS + threadIdx.x;
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < TOKEN_SPLIT; ++q) sum += part[threadIdx.x][q];
+    if (out < H) y[static_cast<int64_t>(t) * H + out] = to_bf16_bits(sum);
+  }
 }
 
 template <typename T>
@@ -600,10 +618,10 @@ cudaError_t launch_token(const void* x, const void* Wg, const void* Wu,
   auto kern = wdt == LCE_F32 ? k_token_down<float> : k_token_down<__nv_bfloat16>;
   return launch_early(
       kern,
-      dim3(static_cast<unsigned>(ceil_div(H, TOKEN_WARPS)),
+      dim3(static_cast<unsigned>(ceil_div(H, TOKEN_HS)),
            static_cast<unsigned>(L)),
-      TOKEN_WARPS * 32, 0, s, a, static_cast<const uint4*>(Wd), experts,
-      weights, n, K, h, i, E, static_cast<uint16_t*>(y));
+      TOKEN_SPLIT * TOKEN_HS * 32, 0, s, a, static_cast<const uint4*>(Wd),
+      experts, weights, n, K, h, i, E, static_cast<uint16_t*>(y));
 }
 
 cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,
