@@ -34,15 +34,19 @@ __device__ __forceinline__ void load_slots(const int32_t* experts, int64_t n,
     e[q] = expert_of(experts, n, i0 + 32 * q + lane, E, err);
 }
 
-// Counts a warp's slots into cnt[expert].
+// Counts a warp's slots into cnt[expert]; same[q] gets the lanes whose slot q
+// goes to this lane's expert.
 template <int ITEMS>
-__device__ __forceinline__ void count_slots(const int (&e)[ITEMS], int* cnt) {
+__device__ __forceinline__ void count_slots(const int (&e)[ITEMS],
+                                            unsigned (&same)[ITEMS],
+                                            int* cnt) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
+  for (int q = 0; q < ITEMS; ++q) same[q] = __match_any_sync(FULL, e[q]);
+#pragma unroll
   for (int q = 0; q < ITEMS; ++q) {
-    const unsigned same = __match_any_sync(FULL, e[q]);
-    if (e[q] >= 0 && (same & ((1u << lane) - 1u)) == 0u)
-      cnt[e[q]] += __popc(same);
+    if (e[q] >= 0 && (same[q] & ((1u << lane) - 1u)) == 0u)
+      cnt[e[q]] += __popc(same[q]);
     __syncwarp();
   }
 }
@@ -50,15 +54,15 @@ __device__ __forceinline__ void count_slots(const int (&e)[ITEMS], int* cnt) {
 // Gives a warp's slots their rows, in slot order; cnt[e] holds the position
 // in its segment of the warp's next slot of e.
 template <int ITEMS>
-__device__ __forceinline__ void place_slots(const int (&e)[ITEMS], int64_t n,
-                                            int64_t i0, int* cnt,
+__device__ __forceinline__ void place_slots(const int (&e)[ITEMS],
+                                            const unsigned (&same)[ITEMS],
+                                            int64_t n, int64_t i0, int* cnt,
                                             const int* start, const Plan& p) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int q = 0; q < ITEMS; ++q) {
     const int64_t i = i0 + 32 * q + lane;
-    const unsigned same = __match_any_sync(FULL, e[q]);
-    const int before = __popc(same & ((1u << lane) - 1u));
+    const int before = __popc(same[q] & ((1u << lane) - 1u));
     int at = 0;
     if (e[q] >= 0) at = cnt[e[q]];
     __syncwarp();
@@ -66,7 +70,7 @@ __device__ __forceinline__ void place_slots(const int (&e)[ITEMS], int64_t n,
       const int r = start[e[q]] + at + before;
       p.slot[r] = static_cast<int>(i);
       p.row[i] = r;
-      if (before == 0) cnt[e[q]] = at + __popc(same);
+      if (before == 0) cnt[e[q]] = at + __popc(same[q]);
     } else if (i < n) {
       p.row[i] = -1;
     }
@@ -140,10 +144,11 @@ __global__ void __launch_bounds__(1024)
   const int warp = threadIdx.x >> 5;
   const int i0 = warp * 32 * ITEMS;
   int e[ITEMS];
+  unsigned same[ITEMS];
   if (warp < workers) load_slots<ITEMS>(experts, n, i0, E, e, err);
   for (int i = threadIdx.x; i < workers * E; i += blockDim.x) cnt[i] = 0;
   __syncthreads();
-  if (warp < workers) count_slots<ITEMS>(e, cnt + warp * E);
+  if (warp < workers) count_slots<ITEMS>(e, same, cnt + warp * E);
   __syncthreads();
   int total = 0;
   if (threadIdx.x < E)
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(1024)
   lay_out(total, E, tile_m, p, start, totals);
   __syncthreads();
   if (warp < workers)
-    place_slots<ITEMS>(e, n, i0, cnt + warp * E, start, p);
+    place_slots<ITEMS>(e, same, n, i0, cnt + warp * E, start, p);
 }
 
 constexpr int CHUNK_WARPS = 8;
@@ -184,16 +189,17 @@ __global__ void __launch_bounds__(1024) k_plan_layout(int E, int chunks,
   __shared__ int start[MAX_EXPERTS], cnt[MAX_EXPERTS];
   begin_early();
   const int lane = threadIdx.x & 31;
-  for (int e = threadIdx.x >> 5; e < E; e += 32) {
-    int* h = p.hist + static_cast<int64_t>(e) * chunks;
-    int before = 0;
-    for (int c0 = 0; c0 < chunks; c0 += 128) {
+  // four experts to a warp at a time, so that their loads overlap
+  for (int e0 = (threadIdx.x >> 5) * 4; e0 < E; e0 += 128) {
+    int before[4] = {0, 0, 0, 0};
+    for (int c0 = 0; c0 < chunks; c0 += 32) {
+      const int at = c0 + lane;
       int c[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = c0 + 32 * q + lane;
-        c[q] = at < chunks ? h[at] : 0;
-      }
+      for (int q = 0; q < 4; ++q)
+        c[q] = e0 + q < E && at < chunks
+                   ? p.hist[static_cast<int64_t>(e0 + q) * chunks + at]
+                   : 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         int r = c[q];
@@ -202,12 +208,16 @@ __global__ void __launch_bounds__(1024) k_plan_layout(int E, int chunks,
           const int a = __shfl_up_sync(FULL, r, o);
           if (lane >= o) r += a;
         }
-        const int at = c0 + 32 * q + lane;
-        if (at < chunks) h[at] = before + r - c[q];
-        before += __shfl_sync(FULL, r, 31);
+        if (e0 + q < E && at < chunks)
+          p.hist[static_cast<int64_t>(e0 + q) * chunks + at] =
+              before[q] + r - c[q];
+        before[q] += __shfl_sync(FULL, r, 31);
       }
     }
-    if (lane == 0) cnt[e] = before;
+    if (lane == 0)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (e0 + q < E) cnt[e0 + q] = before[q];
   }
   __syncthreads();
   const int c = threadIdx.x < E ? cnt[threadIdx.x] : 0;
@@ -226,10 +236,11 @@ __global__ void __launch_bounds__(CHUNK_WARPS * 32)
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * PLAN_CHUNK +
                      warp * (32 * ITEMS);
   int mine[ITEMS];
+  unsigned same[ITEMS];
   load_slots<ITEMS>(experts, n, i0, E, mine, nullptr);
   __syncthreads();
   begin_early();
-  count_slots<ITEMS>(mine, cnt + warp * E);
+  count_slots<ITEMS>(mine, same, cnt + warp * E);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int before = p.hist[static_cast<int64_t>(e) * chunks + blockIdx.x];
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(CHUNK_WARPS * 32)
     start[e] = p.seg[e].x;
   }
   __syncthreads();
-  place_slots<ITEMS>(mine, n, i0, cnt + warp * E, start, p);
+  place_slots<ITEMS>(mine, same, n, i0, cnt + warp * E, start, p);
 }
 
 // Eight columns of a token per thread (threads x: columns, y: tokens): read
