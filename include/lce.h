@@ -36,8 +36,8 @@
  *     Calls are asynchronous on that stream; none synchronises the host,
  *     except lce_get_error.
  *   - Argument errors are returned synchronously, before anything is
- *     queued. Errors found on the device (a label out of range, a bounded
- *     wait that expired) set the library's device error word, read by
+ *     queued. Errors found on the device (a label or an expert index out of
+ *     range, a bounded wait that expired) set the library's device error word, read by
  *     lce_get_error; the kernels never trap.
  *   - Inputs of dtype LCE_F32 are rounded to bf16 on the device (into the
  *     workspace) before the tensor-core contractions; accumulation is fp32.
@@ -425,9 +425,10 @@ lce_status lce_combine_shards(const double* sums, const int64_t* n_local,
 
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
- * current device. Returns LCE_ERR_TIMEOUT or LCE_ERR_LABEL_RANGE if a kernel
- * raised one since the last call (timeout first), LCE_ERR_CUDA if the
- * synchronisation failed, else LCE_OK. The word is shared by all streams of
+ * current device. Returns LCE_ERR_TIMEOUT, LCE_ERR_LABEL_RANGE or
+ * LCE_ERR_EXPERT_RANGE if a kernel raised one since the last call (the first
+ * of them in this order), LCE_ERR_CUDA if the synchronisation failed, else
+ * LCE_OK. The word is shared by all streams of
  * the device.
  */
 lce_status lce_get_error(void* stream);
@@ -616,8 +617,13 @@ lce_status lce_route_backward(const void* logits, lce_dtype dt,
  * H % 8 == 0, I % 8 == 0, 1 <= E <= 1024, 1 <= top_k <= 32, L top_k <= 2^30.
  * L = 0: nothing to do forward, zero weight gradients backward.
  * Accumulation is fp32; a (and dg, du, w a) are rounded to bf16 between the
- * contractions, the sum over a token's slots is rounded once. Results do not
- * depend on the order of execution (no floating-point atomics).
+ * contractions, a slot's contribution to y or dx to 2^-12 of itself (fp16
+ * under a power of two per row and 128 columns), and the sum over a token's
+ * slots, in fp32 and in slot order, once to bf16. dweights comes from unrounded
+ * g, u and da'. Results do not depend on the order of execution (no
+ * floating-point atomics).
+ * Few slots (at most 64, hardly any two on one expert) are computed slot by
+ * slot without a grouped contraction, a in fp32.
  */
 size_t lce_experts_workspace_size(int64_t L, int64_t H, int64_t I, int64_t E,
                                   int64_t top_k, int backward);

@@ -288,3 +288,53 @@ def test_rows_past_32_bit_offsets():
     want = ref.experts_mlp(*args, e[at].cpu().numpy(), to64(x[at]))
     assert rel_fro(to64(y[at]), want[0]) <= 2 * R
     assert rel_fro(to64(dx[at]), want[1]) <= 2 * R
+
+
+def test_layer_captured_with_its_backward():
+    """Router, experts and their gradients through autograd inside a captured
+    graph; the replay gives the eager gradients' bits. (The eager graph is
+    freed first: while one is alive, torch keeps the leaves' accumulation on
+    the stream it was built on, and no captured backward may depend on it.)"""
+    import chunked_lm_head_gemm_gb300 as lce
+    dev = require_gpu()
+    (x, Wg, Wu, Wd, _, _), dy = draw(dev, 300, 128, 136, 8, 2, seed=12)
+    z = torch.randn(300, 8, device=dev)
+    leaves = [t.requires_grad_(True) for t in (x, Wg, Wu, Wd, z)]
+
+    def layer():
+        w, e = lce.route_experts(leaves[4], 2)
+        return lce.experts_mlp(*leaves[:4], w, e)
+    y = layer()
+    want = torch.autograd.grad(y, leaves, dy)
+    y_want = y.detach()
+    del y
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(layer(), leaves, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer()
+        grads = torch.autograd.grad(y, leaves, dy)
+    graph.replay()
+    assert torch.equal(y, y_want)
+    for a, b in zip(grads, want):
+        assert torch.equal(a, b)
+    assert lce.get_error() == 0
+
+
+def test_example_step():
+    """examples/sparse_mlp_step.py: router, experts and the head's loss train
+    together."""
+    import importlib.util
+    import os
+    require_gpu()
+    path = os.path.join(os.path.dirname(os.path.dirname(
+        os.path.abspath(__file__))), "examples", "sparse_mlp_step.py")
+    spec = importlib.util.spec_from_file_location("sparse_mlp_step", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses = mod.run(steps=6)
+    assert len(losses) == 6 and all(math.isfinite(v) for v in losses)
+    assert losses[-1] < losses[0]
