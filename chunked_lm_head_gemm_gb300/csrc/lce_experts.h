@@ -33,10 +33,10 @@ struct PlanHead {
   int rows;   // padded rows
 };
 
-// A row tile: `rows` padded rows (at most 128, or 256 on CTA pairs) from row0
-// of one expert.
+// What a row tile (of at most tile_m rows) knows of its expert: the first of
+// the expert's tiles, and its segment's first row and padded rows.
 struct RowTile {
-  int expert, row0, rows, pad;
+  int expert, first, row0, rows;
 };
 
 // The plan, in device memory.

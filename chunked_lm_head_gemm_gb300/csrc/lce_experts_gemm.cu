@@ -14,13 +14,20 @@
 // TMA instead (four rows to an instruction, one instruction to a lane) needs
 // no copy but held every contraction to 37 ns an instruction per SM, 32 of
 // them a stage: UP ran at 540 TFLOP/s (L = 32768, H = 2048, I = 768, E = 128,
-// top 8), from copies at 1690.
+// top 8), from copies at 1690; gathering by the threads (16-byte asynchronous
+// copies of four warps, three stages ahead) at 418.
 //
 // Work: units are 128 x 256 output tiles (UP and DGU 128 x 128 of a, whose
 // accumulator columns are g | u), walked in a static stride by one CTA per
-// SM with the roles of k_gemm: producer warp, MMA lane, four epilogue warps;
-// or 256 x 256 tiles by CTA pairs (PAIR). A unit's accumulation is split into parts, each with its own columns,
-// number of buffers and K loop.
+// SM with the roles of k_gemm: producer warp, MMA lane, epilogue warps; or 256
+// x 256 tiles by CTA pairs (PAIR). A unit's accumulation is split into parts,
+// each with its own columns, number of buffers and K loop.
+//
+// Bound, at L = 32768, H = 2048, I = 768, E = 128, top 8: UP runs at the
+// tensor cores' rate (1690 TFLOP/s, 82% of the pipe's cycles); the others at
+// what L2 gives the SMs, 16 to 18.6 TB/s in each of them, for an operand
+// tile of 32 KB a K block and CTA: DOWN 1440 (K = 768), DX 1520, DGU 1344 (its
+// da' part has half the columns for the same rows), GRAD 1590 TFLOP/s.
 #include <cuda_fp16.h>
 
 #include "lce_device.cuh"
@@ -121,19 +128,33 @@ __device__ __forceinline__ void load_cols_of(uint32_t dst,
 }
 
 // ---- the uses ----------------------------------------------------------------
+constexpr int GROUP_N = 8;
+
 struct RowUnits {
   __device__ static int units(const Geom& g) {
     return g.head->tiles * g.num_n;
   }
+  // An expert's units in groups of GROUP_N column tiles, its row tiles inside
+  // a group: what runs at once then reads some 8 panels of weights and 10 of
+  // rows, where a row tile after the other would stream all of a wide
+  // expert's weights once per row tile. L = 8192, H = 4096, I = 8192, E = 8,
+  // top 2 (134 MB of Wg_e and Wu_e): UP 1386 -> 1202 us.
   __device__ static Unit unit(const Geom& g, int u) {
-    const int t = u / g.num_n;
-    const int4 r = reinterpret_cast<const int4*>(g.tile)[t];
-    return Unit{r.x,
-                r.y + g.rank * BM,
-                min(max(r.z - g.rank * BM, 0), BM),
-                r.z,
-                t,
-                u - t * g.num_n,
+    const int4 x = reinterpret_cast<const int4*>(g.tile)[u / g.num_n];
+    const int first = x.y, row0 = x.z, rows = x.w;
+    const int tiles = (rows + g.tile_m - 1) / g.tile_m;
+    const int r = u - first * g.num_n;
+    const int n0 = r / (tiles * GROUP_N) * GROUP_N;
+    const int in = r - n0 * tiles;
+    const int width = min(GROUP_N, g.num_n - n0);
+    const int m = in / width;
+    const int both = min(g.tile_m, rows - m * g.tile_m);
+    return Unit{x.x,
+                row0 + m * g.tile_m + g.rank * BM,
+                min(max(both - g.rank * BM, 0), BM),
+                both,
+                m,
+                n0 + in - m * width,
                 0};
   }
 };
@@ -281,9 +302,8 @@ struct OpGrad : GradUnits {
 // ---- epilogues ---------------------------------------------------------------
 // Each runs on a warp's 32 rows and its half of the columns of a finished
 // unit (eight epilogue warps: two to each lane quarter of tensor memory;
-// taddr is the quarter). Four warps, one to a quarter, left DGU waiting: with
-// eight DGU 1906 -> DGU8 us, DOWN 596 -> DOWN8 us, DWD 600 -> DWD8 us (L =
-// 32768, H = 2048, I = 768, E = 128, top 8).
+// taddr is the quarter). Against four warps DGU 1906 -> 1873 us, dWd 600 ->
+// 582 us (L = 32768, H = 2048, I = 768, E = 128, top 8).
 
 // a = silu(g) u in bf16.
 struct EpiUp : EpiBase {

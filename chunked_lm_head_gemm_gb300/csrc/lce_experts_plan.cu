@@ -117,9 +117,8 @@ __device__ __forceinline__ void lay_out(int c, int E, int tile_m,
     start[e] = row0;
     cnt[e] = c;
     p.seg[e] = make_int2(row0, rows);
-    int at = t - tiles;
-    for (int q = 0; q < rows; q += tile_m)
-      p.tile[at++] = RowTile{e, row0 + q, min(tile_m, rows - q), 0};
+    for (int q = 0; q < tiles; ++q)
+      p.tile[t - tiles + q] = RowTile{e, t - tiles, row0, rows};
     if (e == E - 1) *p.head = PlanHead{t, r};
   }
   __syncthreads();
