@@ -305,15 +305,39 @@ struct OpGrad : GradUnits {
 // taddr is the quarter). Against four warps DGU 1906 -> 1873 us, dWd 600 ->
 // 582 us (L = 32768, H = 2048, I = 768, E = 128, top 8).
 
+// A unit's accumulators go back to the MMA as soon as the warp has read them
+// (release(), once per unit), before the last values are worked on and stored.
+template <int PARTS, bool PAIR>
+struct Release {
+  uint32_t bar0, bar1;
+  bool done;
+  __device__ __forceinline__ void operator()() {
+    if (done) return;
+    done = true;
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31u) == 0) {
+      if (PAIR) {
+        mbar_arrive_cluster(mapa_shared(bar0, 0));
+        if (PARTS == 2) mbar_arrive_cluster(mapa_shared(bar1, 0));
+      } else {
+        mbar_arrive(bar0);
+        if (PARTS == 2) mbar_arrive(bar1);
+      }
+    }
+  }
+};
+
 // a = silu(g) u in bf16.
 struct EpiUp : EpiBase {
   struct Params {
     int unused;
   };
+  template <class R>
   __device__ __forceinline__ void tile(const Params&, const Maps& m,
                                        const Geom& g, const Unit& u,
                                        uint32_t taddr, int r, int half,
-                                       int i) {
+                                       int i, R& release) {
     const int wr = r & ~31;
     if (wr >= u.rows) return;
     const uint32_t t0 = taddr + (i & 1) * 256;
@@ -324,6 +348,7 @@ struct EpiUp : EpiBase {
       float gv[32], uv[32];
       tmem_ld32(t0 + c * 32, gv);
       tmem_ld32(t0 + 128 + c * 32, uv);
+      if (c == 2 * half + 1) release();
 #pragma unroll
       for (int k = 0; k < 32; ++k) uv[k] *= gv[k] * sigmoid_fast(gv[k]);
       store_box(uv, j0, u.row0 + wr, &m.s0);
@@ -343,10 +368,11 @@ struct EpiRows : EpiBase {
   struct Params {
     float* scale;  // [max_rows][2 num_n]
   };
+  template <class R>
   __device__ __forceinline__ void tile(const Params& p, const Maps& m,
                                        const Geom& g, const Unit& u,
                                        uint32_t taddr, int r, int half,
-                                       int i) {
+                                       int i, R& release) {
     const int wr = r & ~31;
     if (wr >= u.rows) return;
     const int c0 = u.n * 256 + half * 128;
@@ -356,6 +382,7 @@ struct EpiRows : EpiBase {
     float v[2][64];  // columns past H are zero
     tmem_ld64(t0, v[0]);
     tmem_ld64(t0 + 64, v[1]);
+    release();
     float mx = 0.f;
 #pragma unroll
     for (int k = 0; k < 64; ++k)
@@ -403,10 +430,11 @@ struct EpiDgu : EpiBase {
     float* part;
     int64_t stride;
   };
+  template <class R>
   __device__ __forceinline__ void tile(const Params& p, const Maps& m,
                                        const Geom& g, const Unit& u,
                                        uint32_t taddr, int r, int half,
-                                       int i) {
+                                       int i, R& release) {
     const int wr = r & ~31;
     if (wr >= u.rows) return;
     const int slot = g.slot[u.row0 + r];
@@ -425,6 +453,7 @@ struct EpiDgu : EpiBase {
       tmem_ld32(taddr + c * 32, gv);
       tmem_ld32(taddr + 128 + c * 32, uv);
       tmem_ld32(tda + c * 32, da);
+      if (c == 2 * half + 1) release();
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         const float s = sigmoid_fast(gv[k]);
@@ -483,10 +512,11 @@ struct EpiWeights : EpiBase {
     ++nstored;
   }
 
+  template <class R>
   __device__ __forceinline__ void tile(const Params& p, const Maps& m,
                                        const Geom& g, const Unit& u,
                                        uint32_t taddr, int r, int half,
-                                       int i) {
+                                       int i, R& release) {
     float* base = p.out[u.which];
     const CUtensorMap* map =
         u.which == 0 ? &m.s0 : u.which == 1 ? &m.s1 : &m.s2;
@@ -502,6 +532,7 @@ struct EpiWeights : EpiBase {
       float v[32];
       if (u.rows > 0) {
         tmem_ld32(taddr + (i & 1) * 256 + c * 32, v);
+        if (c == 4 * half + 3) release();
       } else {
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = 0.f;
@@ -752,23 +783,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool got = mbar_wait(bars.tfull(i & 1), (i >> 1) & 1, ctx, true);
       if (!__all_sync(FULL, got)) break;
       tc_fence_after();
+      Release<Op::PARTS, PAIR> release{
+          bars.tempty(0, Op::P0::BUFS == 2 ? (i & 1) : 0),
+          bars.tempty(1, Op::P1::BUFS == 2 ? (i & 1) : 0), false};
       epi.tile(p, maps, g, t, tmem + (static_cast<uint32_t>(q * 32) << 16), r,
-               half, i);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        const uint32_t b0 =
-            bars.tempty(0, Op::P0::BUFS == 2 ? (i & 1) : 0);
-        const uint32_t b1 =
-            bars.tempty(1, Op::P1::BUFS == 2 ? (i & 1) : 0);
-        if (PAIR) {
-          mbar_arrive_cluster(mapa_shared(b0, 0));
-          if (Op::PARTS == 2) mbar_arrive_cluster(mapa_shared(b1, 0));
-        } else {
-          mbar_arrive(b0);
-          if (Op::PARTS == 2) mbar_arrive(b1);
-        }
-      }
+               half, i, release);
+      release();
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
