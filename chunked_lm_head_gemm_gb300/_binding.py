@@ -820,7 +820,7 @@ def route_forward(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
         raise ValueError("bias must be a contiguous CUDA float32 [E] tensor")
     shape = (L, max(top_k, 0))
     weights = (weights_out if weights_out is not None
-               else logits.new_empty(shape))
+               else torch.empty(shape, dtype=logits.dtype, device=dev))
     experts = (experts_out if experts_out is not None
                else torch.empty(shape, dtype=torch.int32, device=dev))
     st = lib.lce_route_forward(logits.data_ptr(), code, _ptr(bias), L, E,
