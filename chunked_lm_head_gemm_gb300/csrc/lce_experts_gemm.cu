@@ -517,7 +517,7 @@ struct EpiWeights : EpiBase {
                                        const Geom& g, const Unit& u,
                                        uint32_t taddr, int r, int half,
                                        int i, R& release) {
-    float* base = p.out[u.which];
+    float* base = u.which == 0 ? p.out[0] : u.which == 1 ? p.out[1] : p.out[2];
     const CUtensorMap* map =
         u.which == 0 ? &m.s0 : u.which == 1 ? &m.s1 : &m.s2;
     const int rows = u.which == 0 ? g.H : g.I;
