@@ -63,12 +63,19 @@ cudaError_t launch_gather(const Plan& p, int64_t L, int K, int E, int64_t H,
                           uint16_t* out_y, bool zero, cudaStream_t s);
 
 // out[t][:] = sum_k w[t][k] rows[row(t, k)][:] in bf16, k in order, dropped
-// slots left out (w NULL: weights 1). rows: fp16 times the scale of each row
-// and 128 columns.
+// slots left out. rows: fp16 times the scale of each row and 128 columns.
 cudaError_t launch_combine(const uint16_t* rows, const float* scale,
                            const int* row, const void* w, lce_dtype wdt,
                            int64_t L, int K, int64_t H, void* out,
                            cudaStream_t s);
+// The backward's sums, in one launch: dx likewise with weights 1 (NULL: none),
+// and dweights[slot] = sum over the column pieces of part[piece][row], in order
+// (NULL: none).
+cudaError_t launch_backward_sums(const uint16_t* rows, const float* scale,
+                                 const int* row, int64_t L, int K, int64_t H,
+                                 void* dx, const float* part, int64_t stride,
+                                 int pieces, lce_dtype wdt, void* dweights,
+                                 cudaStream_t s);
 
 // The forward of few slots without a plan (a: fp32 [L K][I] scratch).
 cudaError_t launch_token(const void* x, const void* Wg, const void* Wu,
@@ -76,11 +83,6 @@ cudaError_t launch_token(const void* x, const void* Wg, const void* Wu,
                          const int32_t* experts, int64_t L, int K, int64_t H,
                          int64_t I, int E, float* a, void* y, unsigned* err,
                          cudaStream_t s);
-
-// dweights[slot] = sum over the column pieces of part[piece][row], in order.
-cudaError_t launch_dweights(const float* part, int64_t stride, int pieces,
-                            const int* row, int64_t n, lce_dtype wdt,
-                            void* dweights, cudaStream_t s);
 
 // ---- grouped contractions ----------------------------------------------------
 struct ExpertsArgs {

@@ -264,23 +264,18 @@ lce_status lce_experts_backward(const void* x, const void* Wg, const void* Wu,
   LCE_TRY(make_plan(z, experts, x, dy, a, s));
   LCE_TRY(timed(LCE_K_EXPERTS_DGU, 3 * slot_flops, s,
                 [&] { return launch_experts_dgu(a, s); }));
-  if (dweights)
-    LCE_TRY(timed(LCE_K_EXPERTS_COMBINE, 0, s, [&] {
-      return cuda_try(
-          launch_dweights(a.part, a.max_rows,
-                          2 * static_cast<int>(ceil_div(I, 128)), a.plan.row,
-                          L * top_k, weights_dt, dweights, s),
-          "experts_dweights");
-    }));
-  if (dx) {
+  if (dx)
     LCE_TRY(timed(LCE_K_EXPERTS_DX, 2 * slot_flops, s,
                   [&] { return launch_experts_dx(a, s); }));
+  if (dx || dweights)
     LCE_TRY(timed(LCE_K_EXPERTS_COMBINE, 0, s, [&] {
-      return cuda_try(launch_combine(a.rows_out, a.rows_scale, a.plan.row,
-                                     nullptr, LCE_F32, L, K, H, dx, s),
-                      "experts_combine");
+      return cuda_try(
+          launch_backward_sums(a.rows_out, a.rows_scale, a.plan.row, L, K, H,
+                               dx, a.part, a.max_rows,
+                               2 * static_cast<int>(ceil_div(I, 128)),
+                               weights_dt, dweights, s),
+          "experts_combine");
     }));
-  }
   if (dWd || dWg) {
     a.dWg = dWg;
     a.dWu = dWu;

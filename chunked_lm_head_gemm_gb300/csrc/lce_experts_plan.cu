@@ -295,14 +295,47 @@ __device__ __forceinline__ float weight_at(const void* w, int64_t i) {
   return static_cast<float>(static_cast<const T*>(w)[i]);
 }
 
+// The routing weights' gradients: a slot's column pieces, in order.
+struct DweightsArgs {
+  const float* part;  // [pieces][stride]
+  int64_t stride, n;
+  int pieces;
+  const int* row;
+  void* out;          // NULL: none
+  int f32;
+};
+__device__ __forceinline__ void sum_dweights(const DweightsArgs& d, int64_t i) {
+  if (i >= d.n) return;
+  const int r = d.row[i];
+  float sum = 0.f;
+  if (r >= 0)
+    for (int t = 0; t < d.pieces; ++t) sum += d.part[t * d.stride + r];
+  if (d.f32)
+    static_cast<float*>(d.out)[i] = sum;
+  else
+    static_cast<__nv_bfloat16*>(d.out)[i] = __float2bfloat16_rn(sum);
+}
+
+__global__ void __launch_bounds__(256) k_dweights(const DweightsArgs d) {
+  begin_early();
+  sum_dweights(d, blockIdx.x * static_cast<int64_t>(256) + threadIdx.x);
+}
+
 // Eight columns of a token per thread (threads x: columns, y: tokens); a
 // token's rows are added in fp32 in the order of its slots, KB loads in
-// flight. Bound by the rows' bytes.
+// flight. Bound by the rows' bytes. Further blocks sum dweights, if wanted.
 template <typename T, bool WEIGHTED, int KB>
 __global__ void __launch_bounds__(256)
     k_combine(const uint16_t* rows, const float* scale, const int* row,
-              const void* w, int64_t L, int K, int H, uint16_t* out) {
+              const void* w, int64_t L, int K, int H, uint16_t* out,
+              unsigned token_blocks, const DweightsArgs d) {
   begin_early();
+  if (blockIdx.x >= token_blocks) {  // the blocks past the tokens'
+    if (blockIdx.y == 0)
+      sum_dweights(d, (blockIdx.x - token_blocks) * static_cast<int64_t>(256) +
+                          threadIdx.y * blockDim.x + threadIdx.x);
+    return;
+  }
   const int64_t t =
       blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y;
   const int h = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
@@ -505,20 +538,6 @@ __global__ void __launch_bounds__(TOKEN_SPLIT * TOKEN_HS * 32)
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256)
-    k_dweights(const float* part, int64_t stride, int tiles, const int* row,
-               int64_t n, T* out) {
-  begin_early();
-  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (i >= n) return;
-  const int r = row[i];
-  float sum = 0.f;
-  if (r >= 0)
-    for (int t = 0; t < tiles; ++t) sum += part[t * stride + r];
-  out[i] = static_cast<T>(sum);
-}
-
 cudaError_t allow_smem(const void* kernel, size_t bytes) {
   if (bytes <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kernel,
@@ -587,15 +606,18 @@ namespace {
 template <typename T, bool WEIGHTED>
 cudaError_t launch_combine_t(const uint16_t* rows, const float* scale,
                              const int* row, const void* w, int64_t L, int K,
-                             int64_t H, uint16_t* out, cudaStream_t s) {
+                             int64_t H, uint16_t* out, const DweightsArgs& d,
+                             cudaStream_t s) {
   const dim3 block = row_block(H);
-  const dim3 grid(static_cast<unsigned>(ceil_div(L, block.y)),
+  const unsigned tokens = static_cast<unsigned>(ceil_div(L, block.y));
+  const unsigned more = d.out ? static_cast<unsigned>(ceil_div(d.n, 256)) : 0u;
+  const dim3 grid(tokens + more,
                   static_cast<unsigned>(ceil_div(H, block.x * 8)));
   auto kern = K <= 2   ? k_combine<T, WEIGHTED, 2>
               : K <= 4 ? k_combine<T, WEIGHTED, 4>
                        : k_combine<T, WEIGHTED, 8>;
   return launch_early(kern, grid, block, 0, s, rows, scale, row, w, L, K,
-                      static_cast<int>(H), out);
+                      static_cast<int>(H), out, tokens, d);
 }
 }  // namespace
 
@@ -604,12 +626,26 @@ cudaError_t launch_combine(const uint16_t* rows, const float* scale,
                            int64_t L, int K, int64_t H, void* out,
                            cudaStream_t s) {
   uint16_t* o = static_cast<uint16_t*>(out);
-  if (!w)
-    return launch_combine_t<float, false>(rows, scale, row, w, L, K, H, o, s);
   if (wdt == LCE_F32)
-    return launch_combine_t<float, true>(rows, scale, row, w, L, K, H, o, s);
+    return launch_combine_t<float, true>(rows, scale, row, w, L, K, H, o, {},
+                                         s);
   return launch_combine_t<__nv_bfloat16, true>(rows, scale, row, w, L, K, H, o,
-                                               s);
+                                               {}, s);
+}
+
+cudaError_t launch_backward_sums(const uint16_t* rows, const float* scale,
+                                 const int* row, int64_t L, int K, int64_t H,
+                                 void* dx, const float* part, int64_t stride,
+                                 int pieces, lce_dtype wdt, void* dweights,
+                                 cudaStream_t s) {
+  const DweightsArgs d{part, stride, L * K, pieces, row, dweights,
+                       wdt == LCE_F32};
+  if (dx)
+    return launch_combine_t<float, false>(rows, scale, row, nullptr, L, K, H,
+                                          static_cast<uint16_t*>(dx), d, s);
+  if (!dweights) return cudaSuccess;
+  return launch_early(k_dweights, static_cast<unsigned>(ceil_div(d.n, 256)),
+                      256, 0, s, d);
 }
 
 cudaError_t launch_token(const void* x, const void* Wg, const void* Wu,
@@ -632,17 +668,6 @@ cudaError_t launch_token(const void* x, const void* Wg, const void* Wu,
            static_cast<unsigned>(L)),
       TOKEN_SPLIT * TOKEN_HS * 32, 0, s, a, static_cast<const uint4*>(Wd),
       experts, weights, n, K, h, i, E, static_cast<uint16_t*>(y));
-}
-
-cudaError_t launch_dweights(const float* part, int64_t stride, int tiles,
-                            const int* row, int64_t n, lce_dtype wdt,
-                            void* dweights, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(ceil_div(n, 256));
-  if (wdt == LCE_F32)
-    return launch_early(k_dweights<float>, grid, 256, 0, s, part, stride,
-                        tiles, row, n, static_cast<float*>(dweights));
-  return launch_early(k_dweights<__nv_bfloat16>, grid, 256, 0, s, part, stride,
-                      tiles, row, n, static_cast<__nv_bfloat16*>(dweights));
 }
 
 }  // namespace lce
