@@ -135,12 +135,6 @@ ExpertsArgs arguments(const Sizes& z, const Layout& w, uint8_t* ws,
   return a;
 }
 
-#define LCE_TRY(call)              \
-  do {                             \
-    const lce_status st_ = (call); \
-    if (st_ != LCE_OK) return st_; \
-  } while (0)
-
 lce_status cuda_try(cudaError_t e, const char* where) {
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, where);
 }

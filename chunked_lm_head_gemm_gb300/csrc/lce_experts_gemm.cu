@@ -869,12 +869,6 @@ lce_status launch(const char* what, const Maps& m, const Geom& g,
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, what);
 }
 
-#define LCE_TRY(call)                       \
-  do {                                      \
-    const lce_status st_ = (call);          \
-    if (st_ != LCE_OK) return st_;          \
-  } while (0)
-
 }  // namespace
 
 lce_status launch_experts_up(const ExpertsArgs& a, cudaStream_t s) {

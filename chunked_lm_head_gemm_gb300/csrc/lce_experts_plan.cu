@@ -90,7 +90,7 @@ __device__ __forceinline__ int tiles_of(int c, int tile_m) {
 // each segment's row, cnt[] (shared) the counts.
 __device__ __forceinline__ void lay_out(int c, int E, int tile_m,
                                         const Plan& p, int* start, int* cnt) {
-  __shared__ int warp_rows[32], warp_tiles[32];
+  __shared__ int warp_rows[32], warp_tiles[32], first_tile[MAX_EXPERTS];
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   if (e >= E) c = 0;
   const int rows = padded(c), tiles = tiles_of(c, tile_m);
@@ -116,20 +116,21 @@ __device__ __forceinline__ void lay_out(int c, int E, int tile_m,
     const int row0 = r - rows;
     start[e] = row0;
     cnt[e] = c;
+    first_tile[e] = t - tiles;
     p.seg[e] = make_int2(row0, rows);
-    for (int q = 0; q < tiles; ++q)
-      p.tile[t - tiles + q] = RowTile{e, t - tiles, row0, rows};
     if (e == E - 1) *p.head = PlanHead{t, r};
   }
   __syncthreads();
-  // padding rows: a warp to an expert, so that the stores are contiguous
+  // tiles and padding rows: a warp to an expert, its stores contiguous
   for (int x = warp; x < E; x += 32) {
-    const int n = cnt[x];
-    for (int q = n + lane; q < padded(n); q += 32) p.slot[start[x] + q] = -1;
+    const int n = cnt[x], end = padded(n), first = first_tile[x];
+    for (int q = lane; q < tiles_of(n, tile_m); q += 32)
+      p.tile[first + q] = RowTile{x, first, start[x], end};
+    for (int q = n + lane; q < end; q += 32) p.slot[start[x] + q] = -1;
   }
 }
 
-// Few slots: the whole plan in one block (a launch instead of four). Each of
+// Few slots: the whole plan in one block (a launch instead of three). Each of
 // `workers` warps takes 32 ITEMS slots.
 template <int ITEMS>
 __global__ void __launch_bounds__(1024)

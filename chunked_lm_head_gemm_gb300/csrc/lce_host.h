@@ -9,6 +9,13 @@
 #include "../../include/lce.h"
 #include "lce_internal.h"
 
+// Returns a status that is not LCE_OK to the caller.
+#define LCE_TRY(call)              \
+  do {                             \
+    const lce_status st_ = (call); \
+    if (st_ != LCE_OK) return st_; \
+  } while (0)
+
 namespace lce {
 
 struct DeviceInfo {

@@ -542,8 +542,8 @@ lce_status lce_mlp_backward(const void* x, const void* Wg, const void* Wu,
  *   weights w_k = scale * s_{e_k}, or with renormalize
  *           scale * s_{e_k} / sum_k s_{e_k} (0 where that sum is 0).
  * A row whose logits are all -inf has scores and weights 0. Scores are
- * computed in fp32; two keys closer than its error bound are compared in
- * fp64, so the selection is that of exact arithmetic.
+ * computed in fp32; keys or ranks that lie within their fp32 error bounds are
+ * compared in fp64, so the selection is that of fp64 scores.
  *   logits   device [L][E] of dt (LCE_BF16 or LCE_F32)
  *   bias     device [E] float32 or NULL
  *   weights  device [L][top_k] of dt out
