@@ -14,8 +14,9 @@
 // TMA instead (four rows to an instruction, one instruction to a lane) needs
 // no copy but held every contraction to 37 ns an instruction per SM, 32 of
 // them a stage: UP ran at 540 TFLOP/s (L = 32768, H = 2048, I = 768, E = 128,
-// top 8), from copies at 1690; gathering by the threads (16-byte asynchronous
-// copies of four warps, three stages ahead) at 418.
+// top 8), from copies at 1690; gathering by the threads at 418 (16-byte
+// asynchronous copies of four warps, three stages ahead) and at 685 (loads of
+// eight warps into registers, four K blocks ahead).
 //
 // Work: units are 128 x 256 output tiles (UP and DGU 128 x 128 of a, whose
 // accumulator columns are g | u), walked in a static stride by one CTA per
@@ -466,6 +467,10 @@ struct EpiDgu : EpiBase {
         gv[k] = dg;
         da[k] = d * sil;                 // du
         uv[k] = w * a;
+      }
+      if (slot < 0) {  // a padding row adds nothing to a weight gradient
+#pragma unroll           // (0 times an infinite weight is NaN)
+        for (int k = 0; k < 32; ++k) gv[k] = da[k] = uv[k] = 0.f;
       }
       store_box(gv, j0, u.row0 + wr, &m.s0);
       store_box(da, j0, u.row0 + wr, &m.s1);

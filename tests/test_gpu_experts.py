@@ -181,6 +181,30 @@ def test_not_finite_stays_in_its_place(L):
     assert lce.get_error() == 0
 
 
+def test_infinite_weight_of_an_expert_with_one_row():
+    """Infinities come out where the definition has them: the rows that pad
+    an expert's single one add none and no NaN."""
+    import chunked_lm_head_gemm_gb300 as lce
+    dev = require_gpu()
+    args, dy = draw(dev, 200, 64, 72, 6, 1, seed=8)
+    e = torch.randint(0, 5, (200, 1),
+                      generator=torch.Generator().manual_seed(2))
+    e[1] = 5
+    args[5] = e.to(torch.int32).to(dev)
+    args[3][5, 3, 7] = math.inf
+    got = run(args, dy)
+    with np.errstate(invalid="ignore"):
+        want = ref.experts_mlp(*[to64(t) for t in args[:5]],
+                               args[5].cpu().numpy(), to64(dy))
+    assert np.isinf(want[2][5, 7]).all() and np.isinf(want[3][5, 7]).all()
+    for name, a, r in zip(("y", "dx", "dWg", "dWu", "dWd", "dw"), got, want):
+        a = to64(a)
+        wild = ~np.isfinite(r)
+        assert np.array_equal(np.isnan(a), np.isnan(r)), name
+        assert np.array_equal(a[wild], r[wild], equal_nan=True), name
+    assert lce.get_error() == 0
+
+
 @pytest.mark.parametrize("L", [1, 7, 600])
 def test_same_bits_on_another_stream_and_in_a_graph(L):
     import chunked_lm_head_gemm_gb300 as lce
