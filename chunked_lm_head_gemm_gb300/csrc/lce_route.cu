@@ -818,7 +818,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, PER <= 8 ? 8 : 4)
       const float size = biased ? big : s_max;
       const float err = key_error(s_max, 0.f, a.scoring) + 0x1p-22f * size;
       const bool close = hi > -INFINITY && !(lo - hi > 4.f * err);
-      if (softmax) {
+      // an infinite key leaves no border to collect a group's largest by
+      if (softmax || !(err < INFINITY)) {  // sigmoid: the same for the warp
         slow |= close;
       } else if (__any_sync(FULL, close)) {
         // ranks in 64 bits, a lane to a group: the exact values of the keys

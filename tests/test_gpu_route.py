@@ -279,3 +279,23 @@ def test_many_rows_like_few(E, K, dtype, kw, biased, masked):
             tol = np.abs(b) * (6 * SCORE + torch.finfo(dtype).eps) + 1e-37
             assert (np.nan_to_num(np.abs(a - b)) <= np.nan_to_num(tol)).all()
     assert lce.get_error() == 0
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("E,G,kept", [(32, 8, 2), (12, 6, 3), (96, 32, 5),
+                                      (21, 7, 2)])
+def test_infinite_biases_in_many_rows(E, G, kept, top, scoring):
+    """Experts that an infinite bias forces (or bars), among groups so small
+    that all their experts are candidates, in a call of many rows: one forced
+    expert, two of one group, three of different groups, some masked."""
+    dev = require_gpu()
+    inf = math.inf
+    z = draw(3001, E, torch.float32, seed=E + top, masked=0.2)
+    for forced in ([E - 1], [E - 2, E - 1], [0, E // 2, E - 1]):
+        bias = 0.1 * torch.randn(E,
+                                 generator=torch.Generator().manual_seed(6))
+        bias[forced] = inf
+        bias[1] = -inf
+        check(z, dev, 4, bias=bias, scoring=scoring, n_group=G,
+              topk_group=kept, group_top=top)
