@@ -85,12 +85,18 @@ __device__ __forceinline__ int tiles_of(int c, int tile_m) {
   return (padded(c) + tile_m - 1) / tile_m;
 }
 
+// Static shared memory of lay_out, in 32-bit words.
+constexpr int LAY_OUT_WORDS = 32 + 32 + MAX_EXPERTS;
+
 // One block of 1024 threads: segments, tiles and padding rows from the
 // experts' counts (c: thread e's expert). start[] (shared, E + 1 entries) gets
 // each segment's row, cnt[] (shared) the counts.
 __device__ __forceinline__ void lay_out(int c, int E, int tile_m,
                                         const Plan& p, int* start, int* cnt) {
-  __shared__ int warp_rows[32], warp_tiles[32], first_tile[MAX_EXPERTS];
+  __shared__ int fixed[LAY_OUT_WORDS];
+  int* warp_rows = fixed;
+  int* warp_tiles = fixed + 32;
+  int* first_tile = fixed + 64;
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   if (e >= E) c = 0;
   const int rows = padded(c), tiles = tiles_of(c, tile_m);
@@ -539,11 +545,17 @@ __global__ void __launch_bounds__(TOKEN_SPLIT * TOKEN_HS * 32)
   }
 }
 
-cudaError_t allow_smem(const void* kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes));
+// Lets k_plan_small take its largest size where this call's, beside the
+// static arrays, is above the default limit. The limit is one value for all
+// threads of the process: set to a call's own size, another thread's smaller
+// call would lower it before the launch.
+cudaError_t allow_plan_small(const void* kernel, size_t bytes) {
+  constexpr size_t STATIC = sizeof(int) * LAY_OUT_WORDS;
+  if (bytes + STATIC <= 48 * 1024) return cudaSuccess;
+  constexpr int LARGEST = sizeof(int) * (32 + 2) * MAX_EXPERTS;
+  static_assert(LARGEST + STATIC <= 227 * 1024, "shared memory of a block");
+  return cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LARGEST);
 }
 
 }  // namespace
@@ -551,17 +563,17 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
 cudaError_t launch_plan(const int32_t* experts, int64_t n, int E, int tile_m,
                         const Plan& p, unsigned* err, cudaStream_t s) {
   cudaError_t e;
-  // slots of a lane: one while 32 warps suffice
-  const int few = n <= 1024 ? 1 : PLAN_SMALL / 1024;
-  const size_t small_smem =
-      sizeof(int) * (ceil_div(n, 32 * few) + 2) * static_cast<size_t>(E);
-  if (n <= PLAN_SMALL && small_smem <= 200 * 1024) {
+  if (n <= PLAN_SMALL) {
+    // slots of a lane: one while 32 warps suffice
+    const int few = n <= 1024 ? 1 : PLAN_SMALL / 1024;
+    const size_t smem =
+        sizeof(int) * (ceil_div(n, 32 * few) + 2) * static_cast<size_t>(E);
     auto kern = few == 1 ? k_plan_small<1> : k_plan_small<PLAN_SMALL / 1024>;
-    if ((e = allow_smem(reinterpret_cast<const void*>(kern), small_smem)) !=
+    if ((e = allow_plan_small(reinterpret_cast<const void*>(kern), smem)) !=
         cudaSuccess)
       return e;
-    kern<<<1, 1024, small_smem, s>>>(experts, static_cast<int>(n), E, tile_m,
-                                     p, err);
+    kern<<<1, 1024, smem, s>>>(experts, static_cast<int>(n), E, tile_m, p,
+                               err);
     return cudaGetLastError();
   }
   const int chunks = static_cast<int>(ceil_div(n, PLAN_CHUNK));
@@ -571,10 +583,9 @@ cudaError_t launch_plan(const int32_t* experts, int64_t n, int E, int tile_m,
   if ((e = launch_early(k_plan_layout, 1, 1024, 0, s, E, chunks, tile_m, p)) !=
       cudaSuccess)
     return e;
+  static_assert(sizeof(int) * (CHUNK_WARPS + 1) * MAX_EXPERTS <= 48 * 1024,
+                "default limit");
   const size_t smem = sizeof(int) * (CHUNK_WARPS + 1) * static_cast<size_t>(E);
-  if ((e = allow_smem(reinterpret_cast<const void*>(k_plan_place), smem)) !=
-      cudaSuccess)
-    return e;
   return launch_early(k_plan_place, chunks, CHUNK_WARPS * 32, smem, s, experts,
                       n, E, chunks, p);
 }

@@ -362,3 +362,64 @@ def test_example_step():
     losses = mod.run(steps=6)
     assert len(losses) == 6 and all(math.isfinite(v) for v in losses)
     assert losses[-1] < losses[0]
+
+
+def _child(code):
+    """Runs `code` in a process of its own, in which no earlier call has
+    changed a kernel's limits."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, timeout=300,
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("E,L", [(384, 109), (384, 120), (384, 433),
+                                 (384, 480), (1024, 40), (1024, 160)])
+def test_plans_near_the_default_shared_memory(E, L):
+    """Counters of the one-block plan that fit 48 KB alone but not beside the
+    kernel's static arrays, as the first call of a process."""
+    require_gpu()
+    _child("from tests import test_gpu_experts as t\n"
+           "import chunked_lm_head_gemm_gb300 as lce\n"
+           "dev = t.require_gpu()\n"
+           f"args, dy = t.draw(dev, {L}, 64, 8, {E}, 8, seed={L})\n"
+           "t.compare(t.run(args, dy), args, dy)\n"
+           "assert lce.get_error() == 0\n")
+
+
+def test_plans_of_different_sizes_from_many_threads():
+    """A plan of more shared memory is not refused because another thread
+    queues smaller ones."""
+    import threading
+    import chunked_lm_head_gemm_gb300 as lce
+    dev = require_gpu()
+    lib, work, refused = lce.load(), [], []
+    for L in (128, 64) * 4:
+        args, _ = draw(dev, L, 8, 8, 1024, 8, seed=L)
+        want = lce.experts_forward(*args)
+        ws = dirty(lce.experts_workspace_size(L, 8, 8, 1024, 8), dev)
+        y = torch.empty_like(want)
+        call = (*(t.data_ptr() for t in args[:5]), 0, args[5].data_ptr(), L, 8,
+                8, 1024, 8, y.data_ptr(), ws.data_ptr(), ws.numel(),
+                torch.cuda.Stream().cuda_stream)
+        work.append((args, ws, want, y, call))
+    torch.cuda.synchronize()
+
+    def loop(call):  # the C call alone, so that the threads meet inside it
+        for _ in range(2000):
+            status = lib.lce_experts_forward(*call)
+            if status:
+                refused.append(status)
+    threads = [threading.Thread(target=loop, args=(w[4],)) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, (len(refused), refused[0])
+    for _, _, want, y, _ in work:
+        assert torch.equal(y, want)
+    assert lce.get_error() == 0
