@@ -1192,6 +1192,16 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 constexpr int64_t MANY_MIN = 3000;
 constexpr int MANY_MAX_E = 512;  // shared memory of the keys
 
+// The largest size of any call: a group's stride is below its experts + 32,
+// and what a warp of k_route_many adds to that is less.
+constexpr int MAX_WARP_BYTES = LIST_BYTES + 8 * (MAX_E + 31 * MAX_GROUPS);
+constexpr int MAX_ROUTE_SMEM = ROUTE_WARPS * MAX_WARP_BYTES;
+static_assert(MAX_WARP_BYTES % 16 == 0, "rows of doubles");
+static_assert(MANY_ROWS * ((MANY_MAX_E + 31) * 4 + MANY_LIST * 8 +
+                           (MANY_K + 2) * 8 + 2 * MAX_GROUPS * 4) <=
+                  MAX_WARP_BYTES,
+              "k_route_many's part");
+
 template <typename T, int PER, int V>
 cudaError_t launch_route_t(const RouteArgs& args, cudaStream_t s) {
   RouteArgs a = args;
@@ -1204,9 +1214,10 @@ cudaError_t launch_route_t(const RouteArgs& args, cudaStream_t s) {
   const size_t smem = sizeof(double) * ROUTE_WARPS * a.warp_smem;
   auto kern = many ? k_route_many<T, PER, V> : k_route<T, PER, V>;
   if (smem > 48 * 1024) {
+    // one value for every call: the limit is the process's, and another
+    // thread may launch between this and the launch below
     cudaError_t e = cudaFuncSetAttribute(
-        kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        static_cast<int>(smem));
+        kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_ROUTE_SMEM);
     if (e != cudaSuccess) return e;
   }
   const unsigned grid = static_cast<unsigned>(

@@ -299,3 +299,73 @@ def test_infinite_biases_in_many_rows(E, G, kept, top, scoring):
         bias[1] = -inf
         check(z, dev, 4, bias=bias, scoring=scoring, n_group=G,
               topk_group=kept, group_top=top)
+
+
+HAMMER = r"""
+#include <pthread.h>
+#include <stdint.h>
+typedef int (*route_fn)(const void*, int, const float*, int64_t, int64_t,
+                        const void*, void*, int32_t*, void*);
+struct call {
+  route_fn f;
+  const void* logits;
+  int64_t L, E;
+  const void* opts;
+  void *weights, *experts, *stream;
+  int64_t times, refused;
+};
+static void* run(void* p) {
+  struct call* c = p;
+  for (int64_t i = 0; i < c->times; ++i)
+    c->refused += c->f(c->logits, 1, 0, c->L, c->E, c->opts, c->weights,
+                       c->experts, c->stream) != 0;
+  return 0;
+}
+void hammer(struct call* calls, int n) {
+  pthread_t t[16];
+  for (int i = 0; i < n; ++i) pthread_create(&t[i], 0, run, &calls[i]);
+  for (int i = 0; i < n; ++i) pthread_join(t[i], 0);
+}
+"""
+
+
+def test_group_ranks_of_different_sizes_from_many_threads(tmp_path):
+    """A call whose group ranks need more shared memory is not refused
+    because another thread queues calls that need less. (Threads of a C
+    helper: Python's meet too seldom inside the calls.)"""
+    import ctypes
+    import subprocess
+    dev = require_gpu()
+    import chunked_lm_head_gemm_gb300 as lce
+    from chunked_lm_head_gemm_gb300 import _binding as B
+    (tmp_path / "hammer.c").write_text(HAMMER)
+    so = tmp_path / "hammer.so"
+    subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-pthread", "-o", so,
+                    tmp_path / "hammer.c"], check=True)
+
+    class Call(ctypes.Structure):
+        _fields_ = [(n, ctypes.c_void_p) for n in ("f", "logits")] + [
+            (n, ctypes.c_int64) for n in ("L", "E")] + [
+            (n, ctypes.c_void_p) for n in ("opts", "weights", "experts",
+                                           "stream")] + [
+            (n, ctypes.c_int64) for n in ("times", "refused")]
+    f = ctypes.cast(lce.load().lce_route_forward, ctypes.c_void_p).value
+    keep, calls = [], (Call * 8)()
+    for i in range(8):
+        E, G = ((1020, 30), (884, 26))[i % 2]
+        z = draw(64, E, torch.float32, seed=E).to(dev)
+        want = lce.route_forward(z, 8, n_group=G, topk_group=4, group_top=2)
+        got = [torch.empty_like(t) for t in want]
+        opts = B.RouteOpts(0, 8, G, 4, 2, 1, 1.0)
+        stream = torch.cuda.Stream()
+        keep.append((z, want, got, opts, stream))
+        calls[i] = Call(f, z.data_ptr(), 64, E, ctypes.addressof(opts),
+                        got[0].data_ptr(), got[1].data_ptr(),
+                        stream.cuda_stream, 10000, 0)
+    torch.cuda.synchronize()
+    ctypes.CDLL(str(so)).hammer(calls, 8)
+    torch.cuda.synchronize()
+    assert [c.refused for c in calls] == [0] * 8
+    for _, want, got, _, _ in keep:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert lce.get_error() == 0
