@@ -565,7 +565,13 @@ __device__ __forceinline__ void route_row(const RouteArgs& a, int64_t row,
       const unsigned past = apart_of >> (a.K - 1) << (a.K - 1);
       const int end = past ? __ffs(past) - 1 : found - 1;
       const unsigned before = end >= 31 ? 0x7fffffffu : (1u << end) - 1u;
-      if ((fine & before) != before)  // the same for the whole warp
+      // a key further down with a larger score has a larger error, which may
+      // reach over the step
+      const float reach =
+          warp_max(lane > end && lane < found ? x + err : -INFINITY);
+      const bool clear = __shfl_sync(FULL, x - err, end) > reach ||
+                         reach == -INFINITY;
+      if ((fine & before) != before || !clear)  // the same for the whole warp
         mine = rank_exact<T, PER, V>(a, zr, lane < found, mine, jz, jb, lane,
                                      list);
     }
@@ -943,6 +949,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, PER <= 8 ? 8 : 4)
   // ---- their order ---------------------------------------------------------------
   uint2* fall = sorted + r * (MANY_K + 2);
   const int count = min(found, MANY_LIST);
+  float reach = -INFINITY;  // how far up a key beyond the chosen may belong
   for (int c = s; c < count; c += MANY_LANES) {
     const uint2 own = list[c];
     const float v = __uint_as_float(own.x);
@@ -954,6 +961,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, PER <= 8 ? 8 : 4)
       if (ov > v || (ov == v && o.y < own.y)) ++rank;
     }
     if (rank <= MANY_K) fall[rank] = own;
+    if (biased && softmax && rank >= a.K && v > -INFINITY)
+      reach = fmaxf(reach, v + key_error(v, a.bias[own.y], a.scoring));
   }
   __syncwarp();
   const int64_t row = row0 + r;
@@ -975,6 +984,14 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, PER <= 8 ? 8 : 4)
         close = true;
     }
     if (softmax) {
+      // a larger score has a larger error: every key beyond the chosen is
+      // held against the last of them, not the next one alone
+      reach = lanes_max(reach);
+      if (count > a.K && reach > -INFINITY) {
+        const uint2 last = fall[a.K - 1];
+        const float x = __uint_as_float(last.x);
+        close |= !(x - key_error(x, a.bias[last.y], a.scoring) > reach);
+      }
       slow |= close;  // the exact scores need the row's sum
     } else if (__any_sync(FULL, close)) {
       // the order in 64 bits: exact keys of the candidates as ordered

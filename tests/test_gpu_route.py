@@ -369,3 +369,32 @@ def test_group_ranks_of_different_sizes_from_many_threads(tmp_path):
     for _, want, got, _, _ in keep:
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert lce.get_error() == 0
+
+
+@pytest.mark.parametrize("E", [512, 1000], ids=["many", "few"])
+def test_a_large_score_just_below_the_border(E):
+    """Softmax scores with a bias, top 1: two experts whose keys are their
+    biases (no score to speak of), 2^-23 apart, and right below them one with
+    half the row's mass, whose fp32 key is off by more than that. The row is
+    searched for: of 20000, the one whose fp32 score falls furthest short."""
+    dev = require_gpu()
+    import chunked_lm_head_gemm_gb300 as lce
+    L = 20000
+    d = torch.linspace(math.log(E) - 0.7, math.log(E) + 0.7, L)
+    z = -d[:, None].expand(L, E).contiguous()
+    z[:, 0] = 0.0
+    z[:, [40, 80]] = -60.0
+    w, e = lce.route_forward(z.to(dev), 1, renormalize=False)
+    assert (e == 0).all()
+    score = 1.0 / (1.0 + (E - 3) * np.exp(-to64(d)) + 2 * math.exp(-60.0))
+    short = score - to64(w)[:, 0]
+    i = int(short.argmax())
+    gap = 1.25e-7
+    assert short[i] > 1.02 * gap  # else the row shows nothing
+    bias = torch.full((E,), -10.0)
+    bias[0], bias[40], bias[80] = -w[i, 0].cpu(), gap, 2.0 ** -40
+    assert ref.select(to64(z[i]), 1, bias=bias.double().numpy()) == [0]
+    _, e = lce.route_forward(z[i].expand(L, E).contiguous().to(dev), 1,
+                             bias=bias.to(dev))
+    assert (e == 0).all()
+    assert lce.get_error() == 0
