@@ -799,6 +799,21 @@ def _check_logits(logits):
     return _dtype_code(logits)
 
 
+def _check_out(name, t, shape, dtype, device):
+    """An output the caller gives is written as it stands."""
+    if (t.shape != shape or t.dtype is not dtype or t.device != device or
+            not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of "
+                         f"shape {tuple(shape)} on {device}")
+    return t
+
+
+def _check_workspace(workspace, device):
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
 def route_forward(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
                   bias=None, n_group: int = 1, topk_group: int = 1,
                   group_top: int = 1, renormalize: bool = True,
@@ -819,10 +834,16 @@ def route_forward(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
                                  bias.is_contiguous()):
         raise ValueError("bias must be a contiguous CUDA float32 [E] tensor")
     shape = (L, max(top_k, 0))
-    weights = (weights_out if weights_out is not None
-               else torch.empty(shape, dtype=logits.dtype, device=dev))
-    experts = (experts_out if experts_out is not None
-               else torch.empty(shape, dtype=torch.int32, device=dev))
+    if weights_out is not None:
+        weights = _check_out("weights_out", weights_out, shape, logits.dtype,
+                             dev)
+    else:
+        weights = torch.empty(shape, dtype=logits.dtype, device=dev)
+    if experts_out is not None:
+        experts = _check_out("experts_out", experts_out, shape, torch.int32,
+                             dev)
+    else:
+        experts = torch.empty(shape, dtype=torch.int32, device=dev)
     st = lib.lce_route_forward(logits.data_ptr(), code, _ptr(bias), L, E,
                                opts, weights.data_ptr(),
                                experts.data_ptr(), _stream_ptr(dev))
@@ -847,7 +868,11 @@ def route_backward(logits: torch.Tensor, experts: torch.Tensor,
         raise ValueError("dweights must be a contiguous CUDA [L,top_k] tensor "
                          "of logits' dtype")
     opts = _route_opts(scoring, k, 1, 1, 1, renormalize, scale)
-    out = dlogits_out if dlogits_out is not None else torch.empty_like(logits)
+    if dlogits_out is not None:
+        out = _check_out("dlogits_out", dlogits_out, logits.shape,
+                         logits.dtype, dev)
+    else:
+        out = torch.empty_like(logits)
     st = lib.lce_route_backward(logits.data_ptr(), code, experts.data_ptr(),
                                 dweights.data_ptr(), L, E, opts,
                                 out.data_ptr(), _stream_ptr(dev))
@@ -907,7 +932,12 @@ def experts_forward(x, Wg, Wu, Wd, weights, experts, workspace=None,
     if workspace is None:
         workspace = torch.empty(experts_workspace_size(L, H, I, E, K),
                                 dtype=torch.uint8, device=dev)
-    y = y_out if y_out is not None else torch.empty_like(x)
+    else:
+        _check_workspace(workspace, dev)
+    if y_out is not None:
+        y = _check_out("y_out", y_out, x.shape, x.dtype, dev)
+    else:
+        y = torch.empty_like(x)
     st = load().lce_experts_forward(
         x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
         weights.data_ptr(), code, experts.data_ptr(), L, H, I, E, K,
@@ -936,6 +966,8 @@ def experts_backward(x, Wg, Wu, Wd, weights, experts, dy, workspace=None,
     if workspace is None:
         workspace = torch.empty(experts_workspace_size(L, H, I, E, K, True),
                                 dtype=torch.uint8, device=x.device)
+    else:
+        _check_workspace(workspace, x.device)
     dx = dWg = dWu = dWd = dw = None
     if compute_dx:
         dx = torch.empty_like(x)
