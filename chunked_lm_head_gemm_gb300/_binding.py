@@ -243,10 +243,12 @@ def _stream_ptr(device) -> int:
     """The device's current stream (device None: the current device's)."""
     if isinstance(device, str):
         device = torch.device(device)
-    index = getattr(device, "index", device)
-    if index is None:
-        index = torch.cuda.current_device()
-    return torch._C._cuda_getCurrentRawStream(index)
+    if isinstance(device, torch.device):
+        if device.type != "cuda":  # its pointers must not reach a kernel
+            raise ValueError(f"expected a CUDA device, got {device}")
+        if device.index is not None:
+            return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _dtype_code(t: torch.Tensor) -> int:

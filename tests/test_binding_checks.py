@@ -91,3 +91,23 @@ def test_output_and_workspace_of_the_experts(lib):
     assert lce.experts_forward(*args, workspace=ws, y_out=y) is y
     lce.experts_backward(*args, x, workspace=ws)
     assert len(lib.calls) == 2
+
+
+def test_host_tensors_are_refused_before_the_library(monkeypatch):
+    """Calls that take their stream from a tensor's device refuse a host
+    tensor, as does a stream of a device that is none."""
+    rec = Recorder()
+    monkeypatch.setattr(B, "load", lambda *a: rec)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0,
+                        raising=False)
+    one = torch.ones(1)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.shard_sums(one, torch.ones(1, dtype=torch.int64))
+    with pytest.raises(ValueError, match="CUDA"):
+        B.scale_gradients(torch.ones(2, 8), None, one)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.tc_gemm(one, one, 1, 1, 1, False, False)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.get_error("cpu")
+    assert not rec.calls
