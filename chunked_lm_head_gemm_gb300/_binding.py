@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -785,14 +786,24 @@ def mlp_backward(x, Wg, Wu, Wd, dy, chunk_rows: int = 0, workspace=None,
 
 
 @functools.lru_cache(maxsize=256)
+def _route_opts_of(*values):
+    """The lce_route_opts pointer of plain values, its fields in order."""
+    if not all(-2 ** 31 <= v < 2 ** 31 for v in values[1:5]):
+        raise ValueError("top_k, n_group, topk_group and group_top must fit "
+                         "in 32 bits")
+    return ctypes.pointer(RouteOpts(*values))
+
+
 def _route_opts(scoring, top_k, n_group, topk_group, group_top, renormalize,
                 scale):
     if scoring not in SCORING:
         raise ValueError(f"scoring must be one of {sorted(SCORING)}, got "
                          f"{scoring!r}")
-    return ctypes.pointer(RouteOpts(SCORING[scoring], top_k, n_group,
-                                    topk_group, group_top,
-                                    int(bool(renormalize)), scale))
+    # kept by value: a number that lives in a tensor is read at each call
+    return _route_opts_of(SCORING[scoring], operator.index(top_k),
+                          operator.index(n_group), operator.index(topk_group),
+                          operator.index(group_top), int(bool(renormalize)),
+                          float(scale))
 
 
 def _check_logits(logits):

@@ -111,3 +111,24 @@ def test_host_tensors_are_refused_before_the_library(monkeypatch):
     with pytest.raises(ValueError, match="CUDA"):
         B.get_error("cpu")
     assert not rec.calls
+
+
+def test_options_are_the_values_at_the_call(lib):
+    """A scale that lives in a tensor is read at each call, and options that
+    the C struct cannot hold are refused, not cut to 32 bits."""
+    z, e, dw = t(6, 16), t(6, 4, dtype=I32), t(6, 4)
+    scale = torch.tensor(2.5)
+    for value in (2.5, 4.0):
+        scale.fill_(value)
+        lce.route_forward(z, 4, scale=scale)
+        lce.route_backward(z, e, dw, scale=scale)
+        assert lib.calls[-2][1][5].contents.scale == value
+        assert lib.calls[-1][1][6].contents.scale == value
+    n = len(lib.calls)
+    for kw in (dict(n_group=2 ** 32 + 1), dict(topk_group=2 ** 32 + 1),
+               dict(group_top=1 - 2 ** 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            lce.route_forward(z, 4, **kw)
+    with pytest.raises(ValueError, match="scoring"):
+        lce.route_forward(z, 4, scoring="tanh")
+    assert len(lib.calls) == n
