@@ -14,6 +14,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import build as _build
 
@@ -1135,6 +1136,7 @@ class RouteExperts(torch.autograd.Function):
         return weights, experts
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dweights, _):
         logits, experts = ctx.saved_tensors
         dlogits = None
@@ -1165,6 +1167,7 @@ class ExpertsMLP(torch.autograd.Function):
         return experts_forward(x, Wg, Wu, Wd, weights, experts)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         need = ctx.needs_input_grad
         if not any(need[:5]):

@@ -423,3 +423,21 @@ def test_plans_of_different_sizes_from_many_threads():
     for _, _, want, y, _ in work:
         assert torch.equal(y, want)
     assert lce.get_error() == 0
+
+
+def test_second_derivatives_are_refused():
+    """The gradients carry no graph of their own: differentiating them again
+    is an error, not a missing term."""
+    import chunked_lm_head_gemm_gb300 as lce
+    dev = require_gpu()
+    (x, Wg, Wu, Wd, w, e), _ = draw(dev, 20, 64, 72, 4, 2, seed=13)
+    x.requires_grad_(True)
+    z = torch.randn(20, 4, device=dev, requires_grad=True)
+    for leaf, out in ((x, lce.experts_mlp(x, Wg, Wu, Wd, w, e)),
+                      (z, lce.route_experts(z, 2)[0])):
+        g, = torch.autograd.grad((out.float() ** 2).sum(), leaf,
+                                 create_graph=True)
+        loss = (g.float() ** 2).sum() + (leaf.float() ** 2).sum()
+        with pytest.raises(RuntimeError, match="twice"):
+            loss.backward()
+    assert lce.get_error() == 0
