@@ -1222,14 +1222,17 @@ static_assert(MANY_ROWS * ((MANY_MAX_E + 31) * 4 + MANY_LIST * 8 +
 template <typename T, int PER, int V>
 cudaError_t launch_route_t(const RouteArgs& args, cudaStream_t s) {
   RouteArgs a = args;
-  const bool many =
-      a.L >= MANY_MIN && a.K <= MANY_K && a.E <= MANY_MAX_E;
+  constexpr bool FITS = 32 * PER <= MANY_MAX_E;  // by_width: E <= 32 PER
+  const bool many = FITS && a.L >= MANY_MIN && a.K <= MANY_K;
   int bytes = LIST_BYTES + (a.groups > 1 ? 8 * a.groups * a.gg.stride : 0);
   if (many && many_bytes(a.E, a.groups) > bytes)
     bytes = many_bytes(a.E, a.groups);
   a.warp_smem = (bytes + 15) / 16 * 2;
   const size_t smem = sizeof(double) * ROUTE_WARPS * a.warp_smem;
-  auto kern = many ? k_route_many<T, PER, V> : k_route<T, PER, V>;
+  auto kern = k_route<T, PER, V>;
+  if constexpr (FITS) {
+    if (many) kern = k_route_many<T, PER, V>;
+  }
   if (smem > 48 * 1024) {
     // one value for every call: the limit is the process's, and another
     // thread may launch between this and the launch below
