@@ -67,6 +67,29 @@ def test_traffic_lookup_follows_the_kernel_source(tmp_path, monkeypatch):
     assert bench.load_traffic("gemm_dW", "qwen3-4b") is None
 
 
+def test_source_hash_is_of_the_measured_kernels(tmp_path, monkeypatch):
+    """The sparse MLP's files, which no measured kernel comes from, leave the
+    committed DRAM traffic valid; the contractions' and the host layer's do
+    not."""
+    import shutil
+    sys.path.insert(0, ROOT)
+    import bench
+    csrc = tmp_path / "chunked_lm_head_gemm_gb300" / "csrc"
+    shutil.copytree(os.path.join(ROOT, "chunked_lm_head_gemm_gb300", "csrc"),
+                    csrc)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    base = bench.source_hash()
+    for name, same in (("lce_route.cu", True), ("lce_experts.h", True),
+                       ("lce_experts_gemm.cu", True),
+                       ("lce_gemm_store.cu", False), ("lce_api.cu", False),
+                       ("lce_device.cuh", False)):
+        text = (csrc / name).read_text()
+        (csrc / name).write_text(text + "\nint added;\n")
+        assert (bench.source_hash() == base) == same, name
+        (csrc / name).write_text(text)
+    assert bench.source_hash() == base
+
+
 def test_oracle_sample_is_bounded():
     sys.path.insert(0, ROOT)
     import bench
