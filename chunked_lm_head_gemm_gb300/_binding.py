@@ -692,7 +692,8 @@ def backward_slice_exp(h, W_slice, labels, lse, dloss, v0: int, V_total: int,
 
 def get_error(device=None) -> int:
     """Synchronises the current stream and returns (and clears) the device
-    error status: LCE_OK, LCE_ERR_LABEL_RANGE or LCE_ERR_TIMEOUT."""
+    error status: LCE_OK, LCE_ERR_TIMEOUT, LCE_ERR_LABEL_RANGE or
+    LCE_ERR_EXPERT_RANGE."""
     return load().lce_get_error(_stream_ptr(device))
 
 

@@ -29,7 +29,7 @@ constexpr int PLAN_CHUNK = 2048; // slots of one counting block
 constexpr int PLAN_SMALL = 4096; // up to here one block makes the plan
 
 struct PlanHead {
-  int tiles;  // row tiles of at most 128 rows
+  int tiles;  // row tiles of at most tile_m rows (launch_plan)
   int rows;   // padded rows
 };
 

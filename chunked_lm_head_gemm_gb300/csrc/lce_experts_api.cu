@@ -17,12 +17,13 @@ struct Sizes {
 // Whether the forward takes its slots one by one on the CUDA cores
 // (launch_token), each reading its expert's weights, instead of planning tiles
 // for the tensor cores, which read the weights of every expert hit once but
-// cost about 18 us of small launches. Both read at 5.6 to 5.9 TB/s, so the
-// border is where the weights read again are 100 MB: slots - (experts hit)
+// cost about 18 us of small launches. That is what some 100 MB take to read,
+// so the border is where as much is read again: slots - (experts hit)
 // experts' weights, with the slots falling evenly. At H = 2048, I = 768, E =
-// 128 the two take 60 and 70 us for 32 slots, 112 and 92 us for 64; at I =
-// 4096, E = 8 they take 47 and 59 us for 4 slots, 80 and 77 us for 8. (At most
-// 64 slots: their fp32 activations fit the bf16 rows of a planned call.)
+// 128 the two take 60 and 70 us for 32 slots (302 MB slot by slot), 112 and 92
+// us for 64 (604 MB); at H = 2048, I = 4096, E = 8 they take 47 and 59 us for
+// 4 slots (201 MB), 80 and 77 us for 8 (403 MB). (At most 64 slots: their fp32
+// activations fit the bf16 rows of a planned call.)
 bool takes_tokens(const Sizes& z) {
   const double n = static_cast<double>(z.L) * z.K;
   if (n > 64) return false;

@@ -24,11 +24,14 @@
 // x 256 tiles by CTA pairs (PAIR). A unit's accumulation is split into parts,
 // each with its own columns, number of buffers and K loop.
 //
-// Bound, at L = 32768, H = 2048, I = 768, E = 128, top 8: UP runs at the
-// tensor cores' rate (1690 TFLOP/s, 82% of the pipe's cycles); the others at
-// what L2 gives the SMs, 16 to 18.6 TB/s in each of them, for an operand
-// tile of 32 KB a K block and CTA: DOWN 1440 (K = 768), DX 1520, DGU 1344 (its
-// da' part has half the columns for the same rows), GRAD 1590 TFLOP/s.
+// Rates, at L = 32768, H = 2048, I = 768, E = 128, top 8 (on pairs): UP 1690
+// TFLOP/s, GRAD 1590, DX 1520, DOWN 1440 (K = 768), DGU 1344 (its da' part has
+// half the columns for the same rows). With a quarter of the experts and
+// tokens the tensor pipe is active in 80, 78, 69, 64 and 60% of the cycles and
+// the SMs take 13.6, 13.0, 12.0, 11.4 and 12.3 TB/s of operands, at half of
+// L2's peak rate. UP and GRAD are near what a plain product sustains under the
+// power limit (1727 TFLOP/s); what holds the others below it is neither the
+// tensor pipe nor L2's rate, and has not been found.
 #include <cuda_fp16.h>
 
 #include "lce_device.cuh"
@@ -359,9 +362,10 @@ struct EpiUp : EpiBase {
 
 // Rows of H columns for the sum over a token's slots, in fp16 under a power
 // of two for each row and 128 columns: the largest finite value of the
-// piece lands in [2^14, 2^15), so a value is off by 2^-12 of itself at most
-// (2^-25 of the piece's largest below that), an eighth of a bf16 rounding, at
-// half the bytes of fp32. Infinities and NaN stay what they are. Against fp32
+// piece lands in [2^14, 2^15), so a value is off by 2^-11 of itself at most
+// (below 2^-14, where fp16's steps stay 2^-24, by 2^-39 of the piece's
+// largest), an eighth of a bf16 rounding, at half the bytes of fp32.
+// Infinities and NaN stay what they are. Against fp32
 // rows stored straight from registers: DOWN 1149 -> 592 us, DX 1303 ->
 // 1079 us, the two sums 694 -> 477 us (L = 32768, H = 2048, I = 768, E =
 // 128, top 8).
@@ -480,7 +484,11 @@ struct EpiDgu : EpiBase {
   }
 };
 
-// An expert's weight gradient, bf16 or fp32, zero where it has no rows.
+// An expert's weight gradient, bf16 or fp32, zero where it has no rows. fp32
+// goes straight from registers, a row to a lane, which costs more than its
+// twice the bytes: against bf16 GRAD takes 1860 and 1580 us (L = 32768, H =
+// 2048, I = 768, E = 128, top 8), 216 and 126 us (L = 8192, H = 1024, I = 512,
+// E = 64, top 6), 39 and 23 us (L = 1537, H = 1000, I = 424, E = 10, top 2).
 struct EpiWeights : EpiBase {
   struct Params {
     float* out[3];  // fp32 gradients: dWd [E][H][I], dWg and dWu [E][I][H];

@@ -390,9 +390,11 @@ __global__ void __launch_bounds__(256)
 // reading the chosen experts' weights once: 75 MB, 11 us, for one token at H
 // = 2048, I = 768, top 8. So every warp of k_token_up is resident at once
 // (40 registers, two 16-byte loads of each matrix in flight a lane; with four
-// there are two waves of warps, 25 us against 22 for both kernels), and
-// k_token_down fetches its weights before k_token_up has ended. Fetching the
-// rows by bulk copies into shared memory took 26 us.
+// there are two waves of warps, 25 us against 22 for both kernels).
+// k_token_down is launched early: its blocks (20 K registers) do not fit beside
+// the ten of k_token_up on a full SM (51 K of 64 K), but take their places as
+// they leave, and load their first weights before k_token_up as a whole has
+// ended. Fetching the rows by bulk copies into shared memory took 26 us.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -468,9 +470,8 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 12)
 }
 
 // y[t][h] = sum_k w_k Wd_e[h] . a[t, k]: TOKEN_SPLIT warps to an (t, h), each
-// with every TOKEN_SPLIT-th slot, two at a time; their first loads are on
-// their way before k_token_up is waited for. The warps' sums are added in
-// order.
+// with every TOKEN_SPLIT-th slot, two at a time; a warp's first loads are on
+// their way before it waits for k_token_up. The warps' sums are added in order.
 constexpr int TOKEN_SPLIT = 4;
 constexpr int TOKEN_HS = 2;  // (t, h) of a block
 

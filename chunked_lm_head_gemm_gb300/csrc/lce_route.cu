@@ -1,7 +1,8 @@
-// Routing of tokens to experts (lce_route_forward / lce_route_backward): one
-// warp per row of router logits. Scores, group ranks, the top_k selection
-// and the weights stay in registers; a row is read once and only its top_k
-// weights and indices are written.
+// Routing of tokens to experts (lce_route_forward / lce_route_backward): a
+// warp to a row of router logits (k_route), or four rows to a warp where there
+// are many (k_route_many). A row is read once, its scores, group ranks and
+// top_k selection stay on the SM (in registers; k_route_many's keys in shared
+// memory), and only its top_k weights and indices are written.
 //
 // Bound: the logits' bytes (67 MB at L = 65536, E = 256 in fp32), but the
 // instructions of the selection come first. So the selection does not search
@@ -12,7 +13,7 @@
 // need them, with the fast exponential; the chosen ones again, exactly.
 // Against top_k rounds of two warp-wide reductions over the whole row, both a
 // warp to a row: L = 32768, E = 128, top 8 of bf16 39 -> 31 us; L = 65536, E =
-// 256 in 8 groups with a bias 223 -> 121 us.
+// 256 in 8 groups with a bias 223 -> 121 us, which k_route_many does in 61.
 #include <math.h>
 
 #include <type_traits>

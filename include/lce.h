@@ -617,7 +617,7 @@ lce_status lce_route_backward(const void* logits, lce_dtype dt,
  * H % 8 == 0, I % 8 == 0, 1 <= E <= 1024, 1 <= top_k <= 32, L top_k <= 2^30.
  * L = 0: nothing to do forward, zero weight gradients backward.
  * Accumulation is fp32; a (and dg, du, w a) are rounded to bf16 between the
- * contractions, a slot's contribution to y or dx to 2^-12 of itself (fp16
+ * contractions, a slot's contribution to y or dx to 2^-11 of itself (fp16
  * under a power of two per row and 128 columns), and the sum over a token's
  * slots, in fp32 and in slot order, once to bf16. dweights comes from unrounded
  * g, u and da'. Results do not depend on the order of execution (no
