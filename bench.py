@@ -121,12 +121,13 @@ def _code_only(text: str) -> str:
 
 def source_hash() -> str:
     """Hash of the CUDA library's code (comments and spacing ignored) but for
-    the sparse MLP's own files: no kernel measured here is compiled from
-    them."""
+    the files of the sparse MLP, the norms, the balance loss and the gradient
+    clipping: no kernel measured here is compiled from them."""
     csrc = os.path.join(ROOT, "chunked_lm_head_gemm_gb300", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(csrc)):
-        if f.startswith(("lce_route", "lce_experts")):
+        if f.startswith(("lce_route", "lce_experts", "lce_norm",
+                         "lce_balance", "lce_grads", "lce_vec")):
             continue
         if f.endswith((".cu", ".cuh", ".h")):
             h.update(f.encode())

@@ -35,6 +35,9 @@ LCE_F32 = 1
 
 SCORING = {"softmax": 0, "sigmoid": 1}
 
+LAYER_NORM = 0
+RMS_NORM = 1
+
 IGNORE_INDEX = -100
 
 EXPORTED = ("lce_workspace_size", "lce_default_chunk_rows", "lce_forward",
@@ -54,9 +57,13 @@ EXPORTED = ("lce_workspace_size", "lce_default_chunk_rows", "lce_forward",
             "lce_forward_slice_exp_ex", "lce_backward_slice_exp_ex",
             "lce_route_forward", "lce_route_backward",
             "lce_experts_workspace_size", "lce_experts_forward",
-            "lce_experts_backward")
+            "lce_experts_backward", "lce_norm_forward", "lce_norm_backward",
+            "lce_norm_workspace_size", "lce_balance_forward",
+            "lce_balance_backward", "lce_balance_workspace_size",
+            "lce_expert_counts", "lce_grad_norm", "lce_clip_grads",
+            "lce_grad_norm_workspace_size")
 
-KERNEL_KINDS = 33
+KERNEL_KINDS = 40
 
 
 class LossOpts(ctypes.Structure):
@@ -217,6 +224,31 @@ def load(build_if_missing: bool = False):
                                              i64, i64, i64, i64, i32, p, p, p,
                                              p, p, p, sz, p]
         lib.lce_experts_backward.restype = i32
+        f32 = ctypes.c_float
+        lib.lce_norm_workspace_size.argtypes = [i64, i64]
+        lib.lce_norm_workspace_size.restype = sz
+        lib.lce_norm_forward.argtypes = [i32, p, i32, p, p, i32, i64, i64, f32,
+                                         p, p, p, p]
+        lib.lce_norm_forward.restype = i32
+        lib.lce_norm_backward.argtypes = [i32, p, i32, p, i32, p, p, p, i64,
+                                          i64, i32, p, p, p, p, sz, p]
+        lib.lce_norm_backward.restype = i32
+        lib.lce_balance_workspace_size.argtypes = [i64, i64]
+        lib.lce_balance_workspace_size.restype = sz
+        lib.lce_balance_forward.argtypes = [p, i32, p, p, i64, i64, i64, i32,
+                                            f32, p, p, p, p, sz, p]
+        lib.lce_balance_forward.restype = i32
+        lib.lce_balance_backward.argtypes = [p, i32, p, i64, i64, i32, p, p, p,
+                                             p]
+        lib.lce_balance_backward.restype = i32
+        lib.lce_expert_counts.argtypes = [p, p, i64, i64, i64, p, p]
+        lib.lce_expert_counts.restype = i32
+        lib.lce_grad_norm_workspace_size.argtypes = [i64]
+        lib.lce_grad_norm_workspace_size.restype = sz
+        lib.lce_grad_norm.argtypes = [p, p, p, i64, p, p, sz, p]
+        lib.lce_grad_norm.restype = i32
+        lib.lce_clip_grads.argtypes = [p, p, p, p, i64, p, f32, p]
+        lib.lce_clip_grads.restype = i32
         lib.lce_set_cta_pair.argtypes = [i32]
         lib.lce_set_cta_pair.restype = i32
         lib.lce_get_cta_pair.argtypes = []
@@ -1003,6 +1035,359 @@ def experts_backward(x, Wg, Wu, Wd, weights, experts, dy, workspace=None,
     return dx, dWg, dWu, dWd, dw
 
 
+def _call(name, device, *args):
+    """One call of the library with the tensors' device current, on that
+    device's current stream (the last argument)."""
+    fn = getattr(load(), name)
+    if device.index is None or device.index == torch.cuda.current_device():
+        st = fn(*args, _stream_ptr(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream_ptr(device))
+    if st:
+        _check(st, name)
+
+
+def _check_rows(name, t, shape, dtype, device):
+    """An input of known shape and type, as the C ABI reads it."""
+    if (t.shape != shape or t.dtype is not dtype or not t.is_cuda or
+            t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of "
+                         f"shape {tuple(shape)} on {device}")
+    return t
+
+
+def _check_norm(x, weight, bias):
+    """Sizes and type codes (of x, of the parameters) of a norm's inputs."""
+    if not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA [L,H] tensor")
+    code = param = _dtype_code(x)
+    L, H = x.shape
+    first = None
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        param = _dtype_code(t)
+        first = t if first is None else first
+        _check_rows(name, t, (H,), first.dtype, x.device)
+    return L, H, code, param
+
+
+@functools.lru_cache(maxsize=1024)
+def norm_workspace_size(L: int, H: int) -> int:
+    """Bytes of workspace that a norm's backward needs for the parameters'
+    gradients."""
+    n = load().lce_norm_workspace_size(L, H)
+    if n == 0:
+        raise ValueError(f"invalid norm sizes L={L} H={H}")
+    return n
+
+
+def _norm_forward(kind, x, weight, bias, eps, y_out, save_stats):
+    L, H, code, param = _check_norm(x, weight, bias)
+    dev = x.device
+    if y_out is not None:
+        y = _check_out("y_out", y_out, x.shape, x.dtype, dev)
+    else:
+        y = torch.empty_like(x)
+    mean = rstd = None
+    if save_stats:
+        rstd = torch.empty(L, dtype=torch.float32, device=dev)
+        if kind == LAYER_NORM:
+            mean = torch.empty(L, dtype=torch.float32, device=dev)
+    _call("lce_norm_forward", dev, kind, x.data_ptr(), code, _ptr(weight),
+          _ptr(bias), param, L, H, float(eps), y.data_ptr(), _ptr(mean),
+          _ptr(rstd))
+    return y, mean, rstd
+
+
+def _norm_backward(kind, x, weight, mean, rstd, dy, grad_dtype, workspace,
+                   dx_out, compute_dx, compute_dweight, compute_dbias):
+    L, H, code, param = _check_norm(x, weight, None)
+    dev = x.device
+    _check_rows("dy", dy, x.shape, x.dtype, dev)
+    _check_rows("rstd", rstd, (L,), torch.float32, dev)
+    if kind == LAYER_NORM:
+        _check_rows("mean", mean, (L,), torch.float32, dev)
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("grad_dtype must be float32 or bfloat16")
+    dx = dw = db = None
+    if compute_dx:
+        if dx_out is not None:
+            dx = _check_out("dx_out", dx_out, x.shape, x.dtype, dev)
+        else:
+            dx = torch.empty_like(x)
+    if compute_dweight:
+        dw = torch.empty(H, dtype=grad_dtype, device=dev)
+    if compute_dbias:
+        db = torch.empty(H, dtype=grad_dtype, device=dev)
+    bytes_ = 0
+    if workspace is not None:
+        _check_workspace(workspace, dev)
+        bytes_ = workspace.numel() * workspace.element_size()
+    elif compute_dweight or compute_dbias:
+        bytes_ = norm_workspace_size(L, H)
+        workspace = torch.empty(bytes_, dtype=torch.uint8, device=dev)
+    _call("lce_norm_backward", dev, kind, x.data_ptr(), code, _ptr(weight),
+          param, _ptr(mean), rstd.data_ptr(), dy.data_ptr(), L, H,
+          LCE_F32 if grad_dtype == torch.float32 else LCE_BF16, _ptr(dx),
+          _ptr(dw), _ptr(db), _ptr(workspace), bytes_)
+    return dx, dw, db
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5,
+                       y_out=None, save_stats: bool = True):
+    """Layer norm of the rows of x [L,H] (bf16 or fp32): returns (y of x's
+    type, mean [L], rstd [L] fp32, what the backward needs; None with
+    save_stats=False). weight and bias: [H], both bf16 or both fp32, or None.
+    y_out may be x (lce_norm_forward)."""
+    return _norm_forward(LAYER_NORM, x, weight, bias, eps, y_out, save_stats)
+
+
+def layer_norm_backward(x, weight, mean, rstd, dy, grad_dtype=torch.float32,
+                        workspace=None, dx_out=None, compute_dx: bool = True,
+                        compute_dweight: bool = True,
+                        compute_dbias: bool = True):
+    """Returns (dx [L,H] of x's type, dweight, dbias [H] of grad_dtype) for
+    upstream gradient dy. compute_* = False skips that gradient (None);
+    dx_out may be dy or x (lce_norm_backward)."""
+    return _norm_backward(LAYER_NORM, x, weight, mean, rstd, dy, grad_dtype,
+                          workspace, dx_out, compute_dx, compute_dweight,
+                          compute_dbias)
+
+
+def rms_norm_forward(x, weight=None, eps: float = 1e-6, y_out=None,
+                     save_stats: bool = True):
+    """RMS norm of the rows of x [L,H]: returns (y, rstd [L]), as
+    layer_norm_forward without the mean and the bias."""
+    y, _, rstd = _norm_forward(RMS_NORM, x, weight, None, eps, y_out,
+                               save_stats)
+    return y, rstd
+
+
+def rms_norm_backward(x, weight, rstd, dy, grad_dtype=torch.float32,
+                      workspace=None, dx_out=None, compute_dx: bool = True,
+                      compute_dweight: bool = True):
+    """Returns (dx, dweight) of rms_norm_forward, as layer_norm_backward."""
+    dx, dw, _ = _norm_backward(RMS_NORM, x, weight, None, rstd, dy, grad_dtype,
+                               workspace, dx_out, compute_dx, compute_dweight,
+                               False)
+    return dx, dw
+
+
+def _check_mask(mask, L, device):
+    if mask is not None:
+        _check_rows("mask", mask, (L,), torch.bool, device)
+    return mask
+
+
+def _check_slots(experts, L, device):
+    _check_experts(experts, L)
+    if experts.device != device:
+        raise ValueError(f"experts must be on {device}")
+    return experts.shape[1]
+
+
+@functools.lru_cache(maxsize=1024)
+def balance_workspace_size(L: int, E: int) -> int:
+    n = load().lce_balance_workspace_size(L, E)
+    if n == 0:
+        raise ValueError(f"invalid balance sizes L={L} E={E}")
+    return n
+
+
+def _scoring_code(scoring):
+    if scoring not in SCORING:
+        raise ValueError(f"scoring must be one of {sorted(SCORING)}, got "
+                         f"{scoring!r}")
+    return SCORING[scoring]
+
+
+def balance_forward(logits, experts, scoring: str = "softmax",
+                    coef: float = 1.0, mask=None, workspace=None):
+    """The routing's balance loss coef * sum_e f_e mean_t p_te of router logits
+    [L,E] (bf16 or fp32) and their experts int32 [L,top_k] (-1: dropped), over
+    the tokens whose mask (bool [L]) is set: returns (loss [] fp32, counts [E]
+    int32, slopes [E] fp32, what the backward needs) (lce_balance_forward)."""
+    code = _check_logits(logits)
+    L, E = logits.shape
+    dev = logits.device
+    K = _check_slots(experts, L, dev)
+    _check_mask(mask, L, dev)
+    score = _scoring_code(scoring)
+    if workspace is None:
+        workspace = torch.empty(balance_workspace_size(L, E),
+                                dtype=torch.uint8, device=dev)
+    else:
+        _check_workspace(workspace, dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    slopes = torch.empty(E, dtype=torch.float32, device=dev)
+    _call("lce_balance_forward", dev, logits.data_ptr(), code,
+          experts.data_ptr(), _ptr(mask), L, E, K, score, float(coef),
+          loss.data_ptr(), counts.data_ptr(), slopes.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return loss, counts, slopes
+
+
+def balance_backward(logits, slopes, dloss, scoring: str = "softmax",
+                     mask=None, dlogits_out=None):
+    """dlogits [L,E] (logits' type) of balance_forward for the gradient dloss
+    of the loss (one fp32 value on the device), the counts being constant."""
+    code = _check_logits(logits)
+    L, E = logits.shape
+    dev = logits.device
+    _check_rows("slopes", slopes, (E,), torch.float32, dev)
+    _check_mask(mask, L, dev)
+    score = _scoring_code(scoring)
+    if dloss.numel() != 1:
+        raise ValueError("dloss must be one value")
+    dloss = dloss.reshape(1).to(device=dev, dtype=torch.float32)
+    if dlogits_out is not None:
+        out = _check_out("dlogits_out", dlogits_out, logits.shape,
+                         logits.dtype, dev)
+    else:
+        out = torch.empty_like(logits)
+    _call("lce_balance_backward", dev, logits.data_ptr(), code, _ptr(mask), L,
+          E, score, slopes.data_ptr(), dloss.data_ptr(), out.data_ptr())
+    return out
+
+
+def expert_counts(experts, num_experts: int, mask=None, counts_out=None):
+    """Slots of each expert, int32 [num_experts], of experts int32 [L,top_k]
+    (-1: dropped) over the tokens whose mask (bool [L]) is set."""
+    L = experts.shape[0] if experts.dim() else 0
+    dev = experts.device
+    K = _check_slots(experts, L, dev)
+    _check_mask(mask, L, dev)
+    E = operator.index(num_experts)
+    if counts_out is not None:
+        counts = _check_out("counts_out", counts_out, (E,), torch.int32, dev)
+    else:
+        counts = torch.empty(max(E, 0), dtype=torch.int32, device=dev)
+    _call("lce_expert_counts", dev, experts.data_ptr(), _ptr(mask), L, E, K,
+          counts.data_ptr())
+    return counts
+
+
+def _dense(t):
+    """Whether t's elements fill one run of memory without overlap, in any
+    order of dimensions."""
+    step = 1
+    for stride, n in sorted((s, n) for s, n in zip(t.stride(), t.shape)
+                            if n != 1):
+        if stride != step:
+            return False
+        step *= n
+    return True
+
+
+_GRAD_TYPES = {torch.bfloat16: LCE_BF16, torch.float32: LCE_F32}
+
+
+class _GradTable:
+    """Host arrays of a list of gradients, as the C ABI takes them."""
+
+    def __init__(self, grads):
+        self.grads = list(grads)
+        n = self.n = len(self.grads)
+        ptrs, codes, sizes = [], [], []
+        self.device = self.grads[0].device if n else None
+        for g in self.grads:
+            if not g.is_cuda or g.device != self.device:
+                raise ValueError("gradients must be CUDA tensors on one "
+                                 "device")
+            code = _GRAD_TYPES.get(g.dtype)
+            if code is None:
+                raise TypeError(f"unsupported dtype {g.dtype}; use bfloat16 "
+                                "or float32")
+            if not (g.is_contiguous() or _dense(g)):
+                raise ValueError("gradients must fill their memory without "
+                                 "gaps or overlap")
+            ptrs.append(g.data_ptr())
+            codes.append(code)
+            sizes.append(g.numel())
+        self.ptrs = (ctypes.c_void_p * n)(*ptrs)
+        self.codes = (ctypes.c_int * n)(*codes)
+        self.sizes = (ctypes.c_int64 * n)(*sizes)
+        if not n:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def norm(self, workspace=None):
+        dev = self.device
+        if workspace is None:
+            workspace = torch.empty(grad_norm_workspace_size(self.n),
+                                    dtype=torch.uint8, device=dev)
+        else:
+            _check_workspace(workspace, dev)
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        _call("lce_grad_norm", dev, self.ptrs, self.codes, self.sizes, self.n,
+              norm.data_ptr(), workspace.data_ptr(),
+              workspace.numel() * workspace.element_size())
+        return norm
+
+    def clip(self, norm, max_norm, grads_out):
+        outs = self.ptrs
+        if grads_out is not None:
+            grads_out = list(grads_out)
+            if len(grads_out) != self.n:
+                raise ValueError(f"{len(grads_out)} outputs for {self.n} "
+                                 "gradients")
+            for g, o in zip(self.grads, grads_out):
+                if (o.shape != g.shape or o.dtype is not g.dtype or
+                        o.device != g.device or
+                        not (o.stride() == g.stride() or
+                             o.is_contiguous() and g.is_contiguous())):
+                    raise ValueError("an output must have its gradient's "
+                                     "shape, type, device and strides")
+            outs = (ctypes.c_void_p * self.n)(*[o.data_ptr()
+                                                for o in grads_out])
+        _call("lce_clip_grads", self.device, self.ptrs, outs, self.codes,
+              self.sizes, self.n, norm.data_ptr(), max_norm)
+
+
+def _max_norm(value):
+    value = float(value)
+    if not value >= 0.0:
+        raise ValueError(f"max_norm must not be negative, got {value}")
+    return value
+
+
+@functools.lru_cache(maxsize=1024)
+def grad_norm_workspace_size(n: int) -> int:
+    """Bytes of workspace that grad_norm needs for n gradients."""
+    size = load().lce_grad_norm_workspace_size(n)
+    if size == 0:
+        raise ValueError(f"invalid number of gradients {n}")
+    return size
+
+
+def grad_norm(grads, workspace=None):
+    """sqrt of the sum of all squares of a list of gradients (bf16 or fp32
+    CUDA tensors of any shapes): a fp32 scalar on their device."""
+    return _GradTable(grads).norm(workspace)
+
+
+def clip_grads(grads, norm, max_norm: float, grads_out=None):
+    """Multiplies every gradient by min(1, max_norm / (norm + 1e-6)), in place
+    or into grads_out (tensors laid out as the gradients). norm: one fp32 value
+    on the device, of grad_norm or of a sum over processes."""
+    max_norm = _max_norm(max_norm)
+    table = _GradTable(grads)
+    _check_rows("norm", norm.reshape(-1), (1,), torch.float32, table.device)
+    table.clip(norm, max_norm, grads_out)
+
+
+def clip_grad_norm(grads, max_norm: float, grads_out=None, workspace=None):
+    """clip_grads by the gradients' own norm, which is returned (as it was
+    before the clipping)."""
+    max_norm = _max_norm(max_norm)
+    table = _GradTable(grads)
+    norm = table.norm(workspace)
+    table.clip(norm, max_norm, grads_out)
+    return norm
+
+
 def set_cta_pair(enable: bool):
     """Run the contractions on CTA pairs (cta_group::2) or single CTAs."""
     _check(load().lce_set_cta_pair(1 if enable else 0), "lce_set_cta_pair")
@@ -1185,6 +1570,103 @@ class ExpertsMLP(torch.autograd.Function):
 def experts_mlp(x, Wg, Wu, Wd, weights, experts):
     """The experts' gated MLP (experts_forward) with autograd."""
     return ExpertsMLP.apply(x, Wg, Wu, Wd, weights, experts)
+
+
+class LayerNorm(torch.autograd.Function):
+    """layer_norm_forward under autograd; the parameters' gradients in their
+    own type. dy is made a contiguous tensor of x's type first."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.param_dtype = (x if weight is None and bias is None else
+                           bias if weight is None else weight).dtype
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if not any(need[:3]):
+            return (None,) * 4
+        return layer_norm_backward(
+            x, weight, mean, rstd, dy.to(x.dtype).contiguous(),
+            grad_dtype=ctx.param_dtype, compute_dx=need[0],
+            compute_dweight=need[1], compute_dbias=need[2]) + (None,)
+
+
+class RMSNorm(torch.autograd.Function):
+    """rms_norm_forward under autograd, as LayerNorm."""
+
+    @staticmethod
+    def forward(ctx, x, weight, eps):
+        y, rstd = rms_norm_forward(x, weight, eps)
+        ctx.save_for_backward(x, weight, rstd)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if not any(need[:2]):
+            return (None,) * 3
+        dtype = x.dtype if weight is None else weight.dtype
+        return rms_norm_backward(
+            x, weight, rstd, dy.to(x.dtype).contiguous(), grad_dtype=dtype,
+            compute_dx=need[0], compute_dweight=need[1]) + (None,)
+
+
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(
+        t is not None and t.requires_grad for t in tensors)
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
+    """Layer norm of the rows of x [L,H] with autograd (layer_norm_forward)."""
+    if not _wants_grad(x, weight, bias):  # serving: no statistics are kept
+        return layer_norm_forward(x, weight, bias, eps, save_stats=False)[0]
+    return LayerNorm.apply(x, weight, bias, eps)
+
+
+def rms_norm(x, weight=None, eps: float = 1e-6):
+    """RMS norm of the rows of x [L,H] with autograd (rms_norm_forward)."""
+    if not _wants_grad(x, weight):
+        return rms_norm_forward(x, weight, eps, save_stats=False)[0]
+    return RMSNorm.apply(x, weight, eps)
+
+
+class BalanceLoss(torch.autograd.Function):
+    """balance_forward under autograd: the loss carries gradient to the
+    logits through the scores; the counts are constant."""
+
+    @staticmethod
+    def forward(ctx, logits, experts, scoring, coef, mask):
+        loss, counts, slopes = balance_forward(logits, experts, scoring, coef,
+                                               mask)
+        ctx.scoring = scoring
+        ctx.save_for_backward(logits, slopes, mask)
+        ctx.mark_non_differentiable(counts)
+        return loss, counts
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, _):
+        logits, slopes, mask = ctx.saved_tensors
+        dlogits = None
+        if ctx.needs_input_grad[0]:
+            dlogits = balance_backward(logits, slopes, dloss, ctx.scoring,
+                                       mask)
+        return (dlogits,) + (None,) * 4
+
+
+def balance_loss(logits, experts, scoring: str = "softmax", coef: float = 1.0,
+                 mask=None):
+    """(loss, counts) of the routing's balance, with autograd
+    (balance_forward)."""
+    return BalanceLoss.apply(logits, experts, scoring, coef, mask)
 
 
 def sequence_tiled_mlp(x, Wg, Wu, Wd, chunk_rows: int = 0):

@@ -20,7 +20,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["lce_api.cu", "lce_gemm_loss.cu", "lce_gemm_store.cu",
            "lce_gemm_mlp.cu", "lce_small.cu", "lce_route.cu",
-           "lce_experts_api.cu", "lce_experts_plan.cu", "lce_experts_gemm.cu"]
+           "lce_experts_api.cu", "lce_experts_plan.cu", "lce_experts_gemm.cu",
+           "lce_norm.cu", "lce_balance.cu", "lce_grads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]

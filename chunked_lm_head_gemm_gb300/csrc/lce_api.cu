@@ -53,7 +53,9 @@ const char* const kKindNames[LCE_KERNEL_KINDS] = {
     "combine_slices", "shard_combine",
     "route",        "route_bwd",    "experts_plan",  "experts_up",
     "experts_down", "experts_combine", "experts_dgu", "experts_dx",
-    "experts_grads", "experts_token", "experts_gather"};
+    "experts_grads", "experts_token", "experts_gather",
+    "norm",         "norm_bwd",     "balance",       "balance_bwd",
+    "expert_counts", "grad_norm",   "clip_grads"};
 
 struct ProfRec {
   int kind;

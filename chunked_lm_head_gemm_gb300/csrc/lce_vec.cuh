@@ -1,0 +1,70 @@
+// Device helpers of the row-wise operators (norms, balance loss, gradient
+// clipping): typed loads and stores, warp and block reductions.
+#pragma once
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace lce {
+
+constexpr unsigned ALL_LANES = 0xffffffffu;
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// Element i of an array of either type.
+__device__ __forceinline__ float load_as_float(const void* p, bool f32,
+                                               int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i]
+             : to_float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_from_float(void* p, bool f32, int64_t i,
+                                                 float v) {
+  if (f32)
+    static_cast<float*>(p)[i] = v;
+  else
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+template <typename V>
+__device__ __forceinline__ V lanes_sum(V v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(ALL_LANES, v, o);
+  return v;
+}
+
+// Sums over the block, the same bits in every thread: warps by shuffles, then
+// the warps' sums in warp order. `part` holds 32 values; the block must not
+// use it again before its next barrier.
+template <typename V>
+__device__ __forceinline__ V block_sum(V v, V* part) {
+  v = lanes_sum(v);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  V t = 0;
+  const int warps = (blockDim.x + 31) >> 5;
+  for (int w = 0; w < warps; ++w) t += part[w];
+  return t;
+}
+
+// A kernel launched with launch_early calls the first before it touches what
+// earlier kernels read or write; the second lets the next kernel begin.
+__device__ __forceinline__ void wait_for_earlier() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace lce

@@ -643,6 +643,130 @@ lce_status lce_experts_backward(const void* x, const void* Wg, const void* Wu,
                                 size_t ws_bytes, void* stream);
 
 /*
+ * Layer norm and RMS norm of the rows of x, as a model's blocks have them in
+ * front of the head, the MLPs and the router. No counterpart on the pages. For
+ * a row x of H elements, in fp32:
+ *   mu = mean(x) (RMS norm: 0), r = 1 / sqrt(mean((x - mu)^2) + eps)
+ *   n = (x - mu) r,  y = n weight + bias
+ *   x       device [L][H] of dt (LCE_BF16 or LCE_F32)
+ *   weight  device [H] of param_dt (LCE_BF16 or LCE_F32), or NULL (ones)
+ *   bias    device [H] of param_dt, or NULL (zeros; RMS norm: NULL)
+ *   eps     finite, not negative
+ *   y       device [L][H] of dt out; may be x itself
+ *   mean    device [L] float32 out, or NULL (RMS norm: NULL)
+ *   rstd    device [L] float32 out (r), or NULL
+ * 1 <= H <= 2^20, 0 <= L <= 2^31; L = 0 does nothing. Rows and parameters
+ * need their element's alignment alone; rows that start on 16 bytes are read
+ * 16 bytes at a time.
+ */
+typedef enum { LCE_LAYER_NORM = 0, LCE_RMS_NORM = 1 } lce_norm_kind;
+
+lce_status lce_norm_forward(lce_norm_kind kind, const void* x, lce_dtype dt,
+                            const void* weight, const void* bias,
+                            lce_dtype param_dt, int64_t L, int64_t H, float eps,
+                            void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * The norms' gradient from dy (device [L][H] of dt) and the forward's mean
+ * (RMS norm: NULL) and rstd, with g = dy weight:
+ *   dx = r (g - mean(g) - n mean(g n))   (RMS norm without mean(g))
+ *   dweight = sum over rows of dy n,  dbias = sum over rows of dy
+ *   dx      device [L][H] of dt out; may be dy or x itself
+ *   dweight, dbias  device [H] of grad_dt (LCE_BF16 or LCE_F32) out
+ *   dx, dweight and dbias may each be NULL, and that gradient is not computed;
+ *   not all of them (RMS norm: dbias NULL).
+ *   ws      device, 16-byte aligned, lce_norm_workspace_size() bytes; needed
+ *           for dweight and dbias alone (else NULL)
+ * The sums over rows are formed in fp32 over a few hundred runs of rows, and
+ * the runs added in fp64 in a fixed order. L = 0: zero dweight and dbias.
+ */
+size_t lce_norm_workspace_size(int64_t L, int64_t H);
+lce_status lce_norm_backward(lce_norm_kind kind, const void* x, lce_dtype dt,
+                             const void* weight, lce_dtype param_dt,
+                             const float* mean, const float* rstd,
+                             const void* dy, int64_t L, int64_t H,
+                             lce_dtype grad_dt, void* dx, void* dweight,
+                             void* dbias, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/*
+ * The slots of every expert, and the loss that evens them out. No counterpart
+ * on the pages. The tokens t that take part are those with mask[t] != 0 (all
+ * of them with a NULL mask); N is their number.
+ *   counts_e = #{(t, k) : t takes part, experts[t][k] = e}
+ *   f_e      = E counts_e / (N top_k)                  (1 for an even load)
+ *   p_t      = softmax(z_t), or sigmoid(z_t) / sum sigmoid(z_t)
+ *   loss     = coef sum_e f_e (1/N) sum_t p_te         (0 if N = 0)
+ * A row whose logits are all -inf has p = 0.
+ *   logits   device [L][E] of dt (LCE_BF16 or LCE_F32)
+ *   experts  device int32 [L][top_k]; -1 is a dropped slot; any other index
+ *            outside [0, E) is dropped too and raises LCE_ERR_EXPERT_RANGE.
+ *            Slots and logits of tokens that take no part are not looked at.
+ *   mask     device [L] bytes, or NULL
+ *   loss     device [1] float32 out
+ *   counts   device [E] int32 out
+ *   slopes   device [E] float32 out: coef (f_e - 1) / N, what the backward
+ *            needs of the counts
+ *   ws       device, 16-byte aligned, lce_balance_workspace_size() bytes
+ * 1 <= E <= 1024, 1 <= top_k <= 32, L top_k <= 2^30, coef finite. The sum over
+ * tokens is formed in fp32 over runs of tokens and the runs added in fp64 in a
+ * fixed order.
+ */
+size_t lce_balance_workspace_size(int64_t L, int64_t E);
+lce_status lce_balance_forward(const void* logits, lce_dtype dt,
+                               const int32_t* experts, const uint8_t* mask,
+                               int64_t L, int64_t E, int64_t top_k,
+                               lce_scoring scoring, float coef, float* loss,
+                               int32_t* counts, float* slopes, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * The balance loss's gradient, the counts being constant: dlogits (device
+ * [L][E] of dt out, every element written; 0 for tokens that take no part)
+ *   dz_tj = dloss p_tj d_tj (slopes_j - sum_e slopes_e p_te),
+ * d = 1 (softmax) or 1 - sigmoid(z_tj), from the forward's logits, mask and
+ * slopes and dloss (device [1] float32).
+ */
+lce_status lce_balance_backward(const void* logits, lce_dtype dt,
+                                const uint8_t* mask, int64_t L, int64_t E,
+                                lce_scoring scoring, const float* slopes,
+                                const float* dloss, void* dlogits,
+                                void* stream);
+
+/* lce_balance_forward's counts alone. */
+lce_status lce_expert_counts(const int32_t* experts, const uint8_t* mask,
+                             int64_t L, int64_t E, int64_t top_k,
+                             int32_t* counts, void* stream);
+
+/*
+ * The norm of n gradients taken together, and their clipping, before an
+ * optimizer's step. No counterpart on the pages.
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   out  = min(1, max_norm / (norm + 1e-6)) g
+ *   grads, outs  host arrays of n device pointers; outs[i] may be grads[i]
+ *   dts, sizes   host arrays: type (LCE_BF16 or LCE_F32) and elements of
+ *                each; an empty tensor's pointers are not looked at
+ *   norm         device [1] float32, out of lce_grad_norm (or any other, such
+ *                as the root of squares summed over processes), into
+ *                lce_clip_grads
+ *   max_norm     not negative; with infinity nothing is clipped
+ *   ws           device, 16-byte aligned, lce_grad_norm_workspace_size(n)
+ * The host arrays are read before the call returns. Outputs may not overlap
+ * each other, norm, or a gradient other than their own (LCE_ERR_INVALID_ARG):
+ * the same gradient given twice is refused. Squares are summed so that
+ * neither tiny nor huge gradients are lost (fp32 groups, fp64 sums), in a
+ * fixed order. A norm that is NaN makes every output NaN, an infinite one 0,
+ * or NaN where the gradient is not finite. In place, factor 1 writes nothing.
+ */
+size_t lce_grad_norm_workspace_size(int64_t n);
+lce_status lce_grad_norm(const void* const* grads, const lce_dtype* dts,
+                         const int64_t* sizes, int64_t n, float* norm, void* ws,
+                         size_t ws_bytes, void* stream);
+lce_status lce_clip_grads(const void* const* grads, void* const* outs,
+                          const lce_dtype* dts, const int64_t* sizes, int64_t n,
+                          const float* norm, float max_norm, void* stream);
+
+/*
  * Selects how the tensor-core contractions run, for the whole process:
  * enable = 1: on CTA pairs (a cluster of two SMs issues tcgen05.mma with
  * cta_group::2 on 256 x 256 tiles, each SM staging half of each operand);
@@ -679,7 +803,7 @@ int lce_get_wave_sync(void);
  * per tensor-core contraction, 0 for the other kernels). Host-side state
  * only; events are created on first use and reused.
  */
-#define LCE_KERNEL_KINDS 33
+#define LCE_KERNEL_KINDS 40
 enum {
   LCE_K_COUNT_VALID = 0,
   LCE_K_GEMM_LSE = 1,
@@ -713,7 +837,14 @@ enum {
   LCE_K_EXPERTS_DX = 29,
   LCE_K_EXPERTS_GRADS = 30,
   LCE_K_EXPERTS_TOKEN = 31,
-  LCE_K_EXPERTS_GATHER = 32
+  LCE_K_EXPERTS_GATHER = 32,
+  LCE_K_NORM = 33,
+  LCE_K_NORM_BWD = 34,
+  LCE_K_BALANCE = 35,
+  LCE_K_BALANCE_BWD = 36,
+  LCE_K_EXPERT_COUNTS = 37,
+  LCE_K_GRAD_NORM = 38,
+  LCE_K_CLIP_GRADS = 39
 };
 
 typedef struct {
