@@ -7,6 +7,7 @@ built or the device is not sm_103, calls raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import operator
@@ -61,7 +62,7 @@ EXPORTED = ("lce_workspace_size", "lce_default_chunk_rows", "lce_forward",
             "lce_norm_workspace_size", "lce_balance_forward",
             "lce_balance_backward", "lce_balance_workspace_size",
             "lce_expert_counts", "lce_grad_norm", "lce_clip_grads",
-            "lce_grad_norm_workspace_size")
+            "lce_grad_norm_workspace_size", "lce_clip_grad_norm")
 
 KERNEL_KINDS = 40
 
@@ -249,6 +250,8 @@ def load(build_if_missing: bool = False):
         lib.lce_grad_norm.restype = i32
         lib.lce_clip_grads.argtypes = [p, p, p, p, i64, p, f32, p]
         lib.lce_clip_grads.restype = i32
+        lib.lce_clip_grad_norm.argtypes = [p, p, p, p, i64, f32, p, p, sz, p]
+        lib.lce_clip_grad_norm.restype = i32
         lib.lce_set_cta_pair.argtypes = [i32]
         lib.lce_set_cta_pair.restype = i32
         lib.lce_get_cta_pair.argtypes = []
@@ -1038,8 +1041,9 @@ def experts_backward(x, Wg, Wu, Wd, weights, experts, dy, workspace=None,
 def _call(name, device, *args):
     """One call of the library with the tensors' device current, on that
     device's current stream (the last argument)."""
-    fn = getattr(load(), name)
-    if device.index is None or device.index == torch.cuda.current_device():
+    fn = getattr(_lib or load(), name)
+    index = device.index
+    if index is None or index == torch._C._cuda_getDevice():
         st = fn(*args, _stream_ptr(device))
     else:
         with torch.cuda.device(device):
@@ -1283,67 +1287,73 @@ def _dense(t):
 
 
 _GRAD_TYPES = {torch.bfloat16: LCE_BF16, torch.float32: LCE_F32}
+_dtype_of = operator.attrgetter("dtype")
+
+
+def _host_array(kind, code, values):
+    """A C array of a list of numbers (array's conversion is the fast one)."""
+    return (kind * len(values)).from_buffer(array.array(code, values))
 
 
 class _GradTable:
-    """Host arrays of a list of gradients, as the C ABI takes them."""
+    """Host arrays of a list of gradients, as the C ABI takes them. A list has
+    hundreds of tensors: each property is asked of all of them at once."""
 
     def __init__(self, grads):
-        self.grads = list(grads)
-        n = self.n = len(self.grads)
-        ptrs, codes, sizes = [], [], []
-        self.device = self.grads[0].device if n else None
-        for g in self.grads:
-            if not g.is_cuda or g.device != self.device:
-                raise ValueError("gradients must be CUDA tensors on one "
-                                 "device")
-            code = _GRAD_TYPES.get(g.dtype)
-            if code is None:
-                raise TypeError(f"unsupported dtype {g.dtype}; use bfloat16 "
-                                "or float32")
-            if not (g.is_contiguous() or _dense(g)):
-                raise ValueError("gradients must fill their memory without "
-                                 "gaps or overlap")
-            ptrs.append(g.data_ptr())
-            codes.append(code)
-            sizes.append(g.numel())
-        self.ptrs = (ctypes.c_void_p * n)(*ptrs)
-        self.codes = (ctypes.c_int * n)(*codes)
-        self.sizes = (ctypes.c_int64 * n)(*sizes)
+        grads = self.grads = list(grads)
+        n = self.n = len(grads)
         if not n:
             self.device = torch.device("cuda", torch.cuda.current_device())
-
-    def norm(self, workspace=None):
-        dev = self.device
-        if workspace is None:
-            workspace = torch.empty(grad_norm_workspace_size(self.n),
-                                    dtype=torch.uint8, device=dev)
         else:
-            _check_workspace(workspace, dev)
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        _call("lce_grad_norm", dev, self.ptrs, self.codes, self.sizes, self.n,
-              norm.data_ptr(), workspace.data_ptr(),
-              workspace.numel() * workspace.element_size())
-        return norm
+            self.device = grads[0].device
+            if (not grads[0].is_cuda or
+                    len(set(map(torch.Tensor.get_device, grads))) > 1):
+                raise ValueError("gradients must be CUDA tensors on one "
+                                 "device")
+        try:
+            codes = [_GRAD_TYPES[t] for t in map(_dtype_of, grads)]
+        except KeyError as e:
+            raise TypeError(f"unsupported dtype {e.args[0]}; use bfloat16 or "
+                            "float32") from None
+        self.flat = all(map(torch.Tensor.is_contiguous, grads))
+        if not self.flat and not all(map(_dense, grads)):
+            raise ValueError("gradients must fill their memory without gaps "
+                             "or overlap")
+        self.ptrs = _host_array(ctypes.c_void_p, "Q",
+                                list(map(torch.Tensor.data_ptr, grads)))
+        self.codes = _host_array(ctypes.c_int, "i", codes)
+        self.sizes = _host_array(ctypes.c_int64, "q",
+                                 list(map(torch.Tensor.numel, grads)))
 
-    def clip(self, norm, max_norm, grads_out):
-        outs = self.ptrs
-        if grads_out is not None:
-            grads_out = list(grads_out)
-            if len(grads_out) != self.n:
-                raise ValueError(f"{len(grads_out)} outputs for {self.n} "
-                                 "gradients")
-            for g, o in zip(self.grads, grads_out):
-                if (o.shape != g.shape or o.dtype is not g.dtype or
-                        o.device != g.device or
-                        not (o.stride() == g.stride() or
-                             o.is_contiguous() and g.is_contiguous())):
-                    raise ValueError("an output must have its gradient's "
-                                     "shape, type, device and strides")
-            outs = (ctypes.c_void_p * self.n)(*[o.data_ptr()
-                                                for o in grads_out])
-        _call("lce_clip_grads", self.device, self.ptrs, outs, self.codes,
-              self.sizes, self.n, norm.data_ptr(), max_norm)
+    def outputs(self, grads_out):
+        """The outputs' pointers: the gradients' own without grads_out."""
+        if grads_out is None:
+            return self.ptrs
+        grads, outs = self.grads, list(grads_out)
+        if len(outs) != self.n:
+            raise ValueError(f"{len(outs)} outputs for {self.n} gradients")
+        codes = list(map(_GRAD_TYPES.get, map(_dtype_of, outs)))
+        sizes = list(map(torch.Tensor.numel, outs))
+        same = (codes == list(self.codes) and sizes == list(self.sizes) and
+                set(map(torch.Tensor.get_device, outs)) ==
+                set(map(torch.Tensor.get_device, grads[:1])))
+        if same and not (self.flat and
+                         all(map(torch.Tensor.is_contiguous, outs))):
+            same = all(o.shape == g.shape and o.stride() == g.stride() or
+                       o.is_contiguous() and g.is_contiguous()
+                       for o, g in zip(outs, grads))
+        if not same:
+            raise ValueError("an output must have its gradient's type, device "
+                             "and number of elements, and be contiguous or "
+                             "laid out as the gradient")
+        return _host_array(ctypes.c_void_p, "Q",
+                           list(map(torch.Tensor.data_ptr, outs)))
+
+    def workspace(self, workspace):
+        if workspace is not None:
+            return _check_workspace(workspace, self.device)
+        return torch.empty(grad_norm_workspace_size(self.n),
+                           dtype=torch.uint8, device=self.device)
 
 
 def _max_norm(value):
@@ -1365,17 +1375,26 @@ def grad_norm_workspace_size(n: int) -> int:
 def grad_norm(grads, workspace=None):
     """sqrt of the sum of all squares of a list of gradients (bf16 or fp32
     CUDA tensors of any shapes): a fp32 scalar on their device."""
-    return _GradTable(grads).norm(workspace)
+    table = _GradTable(grads)
+    dev = table.device
+    ws = table.workspace(workspace)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    _call("lce_grad_norm", dev, table.ptrs, table.codes, table.sizes, table.n,
+          norm.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return norm
 
 
 def clip_grads(grads, norm, max_norm: float, grads_out=None):
     """Multiplies every gradient by min(1, max_norm / (norm + 1e-6)), in place
-    or into grads_out (tensors laid out as the gradients). norm: one fp32 value
-    on the device, of grad_norm or of a sum over processes."""
+    or into grads_out (tensors laid out as the gradients; contiguous ones may
+    differ in shape, such as slices of a flat buffer). norm: one fp32 value
+    on the device, of grad_norm or of a sum over processes. Gradients or
+    outputs that overlap are refused."""
     max_norm = _max_norm(max_norm)
     table = _GradTable(grads)
     _check_rows("norm", norm.reshape(-1), (1,), torch.float32, table.device)
-    table.clip(norm, max_norm, grads_out)
+    _call("lce_clip_grads", table.device, table.ptrs, table.outputs(grads_out),
+          table.codes, table.sizes, table.n, norm.data_ptr(), max_norm)
 
 
 def clip_grad_norm(grads, max_norm: float, grads_out=None, workspace=None):
@@ -1383,8 +1402,13 @@ def clip_grad_norm(grads, max_norm: float, grads_out=None, workspace=None):
     before the clipping)."""
     max_norm = _max_norm(max_norm)
     table = _GradTable(grads)
-    norm = table.norm(workspace)
-    table.clip(norm, max_norm, grads_out)
+    dev = table.device
+    outs = table.outputs(grads_out)
+    ws = table.workspace(workspace)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    _call("lce_clip_grad_norm", dev, table.ptrs, outs, table.codes,
+          table.sizes, table.n, max_norm, norm.data_ptr(), ws.data_ptr(),
+          ws.numel() * ws.element_size())
     return norm
 
 

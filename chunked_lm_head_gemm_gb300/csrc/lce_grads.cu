@@ -1,21 +1,27 @@
 // The norm of many gradients together, and their clipping (lce_grad_norm /
-// lce_clip_grads).
+// lce_clip_grads / lce_clip_grad_norm).
 //
 // norm = sqrt(sum of all g^2), out = min(1, max_norm / (norm + 1e-6)) g. A
-// launch takes a table of tensors as its argument; their elements are cut into
-// chunks, and a block takes every gridDim-th chunk.
+// launch takes a table of tensors as its argument. The 16-byte vectors of a
+// tensor are cut into chunks of 32 KB, and a block takes every gridDim-th
+// chunk; elements before the first and behind the last whole vector go with
+// the tensor's first chunk.
 //
-// Squares of a group of a few elements are added in fp32, groups in fp64. A
-// group whose sum leaves the range in which fp32 squares are exact to their
-// rounding is added again in fp64 from the elements, so gradients far below
-// 1e-19 or above 1e19 count in full.
+// Squares of four vectors (16 or 32 elements) are added in fp32, groups in
+// fp64. A group whose sum leaves the range in which fp32 squares are exact to
+// their rounding is added again in fp64 from the elements, so gradients far
+// below 1e-19 or above 1e19 count in full.
 //
 // Bound: the bytes of the gradients, read for the norm, read and written for
-// the clipping.
+// the clipping, which starts from the end, where the first pass has left them
+// in L2.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include <algorithm>
 #include <new>
+#include <tuple>
+#include <utility>
 
 #include "lce_host.h"
 #include "lce_vec.cuh"
@@ -23,21 +29,31 @@
 namespace lce {
 namespace {
 
-constexpr int TABLE = 96;        // tensors of a launch
+constexpr int TABLE = 256;  // tensors of a launch
 constexpr int GRAD_BLOCKS = 608;
 constexpr int GRAD_THREADS = 256;
-constexpr int64_t CHUNK = 16384;  // elements
+constexpr int UNROLL = 8;  // vectors of a chunk that a thread holds
+constexpr int CHUNK = GRAD_THREADS * UNROLL;  // vectors
+constexpr int GROUP = 4;   // vectors whose squares are added in fp32
 
 struct GradTable {
   const void* grad[TABLE];
   void* out[TABLE];
   int64_t size[TABLE];
-  int64_t first[TABLE + 1];  // chunks before a tensor's own
+  int first[TABLE + 1];  // chunks before a tensor's own
   uint8_t f32[TABLE];
   int count;
 };
 
-__device__ __forceinline__ int tensor_of(const GradTable& t, int64_t chunk) {
+// A chunk of a table: vectors [v0, v1) of its tensor's whole ones, which begin
+// `head` elements into it.
+struct Piece {
+  int k;
+  bool f32, ends;  // ends: with the elements outside the whole vectors
+  int64_t head, whole, v0, v1;
+};
+
+__device__ __forceinline__ Piece piece_of(const GradTable& t, int chunk) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -46,69 +62,241 @@ __device__ __forceinline__ int tensor_of(const GradTable& t, int64_t chunk) {
     else
       hi = mid - 1;
   }
-  return lo;
+  Piece p;
+  p.k = lo;
+  p.f32 = t.f32[lo];
+  const int shift = p.f32 ? 2 : 1;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(t.grad[lo]);
+  const int64_t n = t.size[lo];
+  p.head = static_cast<int64_t>((16 - (a & 15)) & 15) >> shift;
+  p.head = min(p.head, n);
+  p.whole = (n - p.head) >> (4 - shift);
+  const int64_t c = chunk - t.first[lo];
+  p.ends = c == 0;
+  p.v0 = c * CHUNK;
+  p.v1 = min(p.v0 + CHUNK, p.whole);
+  return p;
 }
 
-template <int N>
-__device__ __forceinline__ void add_squares(const float (&v)[N], double& sum) {
-  float s = 0.f;
-  bool any = false;
+__device__ __forceinline__ void unpack(uint4 q, bool f32, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    s = fmaf(v[i], v[i], s);
-    any |= v[i] != 0.f;
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(f32 ? w[i] : w[i] << 16);
+    v[2 * i + 1] = f32 ? 0.f : __uint_as_float(w[i] & 0xffff0000u);
   }
-  if (s >= 1e-28f && s <= 1e37f) {
+}
+
+__device__ __forceinline__ bool in_range(float s) {
+  return s >= 1e-28f && s <= 1e37f;
+}
+
+__device__ __forceinline__ double square64(float v) {
+  return static_cast<double>(v) * static_cast<double>(v);
+}
+
+// Squares of a group; 0 stands for absent elements.
+__device__ __forceinline__ void add_squares(const uint4 (&q)[GROUP], bool f32,
+                                            double& sum) {
+  float s = 0.f;
+  uint32_t any = 0;
+#pragma unroll
+  for (int g = 0; g < GROUP; ++g) {
+    const uint32_t w[4] = {q[g].x, q[g].y, q[g].z, q[g].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      any |= w[i];
+      if (f32) {
+        const float v = __uint_as_float(w[i]);
+        s = fmaf(v, v, s);
+      } else {
+        const float a = __uint_as_float(w[i] << 16);
+        const float b = __uint_as_float(w[i] & 0xffff0000u);
+        s = fmaf(a, a, s);
+        s = fmaf(b, b, s);
+      }
+    }
+  }
+  if (in_range(s)) {
     sum += static_cast<double>(s);
-  } else if (any) {
-    for (int i = 0; i < N; ++i)
-      sum += static_cast<double>(v[i]) * static_cast<double>(v[i]);
+  } else if (any & (f32 ? 0x7fffffffu : 0x7fff7fffu)) {
+#pragma unroll
+    for (int g = 0; g < GROUP; ++g) {
+      float v[8];
+      unpack(q[g], f32, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += square64(v[i]);
+    }
+  }
+}
+
+// A block's share of the squares, blocks taking chunks first, first + step...
+__device__ __forceinline__ double squares(const GradTable& t, int first,
+                                          int step) {
+  double sum = 0.0;
+  for (int c = first; c < t.first[t.count]; c += step) {
+    const Piece p = piece_of(t, c);
+    const uint4* v = reinterpret_cast<const uint4*>(
+        static_cast<const char*>(t.grad[p.k]) + p.head * (p.f32 ? 4 : 2));
+    uint4 q[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int64_t i = p.v0 + u * GRAD_THREADS + threadIdx.x;
+      q[u] = i < p.v1 ? v[i] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; u += GROUP) {
+      uint4 g[GROUP];
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) g[i] = q[u + i];
+      if (p.f32)
+        add_squares(g, true, sum);
+      else
+        add_squares(g, false, sum);
+    }
+    if (p.ends) {
+      const int64_t body = p.whole * (p.f32 ? 4 : 8);
+      const int64_t rest = t.size[p.k] - body;  // before and behind
+      if (threadIdx.x < rest) {
+        const int64_t i =
+            threadIdx.x < p.head ? threadIdx.x : threadIdx.x + body;
+        sum += square64(load_as_float(t.grad[p.k], p.f32, i));
+      }
+    }
+  }
+  return sum;
+}
+
+// The factor of a norm: NaN for a norm that is NaN.
+__device__ __forceinline__ float factor(float norm, float max_norm) {
+  const double r =
+      static_cast<double>(max_norm) / (static_cast<double>(norm) + 1e-6);
+  return isinf(max_norm) || r >= 1.0 ? 1.f : static_cast<float>(r);
+}
+
+__device__ __forceinline__ uint4 scaled(uint4 q, bool f32, float scale) {
+  uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = f32 ? __float_as_uint(__uint_as_float(w[i]) * scale)
+               : pack_bf16x2(__uint_as_float(w[i] << 16) * scale,
+                             __uint_as_float(w[i] & 0xffff0000u) * scale);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Chunks from the last one down. An output that does not lie like its
+// gradient relative to 16 bytes is written element by element.
+__device__ __forceinline__ void clip(const GradTable& t, int first, int step,
+                                     float scale) {
+  const int chunks = t.first[t.count];
+  for (int c = chunks - 1 - first; c >= 0; c -= step) {
+    const Piece p = piece_of(t, c);
+    const void* grad = t.grad[p.k];
+    void* out = t.out[p.k];
+    if (scale == 1.f && out == grad) continue;
+    const int per = p.f32 ? 4 : 8, size = p.f32 ? 4 : 2;
+    if (((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(out)) &
+         15) == 0) {
+      const uint4* v = reinterpret_cast<const uint4*>(
+          static_cast<const char*>(grad) + p.head * size);
+      uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(out) +
+                                          p.head * size);
+      uint4 q[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int64_t i = p.v0 + u * GRAD_THREADS + threadIdx.x;
+        if (i < p.v1) q[u] = __ldcs(v + i);
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int64_t i = p.v0 + u * GRAD_THREADS + threadIdx.x;
+        if (i < p.v1) __stcs(o + i, scaled(q[u], p.f32, scale));
+      }
+    } else {
+      const int64_t i1 = p.head + p.v1 * per;
+#pragma unroll 8
+      for (int64_t i = p.head + p.v0 * per + threadIdx.x; i < i1;
+           i += GRAD_THREADS)
+        store_from_float(out, p.f32, i, load_as_float(grad, p.f32, i) * scale);
+    }
+    if (p.ends) {
+      const int64_t body = p.whole * per;
+      if (threadIdx.x < t.size[p.k] - body) {
+        const int64_t i =
+            threadIdx.x < p.head ? threadIdx.x : threadIdx.x + body;
+        store_from_float(out, p.f32, i, load_as_float(grad, p.f32, i) * scale);
+      }
+    }
   }
 }
 
 __global__ void __launch_bounds__(GRAD_THREADS)
     k_grad_squares(const __grid_constant__ GradTable t, double* part) {
   __shared__ double warps[32];
-  double sum = 0.0;
-  for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int k = tensor_of(t, c);
-    const int64_t i0 = (c - t.first[k]) * CHUNK;
-    const int64_t i1 = min(i0 + CHUNK, t.size[k]);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += GRAD_THREADS) {
-      const float v[1] = {load_as_float(t.grad[k], t.f32[k], i)};
-      add_squares(v, sum);
-    }
-  }
-  sum = block_sum(sum, warps);
+  const double sum = block_sum(squares(t, blockIdx.x, gridDim.x), warps);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(1024)
+// The norm of all blocks' squares, the same bits in every thread of any block.
+__device__ __forceinline__ float norm_of(const double* part, int64_t n,
+                                         double* warps) {
+  double sum = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += GRAD_THREADS) sum += part[i];
+  return static_cast<float>(sqrt(block_sum(sum, warps)));
+}
+
+__global__ void __launch_bounds__(GRAD_THREADS)
     k_grad_norm(const double* part, int64_t n, float* norm) {
   __shared__ double warps[32];
-  double sum = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) sum += part[i];
-  sum = block_sum(sum, warps);
-  if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(sum));
+  wait_for_earlier();
+  const float v = norm_of(part, n, warps);
+  if (threadIdx.x == 0) *norm = v;
 }
 
 __global__ void __launch_bounds__(GRAD_THREADS)
     k_clip(const __grid_constant__ GradTable t, const float* norm,
            float max_norm) {
-  const double r =
-      static_cast<double>(max_norm) / (static_cast<double>(*norm) + 1e-6);
-  // a norm that is NaN makes every gradient NaN
-  const float scale = isinf(max_norm) || r >= 1.0 ? 1.f : static_cast<float>(r);
-  for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int k = tensor_of(t, c);
-    if (scale == 1.f && t.out[k] == t.grad[k]) continue;
-    const int64_t i0 = (c - t.first[k]) * CHUNK;
-    const int64_t i1 = min(i0 + CHUNK, t.size[k]);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += GRAD_THREADS)
-      store_from_float(t.out[k], t.f32[k], i,
-                       load_as_float(t.grad[k], t.f32[k], i) * scale);
-  }
+  clip(t, blockIdx.x, gridDim.x, factor(*norm, max_norm));
 }
+
+// Clipping behind k_grad_squares: every block forms the norm for itself.
+__global__ void __launch_bounds__(GRAD_THREADS)
+    k_norm_clip(const __grid_constant__ GradTable t, const double* part,
+                int64_t n, float max_norm, float* norm) {
+  __shared__ double warps[32];
+  wait_for_earlier();
+  const float v = norm_of(part, n, warps);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+  clip(t, blockIdx.x, gridDim.x, factor(v, max_norm));
+}
+
+// Few chunks: one cluster does it all, its blocks' sums passed through
+// distributed shared memory.
+constexpr int SMALL_BLOCKS = 8;
+__global__ void __launch_bounds__(GRAD_THREADS)
+    k_clip_small(const __grid_constant__ GradTable t, float max_norm,
+                 float* norm) {
+  namespace cg = cooperative_groups;
+  __shared__ double warps[32];
+  __shared__ double sums[SMALL_BLOCKS];
+  cg::cluster_group cluster = cg::this_cluster();
+  // every block has begun before another writes its shared memory
+  auto begun = cluster.barrier_arrive();
+  const double sum = block_sum(squares(t, blockIdx.x, SMALL_BLOCKS), warps);
+  cluster.barrier_wait(std::move(begun));
+  if (threadIdx.x < SMALL_BLOCKS)
+    *cluster.map_shared_rank(&sums[blockIdx.x], threadIdx.x) = sum;
+  cluster.sync();
+  double all = 0.0;
+  for (int i = 0; i < SMALL_BLOCKS; ++i) all += sums[i];
+  const float v = static_cast<float>(sqrt(all));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+  // the chunks that this block has read: those it takes from the end are
+  // another's, whose reads the cluster's barrier has ended
+  clip(t, blockIdx.x, SMALL_BLOCKS, factor(v, max_norm));
+}
+
+constexpr int64_t MAX_ELEMENTS = 1ll << 40;
 
 int64_t bytes_of(lce_dtype dt, int64_t n) { return n * (dt == LCE_F32 ? 4 : 2); }
 
@@ -116,9 +304,12 @@ lce_status check(const void* const* grads, const lce_dtype* dts,
                  const int64_t* sizes, int64_t n) {
   if (n < 0 || n > (1 << 20)) return LCE_ERR_INVALID_ARG;
   if (n > 0 && (!grads || !dts || !sizes)) return LCE_ERR_INVALID_ARG;
+  int64_t total = 0;  // chunks are counted in 32 bits
   for (int64_t i = 0; i < n; ++i) {
     if (dts[i] != LCE_BF16 && dts[i] != LCE_F32) return LCE_ERR_UNSUPPORTED;
-    if (sizes[i] < 0 || sizes[i] > (1ll << 40)) return LCE_ERR_INVALID_ARG;
+    if (sizes[i] < 0 || sizes[i] > MAX_ELEMENTS - total)
+      return LCE_ERR_INVALID_ARG;
+    total += sizes[i];
     if (sizes[i] > 0 &&
         (!grads[i] || !aligned_to(grads[i], dts[i] == LCE_F32 ? 4 : 2)))
       return LCE_ERR_INVALID_ARG;
@@ -160,35 +351,103 @@ lce_status check_disjoint(const void* const* grads, void* const* outs,
   return ok ? LCE_OK : LCE_ERR_INVALID_ARG;
 }
 
-// Calls launch(table, index) for every table of up to TABLE tensors.
+lce_status check_outputs(const void* const* grads, void* const* outs,
+                         const lce_dtype* dts, const int64_t* sizes, int64_t n,
+                         const float* norm, float max_norm) {
+  if (n > 0 && !outs) return LCE_ERR_INVALID_ARG;
+  if (!norm || !aligned_to(norm, 4) || !(max_norm >= 0.f))
+    return LCE_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < n; ++i)
+    if (sizes[i] > 0 &&
+        (!outs[i] || !aligned_to(outs[i], dts[i] == LCE_F32 ? 4 : 2)))
+      return LCE_ERR_INVALID_ARG;
+  return check_disjoint(grads, outs, dts, sizes, n, norm);
+}
+
+// Chunks of a tensor, one at least.
+int64_t chunks_of(const void* grad, lce_dtype dt, int64_t n) {
+  const int64_t size = dt == LCE_F32 ? 4 : 2;
+  const int64_t head =
+      (16 - (reinterpret_cast<uintptr_t>(grad) & 15)) % 16 / size;
+  const int64_t whole = n > head ? (n - head) / (16 / size) : 0;
+  return whole > CHUNK ? ceil_div(whole, CHUNK) : 1;
+}
+
+// Calls launch(table, blocks) for every table of up to TABLE tensors.
 template <class F>
 cudaError_t each_table(const void* const* grads, void* const* outs,
                        const lce_dtype* dts, const int64_t* sizes, int64_t n,
                        F&& launch) {
   GradTable t;
-  int index = 0;
   t.count = 0;
   t.first[0] = 0;
   for (int64_t i = 0; i < n; ++i) {
     if (sizes[i] > 0) {
+      const int64_t chunks = chunks_of(grads[i], dts[i], sizes[i]);
       const int k = t.count++;
       t.grad[k] = grads[i];
       t.out[k] = outs ? outs[i] : nullptr;
       t.size[k] = sizes[i];
       t.f32[k] = dts[i] == LCE_F32;
-      t.first[k + 1] = t.first[k] + ceil_div(sizes[i], CHUNK);
+      t.first[k + 1] = t.first[k] + static_cast<int>(chunks);
     }
     if (t.count == TABLE || (i == n - 1 && t.count > 0)) {
-      const int64_t chunks = t.first[t.count];
-      const int grid =
-          static_cast<int>(chunks < GRAD_BLOCKS ? chunks : GRAD_BLOCKS);
-      launch(t, grid, index++);
-      const cudaError_t e = cudaGetLastError();
+      const int chunks = t.first[t.count];
+      const cudaError_t e =
+          launch(t, chunks < GRAD_BLOCKS ? chunks : GRAD_BLOCKS);
       if (e != cudaSuccess) return e;
       t.count = 0;
     }
   }
   return cudaSuccess;
+}
+
+// Chunks up to which one cluster takes them all.
+constexpr int64_t SMALL_CHUNKS = 32;
+
+// Launches a kernel whose first argument is a table: `early` while the kernel
+// before it still runs (it waits for it itself), or its blocks as one cluster.
+enum class Launch { plain, early, cluster };
+template <class... P, class... A>
+cudaError_t launch_table(void (*kern)(GradTable, P...), Launch how, int blocks,
+                         cudaStream_t s, const GradTable& t, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(GRAD_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (how == Launch::early) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = how == Launch::plain ? 0 : 1;
+  std::tuple<P...> rest(static_cast<P>(args)...);
+  return std::apply(
+      [&](auto&... r) {
+        void* ptrs[] = {const_cast<GradTable*>(&t), static_cast<void*>(&r)...};
+        return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kern),
+                                   ptrs);
+      },
+      rest);
+}
+
+// The squares of every table, a part for each of its blocks.
+cudaError_t launch_squares(const void* const* grads, const lce_dtype* dts,
+                           const int64_t* sizes, int64_t n, double* part,
+                           int64_t* parts, cudaStream_t s) {
+  return each_table(grads, nullptr, dts, sizes, n,
+                    [&](const GradTable& t, int grid) {
+                      double* to = part + *parts;
+                      *parts += grid;
+                      return launch_table(k_grad_squares, Launch::plain, grid,
+                                          s, t, to);
+                    });
 }
 
 }  // namespace
@@ -217,15 +476,10 @@ lce_status lce_grad_norm(const void* const* grads, const lce_dtype* dts,
   double* part = static_cast<double*>(ws);
   int64_t parts = 0;
   ProfScope ps(LCE_K_GRAD_NORM, s);
-  cudaError_t e = each_table(
-      grads, nullptr, dts, sizes, n, [&](const GradTable& t, int grid, int) {
-        k_grad_squares<<<grid, GRAD_THREADS, 0, s>>>(t, part + parts);
-        parts += grid;
-      });
-  if (e == cudaSuccess) {
-    k_grad_norm<<<1, 1024, 0, s>>>(part, parts, norm);
-    e = cudaGetLastError();
-  }
+  cudaError_t e = launch_squares(grads, dts, sizes, n, part, &parts, s);
+  if (e == cudaSuccess)
+    e = launch_early(k_grad_norm, dim3(1), dim3(GRAD_THREADS), 0, s, part,
+                     parts, norm);
   ps.done(0);
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, "grad_norm");
 }
@@ -234,24 +488,61 @@ lce_status lce_clip_grads(const void* const* grads, void* const* outs,
                           const lce_dtype* dts, const int64_t* sizes, int64_t n,
                           const float* norm, float max_norm, void* stream) {
   LCE_TRY(check(grads, dts, sizes, n));
-  if (n > 0 && !outs) return LCE_ERR_INVALID_ARG;
-  if (!norm || !aligned_to(norm, 4) || !(max_norm >= 0.f))
-    return LCE_ERR_INVALID_ARG;
-  for (int64_t i = 0; i < n; ++i)
-    if (sizes[i] > 0 &&
-        (!outs[i] || !aligned_to(outs[i], dts[i] == LCE_F32 ? 4 : 2)))
-      return LCE_ERR_INVALID_ARG;
-  LCE_TRY(check_disjoint(grads, outs, dts, sizes, n, norm));
+  LCE_TRY(check_outputs(grads, outs, dts, sizes, n, norm, max_norm));
   DeviceInfo* dev = nullptr;
   LCE_TRY(device_info(&dev));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ProfScope ps(LCE_K_CLIP_GRADS, s);
   const cudaError_t e = each_table(
-      grads, outs, dts, sizes, n, [&](const GradTable& t, int grid, int) {
-        k_clip<<<grid, GRAD_THREADS, 0, s>>>(t, norm, max_norm);
+      grads, outs, dts, sizes, n, [&](const GradTable& t, int grid) {
+        return launch_table(k_clip, Launch::plain, grid, s, t, norm, max_norm);
       });
   ps.done(0);
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, "clip_grads");
+}
+
+lce_status lce_clip_grad_norm(const void* const* grads, void* const* outs,
+                              const lce_dtype* dts, const int64_t* sizes,
+                              int64_t n, float max_norm, float* norm, void* ws,
+                              size_t ws_bytes, void* stream) {
+  LCE_TRY(check(grads, dts, sizes, n));
+  LCE_TRY(check_outputs(grads, outs, dts, sizes, n, norm, max_norm));
+  if (!ws || !aligned_to(ws, 16)) return LCE_ERR_INVALID_ARG;
+  if (ws_bytes < lce_grad_norm_workspace_size(n)) return LCE_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  LCE_TRY(device_info(&dev));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(ws);
+  int64_t parts = 0, chunks = 0, tensors = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (sizes[i] == 0) continue;
+    ++tensors;
+    chunks += chunks_of(grads[i], dts[i], sizes[i]);
+  }
+  cudaError_t e = cudaSuccess;
+  ProfScope ps(LCE_K_CLIP_GRADS, s);
+  if (tensors > 0 && tensors <= TABLE && chunks <= SMALL_CHUNKS) {
+    e = each_table(grads, outs, dts, sizes, n, [&](const GradTable& t, int) {
+      return launch_table(k_clip_small, Launch::cluster, SMALL_BLOCKS, s, t,
+                          max_norm, norm);
+    });
+  } else {
+    e = launch_squares(grads, dts, sizes, n, part, &parts, s);
+    bool first = true;
+    if (e == cudaSuccess && tensors == 0)
+      e = launch_early(k_grad_norm, dim3(1), dim3(GRAD_THREADS), 0, s, part,
+                       parts, norm);
+    if (e == cudaSuccess)
+      e = each_table(grads, outs, dts, sizes, n,
+                     [&](const GradTable& t, int grid) {
+                       float* to = first ? norm : nullptr;
+                       first = false;
+                       return launch_table(k_norm_clip, Launch::early, grid, s,
+                                           t, part, parts, max_norm, to);
+                     });
+  }
+  ps.done(0);
+  return e == cudaSuccess ? LCE_OK : cuda_fail(e, "clip_grad_norm");
 }
 
 }  // extern "C"

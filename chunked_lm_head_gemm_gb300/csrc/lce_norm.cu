@@ -16,7 +16,6 @@
 // Wider rows are read again where a pass over them needs it.
 #include <math.h>
 
-#include "lce_device.cuh"
 #include "lce_host.h"
 #include "lce_vec.cuh"
 
@@ -50,40 +49,6 @@ constexpr int TEAM_WARPS = 8;     // warps of a block whose teams are lanes
 constexpr int MAX_THREADS = 512;  // of a block that is a team
 constexpr int MAX_FAST_H = EPT * MAX_THREADS;
 constexpr int MAX_STAGES = 8;
-
-template <typename T, int V>
-struct Chunk;  // V elements as they lie in memory
-template <>
-struct Chunk<float, 4> {
-  uint4 q;
-  __device__ __forceinline__ float at(int i) const {
-    return __uint_as_float(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w);
-  }
-  __device__ __forceinline__ void pack(const float* v) {
-    q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
-                   __float_as_uint(v[2]), __float_as_uint(v[3]));
-  }
-};
-template <>
-struct Chunk<__nv_bfloat16, 8> {
-  uint4 q;
-  __device__ __forceinline__ float at(int i) const {
-    const uint32_t w = i < 2 ? q.x : i < 4 ? q.y : i < 6 ? q.z : q.w;
-    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-  }
-  __device__ __forceinline__ void pack(const float* v) {
-    q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  }
-};
-template <typename T>
-struct Chunk<T, 1> {
-  T q;
-  __device__ __forceinline__ float at(int) const { return to_float(q); }
-  __device__ __forceinline__ void pack(const float* v) {
-    q = from_float<T>(v[0]);
-  }
-};
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
                                           uint32_t bytes, uint32_t bar) {

@@ -1,8 +1,7 @@
 // Device helpers of the row-wise operators (norms, balance loss, gradient
 // clipping): typed loads and stores, warp and block reductions.
 #pragma once
-#include <cuda_bf16.h>
-#include <stdint.h>
+#include "lce_device.cuh"
 
 namespace lce {
 
@@ -35,6 +34,53 @@ __device__ __forceinline__ void store_from_float(void* p, bool f32, int64_t i,
     static_cast<float*>(p)[i] = v;
   else
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+template <typename T, int V>
+struct Chunk;  // V elements as they lie in memory
+template <>
+struct Chunk<float, 4> {
+  uint4 q;
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w);
+  }
+  __device__ __forceinline__ void pack(const float* v) {
+    q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                   __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Chunk<__nv_bfloat16, 8> {
+  uint4 q;
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? q.x : i < 4 ? q.y : i < 6 ? q.z : q.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+  __device__ __forceinline__ void pack(const float* v) {
+    q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+};
+template <typename T>
+struct Chunk<T, 1> {
+  T q;
+  __device__ __forceinline__ float at(int) const { return to_float(q); }
+  __device__ __forceinline__ void pack(const float* v) {
+    q = from_float<T>(v[0]);
+  }
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Chunk<T, V> load_chunk(const T* p) {
+  Chunk<T, V> c;
+  c.q = *reinterpret_cast<const decltype(c.q)*>(p);
+  return c;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_chunk(T* p, const float* v) {
+  Chunk<T, V> c;
+  c.pack(v);
+  *reinterpret_cast<decltype(c.q)*>(p) = c.q;
 }
 
 template <typename V>

@@ -745,7 +745,8 @@ lce_status lce_expert_counts(const int32_t* experts, const uint8_t* mask,
  *   out  = min(1, max_norm / (norm + 1e-6)) g
  *   grads, outs  host arrays of n device pointers; outs[i] may be grads[i]
  *   dts, sizes   host arrays: type (LCE_BF16 or LCE_F32) and elements of
- *                each; an empty tensor's pointers are not looked at
+ *                each, 2^40 at most in all; an empty tensor's pointers are not
+ *                looked at
  *   norm         device [1] float32, out of lce_grad_norm (or any other, such
  *                as the root of squares summed over processes), into
  *                lce_clip_grads
@@ -765,6 +766,16 @@ lce_status lce_grad_norm(const void* const* grads, const lce_dtype* dts,
 lce_status lce_clip_grads(const void* const* grads, void* const* outs,
                           const lce_dtype* dts, const int64_t* sizes, int64_t n,
                           const float* norm, float max_norm, void* stream);
+
+/*
+ * lce_grad_norm and lce_clip_grads in one call (norm: device [1] float32 out):
+ * fewer launches, one alone for few small gradients. The squares' fp64 sum may
+ * be formed in another order than lce_grad_norm's.
+ */
+lce_status lce_clip_grad_norm(const void* const* grads, void* const* outs,
+                              const lce_dtype* dts, const int64_t* sizes,
+                              int64_t n, float max_norm, float* norm, void* ws,
+                              size_t ws_bytes, void* stream);
 
 /*
  * Selects how the tensor-core contractions run, for the whole process:

@@ -40,6 +40,7 @@ class Recorder:
 def lib(monkeypatch):
     rec = Recorder()
     monkeypatch.setattr(B, "load", lambda *a: rec)
+    monkeypatch.setattr(B, "_lib", None)
     monkeypatch.setattr(B, "_stream_ptr", lambda device: 0)
     sizes = (B.norm_workspace_size, B.balance_workspace_size,
              B.grad_norm_workspace_size)
@@ -143,10 +144,14 @@ def test_balance_inputs(lib):
     assert len(lib.calls) == 2
 
 
-def test_gradient_lists(lib):
+def test_gradient_lists(lib, monkeypatch):
     g = [t(3, 4), t(5, dtype=BF)]
     with pytest.raises(ValueError, match="one device"):
-        lce.grad_norm([t(3), meta(3)])
+        lce.grad_norm([meta(3), t(3)])
+    with monkeypatch.context() as m:
+        m.setattr(torch.Tensor, "get_device", lambda g: g.dim())
+        with pytest.raises(ValueError, match="one device"):
+            lce.grad_norm([t(3), t(3, 1)])
     with pytest.raises(ValueError, match="CUDA"):
         lce.grad_norm([torch.zeros(3)])
     with pytest.raises(TypeError, match="dtype"):
@@ -160,8 +165,9 @@ def test_gradient_lists(lib):
         with pytest.raises(ValueError, match="max_norm"):
             lce.clip_grads(g, t(), bad)
     n = t()
-    for outs in ([t(4, 3), t(5, dtype=BF)], [t(3, 4), t(5)],
-                 [t(4, 3).t(), t(5, dtype=BF)]):
+    for outs in ([t(4, 4), t(5, dtype=BF)], [t(3, 4), t(5)],
+                 [t(4, 3).t(), t(5, dtype=BF)],
+                 [t(3, 4), t(5, dtype=torch.float16)]):
         with pytest.raises(ValueError, match="output"):
             lce.clip_grads(g, n, 1.0, grads_out=outs)
     with pytest.raises(ValueError, match="outputs for"):
@@ -170,9 +176,11 @@ def test_gradient_lists(lib):
         with pytest.raises(ValueError, match="norm"):
             lce.clip_grads(g, bad, 1.0)
     assert not lib.calls
+    lce.clip_grads(g, n, 1.0, grads_out=[t(12), t(5, dtype=BF)])
+    lce.clip_grad_norm([g[0].t(), g[1]], 1.0, grads_out=[t(3, 4).t(), g[1]])
     lce.clip_grad_norm([g[0].t(), g[1]], 1.0)
     name, args = lib.calls[-1]
-    assert name == "lce_clip_grads" and list(args[3]) == [12, 5]
+    assert name == "lce_clip_grad_norm" and list(args[3]) == [12, 5]
     assert list(args[2]) == [B.LCE_F32, B.LCE_BF16]
     assert list(args[0]) == list(args[1]) == [x.data_ptr() for x in g]
 
@@ -198,9 +206,10 @@ def test_a_call_runs_with_its_tensors_device_current(monkeypatch):
             seen.append(args)
             return 0
 
-    monkeypatch.setattr(B, "load", lambda *a: Lib)
+    monkeypatch.setattr(B, "_lib", Lib)
     monkeypatch.setattr(B, "_stream_ptr", lambda d: 100 + d.index)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0,
+                        raising=False)
     monkeypatch.setattr(torch.cuda, "device", Guard)
     B._call("f", torch.device("cuda", 0), 1, 2)
     assert seen == [(1, 2, 100)]
@@ -304,12 +313,16 @@ def test_c_grads(c):
 
     def clip(rows, nrm=P, limit=1.0):
         g, o, d, s, n = table(rows)
-        return c.lce_clip_grads(g, o, d, s, n, nrm, limit, NULL)
+        first = c.lce_clip_grads(g, o, d, s, n, nrm, limit, NULL)
+        assert c.lce_clip_grad_norm(g, o, d, s, n, limit, nrm, P, 1 << 20,
+                                    NULL) == first
+        return first
 
     A, BB = 0x10000, 0x20000
     ok = [(A, A, 1, 100)]
     for rows in ([(0, A, 1, 4)], [(A + 2, A, 1, 4)], [(A, A, 1, -1)],
-                 [(A, A, 1, (1 << 40) + 1)]):
+                 [(A, A, 1, (1 << 40) + 1)],
+                 [(A, A, 1, 1 << 40), (BB, BB, 1, 1)]):
         assert norm(rows) == B.LCE_ERR_INVALID_ARG
         assert clip(rows) == B.LCE_ERR_INVALID_ARG
     assert norm([(A, A, 5, 4)]) == B.LCE_ERR_UNSUPPORTED
@@ -317,6 +330,11 @@ def test_c_grads(c):
     assert norm(ok, ws=NULL) == B.LCE_ERR_INVALID_ARG
     assert norm(ok, size=8) == B.LCE_ERR_WORKSPACE
     assert clip(ok, nrm=NULL) == B.LCE_ERR_INVALID_ARG
+    g, o, d, s, n = table(ok)
+    assert c.lce_clip_grad_norm(g, o, d, s, n, 1.0, P, NULL, 1 << 20,
+                                NULL) == B.LCE_ERR_INVALID_ARG
+    assert c.lce_clip_grad_norm(g, o, d, s, n, 1.0, P, P, 8,
+                                NULL) == B.LCE_ERR_WORKSPACE
     for limit in (-1.0, math.nan):
         assert clip(ok, limit=limit) == B.LCE_ERR_INVALID_ARG
     for rows in ([(A, 0, 1, 4)], [(A, BB + 1, 0, 4)],
