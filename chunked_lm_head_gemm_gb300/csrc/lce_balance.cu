@@ -9,8 +9,15 @@
 // is used, formed in fp64 from the counts, so that an even load, where the
 // differences are small, loses nothing to rounding.
 //
-// Bound: the bytes of the logits (read in each direction) and dlogits.
+// Bound: the bytes of the logits (read in each direction) and dlogits. A team
+// of lanes holds a row, 8 elements to a lane up to 256 experts, so that a warp
+// has several rows of few experts; a lane has the same experts in every row
+// and adds their scores in registers. Exponentials and reciprocals are the
+// approximate instructions (2^-22 of a score).
+#include <cooperative_groups.h>
 #include <math.h>
+
+#include <utility>
 
 #include "lce_host.h"
 #include "lce_vec.cuh"
@@ -20,7 +27,9 @@ namespace {
 
 constexpr int MAX_E = 1024;
 constexpr int WARPS = 8;
-constexpr int64_t MAX_BLOCKS = 304;
+constexpr int64_t MAX_BLOCKS = 608;
+constexpr int JOIN_BLOCKS = 8;  // of one cluster
+constexpr int JOIN_THREADS = 512;
 
 struct BalanceArgs {
   const void* logits;
@@ -28,177 +37,297 @@ struct BalanceArgs {
   const uint8_t* mask;
   int64_t L;
   int E, K;
-  int scoring;
+  int team;  // lanes of a row
   float coef;
   float* loss;
   int32_t* counts;
   float* slopes;
   const float* dloss;
   void* dlogits;
-  float* part_p;    // [blocks][E] sums of p
-  int* part_n;      // [blocks][E + 1] slots of each expert, tokens
+  float* part_p;  // [blocks][E] sums of p
+  int* part_n;    // [blocks][E + 1] slots of each expert, tokens
   int blocks;
   unsigned* err;
 };
 
-__device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+__device__ __forceinline__ float team_max(float v, int team) {
+  for (int o = team >> 1; o > 0; o >>= 1)
     v = fmaxf(v, __shfl_xor_sync(ALL_LANES, v, o));
   return v;
 }
+__device__ __forceinline__ float team_sum(float v, int team) {
+  for (int o = team >> 1; o > 0; o >>= 1)
+    v += __shfl_xor_sync(ALL_LANES, v, o);
+  return v;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 // A row's normalised scores in place of its logits (0 where all are -inf),
-// and with SLOPE the factor of the score's derivative. Element lane + 32 i.
-// Sigmoid scores are taken relative to the row's largest, e^{min(z, 0) - m} /
-// (1 + e^{-|z|}), so that a row of very negative logits keeps its ratios.
-template <int PER, bool SLOPE>
-__device__ __forceinline__ void probabilities(float (&z)[PER],
-                                              float (&slope)[PER], int scoring) {
+// and with SLOPE the factor of a sigmoid score's derivative. Sigmoid scores
+// are taken relative to the row's largest, e^{min(z, 0) - m} / (1 + e^{-|z|}),
+// so that a row of very negative logits keeps its ratios.
+template <int N, bool SIGMOID, bool SLOPE>
+__device__ __forceinline__ void probabilities(float (&z)[N], float (&slope)[N],
+                                              int team) {
   float m = -INFINITY;
-  const bool sig = scoring == LCE_SIGMOID;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) m = fmaxf(m, sig ? fminf(z[i], 0.f) : z[i]);
-  m = lanes_max(m);
+  for (int i = 0; i < N; ++i) m = fmaxf(m, z[i]);
+  m = team_max(m, team);
+  if (SIGMOID) m = fminf(m, 0.f);
   if (m == -INFINITY) m = 0.f;
   float t = 0.f;
+  if (SIGMOID) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (sig) {
-      const float q = expf(-fabsf(z[i])), d = 1.f / (1.f + q);
-      const float e = z[i] < 0.f ? (m == 0.f ? q : expf(z[i] - m)) : 1.f;
-      if (SLOPE) slope[i] = z[i] < 0.f ? d : q * d;
-      z[i] = e * d;
-    } else {
-      z[i] = expf(z[i] - m);
+    for (int i = 0; i < N; ++i) {
+      const float q = ex2(-fabsf(z[i]) * LOG2E);
+      const float d = reciprocal(1.f + q), qd = q * d;
+      const bool low = z[i] < 0.f;
+      if (SLOPE) slope[i] = low ? d : qd;
+      if (m == 0.f)
+        z[i] = low ? qd : d;
+      else
+        z[i] = ex2((z[i] - m) * LOG2E) * d;
+      t += z[i];
     }
-    t += z[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      z[i] = ex2((z[i] - m) * LOG2E);
+      t += z[i];
+    }
   }
-  t = lanes_sum(t);
+  t = team_sum(t, team);
   const float inv = t == 0.f ? 0.f : 1.f / t;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) z[i] *= inv;
+  for (int i = 0; i < N; ++i) z[i] *= inv;
 }
 
-template <typename T, int PER>
-__device__ __forceinline__ void load_row(const T* row, int E, int lane,
-                                         float (&z)[PER]) {
+// The row's elements of a lane, runs of V; -inf beyond E.
+template <typename T, int N, int V>
+__device__ __forceinline__ void load_row(const T* row, bool on, int E, int id,
+                                         int team, Chunk<T, V> (&q)[N / V]) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int j = lane + 32 * i;
-    z[i] = j < E ? to_float(row[j]) : -INFINITY;
+  for (int c = 0; c < N / V; ++c) {
+    const int j = (id + team * c) * V;
+    if (on && j < E) q[c] = load_chunk<T, V>(row + j);
+  }
+}
+template <typename T, int N, int V>
+__device__ __forceinline__ void unpack_row(const Chunk<T, V> (&q)[N / V],
+                                           bool on, int E, int id, int team,
+                                           float (&z)[N]) {
+#pragma unroll
+  for (int c = 0; c < N / V; ++c) {
+    const bool has = on && (id + team * c) * V < E;
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[c * V + i] = has ? q[c].at(i) : -INFINITY;
   }
 }
 
+// Slots of tokens [t0, t1) into hist, a few loads under way at a time.
 __device__ __forceinline__ void count_slots(const int32_t* experts,
                                             const uint8_t* mask, int64_t t0,
                                             int64_t t1, int K, int E, int* hist,
                                             unsigned* err) {
-  for (int64_t i = t0 * K + threadIdx.x; i < t1 * K; i += blockDim.x) {
-    if (mask && !mask[i / K]) continue;
-    const int e = experts[i];
-    if (e >= 0 && e < E)
-      atomicAdd(&hist[e], 1);
-    else if (e != -1)
-      atomicOr(err, ERRBIT_EXPERT_RANGE);
+  constexpr int AHEAD = 4;
+  const int64_t end = t1 * K;
+  for (int64_t i0 = t0 * K + threadIdx.x; i0 < end;
+       i0 += AHEAD * static_cast<int64_t>(blockDim.x)) {
+    int e[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int64_t i = i0 + u * static_cast<int64_t>(blockDim.x);
+      e[u] = -1;
+      if (i < end && (!mask || mask[static_cast<uint32_t>(i) / K]))
+        e[u] = experts[i];
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (static_cast<unsigned>(e[u]) < static_cast<unsigned>(E))
+        atomicAdd(&hist[e[u]], 1);
+      else if (e[u] != -1)
+        atomicOr(err, ERRBIT_EXPERT_RANGE);
+    }
   }
 }
 
-// Block b takes rows [b, b + 1) L / blocks.
-template <typename T, int PER>
+// What the sums over tokens give for expert e: its term of the loss / coef.
+__device__ __forceinline__ double finish(const BalanceArgs& a, int e, int count,
+                                         double p, int tokens) {
+  const double inv = tokens > 0 ? 1.0 / tokens : 0.0;
+  const double f = count * inv * a.E / a.K;
+  a.counts[e] = count;
+  a.slopes[e] = static_cast<float>(a.coef * inv * (f - 1.0));
+  return f * (p * inv);
+}
+
+// Block b counts the slots of tokens [b, b + 1) L / blocks; the rows of logits
+// go to the warps of all blocks in turn.
+template <typename T, int N, int V, bool SIGMOID>
 __global__ void __launch_bounds__(WARPS * 32) k_balance(const BalanceArgs a) {
-  extern __shared__ float smem[];
-  float* sums = smem;                                   // [WARPS][E]
-  int* hist = reinterpret_cast<int*>(smem + WARPS * a.E);  // [E + 1]
+  extern __shared__ float sums[];                       // [WARPS][E]
+  int* hist = reinterpret_cast<int*>(sums + WARPS * a.E);  // [E + 1]
+  __shared__ double part[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int id = lane & (a.team - 1), sub = lane / a.team;
+  const int at_once = 32 / a.team;
   for (int e = threadIdx.x; e <= a.E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
-  const int64_t t0 = a.L * blockIdx.x / a.blocks;
-  const int64_t t1 = a.L * (blockIdx.x + 1) / a.blocks;
-  count_slots(a.experts, a.mask, t0, t1, a.K, a.E, hist, a.err);
-  float acc[PER] = {}, z[PER], unused[PER];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * at_once;
+  const int64_t first =
+      (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * at_once;
+  const T* logits = static_cast<const T*>(a.logits);
+  // the next row is under way while one is computed, its mask one before that
+  auto takes_part = [&](int64_t t) {
+    return t < a.L && (!a.mask || a.mask[t] != 0);
+  };
+  bool on = takes_part(first + sub);
+  bool on_next = takes_part(first + step + sub);
+  Chunk<T, V> q[N / V];
+  load_row<T, N, V>(logits + (first + sub) * a.E, on, a.E, id, a.team, q);
+  count_slots(a.experts, a.mask, a.L * blockIdx.x / a.blocks,
+              a.L * (blockIdx.x + 1) / a.blocks, a.K, a.E, hist, a.err);
+  float acc[N], z[N], unused[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
   int tokens = 0;
-  for (int64_t t = t0 + warp; t < t1; t += WARPS) {
-    if (a.mask && !a.mask[t]) continue;
-    ++tokens;
-    load_row(static_cast<const T*>(a.logits) + t * a.E, a.E, lane, z);
-    probabilities<PER, false>(z, unused, a.scoring);
+  for (int64_t t0 = first; t0 < a.L; t0 += step) {
+    unpack_row<T, N, V>(q, on, a.E, id, a.team, z);
+    tokens += on;
+    const int64_t next = t0 + step + sub;
+    on = on_next;
+    load_row<T, N, V>(logits + next * a.E, on, a.E, id, a.team, q);
+    on_next = takes_part(next + step);
+    probabilities<N, SIGMOID, false>(z, unused, a.team);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] += z[i];
+    for (int i = 0; i < N; ++i) acc[i] += z[i];
   }
-  if (lane == 0) atomicAdd(&hist[a.E], tokens);
+  if (id == 0 && tokens) atomicAdd(&hist[a.E], tokens);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int j = lane + 32 * i;
-    if (j < a.E) sums[warp * a.E + j] = acc[i];
+  for (int i = 0; i < N; ++i) {
+    for (int o = a.team; o < 32; o <<= 1)
+      acc[i] += __shfl_xor_sync(ALL_LANES, acc[i], o);
+    const int j = (id + a.team * (i / V)) * V + i % V;
+    if (sub == 0 && j < a.E) sums[warp * a.E + j] = acc[i];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
-    a.part_n[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + e] = hist[e];
-    if (e == a.E) continue;
+  double term = 0.0;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     float s = 0.f;
     for (int w = 0; w < WARPS; ++w) s += sums[w * a.E + e];
-    a.part_p[static_cast<int64_t>(blockIdx.x) * a.E + e] = s;
+    if (gridDim.x == 1) {
+      term += finish(a, e, hist[e], s, hist[a.E]);
+    } else {
+      a.part_n[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + e] = hist[e];
+      a.part_p[static_cast<int64_t>(blockIdx.x) * a.E + e] = s;
+    }
+  }
+  if (gridDim.x == 1) {
+    term = block_sum(term, part);
+    if (threadIdx.x == 0) *a.loss = static_cast<float>(term * a.coef);
+  } else if (threadIdx.x == 0) {
+    a.part_n[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + a.E] = hist[a.E];
   }
 }
 
-__global__ void __launch_bounds__(1024) k_balance_join(const BalanceArgs a) {
+// The blocks' sums: block r of the cluster has experts r, r + JOIN_BLOCKS, ...
+// A warp's 32 lanes take the blocks of one expert in turn.
+__global__ void __launch_bounds__(JOIN_THREADS)
+    k_balance_join(const BalanceArgs a) {
+  namespace cg = cooperative_groups;
   __shared__ int tokens_of[32];
   __shared__ double part[32];
+  __shared__ double terms[JOIN_BLOCKS];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31;
+  // every block has begun before another writes its shared memory
+  auto begun = cluster.barrier_arrive();
+  wait_for_earlier();
   int n = 0;
   for (int b = threadIdx.x; b < a.blocks; b += blockDim.x)
     n += a.part_n[static_cast<int64_t>(b) * (a.E + 1) + a.E];
   n = block_sum(n, tokens_of);
-  const double inv = n > 0 ? 1.0 / n : 0.0;
   double term = 0.0;
-  const int e = threadIdx.x;
-  if (e < a.E) {
+  for (int e = blockIdx.x + JOIN_BLOCKS * (threadIdx.x >> 5); e < a.E;
+       e += JOIN_BLOCKS * (JOIN_THREADS / 32)) {
     int c = 0;
     double p = 0.0;
-    for (int b = 0; b < a.blocks; ++b) {
+#pragma unroll 4
+    for (int b = lane; b < a.blocks; b += 32) {
       c += a.part_n[static_cast<int64_t>(b) * (a.E + 1) + e];
       p += a.part_p[static_cast<int64_t>(b) * a.E + e];
     }
-    const double f = c * inv * a.E / a.K;
-    term = f * (p * inv);
-    a.counts[e] = c;
-    a.slopes[e] = static_cast<float>(a.coef * inv * (f - 1.0));
+    c = lanes_sum(c);
+    p = lanes_sum(p);
+    if (lane == 0) term += finish(a, e, c, p, n);
   }
-  const double loss = block_sum(term, part) * a.coef;
-  if (threadIdx.x == 0) *a.loss = static_cast<float>(loss);
+  term = block_sum(term, part);
+  cluster.barrier_wait(std::move(begun));
+  if (threadIdx.x == 0)
+    *cluster.map_shared_rank(&terms[blockIdx.x], 0) = term;
+  cluster.sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    double loss = 0.0;
+    for (int r = 0; r < JOIN_BLOCKS; ++r) loss += terms[r];
+    *a.loss = static_cast<float>(loss * a.coef);
+  }
 }
 
-template <typename T, int PER>
+template <typename T, int N, int V, bool SIGMOID>
 __global__ void __launch_bounds__(WARPS * 32)
     k_balance_bwd(const BalanceArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int id = lane & (a.team - 1), sub = lane / a.team;
+  const int at_once = 32 / a.team;
   const float d = *a.dloss;
-  float f[PER], z[PER], slope[PER];
+  float f[N], z[N], slope[N];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int j = lane + 32 * i;
+  for (int i = 0; i < N; ++i) {
+    const int j = (id + a.team * (i / V)) * V + i % V;
     f[i] = j < a.E ? a.slopes[j] * d : 0.f;
   }
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * WARPS + warp; t < a.L;
-       t += static_cast<int64_t>(gridDim.x) * WARPS) {
-    T* out = static_cast<T*>(a.dlogits) + t * a.E;
-    const bool on = !a.mask || a.mask[t];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * at_once;
+  const int64_t first =
+      (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * at_once;
+  const T* logits = static_cast<const T*>(a.logits);
+  auto takes_part = [&](int64_t t) {
+    return t < a.L && (!a.mask || a.mask[t] != 0);
+  };
+  bool on = takes_part(first + sub);
+  bool on_next = takes_part(first + step + sub);
+  Chunk<T, V> q[N / V];
+  load_row<T, N, V>(logits + (first + sub) * a.E, on, a.E, id, a.team, q);
+  for (int64_t t0 = first; t0 < a.L; t0 += step) {
+    unpack_row<T, N, V>(q, on, a.E, id, a.team, z);
+    const bool was_on = on;
+    const int64_t next = t0 + step + sub;
+    on = on_next;
+    load_row<T, N, V>(logits + next * a.E, on, a.E, id, a.team, q);
+    on_next = takes_part(next + step);
+    probabilities<N, SIGMOID, true>(z, slope, a.team);
     float dot = 0.f;
-    if (on) {
-      load_row(static_cast<const T*>(a.logits) + t * a.E, a.E, lane, z);
-      probabilities<PER, true>(z, slope, a.scoring);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) dot = fmaf(f[i], z[i], dot);
-      dot = lanes_sum(dot);
-    }
+    for (int i = 0; i < N; ++i) dot = fmaf(f[i], z[i], dot);
+    dot = team_sum(dot, a.team);
+    if (t0 + sub >= a.L) continue;
+    T* out = static_cast<T*>(a.dlogits) + (t0 + sub) * a.E;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int j = lane + 32 * i;
+    for (int c = 0; c < N / V; ++c) {
+      const int j = (id + a.team * c) * V;
       if (j >= a.E) continue;
-      float v = 0.f;
-      if (on) v = z[i] * (f[i] - dot);
-      if (on && a.scoring == LCE_SIGMOID) v *= slope[i];
-      out[j] = from_float<T>(v);
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int k = c * V + i;
+        o[i] = z[k] * (f[k] - dot);
+        if (SIGMOID) o[i] *= slope[k];
+        if (!was_on) o[i] = 0.f;
+      }
+      store_chunk<T, V>(out + j, o);
     }
   }
 }
@@ -222,9 +351,18 @@ __global__ void __launch_bounds__(COUNT_THREADS)
   }
 }
 
-// Blocks of a forward pass: a warp has a row at least.
-int blocks_of(int64_t L) {
-  const int64_t n = ceil_div(L, WARPS);
+// Elements of a row that a lane holds, and the lanes of its team.
+int held(int64_t E) { return E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+int team_of(int64_t E) {
+  int team = 1;
+  while (team * held(E) < E) team *= 2;
+  return team;
+}
+
+// Blocks of a forward pass: four rows to a team at least, as far as the
+// blocks' sums are worth their joining; one block does it alone.
+int blocks_of(int64_t L, int64_t E) {
+  const int64_t n = ceil_div(L, WARPS * 32 / team_of(E) * 4);
   return static_cast<int>(n < 1 ? 1 : n < MAX_BLOCKS ? n : MAX_BLOCKS);
 }
 
@@ -235,26 +373,66 @@ bool slots_ok(int64_t L, int64_t K) {
   return K >= 1 && K <= 32 && L * K <= (1ll << 30);
 }
 
-template <typename T>
-cudaError_t launch_forward(const BalanceArgs& a, cudaStream_t s) {
+template <typename T, int N, int V>
+cudaError_t forward(const BalanceArgs& a, bool sigmoid, cudaStream_t s) {
+  // at most 9 * 1024 + 1 words, below what needs no attribute
   const size_t smem = (WARPS * a.E + a.E + 1) * sizeof(float);
-  auto kern = a.E <= 128   ? k_balance<T, 4>
-              : a.E <= 256 ? k_balance<T, 8>
-              : a.E <= 512 ? k_balance<T, 16>
-                           : k_balance<T, 32>;
+  auto kern = sigmoid ? k_balance<T, N, V, true> : k_balance<T, N, V, false>;
   kern<<<a.blocks, WARPS * 32, smem, s>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.blocks == 1) return e;
+  return launch_early_cluster(k_balance_join, dim3(JOIN_BLOCKS),
+                              dim3(JOIN_THREADS), 0, s, JOIN_BLOCKS, a);
 }
 
-template <typename T>
-cudaError_t launch_backward(const BalanceArgs& a, int grid, cudaStream_t s) {
-  auto kern = a.E <= 128   ? k_balance_bwd<T, 4>
-              : a.E <= 256 ? k_balance_bwd<T, 8>
-              : a.E <= 512 ? k_balance_bwd<T, 16>
-                           : k_balance_bwd<T, 32>;
+template <typename T, int N, int V>
+cudaError_t backward(const BalanceArgs& a, bool sigmoid, int num_sms,
+                     cudaStream_t s) {
+  const int64_t need = ceil_div(a.L, WARPS * 32 / a.team), most = num_sms * 4;
+  const int grid = static_cast<int>(need < most ? need : most);
+  auto kern = sigmoid ? k_balance_bwd<T, N, V, true>
+                      : k_balance_bwd<T, N, V, false>;
   kern<<<grid, WARPS * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
+
+// Calls f.run<T, N, V>(): by type, row length and alignment.
+template <typename T, class F>
+cudaError_t by_size(int64_t E, bool wide, F&& f) {
+  constexpr int V = 16 / sizeof(T);
+  switch (held(E)) {
+    case 8: return wide ? f.template run<T, 8, V>() : f.template run<T, 8, 1>();
+    case 16:
+      return wide ? f.template run<T, 16, V>() : f.template run<T, 16, 1>();
+    default:
+      return wide ? f.template run<T, 32, V>() : f.template run<T, 32, 1>();
+  }
+}
+template <class F>
+cudaError_t by_type(lce_dtype dt, int64_t E, bool aligned, F&& f) {
+  if (dt == LCE_F32) return by_size<float>(E, aligned && E % 4 == 0, f);
+  return by_size<__nv_bfloat16>(E, aligned && E % 8 == 0, f);
+}
+
+struct Forward {
+  const BalanceArgs& a;
+  bool sigmoid;
+  cudaStream_t s;
+  template <typename T, int N, int V>
+  cudaError_t run() {
+    return forward<T, N, V>(a, sigmoid, s);
+  }
+};
+struct Backward {
+  const BalanceArgs& a;
+  bool sigmoid;
+  int num_sms;
+  cudaStream_t s;
+  template <typename T, int N, int V>
+  cudaError_t run() {
+    return backward<T, N, V>(a, sigmoid, num_sms, s);
+  }
+};
 
 }  // namespace
 }  // namespace lce
@@ -265,7 +443,7 @@ extern "C" {
 
 size_t lce_balance_workspace_size(int64_t L, int64_t E) {
   if (!sizes_ok(L, E)) return 0;
-  return static_cast<size_t>(blocks_of(L)) * (2 * E + 1) * 4;
+  return static_cast<size_t>(blocks_of(L, E)) * (2 * E + 1) * 4;
 }
 
 lce_status lce_balance_forward(const void* logits, lce_dtype dt,
@@ -295,22 +473,18 @@ lce_status lce_balance_forward(const void* logits, lce_dtype dt,
   a.L = L;
   a.E = static_cast<int>(E);
   a.K = static_cast<int>(top_k);
-  a.scoring = scoring;
+  a.team = team_of(E);
   a.coef = coef;
   a.loss = loss;
   a.counts = counts;
   a.slopes = slopes;
-  a.blocks = blocks_of(L);
+  a.blocks = blocks_of(L, E);
   a.part_p = static_cast<float*>(ws);
   a.part_n = reinterpret_cast<int*>(a.part_p + a.blocks * E);
   a.err = dev->err;
   ProfScope ps(LCE_K_BALANCE, s);
-  cudaError_t e = dt == LCE_F32 ? launch_forward<float>(a, s)
-                                : launch_forward<__nv_bfloat16>(a, s);
-  if (e == cudaSuccess) {
-    k_balance_join<<<1, 1024, 0, s>>>(a);
-    e = cudaGetLastError();
-  }
+  const cudaError_t e = by_type(dt, E, aligned_to(logits, 16),
+                                Forward{a, scoring == LCE_SIGMOID, s});
   ps.done(0);
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, "balance");
 }
@@ -338,16 +512,14 @@ lce_status lce_balance_backward(const void* logits, lce_dtype dt,
   a.mask = mask;
   a.L = L;
   a.E = static_cast<int>(E);
-  a.scoring = scoring;
+  a.team = team_of(E);
   a.slopes = const_cast<float*>(slopes);
   a.dloss = dloss;
   a.dlogits = dlogits;
-  const int64_t need = ceil_div(L, WARPS), most = dev->num_sms * 8;
-  const int grid = static_cast<int>(need < most ? need : most);
   ProfScope ps(LCE_K_BALANCE_BWD, s);
-  const cudaError_t e = dt == LCE_F32
-                            ? launch_backward<float>(a, grid, s)
-                            : launch_backward<__nv_bfloat16>(a, grid, s);
+  const cudaError_t e = by_type(
+      dt, E, aligned_to(logits, 16) && aligned_to(dlogits, 16),
+      Backward{a, scoring == LCE_SIGMOID, dev->num_sms, s});
   ps.done(0);
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, "balance_bwd");
 }
