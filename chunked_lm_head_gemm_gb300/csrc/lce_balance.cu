@@ -156,13 +156,16 @@ __device__ __forceinline__ void count_slots(const int32_t* experts,
 }
 
 // What the sums over tokens give for expert e: its term of the loss / coef.
+// f - 1 = (E counts - N K) / (N K), whose numerator is exact.
 __device__ __forceinline__ double finish(const BalanceArgs& a, int e, int count,
                                          double p, int tokens) {
-  const double inv = tokens > 0 ? 1.0 / tokens : 0.0;
-  const double f = count * inv * a.E / a.K;
+  const int64_t slots = static_cast<int64_t>(tokens) * a.K;
+  const int64_t load = static_cast<int64_t>(count) * a.E;
+  const double inv = slots > 0 ? 1.0 / static_cast<double>(slots) : 0.0;
   a.counts[e] = count;
-  a.slopes[e] = static_cast<float>(a.coef * inv * (f - 1.0));
-  return f * (p * inv);
+  a.slopes[e] = static_cast<float>(static_cast<double>(a.coef) * a.K * inv *
+                                   (static_cast<double>(load - slots) * inv));
+  return static_cast<double>(load) * inv * (p * inv * a.K);
 }
 
 // Block b counts the slots of tokens [b, b + 1) L / blocks; the rows of logits
@@ -227,23 +230,25 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance(const BalanceArgs a) {
     }
   }
   if (gridDim.x == 1) {
-    term = block_sum(term, part);
+    term = block_total(term, part);
     if (threadIdx.x == 0) *a.loss = static_cast<float>(term * a.coef);
   } else if (threadIdx.x == 0) {
     a.part_n[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + a.E] = hist[a.E];
   }
 }
 
-// The blocks' sums: block r of the cluster has experts r, r + JOIN_BLOCKS, ...
-// A warp's 32 lanes take the blocks of one expert in turn.
+// The blocks' sums: block r of the cluster has the experts 32 r + 256 i + lane,
+// its warps the blocks in turn.
 __global__ void __launch_bounds__(JOIN_THREADS)
     k_balance_join(const BalanceArgs a) {
   namespace cg = cooperative_groups;
+  constexpr int RUNS = JOIN_THREADS / 32;
   __shared__ int tokens_of[32];
-  __shared__ double part[32];
+  __shared__ LongSum sums[RUNS][32];
+  __shared__ int counts[RUNS][32];
   __shared__ double terms[JOIN_BLOCKS];
   cg::cluster_group cluster = cg::this_cluster();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   // every block has begun before another writes its shared memory
   auto begun = cluster.barrier_arrive();
   wait_for_earlier();
@@ -252,20 +257,40 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     n += a.part_n[static_cast<int64_t>(b) * (a.E + 1) + a.E];
   n = block_sum(n, tokens_of);
   double term = 0.0;
-  for (int e = blockIdx.x + JOIN_BLOCKS * (threadIdx.x >> 5); e < a.E;
-       e += JOIN_BLOCKS * (JOIN_THREADS / 32)) {
+  for (int e0 = 32 * blockIdx.x; e0 < a.E; e0 += 32 * JOIN_BLOCKS) {
+    const int e = e0 + lane;
     int c = 0;
-    double p = 0.0;
-#pragma unroll 4
-    for (int b = lane; b < a.blocks; b += 32) {
-      c += a.part_n[static_cast<int64_t>(b) * (a.E + 1) + e];
-      p += a.part_p[static_cast<int64_t>(b) * a.E + e];
+    LongSum p;
+    for (int b0 = run; b0 < a.blocks; b0 += 8 * RUNS) {
+      float v[8];
+      int k[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int b = b0 + u * RUNS;
+        const bool has = e < a.E && b < a.blocks;
+        v[u] = has ? a.part_p[static_cast<int64_t>(b) * a.E + e] : 0.f;
+        k[u] = has ? a.part_n[static_cast<int64_t>(b) * (a.E + 1) + e] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        p.add(v[u]);
+        c += k[u];
+      }
     }
-    c = lanes_sum(c);
-    p = lanes_sum(p);
-    if (lane == 0) term += finish(a, e, c, p, n);
+    sums[run][lane] = p;
+    counts[run][lane] = c;
+    __syncthreads();
+    if (run == 0 && e < a.E) {
+#pragma unroll
+      for (int q = 1; q < RUNS; ++q) {
+        p.add(sums[q][lane]);
+        c += counts[q][lane];
+      }
+      term += finish(a, e, c, p.value(), n);
+    }
+    __syncthreads();
   }
-  term = block_sum(term, part);
+  if (run == 0) term = lanes_sum(term);
   cluster.barrier_wait(std::move(begun));
   if (threadIdx.x == 0)
     *cluster.map_shared_rank(&terms[blockIdx.x], 0) = term;

@@ -233,16 +233,25 @@ __device__ __forceinline__ void clip(const GradTable& t, int first, int step,
 __global__ void __launch_bounds__(GRAD_THREADS)
     k_grad_squares(const __grid_constant__ GradTable t, double* part) {
   __shared__ double warps[32];
-  const double sum = block_sum(squares(t, blockIdx.x, gridDim.x), warps);
+  const double sum = block_total(squares(t, blockIdx.x, gridDim.x), warps);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// The norm of all blocks' squares, the same bits in every thread of any block.
+// The norm of all blocks' squares, in thread 0: the same bits in any block.
 __device__ __forceinline__ float norm_of(const double* part, int64_t n,
                                          double* warps) {
   double sum = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += GRAD_THREADS) sum += part[i];
-  return static_cast<float>(sqrt(block_sum(sum, warps)));
+  sum = block_total(sum, warps);
+  return threadIdx.x == 0 ? static_cast<float>(sqrt(sum)) : 0.f;
+}
+
+// Thread 0's factor for the block.
+__device__ __forceinline__ float shared_factor(float norm, float max_norm) {
+  __shared__ float scale;
+  if (threadIdx.x == 0) scale = factor(norm, max_norm);
+  __syncthreads();
+  return scale;
 }
 
 __global__ void __launch_bounds__(GRAD_THREADS)
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(GRAD_THREADS)
 __global__ void __launch_bounds__(GRAD_THREADS)
     k_clip(const __grid_constant__ GradTable t, const float* norm,
            float max_norm) {
-  clip(t, blockIdx.x, gridDim.x, factor(*norm, max_norm));
+  clip(t, blockIdx.x, gridDim.x, shared_factor(*norm, max_norm));
 }
 
 // Clipping behind k_grad_squares: every block forms the norm for itself.
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(GRAD_THREADS)
   wait_for_earlier();
   const float v = norm_of(part, n, warps);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
-  clip(t, blockIdx.x, gridDim.x, factor(v, max_norm));
+  clip(t, blockIdx.x, gridDim.x, shared_factor(v, max_norm));
 }
 
 // Few chunks: one cluster does it all, its blocks' sums passed through
@@ -282,18 +291,23 @@ __global__ void __launch_bounds__(GRAD_THREADS)
   cg::cluster_group cluster = cg::this_cluster();
   // every block has begun before another writes its shared memory
   auto begun = cluster.barrier_arrive();
-  const double sum = block_sum(squares(t, blockIdx.x, SMALL_BLOCKS), warps);
+  const double sum = block_total(squares(t, blockIdx.x, SMALL_BLOCKS), warps);
   cluster.barrier_wait(std::move(begun));
-  if (threadIdx.x < SMALL_BLOCKS)
-    *cluster.map_shared_rank(&sums[blockIdx.x], threadIdx.x) = sum;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SMALL_BLOCKS; ++i)
+      *cluster.map_shared_rank(&sums[blockIdx.x], i) = sum;
+  }
   cluster.sync();
-  double all = 0.0;
-  for (int i = 0; i < SMALL_BLOCKS; ++i) all += sums[i];
-  const float v = static_cast<float>(sqrt(all));
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+  float v = 0.f;
+  if (threadIdx.x == 0) {
+    double all = 0.0;
+    for (int i = 0; i < SMALL_BLOCKS; ++i) all += sums[i];
+    v = static_cast<float>(sqrt(all));
+    if (blockIdx.x == 0) *norm = v;
+  }
   // the chunks that this block has read: those it takes from the end are
   // another's, whose reads the cluster's barrier has ended
-  clip(t, blockIdx.x, SMALL_BLOCKS, factor(v, max_norm));
+  clip(t, blockIdx.x, SMALL_BLOCKS, shared_factor(v, max_norm));
 }
 
 constexpr int64_t MAX_ELEMENTS = 1ll << 40;

@@ -37,14 +37,17 @@ struct NormArgs {
   int team;       // threads of a row; a block's for a whole block
   int tile_rows;  // rows that a group takes at a time
   int stages;     // tiles of a group in shared memory
+  uint32_t array_bytes;  // of a tile's place there
   float* part;    // [slabs][2][H] sums of dy n and dy
   int slabs;
   int want_dx;
+  int size;  // bytes of an element
   uint64_t timeout_ns;
   unsigned* err;
 };
 
 constexpr int EPT = 16;           // elements of a row that a thread holds
+constexpr int PAIRS = EPT / 2;   // two elements of fp32 to an instruction
 constexpr int TEAM_WARPS = 8;     // warps of a block whose teams are lanes
 constexpr int MAX_THREADS = 512;  // of a block that is a team
 constexpr int MAX_FAST_H = EPT * MAX_THREADS;
@@ -60,25 +63,29 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
 }
 
 // Sums over a row's team: lanes by shuffles; a block also through shared
-// memory, one barrier a call, with two areas in turn.
+// memory, one barrier a call, with two areas in turn (16 warps at most).
 template <bool BLOCK, int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], int team,
-                                         float (*area)[N][32], int& turn) {
+                                         float (*area)[N][16], int& turn) {
   if (BLOCK) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = lanes_sum(v[i]);
-    float(*p)[32] = area[turn];
+    float(*p)[16] = area[turn];
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) p[i][threadIdx.x >> 5] = v[i];
     }
     __syncthreads();
-    const int warps = blockDim.x >> 5;
+    // absent warps left zeros
+    const int fours = (blockDim.x + 127) >> 7;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float t = p[i][0];
-      for (int w = 1; w < warps; ++w) t += p[i][w];
+      float t = 0.f;
+      for (int w = 0; w < fours; ++w) {
+        const float4 q = *reinterpret_cast<const float4*>(&p[i][4 * w]);
+        t += (q.x + q.y) + (q.z + q.w);
+      }
       v[i] = t;
     }
   } else {
@@ -92,14 +99,17 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int team,
 
 // A group (a warp of lane teams, or the block) and its ring of tiles. A tile
 // is tile_rows rows, one after the other in memory; the group takes tiles
-// first, first + step, ... Without RING the rows are read where they lie.
-template <typename T, bool BLOCK, bool RING, int ARRAYS>
+// first, first + step, ... What is copied is the 16-byte units that cover the
+// tile; a tile whose units reach past the array's ends (the first and last,
+// of arrays that do not begin or end on 16 bytes) is read where it lies.
+template <typename T, bool BLOCK, int ARRAYS>
 struct Tiles {
   const NormArgs& a;
   int64_t tiles, step, next;  // next: the tile to be fetched
   uint32_t ring, bars;
-  uint32_t array_bytes;
   int fetch_stage, stage, phase;
+  uint32_t offset[ARRAYS];  // of the present tile in its stage
+  bool copied[ARRAYS];
   WaitCtx ctx;
 
   __device__ __forceinline__ Tiles(const NormArgs& args, unsigned char* smem,
@@ -110,99 +120,132 @@ struct Tiles {
     tiles = (a.L + a.tile_rows - 1) / a.tile_rows;
     step = static_cast<int64_t>(gridDim.x) * groups;
     next = static_cast<int64_t>(blockIdx.x) * groups + group;
-    array_bytes = static_cast<uint32_t>(a.tile_rows) * a.H * sizeof(T);
-    ring = smem_u32(smem) + group * a.stages * ARRAYS * array_bytes;
+    ring = smem_u32(smem) + group * a.stages * ARRAYS * a.array_bytes;
     bars = smem_u32(bar) + group * MAX_STAGES * 8;
     fetch_stage = stage = phase = 0;
     ctx = WaitCtx{abort_flag, a.err, a.timeout_ns};
-    if (RING) {
-      if (threadIdx.x == 0) {
-        *abort_flag = 0;
-        for (int i = 0; i < groups * MAX_STAGES; ++i)
-          mbar_init(smem_u32(bar) + 8 * i, 1);
-        fence_mbar_init();
-      }
-      __syncthreads();
-      for (int i = 0; i < a.stages; ++i) fetch();
+    if (threadIdx.x == 0) {
+      *abort_flag = 0;
+      for (int i = 0; i < groups * MAX_STAGES; ++i)
+        mbar_init(smem_u32(bar) + 8 * i, 1);
+      fence_mbar_init();
     }
+    __syncthreads();
+    for (int i = 0; i < a.stages; ++i) fetch();
   }
   __device__ __forceinline__ bool leader() const {
     return BLOCK ? threadIdx.x == 0 : (threadIdx.x & 31) == 0;
   }
+  __device__ __forceinline__ const char* array(int i) const {
+    return static_cast<const char*>(i ? a.dy : a.x);
+  }
+  // The units that cover tile t of an array: where they begin, and their
+  // bytes, 0 if they reach past the array.
+  __device__ __forceinline__ uint32_t window(int i, int64_t t,
+                                             uintptr_t* from) const {
+    const int64_t row = t * a.tile_rows, bytes = a.H * sizeof(T);
+    const int64_t rows = min(static_cast<int64_t>(a.tile_rows), a.L - row);
+    const uintptr_t base = reinterpret_cast<uintptr_t>(array(i));
+    const uintptr_t begin = base + row * bytes, end = begin + rows * bytes;
+    *from = begin & ~static_cast<uintptr_t>(15);
+    const uintptr_t to = (end + 15) & ~static_cast<uintptr_t>(15);
+    if (*from < base || to > base + a.L * bytes) return 0;
+    return static_cast<uint32_t>(to - *from);
+  }
   // Fetches the group's next tile into the stage that was read last.
   __device__ __forceinline__ void fetch() {
-    if (!RING) return;
     if (next < tiles && leader()) {
-      const int64_t row = next * a.tile_rows;
-      const int64_t left = a.L - row;
-      const uint32_t bytes =
-          left < a.tile_rows
-              ? static_cast<uint32_t>(left) * a.H * sizeof(T)
-              : array_bytes;
+      uintptr_t from[ARRAYS];
+      uint32_t bytes[ARRAYS], all = 0;
+#pragma unroll
+      for (int i = 0; i < ARRAYS; ++i) all += bytes[i] = window(i, next, &from[i]);
       const uint32_t bar = bars + 8 * fetch_stage;
-      const uint32_t dst = ring + fetch_stage * ARRAYS * array_bytes;
-      mbar_arrive_expect_tx(bar, ARRAYS * bytes);
-      bulk_load(dst, static_cast<const T*>(a.x) + row * a.H, bytes, bar);
-      if (ARRAYS == 2)
-        bulk_load(dst + array_bytes, static_cast<const T*>(a.dy) + row * a.H,
-                  bytes, bar);
+      mbar_arrive_expect_tx(bar, all);
+#pragma unroll
+      for (int i = 0; i < ARRAYS; ++i)
+        if (bytes[i])
+          bulk_load(ring + (fetch_stage * ARRAYS + i) * a.array_bytes,
+                    reinterpret_cast<const void*>(from[i]), bytes[i], bar);
     }
     next += step;
     fetch_stage = fetch_stage + 1 == a.stages ? 0 : fetch_stage + 1;
   }
-  // Waits for the tile of the present stage. (Should the wait run out, which
+  // Waits for tile t in the present stage. (Should the wait run out, which
   // raises the error, the rows are wrong but every barrier is still met.)
-  __device__ __forceinline__ void wait() {
-    if (RING) mbar_wait(bars + 8 * stage, phase, ctx, true);
+  template <int V>
+  __device__ __forceinline__ void wait(int64_t t) {
+#pragma unroll
+    for (int i = 0; i < ARRAYS; ++i) {
+      offset[i] = ring + (stage * ARRAYS + i) * a.array_bytes;
+      copied[i] = true;
+      if (V == 1) {  // else rows begin and end on 16 bytes
+        uintptr_t from;
+        copied[i] = window(i, t, &from) != 0;
+        offset[i] += static_cast<uint32_t>(
+            reinterpret_cast<uintptr_t>(array(i)) +
+            t * a.tile_rows * a.H * sizeof(T) - from);
+      }
+    }
+    mbar_wait(bars + 8 * stage, phase, ctx, true);
   }
   __device__ __forceinline__ void advance() {
     stage = stage + 1 == a.stages ? 0 : stage + 1;
     if (stage == 0) phase ^= 1;
   }
-  // Chunk k of row r of the tile (array 0: x, 1: dy).
+  // Chunk k of row r of the tile, row `row` of the array (0: x, 1: dy).
   template <int V>
-  __device__ __forceinline__ Chunk<T, V> chunk(int array, int64_t row, int r,
+  __device__ __forceinline__ Chunk<T, V> chunk(int i, int64_t row, int r,
                                                int k) const {
     Chunk<T, V> c;
-    if constexpr (RING) {
-      const uint32_t at = ring + (stage * ARRAYS + array) * array_bytes +
-                          (static_cast<uint32_t>(r) * a.H + k * V) * sizeof(T);
+    const uint32_t at =
+        offset[i] + (static_cast<uint32_t>(r) * a.H + k * V) * sizeof(T);
+    if constexpr (V > 1) {
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(c.q.x), "=r"(c.q.y), "=r"(c.q.z), "=r"(c.q.w)
                    : "r"(at)
                    : "memory");
     } else {
-      const T* p = static_cast<const T*>(array ? a.dy : a.x) + row * a.H;
-      c.q = *reinterpret_cast<const decltype(c.q)*>(p + static_cast<int64_t>(k) * V);
+      if (!copied[i])
+        return load_chunk<T, V>(reinterpret_cast<const T*>(array(i)) +
+                                row * a.H + k);
+      if constexpr (sizeof(T) == 4) {
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(c.q) : "r"(at) : "memory");
+      } else {
+        unsigned short bits;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(bits)
+                     : "r"(at)
+                     : "memory");
+        c.q = __ushort_as_bfloat16(bits);
+      }
     }
     return c;
   }
 };
 
-// A thread's columns of weight or bias, `absent` where there is none.
-template <int V, int C>
+// A thread's columns of weight or bias in pairs, `absent` where there is none.
+template <int V>
 __device__ __forceinline__ void load_params(const void* p, bool f32, int H,
                                             int id, int team, float absent,
-                                            float (&w)[EPT]) {
+                                            uint64_t (&w)[PAIRS]) {
+  auto at = [&](int i) {
+    const int j = (id + team * (i / V)) * V + i % V;
+    return j >= H ? 0.f : p ? load_as_float(p, f32, j) : absent;
+  };
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int j = (id + team * c) * V + i;
-      w[c * V + i] = j >= H ? 0.f : p ? load_as_float(p, f32, j) : absent;
-    }
-  }
+  for (int i = 0; i < PAIRS; ++i) w[i] = f2pack(at(2 * i), at(2 * i + 1));
 }
 
 template <typename T, int V, bool BLOCK, bool LAYER>
 __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const NormArgs a) {
   constexpr int C = EPT / V;
-  constexpr bool RING = V > 1;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t bar[TEAM_WARPS * MAX_STAGES];
   __shared__ uint32_t abort_flag;
-  __shared__ float area[2][1][32];
-  Tiles<T, BLOCK, RING, 1> tiles(a, smem, bar, &abort_flag);
+  __shared__ __align__(16) float area[2][1][16];
+  if (threadIdx.x < 32) area[threadIdx.x >> 4][0][threadIdx.x & 15] = 0.f;
+  __syncthreads();
+  Tiles<T, BLOCK, 1> tiles(a, smem, bar, &abort_flag);
   const int team = BLOCK ? blockDim.x : a.team;
   const int id = BLOCK ? threadIdx.x : threadIdx.x & (team - 1);
   const int rows_at_once = BLOCK ? 1 : 32 / team;
@@ -210,65 +253,75 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const NormArgs a) {
   const int chunks = a.H / V;
   const float inv = 1.f / a.H;
   int turn = 0;
-  float w[EPT], b[EPT];
-  load_params<V, C>(a.weight, a.param_f32, a.H, id, team, 1.f, w);
-  if (LAYER) load_params<V, C>(a.bias, a.param_f32, a.H, id, team, 0.f, b);
+  uint64_t w[PAIRS], b[PAIRS];
+  load_params<V>(a.weight, a.param_f32, a.H, id, team, 1.f, w);
+  if (LAYER) load_params<V>(a.bias, a.param_f32, a.H, id, team, 0.f, b);
   const int64_t first =
       BLOCK ? blockIdx.x
             : static_cast<int64_t>(blockIdx.x) * TEAM_WARPS + (threadIdx.x >> 5);
   for (int64_t t = first; t < tiles.tiles; t += tiles.step) {
-    tiles.wait();
+    tiles.template wait<V>(t);
     for (int m = 0; m < a.tile_rows; m += rows_at_once) {
       const int r = m + sub;
       const int64_t row = t * a.tile_rows + r;
       const bool on = row < a.L;
-      float v[EPT], s[1] = {0.f};
+      Chunk<T, V> x[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int k = id + team * c;
-        const bool has = on && k < chunks;
-        Chunk<T, V> q;
-        if (has) q = tiles.template chunk<V>(0, row, r, k);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          v[c * V + i] = has ? q.at(i) : 0.f;
-          if (LAYER) s[0] += v[c * V + i];
-        }
+        x[c] = on && k < chunks ? tiles.template chunk<V>(0, row, r, k)
+                                : no_chunk<T, V>();
       }
-      float mu = 0.f;
+      float mu = 0.f, s[1];
+      uint64_t q = 0;  // a pair of zeros
       if (LAYER) {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) q = add2(q, pair_of(x, i));
+        s[0] = sum_of_pair(q);
         team_sum<BLOCK, 1>(s, team, area, turn);
         mu = s[0] * inv;
-        s[0] = 0.f;
+        q = 0;
       }
+      const uint64_t minus = f2pack(-mu, -mu);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const bool has = id + team * c < chunks;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = v[c * V + i] - mu;
-          if (LAYER) v[c * V + i] = d;
-          if (has) s[0] = fmaf(d, d, s[0]);
+      for (int i = 0; i < PAIRS; ++i) {
+        uint64_t d = pair_of(x, i);
+        if (LAYER) {
+          d = add2(d, minus);
+          // columns past the row's end
+          if constexpr (V == 1) {
+            float lo, hi;
+            f2unpack(d, lo, hi);
+            if (id + team * 2 * i >= chunks) lo = 0.f;
+            if (id + team * (2 * i + 1) >= chunks) hi = 0.f;
+            d = f2pack(lo, hi);
+          } else if (id + team * (2 * i / V) >= chunks) {
+            d = 0;
+          }
         }
+        q = fma2(d, d, q);
       }
+      s[0] = sum_of_pair(q);
       team_sum<BLOCK, 1>(s, team, area, turn);
       if (BLOCK) tiles.fetch();  // every thread has its elements
       const float rs = 1.f / sqrtf(s[0] * inv + a.eps);
+      const uint64_t rs2 = f2pack(rs, rs);
       if (on) {
         T* y = static_cast<T*>(a.y) + row * a.H;
+        float o[EPT];
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+          uint64_t d = pair_of(x, i);
+          if (LAYER) d = add2(d, minus);
+          d = mul2(d, rs2);
+          d = LAYER ? fma2(d, w[i], b[i]) : mul2(d, w[i]);
+          f2unpack(d, o[2 * i], o[2 * i + 1]);
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const int k = id + team * c;
-          if (k >= chunks) continue;
-          float o[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            o[i] = v[c * V + i] * rs * w[c * V + i];
-            if (LAYER) o[i] += b[c * V + i];
-          }
-          Chunk<T, V> q;
-          q.pack(o);
-          *reinterpret_cast<decltype(q.q)*>(y + static_cast<int64_t>(k) * V) = q.q;
+          if (k < chunks)
+            store_chunk<T, V>(y + static_cast<int64_t>(k) * V, &o[c * V]);
         }
         if (id == 0) {
           if (LAYER && a.mean) a.mean[row] = mu;
@@ -288,13 +341,16 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const NormArgs a) {
 template <typename T, int V, bool BLOCK, bool LAYER>
 __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
   constexpr int C = EPT / V;
-  constexpr bool RING = V > 1;
+  constexpr int SUMS = LAYER ? 2 : 1;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t bar[TEAM_WARPS * MAX_STAGES];
   __shared__ uint32_t abort_flag;
-  __shared__ float area[2][2][32];
+  __shared__ __align__(16) float area[2][SUMS][16];
   __shared__ float sums[BLOCK ? 1 : 2 * 32 * EPT];
-  Tiles<T, BLOCK, RING, 2> tiles(a, smem, bar, &abort_flag);
+  for (int i = threadIdx.x; i < 32 * SUMS; i += blockDim.x)
+    (&area[0][0][0])[i] = 0.f;
+  __syncthreads();
+  Tiles<T, BLOCK, 2> tiles(a, smem, bar, &abort_flag);
   const int team = BLOCK ? blockDim.x : a.team;
   const int id = BLOCK ? threadIdx.x : threadIdx.x & (team - 1);
   const int rows_at_once = BLOCK ? 1 : 32 / team;
@@ -302,65 +358,86 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
   const int chunks = a.H / V;
   const float inv = 1.f / a.H;
   int turn = 0;
-  float w[EPT], dw[EPT], db[EPT];
-  load_params<V, C>(a.weight, a.param_f32, a.H, id, team, 1.f, w);
+  uint64_t w[PAIRS], dw[PAIRS], db[PAIRS];
+  load_params<V>(a.weight, a.param_f32, a.H, id, team, 1.f, w);
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < PAIRS; ++i) dw[i] = db[i] = 0;
   const int64_t first =
       BLOCK ? blockIdx.x
             : static_cast<int64_t>(blockIdx.x) * TEAM_WARPS + (threadIdx.x >> 5);
+  // the statistics of the next rows are under way while rows are computed
+  float rs_next = 0.f, mu_next = 0.f;
+  auto look_ahead = [&](int64_t row) {
+    const bool on = row < a.L;
+    rs_next = on ? a.rstd[row] : 0.f;
+    if (LAYER) mu_next = on ? a.mean[row] : 0.f;
+  };
+  look_ahead(first * a.tile_rows + sub);
   for (int64_t t = first; t < tiles.tiles; t += tiles.step) {
-    tiles.wait();
+    tiles.template wait<V>(t);
     for (int m = 0; m < a.tile_rows; m += rows_at_once) {
       const int r = m + sub;
       const int64_t row = t * a.tile_rows + r;
       const bool on = row < a.L;
-      const float rs = on ? a.rstd[row] : 0.f;
-      const float mu = LAYER && on ? a.mean[row] : 0.f;
+      const float rs = rs_next;
+      const uint64_t rs2 = f2pack(rs, rs);
+      const uint64_t minus = f2pack(-mu_next, -mu_next);
+      look_ahead(m + rows_at_once < a.tile_rows
+                     ? row + rows_at_once
+                     : (t + tiles.step) * a.tile_rows + sub);
       Chunk<T, V> x[C], dy[C];
-      float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int k = id + team * c;
-        if (!on || k >= chunks) continue;
-        x[c] = tiles.template chunk<V>(0, row, r, k);
-        dy[c] = tiles.template chunk<V>(1, row, r, k);
+        const bool has = on && k < chunks;
+        x[c] = has ? tiles.template chunk<V>(0, row, r, k) : no_chunk<T, V>();
+        dy[c] = has ? tiles.template chunk<V>(1, row, r, k) : no_chunk<T, V>();
+      }
+      auto normed = [&](int i) {
+        uint64_t n = pair_of(x, i);
+        if (LAYER) n = add2(n, minus);
+        return mul2(n, rs2);
+      };
+      uint64_t sg = 0, sgn = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = dy[c].at(i), n = (x[c].at(i) - mu) * rs;
-          const float g = d * w[c * V + i];
-          dw[c * V + i] = fmaf(d, n, dw[c * V + i]);
-          if (LAYER) {
-            db[c * V + i] += d;
-            s[0] += g;
-          }
-          s[1] = fmaf(g, n, s[1]);
+      for (int i = 0; i < PAIRS; ++i) {
+        const uint64_t d = pair_of(dy, i), dn = mul2(d, normed(i));
+        dw[i] = add2(dw[i], dn);
+        sgn = fma2(dn, w[i], sgn);
+        if (LAYER) {
+          db[i] = add2(db[i], d);
+          sg = fma2(d, w[i], sg);
         }
       }
       if (!a.want_dx) {
-        if (BLOCK) __syncthreads();
-        if (BLOCK) tiles.fetch();
+        if (BLOCK) {
+          __syncthreads();
+          tiles.fetch();
+        }
         continue;
       }
-      team_sum<BLOCK, 2>(s, team, area, turn);
+      float s[SUMS];
+      s[0] = sum_of_pair(sgn);
+      if (LAYER) s[SUMS - 1] = sum_of_pair(sg);
+      team_sum<BLOCK, SUMS>(s, team, area, turn);
       if (BLOCK) tiles.fetch();
-      const float c1 = LAYER ? s[0] * inv : 0.f, c2 = s[1] * inv;
+      const float c2 = -rs * (s[0] * inv);
+      const float c1 = LAYER ? -rs * (s[SUMS - 1] * inv) : 0.f;
+      const uint64_t c22 = f2pack(c2, c2), c12 = f2pack(c1, c1);
       if (on) {
         T* dx = static_cast<T*>(a.y) + row * a.H;
+        float o[EPT];
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+          uint64_t g = mul2(pair_of(dy, i), w[i]);
+          g = LAYER ? fma2(g, rs2, c12) : mul2(g, rs2);
+          f2unpack(fma2(normed(i), c22, g), o[2 * i], o[2 * i + 1]);
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const int k = id + team * c;
-          if (k >= chunks) continue;
-          float o[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float n = (x[c].at(i) - mu) * rs;
-            const float g = dy[c].at(i) * w[c * V + i];
-            o[i] = rs * (g - c1 - n * c2);
-          }
-          Chunk<T, V> q;
-          q.pack(o);
-          *reinterpret_cast<decltype(q.q)*>(dx + static_cast<int64_t>(k) * V) = q.q;
+          if (k < chunks)
+            store_chunk<T, V>(dx + static_cast<int64_t>(k) * V, &o[c * V]);
         }
       }
     }
@@ -372,47 +449,46 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
   }
   if (!a.part) return;
   float* p = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
-  if (BLOCK) {
+  float aw[EPT], ab[EPT];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
+  for (int i = 0; i < PAIRS; ++i) {
+    f2unpack(dw[i], aw[2 * i], aw[2 * i + 1]);
+    f2unpack(db[i], ab[2 * i], ab[2 * i + 1]);
+  }
+  if constexpr (BLOCK) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = (id + team * c) * V + i;
-        if (j >= a.H) continue;
-        p[j] = dw[c * V + i];
-        if (LAYER) p[a.H + j] = db[c * V + i];
+    for (int i = 0; i < EPT; ++i) {
+      const int j = (id + team * (i / V)) * V + i % V;
+      if (j >= a.H) continue;
+      p[j] = aw[i];
+      if (LAYER) p[a.H + j] = ab[i];
+    }
+  } else {
+    // the warp's teams by shuffles, then the warps one after the other
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      for (int o = team; o < 32; o <<= 1) {
+        aw[i] += __shfl_xor_sync(ALL_LANES, aw[i], o);
+        if (LAYER) ab[i] += __shfl_xor_sync(ALL_LANES, ab[i], o);
       }
     }
-    return;
-  }
-  // the warp's teams by shuffles, then the warps one after the other
+    for (int turn_of = 0; turn_of < TEAM_WARPS; ++turn_of) {
+      if ((threadIdx.x >> 5) == turn_of && sub == 0) {
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) {
-    for (int o = team; o < 32; o <<= 1) {
-      dw[i] += __shfl_xor_sync(ALL_LANES, dw[i], o);
-      if (LAYER) db[i] += __shfl_xor_sync(ALL_LANES, db[i], o);
-    }
-  }
-  for (int turn_of = 0; turn_of < TEAM_WARPS; ++turn_of) {
-    if ((threadIdx.x >> 5) == turn_of && sub == 0) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int j = (id + team * c) * V + i;
+        for (int i = 0; i < EPT; ++i) {
+          const int j = (id + team * (i / V)) * V + i % V;
           if (j >= a.H) continue;
-          sums[j] = turn_of ? sums[j] + dw[c * V + i] : dw[c * V + i];
+          sums[j] = turn_of ? sums[j] + aw[i] : aw[i];
           if (LAYER)
-            sums[32 * EPT + j] =
-                turn_of ? sums[32 * EPT + j] + db[c * V + i] : db[c * V + i];
+            sums[32 * EPT + j] = turn_of ? sums[32 * EPT + j] + ab[i] : ab[i];
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
-  }
-  for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
-    p[j] = sums[j];
-    if (LAYER) p[a.H + j] = sums[32 * EPT + j];
+    for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
+      p[j] = sums[j];
+      if (LAYER) p[a.H + j] = sums[32 * EPT + j];
+    }
   }
 }
 
@@ -496,28 +572,37 @@ __global__ void __launch_bounds__(128) k_norm_dparams_wide(const NormArgs a) {
   p[a.H + j] = db;
 }
 
-// The slabs' sums added in fp64: a thread takes every JOIN_RUNS-th slab of a
-// column, then the runs in order.
-constexpr int JOIN_RUNS = 16;
+// The slabs' sums added in a fixed order: a thread takes every JOIN_RUNS-th
+// slab of a column, then the runs in order. (By fp64 additions this took 23 us
+// for 456 slabs of 2 x 2560 columns.)
+constexpr int JOIN_RUNS = 32;
 __global__ void __launch_bounds__(32 * JOIN_RUNS)
     k_norm_join(const float* __restrict__ part, int slabs, int H, void* dweight,
                 void* dbias, int grad_f32) {
-  __shared__ double runs[JOIN_RUNS][32];
+  __shared__ LongSum runs[JOIN_RUNS][32];
   const int col = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int j = blockIdx.x * 32 + col;
   void* out = blockIdx.y ? dbias : dweight;
+  wait_for_earlier();
   if (!out) return;
-  double t = 0.0;
-  if (j < H) {
-#pragma unroll 4
-    for (int s = run; s < slabs; s += JOIN_RUNS)
-      t += part[(static_cast<int64_t>(s) * 2 + blockIdx.y) * H + j];
+  LongSum t;
+  const float* p = part + static_cast<int64_t>(blockIdx.y) * H + j;
+  for (int s0 = run; s0 < slabs; s0 += 8 * JOIN_RUNS) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int s = s0 + u * JOIN_RUNS;
+      v[u] = j < H && s < slabs ? p[static_cast<int64_t>(s) * 2 * H] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) t.add(v[u]);
   }
   runs[run][col] = t;
   __syncthreads();
   if (run == 0 && j < H) {
-    for (int q = 1; q < JOIN_RUNS; ++q) t += runs[q][col];
-    store_from_float(out, grad_f32, j, static_cast<float>(t));
+#pragma unroll
+    for (int q = 1; q < JOIN_RUNS; ++q) t.add(runs[q][col]);
+    store_from_float(out, grad_f32, j, t.rounded());
   }
 }
 
@@ -533,6 +618,8 @@ template <class K>
 cudaError_t resident(K kern, int threads, size_t smem, int* n) {
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, threads, smem);
 }
+
+constexpr int64_t RING_BYTES = 48 * 1024;  // of a block, as far as two stages
 
 struct Geometry {
   bool block;
@@ -558,26 +645,27 @@ Geometry geometry(NormArgs& a, int v, int size, int arrays) {
     while (a.team < need) a.team *= 2;
     const int at_once = 32 / a.team;
     a.tile_rows = at_once;
-    if (v > 1)
-      while (a.tile_rows * a.H * size < 2048 && a.tile_rows < 32)
-        a.tile_rows += at_once;
+    while (a.tile_rows * a.H * size < 2048 && a.tile_rows < 32)
+      a.tile_rows += at_once;
   }
-  a.stages = 1;
-  if (v > 1) {
-    const int groups = g.block ? 1 : TEAM_WARPS;
-    const int64_t stage =
-        static_cast<int64_t>(groups) * arrays * a.tile_rows * a.H * size;
-    const int64_t goal = 48 * 1024;
-    a.stages = static_cast<int>(goal / stage);
-    a.stages = a.stages < 2 ? 2 : a.stages > MAX_STAGES ? MAX_STAGES : a.stages;
-    g.smem = static_cast<size_t>(stage) * a.stages;
-  }
+  // with room for the units at both ends
+  const int64_t bytes = static_cast<int64_t>(a.tile_rows) * a.H * size;
+  a.array_bytes = static_cast<uint32_t>(
+      v > 1 ? bytes : round_up(bytes, 16) + 16);
+  const int64_t stage =
+      static_cast<int64_t>(g.block ? 1 : TEAM_WARPS) * arrays * a.array_bytes;
+  a.stages = static_cast<int>(RING_BYTES / stage);
+  a.stages = a.stages < 2 ? 2 : a.stages > MAX_STAGES ? MAX_STAGES : a.stages;
+  g.smem = static_cast<size_t>(stage) * a.stages;
   return g;
 }
 
-// The most shared memory that any geometry asks for: two stages of two rows
-// of MAX_FAST_H fp32.
-constexpr int MAX_NORM_SMEM = 2 * 2 * MAX_FAST_H * 4;
+// The most shared memory that any geometry asks for: two stages of two arrays,
+// of a row of MAX_FAST_H fp32, or for each warp of a tile that a step of at
+// most 2 KB brought to 2 KB; each with the units at its ends.
+constexpr int MAX_NORM_SMEM = 2 * 2 * TEAM_WARPS * (4096 + 16);
+static_assert(MAX_NORM_SMEM >= 2 * 2 * (MAX_FAST_H * 4 + 32), "a block's row");
+static_assert(32 * EPT * 4 <= 2048, "the step of a tile");
 
 template <class K>
 cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
@@ -596,7 +684,14 @@ cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
     const int64_t most = static_cast<int64_t>(num_sms) * (n < 1 ? 1 : n);
     if (blocks > most) blocks = most;
   }
-  if (a.part && blocks > MAX_SLABS) blocks = MAX_SLABS;
+  if (a.part) {
+    // the slabs' sums are written and read again: no more than the rows' own
+    // bytes, as far as there are SMs
+    const int64_t most = a.L * a.size * 3 / 16;
+    if (blocks > most) blocks = most > num_sms ? most : num_sms;
+    if (blocks > a.L) blocks = a.L;
+    if (blocks > MAX_SLABS) blocks = MAX_SLABS;
+  }
   *grid = static_cast<int>(blocks);
   kern<<<*grid, g.threads, g.smem, s>>>(a);
   return cudaGetLastError();
@@ -614,6 +709,7 @@ cudaError_t rows_fwd(NormArgs& a, int num_sms, cudaStream_t s) {
 template <typename T, int V, bool LAYER>
 cudaError_t rows_bwd(NormArgs& a, int num_sms, cudaStream_t s) {
   const Geometry g = geometry(a, V, sizeof(T), 2);
+  a.size = sizeof(T);
   return g.block ? launch_rows(k_norm_bwd<T, V, true, LAYER>, a, g, num_sms, s,
                                &a.slabs)
                  : launch_rows(k_norm_bwd<T, V, false, LAYER>, a, g, num_sms, s,
@@ -766,10 +862,10 @@ lce_status lce_norm_backward(lce_norm_kind kind, const void* x, lce_dtype dt,
   ProfScope ps(LCE_K_NORM_BWD, s);
   if (L > 0) e = run(a, dev->num_sms, s);
   if (params && e == cudaSuccess) {
-    k_norm_join<<<dim3(static_cast<unsigned>(ceil_div(H, 32)), dbias ? 2 : 1),
-                  32 * JOIN_RUNS, 0, s>>>(a.part, a.slabs, a.H, dweight, dbias,
-                                          grad_dt == LCE_F32);
-    e = cudaGetLastError();
+    e = launch_early(k_norm_join,
+                     dim3(static_cast<unsigned>(ceil_div(H, 32)), dbias ? 2 : 1),
+                     dim3(32 * JOIN_RUNS), 0, s, a.part, a.slabs, a.H, dweight,
+                     dbias, grad_dt == LCE_F32 ? 1 : 0);
   }
   ps.done(0);
   return e == cudaSuccess ? LCE_OK : cuda_fail(e, "norm_bwd");

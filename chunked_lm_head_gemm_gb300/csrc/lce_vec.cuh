@@ -83,6 +83,31 @@ __device__ __forceinline__ void store_chunk(T* p, const float* v) {
   *reinterpret_cast<decltype(c.q)*>(p) = c.q;
 }
 
+// Elements 2 p and 2 p + 1 of a thread's chunks as a packed pair.
+template <typename T, int V, int C>
+__device__ __forceinline__ uint64_t pair_of(const Chunk<T, V> (&q)[C], int p) {
+  if constexpr (V == 1)
+    return f2pack(q[2 * p].at(0), q[2 * p + 1].at(0));
+  else
+    return f2pack(q[2 * p / V].at(2 * p % V), q[2 * p / V].at(2 * p % V + 1));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum_of_pair(uint64_t a) {
+  float lo, hi;
+  f2unpack(a, lo, hi);
+  return lo + hi;
+}
+template <typename T, int V>
+__device__ __forceinline__ Chunk<T, V> no_chunk() {
+  Chunk<T, V> c;
+  memset(&c, 0, sizeof c);
+  return c;
+}
+
 template <typename V>
 __device__ __forceinline__ V lanes_sum(V v) {
 #pragma unroll
@@ -101,6 +126,43 @@ __device__ __forceinline__ V block_sum(V v, V* part) {
   V t = 0;
   const int warps = (blockDim.x + 31) >> 5;
   for (int w = 0; w < warps; ++w) t += part[w];
+  return t;
+}
+
+// A sum of fp32 values to about twice their precision: the rounding of every
+// addition is kept (the two-sum of Knuth) and added at the end. fp64 additions
+// are a sixty-fourth as fast on this chip, and its sums here are many.
+struct LongSum {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    const float s = hi + v, w = s - hi;
+    lo += (hi - (s - w)) + (v - w);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const LongSum& v) {
+    add(v.hi);
+    lo += v.lo;
+  }
+  // an infinite or NaN sum is hi's alone
+  __device__ __forceinline__ double value() const {
+    return isfinite(hi) ? static_cast<double>(hi) + static_cast<double>(lo)
+                        : static_cast<double>(hi);
+  }
+  __device__ __forceinline__ float rounded() const {
+    return isfinite(hi) ? hi + lo : hi;
+  }
+};
+
+// The block's sum in thread 0, warps in order; 0 elsewhere.
+__device__ __forceinline__ double block_total(double v, double* part) {
+  v = lanes_sum(v);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = 0.0;
+  if (threadIdx.x == 0) {
+    const int warps = (blockDim.x + 31) >> 5;
+    for (int w = 0; w < warps; ++w) t += part[w];
+  }
   return t;
 }
 
