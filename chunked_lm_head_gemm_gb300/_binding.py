@@ -1311,7 +1311,8 @@ class _GradTable:
                 raise ValueError("gradients must be CUDA tensors on one "
                                  "device")
         try:
-            codes = [_GRAD_TYPES[t] for t in map(_dtype_of, grads)]
+            codes = self.code_list = [_GRAD_TYPES[t]
+                                      for t in map(_dtype_of, grads)]
         except KeyError as e:
             raise TypeError(f"unsupported dtype {e.args[0]}; use bfloat16 or "
                             "float32") from None
@@ -1322,8 +1323,8 @@ class _GradTable:
         self.ptrs = _host_array(ctypes.c_void_p, "Q",
                                 list(map(torch.Tensor.data_ptr, grads)))
         self.codes = _host_array(ctypes.c_int, "i", codes)
-        self.sizes = _host_array(ctypes.c_int64, "q",
-                                 list(map(torch.Tensor.numel, grads)))
+        self.size_list = list(map(torch.Tensor.numel, grads))
+        self.sizes = _host_array(ctypes.c_int64, "q", self.size_list)
 
     def outputs(self, grads_out):
         """The outputs' pointers: the gradients' own without grads_out."""
@@ -1333,8 +1334,8 @@ class _GradTable:
         if len(outs) != self.n:
             raise ValueError(f"{len(outs)} outputs for {self.n} gradients")
         codes = list(map(_GRAD_TYPES.get, map(_dtype_of, outs)))
-        sizes = list(map(torch.Tensor.numel, outs))
-        same = (codes == list(self.codes) and sizes == list(self.sizes) and
+        same = (codes == self.code_list and
+                list(map(torch.Tensor.numel, outs)) == self.size_list and
                 set(map(torch.Tensor.get_device, outs)) ==
                 set(map(torch.Tensor.get_device, grads[:1])))
         if same and not (self.flat and

@@ -65,68 +65,137 @@ __device__ __forceinline__ float reciprocal(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+__device__ __forceinline__ uint64_t both(float v) { return f2pack(v, v); }
+__device__ __forceinline__ uint64_t ex2_of_pair(uint64_t v) {
+  float lo, hi;
+  f2unpack(v, lo, hi);
+  return f2pack(ex2(lo), ex2(hi));
+}
 
-// A row's normalised scores in place of its logits (0 where all are -inf),
-// and with SLOPE the factor of a sigmoid score's derivative. Sigmoid scores
-// are taken relative to the row's largest, e^{min(z, 0) - m} / (1 + e^{-|z|}),
-// so that a row of very negative logits keeps its ratios.
-template <int N, bool SIGMOID, bool SLOPE>
-__device__ __forceinline__ void probabilities(float (&z)[N], float (&slope)[N],
-                                              int team) {
+// The largest of a row's logits, 0 for a row without one above -inf.
+template <int P>
+__device__ __forceinline__ float row_max(const uint64_t (&z)[P], int team) {
   float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < N; ++i) m = fmaxf(m, z[i]);
-  m = team_max(m, team);
-  if (SIGMOID) m = fminf(m, 0.f);
-  if (m == -INFINITY) m = 0.f;
-  float t = 0.f;
-  if (SIGMOID) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float q = ex2(-fabsf(z[i]) * LOG2E);
-      const float d = reciprocal(1.f + q), qd = q * d;
-      const bool low = z[i] < 0.f;
-      if (SLOPE) slope[i] = low ? d : qd;
-      if (m == 0.f)
-        z[i] = low ? qd : d;
-      else
-        z[i] = ex2((z[i] - m) * LOG2E) * d;
-      t += z[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      z[i] = ex2((z[i] - m) * LOG2E);
-      t += z[i];
-    }
+  for (int i = 0; i < P; ++i) {
+    float lo, hi;
+    f2unpack(z[i], lo, hi);
+    m = max3(m, lo, hi);
   }
-  t = team_sum(t, team);
-  const float inv = t == 0.f ? 0.f : 1.f / t;
-#pragma unroll
-  for (int i = 0; i < N; ++i) z[i] *= inv;
+  m = team_max(m, team);
+  return m == -INFINITY ? 0.f : m;
 }
 
-// The row's elements of a lane, runs of V; -inf beyond E.
-template <typename T, int N, int V>
-__device__ __forceinline__ void load_row(const T* row, bool on, int E, int id,
-                                         int team, Chunk<T, V> (&q)[N / V]) {
+// Below this a sum of sigmoid scores has lost terms to fp32's range.
+constexpr float LEAST_SUM = 1e-30f;
+
+// A row's scores in place of its logits, not yet divided by their sum, which
+// is returned; with SLOPE 1 - s of sigmoid scores (for softmax not written).
+// Two elements to an instruction where there is one. s = 1 / (1 + q), 1 - s = q
+// s with q = e^-z; where q is infinite, s is 0 and 1 - s, of no account, too.
+// Should all sigmoid scores be tiny, they are taken relative to the largest:
+// s e^-m = e^(z - m) / (1 + e^z).
+template <int P, bool SIGMOID, bool SLOPE>
+__device__ __forceinline__ float scores(uint64_t (&z)[P], uint64_t (&slope)[P],
+                                        int team) {
+  uint64_t t = 0;
+  if (!SIGMOID) {
+    const uint64_t minus = both(-row_max(z, team)), log2e = both(LOG2E);
 #pragma unroll
-  for (int c = 0; c < N / V; ++c) {
-    const int j = (id + team * c) * V;
-    if (on && j < E) q[c] = load_chunk<T, V>(row + j);
+    for (int i = 0; i < P; ++i) {
+      z[i] = ex2_of_pair(mul2(add2(z[i], minus), log2e));
+      t = add2(t, z[i]);
+    }
+    return team_sum(sum_of_pair(t), team);
   }
-}
-template <typename T, int N, int V>
-__device__ __forceinline__ void unpack_row(const Chunk<T, V> (&q)[N / V],
-                                           bool on, int E, int id, int team,
-                                           float (&z)[N]) {
+  const uint64_t minus_log2e = both(-LOG2E), one = both(1.f);
+  uint64_t s[P];
 #pragma unroll
-  for (int c = 0; c < N / V; ++c) {
-    const bool has = on && (id + team * c) * V < E;
-#pragma unroll
-    for (int i = 0; i < V; ++i) z[c * V + i] = has ? q[c].at(i) : -INFINITY;
+  for (int i = 0; i < P; ++i) {
+    const uint64_t q = ex2_of_pair(mul2(z[i], minus_log2e));
+    float lo, hi;
+    f2unpack(add2(q, one), lo, hi);
+    s[i] = f2pack(reciprocal(lo), reciprocal(hi));
+    if (SLOPE) {
+      f2unpack(q, lo, hi);
+      slope[i] = mul2(f2pack(fminf(lo, 3e38f), fminf(hi, 3e38f)), s[i]);
+    }
+    t = add2(t, s[i]);
   }
+  float sum = team_sum(sum_of_pair(t), team);
+  // the vote is the warp's: its teams take the shuffles together
+  if (__any_sync(ALL_LANES, sum < LEAST_SUM)) {
+    const float m = row_max(z, team);
+    uint64_t far = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float v[2], e[2], d[2];
+      f2unpack(z[i], v[0], v[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        d[h] = reciprocal(1.f + ex2(v[h] * LOG2E));
+        e[h] = ex2((v[h] - m) * LOG2E) * d[h];
+      }
+      z[i] = f2pack(e[0], e[1]);
+      if (sum < LEAST_SUM) {
+        s[i] = z[i];
+        if (SLOPE) slope[i] = f2pack(d[0], d[1]);
+      }
+      far = add2(far, z[i]);
+    }
+    const float all = team_sum(sum_of_pair(far), team);
+    if (sum < LEAST_SUM) sum = all;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) z[i] = s[i];
+  return sum;
 }
+
+// The rows of a lane: its row's elements, runs of V, ROWS rows a time `apart`
+// rows from each other. Rows that take no part are not read.
+template <typename T, int N, int V, int ROWS>
+struct Rows {
+  const BalanceArgs& a;
+  const int id;
+  bool on[ROWS], on_next[ROWS];
+  Chunk<T, V> q[ROWS][N / V];
+
+  __device__ __forceinline__ bool takes_part(int64_t t) const {
+    return t < a.L && (!a.mask || a.mask[t] != 0);
+  }
+  // The masks of the rows from t on, which are loaded next.
+  __device__ __forceinline__ void look(int64_t t, int64_t apart) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) on_next[r] = takes_part(t + r * apart);
+  }
+  __device__ __forceinline__ void load(int64_t t, int64_t apart) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      on[r] = on_next[r];
+      const T* row = static_cast<const T*>(a.logits) + (t + r * apart) * a.E;
+#pragma unroll
+      for (int c = 0; c < N / V; ++c) {
+        const int j = (id + a.team * c) * V;
+        if (on[r] && j < a.E) q[r][c] = load_chunk<T, V>(row + j);
+      }
+    }
+  }
+  // Row r in pairs; -inf beyond E and for a row that takes no part.
+  __device__ __forceinline__ void unpack(int r, uint64_t (&z)[N / 2]) const {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (V > 1) {
+        const bool has = on[r] && (id + a.team * (2 * i / V)) * V < a.E;
+        z[i] = has ? pair_of(q[r], i) : both(-INFINITY);
+      } else {
+        const int j = id + a.team * 2 * i;
+        z[i] = f2pack(on[r] && j < a.E ? q[r][2 * i].at(0) : -INFINITY,
+                      on[r] && j + a.team < a.E ? q[r][2 * i + 1].at(0)
+                                                : -INFINITY);
+      }
+    }
+  }
+};
 
 // Slots of tokens [t0, t1) into hist, a few loads under way at a time.
 __device__ __forceinline__ void count_slots(const int32_t* experts,
@@ -168,10 +237,14 @@ __device__ __forceinline__ double finish(const BalanceArgs& a, int e, int count,
   return static_cast<double>(load) * inv * (p * inv * a.K);
 }
 
+// Rows that a lane has under way: two while they are short.
+constexpr int rows_of(int n) { return n <= 8 ? 2 : 1; }
+
 // Block b counts the slots of tokens [b, b + 1) L / blocks; the rows of logits
 // go to the warps of all blocks in turn.
 template <typename T, int N, int V, bool SIGMOID>
 __global__ void __launch_bounds__(WARPS * 32) k_balance(const BalanceArgs a) {
+  constexpr int ROWS = rows_of(N), P = N / 2;
   extern __shared__ float sums[];                       // [WARPS][E]
   int* hist = reinterpret_cast<int*>(sums + WARPS * a.E);  // [E + 1]
   __shared__ double part[32];
@@ -180,35 +253,40 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance(const BalanceArgs a) {
   const int at_once = 32 / a.team;
   for (int e = threadIdx.x; e <= a.E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
-  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * at_once;
+  // the next rows are under way while some are computed, their masks before
+  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * at_once * ROWS;
   const int64_t first =
-      (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * at_once;
-  const T* logits = static_cast<const T*>(a.logits);
-  // the next row is under way while one is computed, its mask one before that
-  auto takes_part = [&](int64_t t) {
-    return t < a.L && (!a.mask || a.mask[t] != 0);
-  };
-  bool on = takes_part(first + sub);
-  bool on_next = takes_part(first + step + sub);
-  Chunk<T, V> q[N / V];
-  load_row<T, N, V>(logits + (first + sub) * a.E, on, a.E, id, a.team, q);
+      (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * at_once * ROWS;
+  Rows<T, N, V, ROWS> rows{a, id};
+  rows.look(first + sub, at_once);
+  rows.load(first + sub, at_once);
+  rows.look(first + step + sub, at_once);
   count_slots(a.experts, a.mask, a.L * blockIdx.x / a.blocks,
               a.L * (blockIdx.x + 1) / a.blocks, a.K, a.E, hist, a.err);
-  float acc[N], z[N], unused[N];
+  uint64_t pairs[P];
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  for (int i = 0; i < P; ++i) pairs[i] = 0;
   int tokens = 0;
   for (int64_t t0 = first; t0 < a.L; t0 += step) {
-    unpack_row<T, N, V>(q, on, a.E, id, a.team, z);
-    tokens += on;
-    const int64_t next = t0 + step + sub;
-    on = on_next;
-    load_row<T, N, V>(logits + next * a.E, on, a.E, id, a.team, q);
-    on_next = takes_part(next + step);
-    probabilities<N, SIGMOID, false>(z, unused, a.team);
+    uint64_t z[ROWS][P], unused[P];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] += z[i];
+    for (int r = 0; r < ROWS; ++r) {
+      rows.unpack(r, z[r]);
+      tokens += rows.on[r];
+    }
+    rows.load(t0 + step + sub, at_once);
+    rows.look(t0 + 2 * step + sub, at_once);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const float t = scores<P, SIGMOID, false>(z[r], unused, a.team);
+      const uint64_t inv = both(t == 0.f ? 0.f : 1.f / t);
+#pragma unroll
+      for (int i = 0; i < P; ++i) pairs[i] = fma2(z[r][i], inv, pairs[i]);
+    }
   }
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < P; ++i) f2unpack(pairs[i], acc[2 * i], acc[2 * i + 1]);
   if (id == 0 && tokens) atomicAdd(&hist[a.E], tokens);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -305,54 +383,58 @@ __global__ void __launch_bounds__(JOIN_THREADS)
 template <typename T, int N, int V, bool SIGMOID>
 __global__ void __launch_bounds__(WARPS * 32)
     k_balance_bwd(const BalanceArgs a) {
+  constexpr int ROWS = rows_of(N), P = N / 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int id = lane & (a.team - 1), sub = lane / a.team;
   const int at_once = 32 / a.team;
-  const float d = *a.dloss;
-  float f[N], z[N], slope[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int j = (id + a.team * (i / V)) * V + i % V;
-    f[i] = j < a.E ? a.slopes[j] * d : 0.f;
-  }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * at_once;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * at_once * ROWS;
   const int64_t first =
-      (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * at_once;
-  const T* logits = static_cast<const T*>(a.logits);
-  auto takes_part = [&](int64_t t) {
-    return t < a.L && (!a.mask || a.mask[t] != 0);
+      (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * at_once * ROWS;
+  Rows<T, N, V, ROWS> rows{a, id};
+  rows.look(first + sub, at_once);
+  rows.load(first + sub, at_once);
+  rows.look(first + step + sub, at_once);
+  const float d = *a.dloss;
+  uint64_t f[P];
+  auto slope_of = [&](int i) {
+    const int j = (id + a.team * (i / V)) * V + i % V;
+    return j < a.E ? a.slopes[j] * d : 0.f;
   };
-  bool on = takes_part(first + sub);
-  bool on_next = takes_part(first + step + sub);
-  Chunk<T, V> q[N / V];
-  load_row<T, N, V>(logits + (first + sub) * a.E, on, a.E, id, a.team, q);
+#pragma unroll
+  for (int i = 0; i < P; ++i) f[i] = f2pack(slope_of(2 * i), slope_of(2 * i + 1));
   for (int64_t t0 = first; t0 < a.L; t0 += step) {
-    unpack_row<T, N, V>(q, on, a.E, id, a.team, z);
-    const bool was_on = on;
-    const int64_t next = t0 + step + sub;
-    on = on_next;
-    load_row<T, N, V>(logits + next * a.E, on, a.E, id, a.team, q);
-    on_next = takes_part(next + step);
-    probabilities<N, SIGMOID, true>(z, slope, a.team);
-    float dot = 0.f;
+    uint64_t z[ROWS][P];
+    bool on[ROWS];
 #pragma unroll
-    for (int i = 0; i < N; ++i) dot = fmaf(f[i], z[i], dot);
-    dot = team_sum(dot, a.team);
-    if (t0 + sub >= a.L) continue;
-    T* out = static_cast<T*>(a.dlogits) + (t0 + sub) * a.E;
+    for (int r = 0; r < ROWS; ++r) {
+      rows.unpack(r, z[r]);
+      on[r] = rows.on[r];
+    }
+    rows.load(t0 + step + sub, at_once);
+    rows.look(t0 + 2 * step + sub, at_once);
 #pragma unroll
-    for (int c = 0; c < N / V; ++c) {
-      const int j = (id + a.team * c) * V;
-      if (j >= a.E) continue;
-      float o[V];
+    for (int r = 0; r < ROWS; ++r) {
+      uint64_t slope[P], dots = 0;
+      const float t = scores<P, SIGMOID, true>(z[r], slope, a.team);
+      const float inv = t == 0.f ? 0.f : 1.f / t;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int k = c * V + i;
-        o[i] = z[k] * (f[k] - dot);
-        if (SIGMOID) o[i] *= slope[k];
-        if (!was_on) o[i] = 0.f;
+      for (int i = 0; i < P; ++i) dots = fma2(f[i], z[r][i], dots);
+      const float dot = team_sum(sum_of_pair(dots), a.team) * inv;
+      const int64_t row = t0 + r * at_once + sub;
+      if (row >= a.L) continue;
+      float o[N];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        uint64_t v = mul2(mul2(z[r][i], both(inv)), add2(f[i], both(-dot)));
+        if (SIGMOID) v = mul2(v, slope[i]);
+        f2unpack(on[r] ? v : 0, o[2 * i], o[2 * i + 1]);
       }
-      store_chunk<T, V>(out + j, o);
+      T* out = static_cast<T*>(a.dlogits) + row * a.E;
+#pragma unroll
+      for (int c = 0; c < N / V; ++c) {
+        const int j = (id + a.team * c) * V;
+        if (j < a.E) store_chunk<T, V>(out + j, &o[c * V]);
+      }
     }
   }
 }
@@ -413,7 +495,8 @@ cudaError_t forward(const BalanceArgs& a, bool sigmoid, cudaStream_t s) {
 template <typename T, int N, int V>
 cudaError_t backward(const BalanceArgs& a, bool sigmoid, int num_sms,
                      cudaStream_t s) {
-  const int64_t need = ceil_div(a.L, WARPS * 32 / a.team), most = num_sms * 4;
+  const int64_t need = ceil_div(a.L, WARPS * 32 / a.team * rows_of(N));
+  const int64_t most = num_sms * 4;
   const int grid = static_cast<int>(need < most ? need : most);
   auto kern = sigmoid ? k_balance_bwd<T, N, V, true>
                       : k_balance_bwd<T, N, V, false>;

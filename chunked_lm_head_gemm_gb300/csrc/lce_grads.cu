@@ -184,8 +184,38 @@ __device__ __forceinline__ uint4 scaled(uint4 q, bool f32, float scale) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Chunks from the last one down. An output that does not lie like its
-// gradient relative to 16 bytes is written element by element.
+// Elements [0, head) and [tail, n) of a tensor, fewer than a block's threads.
+__device__ __forceinline__ void clip_ends(const void* grad, void* out, bool f32,
+                                          int64_t head, int64_t tail, int64_t n,
+                                          float scale) {
+  const int64_t i = threadIdx.x < head ? threadIdx.x
+                                       : threadIdx.x - head + tail;
+  if (i < n)
+    store_from_float(out, f32, i, load_as_float(grad, f32, i) * scale);
+}
+
+// 16 bytes from byte `shift` (not 0, a multiple of 2) of two vectors on.
+__device__ __forceinline__ uint4 joined(uint4 a, uint4 b, int shift) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (shift & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (shift & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (shift & 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Chunks from the last one down. An output that does not lie like its gradient
+// relative to 16 bytes is written in its own whole vectors, each joined from
+// the two of the gradient that hold it; those whose two reach past the
+// gradient go with the ends.
 __device__ __forceinline__ void clip(const GradTable& t, int first, int step,
                                      float scale) {
   const int chunks = t.first[t.count];
@@ -194,13 +224,14 @@ __device__ __forceinline__ void clip(const GradTable& t, int first, int step,
     const void* grad = t.grad[p.k];
     void* out = t.out[p.k];
     if (scale == 1.f && out == grad) continue;
-    const int per = p.f32 ? 4 : 8, size = p.f32 ? 4 : 2;
-    if (((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(out)) &
-         15) == 0) {
-      const uint4* v = reinterpret_cast<const uint4*>(
-          static_cast<const char*>(grad) + p.head * size);
-      uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(out) +
-                                          p.head * size);
+    const int64_t n = t.size[p.k];
+    const int lsize = p.f32 ? 2 : 1;  // an element's bytes, as a shift
+    const uintptr_t from = reinterpret_cast<uintptr_t>(grad);
+    const uintptr_t to = reinterpret_cast<uintptr_t>(out);
+    if (((from ^ to) & 15) == 0) {
+      const uint4* v =
+          reinterpret_cast<const uint4*>(from + (p.head << lsize));
+      uint4* o = reinterpret_cast<uint4*>(to + (p.head << lsize));
       uint4 q[UNROLL];
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
@@ -212,21 +243,47 @@ __device__ __forceinline__ void clip(const GradTable& t, int first, int step,
         const int64_t i = p.v0 + u * GRAD_THREADS + threadIdx.x;
         if (i < p.v1) __stcs(o + i, scaled(q[u], p.f32, scale));
       }
-    } else {
-      const int64_t i1 = p.head + p.v1 * per;
-#pragma unroll 8
-      for (int64_t i = p.head + p.v0 * per + threadIdx.x; i < i1;
-           i += GRAD_THREADS)
-        store_from_float(out, p.f32, i, load_as_float(grad, p.f32, i) * scale);
+      if (p.ends)
+        clip_ends(grad, out, p.f32, p.head,
+                  p.head + (p.whole << (4 - lsize)), n, scale);
+      continue;
     }
-    if (p.ends) {
-      const int64_t body = p.whole * per;
-      if (threadIdx.x < t.size[p.k] - body) {
-        const int64_t i =
-            threadIdx.x < p.head ? threadIdx.x : threadIdx.x + body;
-        store_from_float(out, p.f32, i, load_as_float(grad, p.f32, i) * scale);
+    // head: to the output's first whole vector whose bytes in the gradient
+    // begin at its first vector or behind it
+    int64_t head = static_cast<int64_t>((16 - (to & 15)) & 15) >> lsize;
+    const int shift = static_cast<int>((from + (head << lsize)) & 15);
+    if ((head << lsize) < shift) head += 16 >> lsize;
+    const int64_t bytes = ((n - head) << lsize) - (16 - shift);
+    int64_t whole = bytes > 0 ? bytes >> 4 : 0;
+    const int64_t most =
+        static_cast<int64_t>(t.first[p.k + 1] - t.first[p.k]) * CHUNK;
+    whole = min(whole, most);
+    if (whole == 0) head = 0;
+    const uint4* v = reinterpret_cast<const uint4*>(
+        (from + (head << lsize)) & ~static_cast<uintptr_t>(15));
+    uint4* o = reinterpret_cast<uint4*>(to + (head << lsize));
+    const int64_t v1 = min(p.v0 + CHUNK, whole);
+#pragma unroll
+    for (int u0 = 0; u0 < UNROLL; u0 += 4) {
+      uint4 q[4], r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = p.v0 + (u0 + u) * GRAD_THREADS + threadIdx.x;
+        if (i < v1) {
+          q[u] = v[i];
+          r[u] = v[i + 1];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = p.v0 + (u0 + u) * GRAD_THREADS + threadIdx.x;
+        if (i < v1)
+          __stcs(o + i, scaled(joined(q[u], r[u], shift), p.f32, scale));
       }
     }
+    if (p.ends)
+      clip_ends(grad, out, p.f32, head, head + (whole << (4 - lsize)), n,
+                scale);
   }
 }
 
