@@ -27,9 +27,10 @@ namespace {
 
 constexpr int MAX_E = 1024;
 constexpr int WARPS = 8;
-constexpr int64_t MAX_BLOCKS = 608;
+constexpr int64_t SMS = 152;
 constexpr int JOIN_BLOCKS = 8;  // of one cluster
-constexpr int JOIN_THREADS = 512;
+constexpr int JOIN_THREADS = 1024;
+constexpr int JOIN_AHEAD = 10;  // loads of a thread under way
 
 struct BalanceArgs {
   const void* logits;
@@ -50,14 +51,17 @@ struct BalanceArgs {
   unsigned* err;
 };
 
+// Over a row's team; `team` is the same for all of a launch.
 __device__ __forceinline__ float team_max(float v, int team) {
-  for (int o = team >> 1; o > 0; o >>= 1)
-    v = fmaxf(v, __shfl_xor_sync(ALL_LANES, v, o));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < team) v = fmaxf(v, __shfl_xor_sync(ALL_LANES, v, o));
   return v;
 }
 __device__ __forceinline__ float team_sum(float v, int team) {
-  for (int o = team >> 1; o > 0; o >>= 1)
-    v += __shfl_xor_sync(ALL_LANES, v, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < team) v += __shfl_xor_sync(ALL_LANES, v, o);
   return v;
 }
 __device__ __forceinline__ float reciprocal(float v) {
@@ -151,51 +155,71 @@ __device__ __forceinline__ float scores(uint64_t (&z)[P], uint64_t (&slope)[P],
   return sum;
 }
 
-// The rows of a lane: its row's elements, runs of V, ROWS rows a time `apart`
-// rows from each other. Rows that take no part are not read.
-template <typename T, int N, int V, int ROWS>
+// The rows of a lane: its row's elements, runs of V, a row every `step`; the
+// next is under way while one is computed. Rows that take no part are not read.
+template <typename T, int N, int V>
 struct Rows {
-  const BalanceArgs& a;
-  const int id;
-  bool on[ROWS], on_next[ROWS];
-  Chunk<T, V> q[ROWS][N / V];
+  const int id, team, E, L, step;
+  const T* next;         // the row that is loaded next
+  const uint8_t* masks;  // of the row after it
+  int row;               // that row
+  int64_t leap;
+  bool on, on_next;
+  Chunk<T, V> q[N / V];
 
-  __device__ __forceinline__ bool takes_part(int64_t t) const {
-    return t < a.L && (!a.mask || a.mask[t] != 0);
+  __device__ __forceinline__ Rows(const BalanceArgs& a, int id_, int first,
+                                  int step_)
+      : id(id_),
+        team(a.team),
+        E(a.E),
+        L(static_cast<int>(a.L)),
+        step(step_),
+        next(static_cast<const T*>(a.logits) +
+             static_cast<int64_t>(first) * a.E + id_ * V),
+        masks(a.mask ? a.mask + first : nullptr),
+        row(first),
+        leap(static_cast<int64_t>(step_) * a.E) {
+    look();
+    load();
   }
-  // The masks of the rows from t on, which are loaded next.
-  __device__ __forceinline__ void look(int64_t t, int64_t apart) {
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) on_next[r] = takes_part(t + r * apart);
-  }
-  __device__ __forceinline__ void load(int64_t t, int64_t apart) {
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      on[r] = on_next[r];
-      const T* row = static_cast<const T*>(a.logits) + (t + r * apart) * a.E;
-#pragma unroll
-      for (int c = 0; c < N / V; ++c) {
-        const int j = (id + a.team * c) * V;
-        if (on[r] && j < a.E) q[r][c] = load_chunk<T, V>(row + j);
-      }
+  __device__ __forceinline__ void look() {
+    on_next = row < L;
+    if (masks) {
+      if (on_next) on_next = *masks != 0;
+      masks += step;
     }
+    row += step;
   }
-  // Row r in pairs; -inf beyond E and for a row that takes no part.
-  __device__ __forceinline__ void unpack(int r, uint64_t (&z)[N / 2]) const {
+  __device__ __forceinline__ void load() {
+    on = on_next;
+#pragma unroll
+    for (int c = 0; c < N / V; ++c)
+      if (on && (id + team * c) * V < E)
+        q[c] = load_chunk<T, V>(next + team * c * V);
+    next += leap;
+    look();
+  }
+  // The row in pairs; -inf beyond E and for a row that takes no part.
+  __device__ __forceinline__ void unpack(uint64_t (&z)[N / 2]) const {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       if constexpr (V > 1) {
-        const bool has = on[r] && (id + a.team * (2 * i / V)) * V < a.E;
-        z[i] = has ? pair_of(q[r], i) : both(-INFINITY);
+        const bool has = on && (id + team * (2 * i / V)) * V < E;
+        z[i] = has ? pair_of(q, i) : both(-INFINITY);
       } else {
-        const int j = id + a.team * 2 * i;
-        z[i] = f2pack(on[r] && j < a.E ? q[r][2 * i].at(0) : -INFINITY,
-                      on[r] && j + a.team < a.E ? q[r][2 * i + 1].at(0)
-                                                : -INFINITY);
+        const int j = id + team * 2 * i;
+        z[i] = f2pack(on && j < E ? q[2 * i].at(0) : -INFINITY,
+                      on && j + team < E ? q[2 * i + 1].at(0) : -INFINITY);
       }
     }
   }
 };
+
+// Blocks of an SM that the registers leave room for. (131072 x 256 fp32, us of
+// a forward and a backward pass: 81 with 4 blocks of one row under way, 103 with
+// 5, 139 with 6, where registers spill; 87 with 3 blocks of two rows.)
+constexpr int blocks_per_sm(int n) { return n <= 8 ? 4 : n <= 16 ? 2 : 1; }
+static_assert(SMS * 4 <= JOIN_THREADS, "a thread to a block's tokens");
 
 // Slots of tokens [t0, t1) into hist, a few loads under way at a time.
 __device__ __forceinline__ void count_slots(const int32_t* experts,
@@ -237,14 +261,12 @@ __device__ __forceinline__ double finish(const BalanceArgs& a, int e, int count,
   return static_cast<double>(load) * inv * (p * inv * a.K);
 }
 
-// Rows that a lane has under way: two while they are short.
-constexpr int rows_of(int n) { return n <= 8 ? 2 : 1; }
-
 // Block b counts the slots of tokens [b, b + 1) L / blocks; the rows of logits
 // go to the warps of all blocks in turn.
 template <typename T, int N, int V, bool SIGMOID>
-__global__ void __launch_bounds__(WARPS * 32) k_balance(const BalanceArgs a) {
-  constexpr int ROWS = rows_of(N), P = N / 2;
+__global__ void __launch_bounds__(WARPS * 32, blocks_per_sm(N))
+    k_balance(const BalanceArgs a) {
+  constexpr int P = N / 2;
   extern __shared__ float sums[];                       // [WARPS][E]
   int* hist = reinterpret_cast<int*>(sums + WARPS * a.E);  // [E + 1]
   __shared__ double part[32];
@@ -254,35 +276,24 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance(const BalanceArgs a) {
   for (int e = threadIdx.x; e <= a.E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   // the next rows are under way while some are computed, their masks before
-  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * at_once * ROWS;
-  const int64_t first =
-      (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * at_once * ROWS;
-  Rows<T, N, V, ROWS> rows{a, id};
-  rows.look(first + sub, at_once);
-  rows.load(first + sub, at_once);
-  rows.look(first + step + sub, at_once);
+  const int step = gridDim.x * WARPS * at_once;
+  const int first = (blockIdx.x * WARPS + warp) * at_once;
+  Rows<T, N, V> rows(a, id, first + sub, step);
   count_slots(a.experts, a.mask, a.L * blockIdx.x / a.blocks,
               a.L * (blockIdx.x + 1) / a.blocks, a.K, a.E, hist, a.err);
   uint64_t pairs[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) pairs[i] = 0;
   int tokens = 0;
-  for (int64_t t0 = first; t0 < a.L; t0 += step) {
-    uint64_t z[ROWS][P], unused[P];
+  for (int t0 = first; t0 < a.L; t0 += step) {
+    uint64_t z[P], unused[P];
+    rows.unpack(z);
+    tokens += rows.on;
+    rows.load();
+    const float t = scores<P, SIGMOID, false>(z, unused, a.team);
+    const uint64_t inv = both(t == 0.f ? 0.f : reciprocal(t));
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      rows.unpack(r, z[r]);
-      tokens += rows.on[r];
-    }
-    rows.load(t0 + step + sub, at_once);
-    rows.look(t0 + 2 * step + sub, at_once);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const float t = scores<P, SIGMOID, false>(z[r], unused, a.team);
-      const uint64_t inv = both(t == 0.f ? 0.f : 1.f / t);
-#pragma unroll
-      for (int i = 0; i < P; ++i) pairs[i] = fma2(z[r][i], inv, pairs[i]);
-    }
+    for (int i = 0; i < P; ++i) pairs[i] = fma2(z[i], inv, pairs[i]);
   }
   float acc[N];
 #pragma unroll
@@ -330,31 +341,31 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   // every block has begun before another writes its shared memory
   auto begun = cluster.barrier_arrive();
   wait_for_earlier();
-  int n = 0;
-  for (int b = threadIdx.x; b < a.blocks; b += blockDim.x)
-    n += a.part_n[static_cast<int64_t>(b) * (a.E + 1) + a.E];
-  n = block_sum(n, tokens_of);
+  int n = threadIdx.x < a.blocks
+              ? a.part_n[static_cast<int64_t>(threadIdx.x) * (a.E + 1) + a.E]
+              : 0;
   double term = 0.0;
   for (int e0 = 32 * blockIdx.x; e0 < a.E; e0 += 32 * JOIN_BLOCKS) {
     const int e = e0 + lane;
     int c = 0;
     LongSum p;
-    for (int b0 = run; b0 < a.blocks; b0 += 8 * RUNS) {
-      float v[8];
-      int k[8];
+    for (int b0 = run; b0 < a.blocks; b0 += JOIN_AHEAD * RUNS) {
+      float v[JOIN_AHEAD];
+      int k[JOIN_AHEAD];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < JOIN_AHEAD; ++u) {
         const int b = b0 + u * RUNS;
         const bool has = e < a.E && b < a.blocks;
         v[u] = has ? a.part_p[static_cast<int64_t>(b) * a.E + e] : 0.f;
         k[u] = has ? a.part_n[static_cast<int64_t>(b) * (a.E + 1) + e] : 0;
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < JOIN_AHEAD; ++u) {
         p.add(v[u]);
         c += k[u];
       }
     }
+    if (e0 == 32 * blockIdx.x) n = block_sum(n, tokens_of);
     sums[run][lane] = p;
     counts[run][lane] = c;
     __syncthreads();
@@ -381,19 +392,17 @@ __global__ void __launch_bounds__(JOIN_THREADS)
 }
 
 template <typename T, int N, int V, bool SIGMOID>
-__global__ void __launch_bounds__(WARPS * 32)
+__global__ void __launch_bounds__(WARPS * 32, blocks_per_sm(N))
     k_balance_bwd(const BalanceArgs a) {
-  constexpr int ROWS = rows_of(N), P = N / 2;
+  constexpr int P = N / 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int id = lane & (a.team - 1), sub = lane / a.team;
   const int at_once = 32 / a.team;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * at_once * ROWS;
-  const int64_t first =
-      (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * at_once * ROWS;
-  Rows<T, N, V, ROWS> rows{a, id};
-  rows.look(first + sub, at_once);
-  rows.load(first + sub, at_once);
-  rows.look(first + step + sub, at_once);
+  const int step = gridDim.x * WARPS * at_once;
+  const int first = (blockIdx.x * WARPS + warp) * at_once;
+  Rows<T, N, V> rows(a, id, first + sub, step);
+  T* out = static_cast<T*>(a.dlogits) +
+           static_cast<int64_t>(first + sub) * a.E + id * V;
   const float d = *a.dloss;
   uint64_t f[P];
   auto slope_of = [&](int i) {
@@ -402,40 +411,30 @@ __global__ void __launch_bounds__(WARPS * 32)
   };
 #pragma unroll
   for (int i = 0; i < P; ++i) f[i] = f2pack(slope_of(2 * i), slope_of(2 * i + 1));
-  for (int64_t t0 = first; t0 < a.L; t0 += step) {
-    uint64_t z[ROWS][P];
-    bool on[ROWS];
+  for (int t0 = first; t0 < a.L; t0 += step) {
+    uint64_t z[P], slope[P], dots = 0;
+    rows.unpack(z);
+    const bool on = rows.on;
+    rows.load();
+    const float t = scores<P, SIGMOID, true>(z, slope, a.team);
+    const float inv = t == 0.f ? 0.f : reciprocal(t);
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      rows.unpack(r, z[r]);
-      on[r] = rows.on[r];
-    }
-    rows.load(t0 + step + sub, at_once);
-    rows.look(t0 + 2 * step + sub, at_once);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      uint64_t slope[P], dots = 0;
-      const float t = scores<P, SIGMOID, true>(z[r], slope, a.team);
-      const float inv = t == 0.f ? 0.f : 1.f / t;
-#pragma unroll
-      for (int i = 0; i < P; ++i) dots = fma2(f[i], z[r][i], dots);
-      const float dot = team_sum(sum_of_pair(dots), a.team) * inv;
-      const int64_t row = t0 + r * at_once + sub;
-      if (row >= a.L) continue;
+    for (int i = 0; i < P; ++i) dots = fma2(f[i], z[i], dots);
+    const float dot = team_sum(sum_of_pair(dots), a.team) * inv;
+    if (t0 + sub < a.L) {
       float o[N];
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        uint64_t v = mul2(mul2(z[r][i], both(inv)), add2(f[i], both(-dot)));
+        uint64_t v = mul2(mul2(z[i], both(inv)), add2(f[i], both(-dot)));
         if (SIGMOID) v = mul2(v, slope[i]);
-        f2unpack(on[r] ? v : 0, o[2 * i], o[2 * i + 1]);
+        f2unpack(on ? v : 0, o[2 * i], o[2 * i + 1]);
       }
-      T* out = static_cast<T*>(a.dlogits) + row * a.E;
 #pragma unroll
-      for (int c = 0; c < N / V; ++c) {
-        const int j = (id + a.team * c) * V;
-        if (j < a.E) store_chunk<T, V>(out + j, &o[c * V]);
-      }
+      for (int c = 0; c < N / V; ++c)
+        if ((id + a.team * c) * V < a.E)
+          store_chunk<T, V>(out + a.team * c * V, &o[c * V]);
     }
+    out += rows.leap;
   }
 }
 
@@ -470,7 +469,8 @@ int team_of(int64_t E) {
 // blocks' sums are worth their joining; one block does it alone.
 int blocks_of(int64_t L, int64_t E) {
   const int64_t n = ceil_div(L, WARPS * 32 / team_of(E) * 4);
-  return static_cast<int>(n < 1 ? 1 : n < MAX_BLOCKS ? n : MAX_BLOCKS);
+  const int64_t most = SMS * blocks_per_sm(held(E));
+  return static_cast<int>(n < 1 ? 1 : n < most ? n : most);
 }
 
 bool sizes_ok(int64_t L, int64_t E) {
@@ -495,8 +495,8 @@ cudaError_t forward(const BalanceArgs& a, bool sigmoid, cudaStream_t s) {
 template <typename T, int N, int V>
 cudaError_t backward(const BalanceArgs& a, bool sigmoid, int num_sms,
                      cudaStream_t s) {
-  const int64_t need = ceil_div(a.L, WARPS * 32 / a.team * rows_of(N));
-  const int64_t most = num_sms * 4;
+  const int64_t need = ceil_div(a.L, WARPS * 32 / a.team);
+  const int64_t most = num_sms * blocks_per_sm(N);
   const int grid = static_cast<int>(need < most ? need : most);
   auto kern = sigmoid ? k_balance_bwd<T, N, V, true>
                       : k_balance_bwd<T, N, V, false>;
