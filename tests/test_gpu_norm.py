@@ -106,7 +106,9 @@ def test_row_counts(L, H, dtype, layer):
 @KINDS
 @pytest.mark.parametrize("L,H,dtype", [(200003, 128, BF), (100001, 64, F32),
                                        (40000, 1024, BF), (20000, 4096, BF),
-                                       (70001, 33, BF)])
+                                       (70001, 33, BF), (3000, 16384, BF),
+                                       (2000, 9001, F32), (700, 40000, BF),
+                                       (600, 65536, F32)])
 def test_many_rows(L, H, dtype, layer):
     require_gpu()
     check(*make(L, H, dtype, dtype, seed=3), layer, grad_dtype=F32)
