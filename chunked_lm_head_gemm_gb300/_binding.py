@@ -1041,8 +1041,8 @@ def experts_backward(x, Wg, Wu, Wd, weights, experts, dy, workspace=None,
 def _call(name, device, *args):
     """One call of the library with the tensors' device current, on that
     device's current stream (the last argument)."""
-    fn = getattr(_lib or load(), name)
     index = device.index
+    fn = getattr(_lib or load(), name)
     if index is None or index == torch._C._cuda_getDevice():
         st = fn(*args, _stream_ptr(device))
     else:
@@ -1054,27 +1054,38 @@ def _call(name, device, *args):
 
 def _check_rows(name, t, shape, dtype, device):
     """An input of known shape and type, as the C ABI reads it."""
-    if (t.shape != shape or t.dtype is not dtype or not t.is_cuda or
-            t.device != device or not t.is_contiguous()):
+    if (t.dtype is not dtype or t.shape != shape or t.device != device or
+            not t.is_cuda or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of "
                          f"shape {tuple(shape)} on {device}")
     return t
 
 
+_TYPE_CODES = {torch.bfloat16: LCE_BF16, torch.float32: LCE_F32}
+
+
 def _check_norm(x, weight, bias):
-    """Sizes and type codes (of x, of the parameters) of a norm's inputs."""
+    """Device, sizes and type codes (of x, of the parameters) of a norm's
+    inputs."""
     if not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA [L,H] tensor")
-    code = param = _dtype_code(x)
+    code = param = _TYPE_CODES.get(x.dtype)
+    if code is None:
+        _dtype_code(x)  # raises
     L, H = x.shape
-    first = None
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        param = _dtype_code(t)
-        first = t if first is None else first
-        _check_rows(name, t, (H,), first.dtype, x.device)
-    return L, H, code, param
+    device = x.device
+    if weight is not None:
+        param = _TYPE_CODES.get(weight.dtype)
+        if param is None:
+            _dtype_code(weight)
+        _check_rows("weight", weight, (H,), weight.dtype, device)
+    if bias is not None:
+        dtype = bias.dtype if weight is None else weight.dtype
+        param = _TYPE_CODES.get(dtype)
+        if param is None:
+            _dtype_code(bias)
+        _check_rows("bias", bias, (H,), dtype, device)
+    return device, L, H, code, param
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1088,8 +1099,7 @@ def norm_workspace_size(L: int, H: int) -> int:
 
 
 def _norm_forward(kind, x, weight, bias, eps, y_out, save_stats):
-    L, H, code, param = _check_norm(x, weight, bias)
-    dev = x.device
+    dev, L, H, code, param = _check_norm(x, weight, bias)
     if y_out is not None:
         y = _check_out("y_out", y_out, x.shape, x.dtype, dev)
     else:
@@ -1107,8 +1117,7 @@ def _norm_forward(kind, x, weight, bias, eps, y_out, save_stats):
 
 def _norm_backward(kind, x, weight, mean, rstd, dy, grad_dtype, workspace,
                    dx_out, compute_dx, compute_dweight, compute_dbias):
-    L, H, code, param = _check_norm(x, weight, None)
-    dev = x.device
+    dev, L, H, code, param = _check_norm(x, weight, None)
     _check_rows("dy", dy, x.shape, x.dtype, dev)
     _check_rows("rstd", rstd, (L,), torch.float32, dev)
     if kind == LAYER_NORM:
@@ -1286,7 +1295,6 @@ def _dense(t):
     return True
 
 
-_GRAD_TYPES = {torch.bfloat16: LCE_BF16, torch.float32: LCE_F32}
 _dtype_of = operator.attrgetter("dtype")
 
 
@@ -1311,7 +1319,7 @@ class _GradTable:
                 raise ValueError("gradients must be CUDA tensors on one "
                                  "device")
         try:
-            codes = self.code_list = [_GRAD_TYPES[t]
+            codes = self.code_list = [_TYPE_CODES[t]
                                       for t in map(_dtype_of, grads)]
         except KeyError as e:
             raise TypeError(f"unsupported dtype {e.args[0]}; use bfloat16 or "
@@ -1333,7 +1341,7 @@ class _GradTable:
         grads, outs = self.grads, list(grads_out)
         if len(outs) != self.n:
             raise ValueError(f"{len(outs)} outputs for {self.n} gradients")
-        codes = list(map(_GRAD_TYPES.get, map(_dtype_of, outs)))
+        codes = list(map(_TYPE_CODES.get, map(_dtype_of, outs)))
         same = (codes == self.code_list and
                 list(map(torch.Tensor.numel, outs)) == self.size_list and
                 set(map(torch.Tensor.get_device, outs)) ==
