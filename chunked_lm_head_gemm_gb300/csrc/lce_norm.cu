@@ -60,7 +60,7 @@ constexpr int MAX_CLUSTER = 8;
 constexpr int CLUSTER_H = BLOCK_H * MAX_CLUSTER;
 // A row's team. BIG: a block of up to 1024 threads, where the registers allow it
 // (the forward pass of rows on 16 bytes): a block's barrier is a third of a
-// cluster's. 16384 rows of 16384 bf16, layer norm: 249 us against
+// cluster's. 16384 rows of 16384 bf16, layer norm: 217 us against
 // 585.
 enum Mode { LANES, BLOCK, CLUSTER, BIG };
 constexpr int BIG_H = 2 * BLOCK_H;
@@ -134,14 +134,18 @@ __device__ __forceinline__ void team_sum(float (&v)[N], const NormArgs& a,
 
 // A group (a warp of lane teams, or the block) and its ring of tiles. A tile
 // is tile_rows rows, one after the other in memory; the group takes tiles
-// first, first + step, ... What is copied is the 16-byte units that cover the
-// tile; a tile whose units reach past the array's ends (the first and last,
-// of arrays that do not begin or end on 16 bytes) is read where it lies.
-template <typename T, Mode M, int ARRAYS>
+// first, first + step, ... Rows that are not on 16 bytes (V = 1): the 16-byte
+// units that cover the tile are copied; a tile whose units reach past the
+// array's ends (the first and last, of arrays that do not begin or end on 16
+// bytes) is read where it lies.
+template <typename T, int V, Mode M, int ARRAYS>
 struct Tiles {
   const NormArgs& a;
-  int64_t tiles, first, step, next;  // next: the tile to be fetched
-  int rank, column, width;           // of the cluster's slice
+  int64_t tiles, step, tile, next;  // the present tile, the next to be fetched
+  int rank, column, width;          // of the cluster's slice
+  int last_rows;                    // of the last tile
+  int64_t leap;                     // bytes from a tile of the group to the next
+  const char* from[ARRAYS];         // of the tile to be fetched
   uint32_t ring, bars;
   int fetch_stage, stage, phase;
   uint32_t offset[ARRAYS];  // of the present tile in its stage
@@ -157,10 +161,17 @@ struct Tiles {
     rank = M == CLUSTER ? blockIdx.x % a.cluster : 0;
     column = M == CLUSTER ? rank * a.slice : 0;
     width = M == CLUSTER ? min(a.slice, a.H - column) : a.H;
-    tiles = (a.L + a.tile_rows - 1) / a.tile_rows;
+    tiles = M == LANES ? (a.L + a.tile_rows - 1) / a.tile_rows : a.L;
+    last_rows = static_cast<int>(a.L - (tiles - 1) * a.tile_rows);
     step = static_cast<int64_t>(M == CLUSTER ? gridDim.x / a.cluster
                                              : gridDim.x) * groups;
-    first = next = static_cast<int64_t>(block) * groups + group;
+    tile = next = static_cast<int64_t>(block) * groups + group;
+    leap = (M == LANES ? step * a.tile_rows : step) * a.H *
+           static_cast<int64_t>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < ARRAYS; ++i)
+      from[i] = array(i) + (first_row() * a.H + column) *
+                               static_cast<int64_t>(sizeof(T));
     ring = smem_u32(smem) + group * a.stages * ARRAYS * a.array_bytes;
     bars = smem_u32(bar) + group * MAX_STAGES * 8;
     fetch_stage = stage = phase = 0;
@@ -184,65 +195,73 @@ struct Tiles {
   __device__ __forceinline__ const char* array(int i) const {
     return static_cast<const char*>(i ? a.dy : a.x);
   }
-  // The units that cover tile t of an array: where they begin, and their
-  // bytes, 0 if they reach past the array.
-  __device__ __forceinline__ uint32_t window(int i, int64_t t,
-                                             uintptr_t* from) const {
-    const int64_t row = t * a.tile_rows, bytes = a.H * sizeof(T);
-    const int64_t rows = min(static_cast<int64_t>(a.tile_rows), a.L - row);
+  __device__ __forceinline__ int64_t first_row() const {
+    return M == LANES ? tile * a.tile_rows : tile;
+  }
+  __device__ __forceinline__ int rows_of(int64_t t) const {
+    return M != LANES ? 1 : t == tiles - 1 ? last_rows : a.tile_rows;
+  }
+  // The units that cover the bytes of tile t of array i that begin at `begin`:
+  // their own begin, and their bytes, 0 if they reach past the array.
+  __device__ __forceinline__ uint32_t window(int i, int64_t t, uintptr_t begin,
+                                             uintptr_t* at) const {
+    const uint32_t bytes = ((rows_of(t) - 1) * a.H + width) * sizeof(T);
+    *at = begin;
+    if (V > 1) return bytes;
+    *at = begin & ~static_cast<uintptr_t>(15);
+    const uintptr_t to = (begin + bytes + 15) & ~static_cast<uintptr_t>(15);
     const uintptr_t base = reinterpret_cast<uintptr_t>(array(i));
-    const uintptr_t begin = base + row * bytes + column * sizeof(T);
-    const uintptr_t end = begin + (rows - 1) * bytes + width * sizeof(T);
-    *from = begin & ~static_cast<uintptr_t>(15);
-    const uintptr_t to = (end + 15) & ~static_cast<uintptr_t>(15);
-    if (*from < base || to > base + a.L * bytes) return 0;
-    return static_cast<uint32_t>(to - *from);
+    if (*at < base || to > base + a.L * a.H * sizeof(T)) return 0;
+    return static_cast<uint32_t>(to - *at);
   }
   // Fetches the group's next tile into the stage that was read last.
   __device__ __forceinline__ void fetch() {
     if (next < tiles && leader()) {
-      uintptr_t from[ARRAYS];
+      uintptr_t at[ARRAYS];
       uint32_t bytes[ARRAYS], all = 0;
 #pragma unroll
-      for (int i = 0; i < ARRAYS; ++i) all += bytes[i] = window(i, next, &from[i]);
+      for (int i = 0; i < ARRAYS; ++i)
+        all += bytes[i] = window(
+            i, next, reinterpret_cast<uintptr_t>(from[i]), &at[i]);
       const uint32_t bar = bars + 8 * fetch_stage;
       mbar_arrive_expect_tx(bar, all);
 #pragma unroll
       for (int i = 0; i < ARRAYS; ++i)
-        if (bytes[i])
+        if (V > 1 || bytes[i])
           bulk_load(ring + (fetch_stage * ARRAYS + i) * a.array_bytes,
-                    reinterpret_cast<const void*>(from[i]), bytes[i], bar);
+                    reinterpret_cast<const void*>(at[i]), bytes[i], bar);
     }
+#pragma unroll
+    for (int i = 0; i < ARRAYS; ++i) from[i] += leap;
     next += step;
     fetch_stage = fetch_stage + 1 == a.stages ? 0 : fetch_stage + 1;
   }
-  // Waits for tile t in the present stage. (Should the wait run out, which
-  // raises the error, the rows are wrong but every barrier is still met.)
-  template <int V>
-  __device__ __forceinline__ void wait(int64_t t) {
+  // Waits for the present tile and returns its rows. (Should the wait run out,
+  // which raises the error, they are wrong but every barrier is still met.)
+  __device__ __forceinline__ int wait() {
 #pragma unroll
     for (int i = 0; i < ARRAYS; ++i) {
       offset[i] = ring + (stage * ARRAYS + i) * a.array_bytes;
       copied[i] = true;
-      if (V == 1) {  // else rows begin and end on 16 bytes
-        uintptr_t from;
-        copied[i] = window(i, t, &from) != 0;
-        offset[i] += static_cast<uint32_t>(
-            reinterpret_cast<uintptr_t>(array(i)) +
-            (t * a.tile_rows * a.H + column) * sizeof(T) - from);
+      if (V == 1) {
+        const uintptr_t begin = reinterpret_cast<uintptr_t>(array(i)) +
+                                (first_row() * a.H + column) * sizeof(T);
+        uintptr_t at;
+        copied[i] = window(i, tile, begin, &at) != 0;
+        offset[i] += static_cast<uint32_t>(begin - at);
       }
     }
     mbar_wait(bars + 8 * stage, phase, ctx, true);
+    return M == LANES ? rows_of(tile) : 1;
   }
+  __device__ __forceinline__ bool more() const { return tile < tiles; }
   __device__ __forceinline__ void advance() {
+    tile += step;
     stage = stage + 1 == a.stages ? 0 : stage + 1;
     if (stage == 0) phase ^= 1;
   }
-  // Chunk k of the slice of row r of the tile, row `row` of the array (0: x,
-  // 1: dy).
-  template <int V>
-  __device__ __forceinline__ Chunk<T, V> chunk(int i, int64_t row, int r,
-                                               int k) const {
+  // Chunk k of row r of the present tile's slice (array 0: x, 1: dy).
+  __device__ __forceinline__ Chunk<T, V> chunk(int i, int r, int k) const {
     Chunk<T, V> c;
     const uint32_t at =
         offset[i] + (static_cast<uint32_t>(r) * a.H + k * V) * sizeof(T);
@@ -254,7 +273,7 @@ struct Tiles {
     } else {
       if (!copied[i])
         return load_chunk<T, V>(reinterpret_cast<const T*>(array(i)) +
-                                row * a.H + column + k);
+                                (first_row() + r) * a.H + column + k);
       if constexpr (sizeof(T) == 4) {
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(c.q) : "r"(at) : "memory");
       } else {
@@ -294,7 +313,7 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
   for (int i = threadIdx.x; i < 2 * AREA<M>; i += blockDim.x)
     (&area[0][0][0])[i] = 0.f;
   __syncthreads();
-  Tiles<T, M, 1> tiles(a, smem, bar, &abort_flag);
+  Tiles<T, V, M, 1> tiles(a, smem, bar, &abort_flag);
   const int team = M == LANES ? a.team : blockDim.x;
   const int id = M == LANES ? threadIdx.x & (team - 1) : threadIdx.x;
   const int rows_at_once = M == LANES ? 32 / team : 1;
@@ -308,18 +327,18 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
   if (LAYER)
     load_params<V>(a.bias, a.param_f32, tiles.column, tiles.width, id, team,
                    0.f, b);
-  for (int64_t t = tiles.first; t < tiles.tiles; t += tiles.step) {
-    tiles.template wait<V>(t);
-    for (int m = 0; m < a.tile_rows; m += rows_at_once) {
+  for (; tiles.more(); tiles.advance()) {
+    const int rows = tiles.wait();
+    const int64_t row0 = tiles.first_row();
+    T* out = static_cast<T*>(a.y) + row0 * a.H + tiles.column + id * V;
+    for (int m = 0; m < rows; m += rows_at_once) {
       const int r = m + sub;
-      const int64_t row = t * a.tile_rows + r;
-      const bool on = row < a.L;
+      const bool on = r < rows;
       Chunk<T, V> x[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int k = id + team * c;
-        x[c] = on && k < chunks ? tiles.template chunk<V>(0, row, r, k)
-                                : no_chunk<T, V>();
+        x[c] = on && k < chunks ? tiles.chunk(0, r, k) : no_chunk<T, V>();
       }
       float mu = 0.f, s[1];
       uint64_t q = 0;  // a pair of zeros
@@ -353,10 +372,9 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
       s[0] = sum_of_pair(q);
       team_sum<M, 1>(s, a, tiles.rank, area, turn);
       if (M != LANES) tiles.fetch();  // every thread has its elements
-      const float rs = 1.f / sqrtf(s[0] * inv + a.eps);
+      const float rs = rsqrtf(s[0] * inv + a.eps);
       const uint64_t rs2 = f2pack(rs, rs);
       if (on) {
-        T* y = static_cast<T*>(a.y) + row * a.H + tiles.column;
         float o[EPT];
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
@@ -368,13 +386,12 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const int k = id + team * c;
-          if (k < chunks)
-            store_chunk<T, V>(y + static_cast<int64_t>(k) * V, &o[c * V]);
+          if (id + team * c < chunks)
+            store_chunk<T, V>(out + r * a.H + team * c * V, &o[c * V]);
         }
         if (id == 0 && tiles.rank == 0) {
-          if (LAYER && a.mean) a.mean[row] = mu;
-          if (a.rstd) a.rstd[row] = rs;
+          if (LAYER && a.mean) a.mean[row0 + r] = mu;
+          if (a.rstd) a.rstd[row0 + r] = rs;
         }
       }
     }
@@ -382,7 +399,6 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
       __syncwarp();
       tiles.fetch();
     }
-    tiles.advance();
   }
   if (M == CLUSTER) cluster_sync();  // no block ends before its sums are read
 }
@@ -400,7 +416,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
   for (int i = threadIdx.x; i < 2 * SUMS * AREA<M>; i += blockDim.x)
     (&area[0][0][0])[i] = 0.f;
   __syncthreads();
-  Tiles<T, M, 2> tiles(a, smem, bar, &abort_flag);
+  Tiles<T, V, M, 2> tiles(a, smem, bar, &abort_flag);
   const int team = M == LANES ? a.team : blockDim.x;
   const int id = M == LANES ? threadIdx.x & (team - 1) : threadIdx.x;
   const int rows_at_once = M == LANES ? 32 / team : 1;
@@ -413,33 +429,39 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
                  team, 1.f, w);
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) dw[i] = db[i] = 0;
-  // the statistics of the next rows are under way while rows are computed
+  // the statistics of the next tile, a lane to a row, are under way while one
+  // is computed
+  const int lane = M == LANES ? threadIdx.x & 31 : 0;
   float rs_next = 0.f, mu_next = 0.f;
-  auto look_ahead = [&](int64_t row) {
-    const bool on = row < a.L;
+  auto look_ahead = [&](int64_t t) {
+    const bool on = t < tiles.tiles && lane < tiles.rows_of(t);
+    const int64_t row = (M == LANES ? t * a.tile_rows : t) + lane;
     rs_next = on ? a.rstd[row] : 0.f;
     if (LAYER) mu_next = on ? a.mean[row] : 0.f;
   };
-  look_ahead(tiles.first * a.tile_rows + sub);
-  for (int64_t t = tiles.first; t < tiles.tiles; t += tiles.step) {
-    tiles.template wait<V>(t);
-    for (int m = 0; m < a.tile_rows; m += rows_at_once) {
+  look_ahead(tiles.tile);
+  for (; tiles.more(); tiles.advance()) {
+    const int rows = tiles.wait();
+    const float rs_tile = rs_next, mu_tile = mu_next;
+    look_ahead(tiles.tile + tiles.step);
+    T* out =
+        static_cast<T*>(a.y) + tiles.first_row() * a.H + tiles.column + id * V;
+    for (int m = 0; m < rows; m += rows_at_once) {
       const int r = m + sub;
-      const int64_t row = t * a.tile_rows + r;
-      const bool on = row < a.L;
-      const float rs = rs_next;
-      const uint64_t rs2 = f2pack(rs, rs);
-      const uint64_t minus = f2pack(-mu_next, -mu_next);
-      look_ahead(m + rows_at_once < a.tile_rows
-                     ? row + rows_at_once
-                     : (t + tiles.step) * a.tile_rows + sub);
+      const bool on = r < rows;
+      float rs = rs_tile, mu = mu_tile;
+      if (M == LANES) {
+        rs = __shfl_sync(ALL_LANES, rs_tile, r);
+        if (LAYER) mu = __shfl_sync(ALL_LANES, mu_tile, r);
+      }
+      const uint64_t rs2 = f2pack(rs, rs), minus = f2pack(-mu, -mu);
       Chunk<T, V> x[C], dy[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int k = id + team * c;
         const bool has = on && k < chunks;
-        x[c] = has ? tiles.template chunk<V>(0, row, r, k) : no_chunk<T, V>();
-        dy[c] = has ? tiles.template chunk<V>(1, row, r, k) : no_chunk<T, V>();
+        x[c] = has ? tiles.chunk(0, r, k) : no_chunk<T, V>();
+        dy[c] = has ? tiles.chunk(1, r, k) : no_chunk<T, V>();
       }
       auto normed = [&](int i) {
         uint64_t n = pair_of(x, i);
@@ -473,7 +495,6 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
       const float c1 = LAYER ? -rs * (s[SUMS - 1] * inv) : 0.f;
       const uint64_t c22 = f2pack(c2, c2), c12 = f2pack(c1, c1);
       if (on) {
-        T* dx = static_cast<T*>(a.y) + row * a.H + tiles.column;
         float o[EPT];
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
@@ -483,9 +504,8 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const int k = id + team * c;
-          if (k < chunks)
-            store_chunk<T, V>(dx + static_cast<int64_t>(k) * V, &o[c * V]);
+          if (id + team * c < chunks)
+            store_chunk<T, V>(out + r * a.H + team * c * V, &o[c * V]);
         }
       }
     }
@@ -493,7 +513,6 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
       __syncwarp();
       tiles.fetch();
     }
-    tiles.advance();
   }
   if (M == CLUSTER) cluster_sync();  // no block ends before its sums are read
   if (!a.part) return;
