@@ -150,6 +150,9 @@ struct Tiles {
   int fetch_stage, stage, phase;
   uint32_t offset[ARRAYS];  // of the present tile in its stage
   bool copied[ARRAYS];
+  bool gave_up;            // a wait ran out: nothing more is fetched
+  int64_t lost, lost_end;  // its tile, and the one that would be fetched next
+  int lost_stage, lost_phase;
   WaitCtx ctx;
 
   __device__ __forceinline__ Tiles(const NormArgs& args, unsigned char* smem,
@@ -175,6 +178,7 @@ struct Tiles {
     ring = smem_u32(smem) + group * a.stages * ARRAYS * a.array_bytes;
     bars = smem_u32(bar) + group * MAX_STAGES * 8;
     fetch_stage = stage = phase = 0;
+    gave_up = false;
     ctx = WaitCtx{abort_flag, a.err, a.timeout_ns};
     if (threadIdx.x == 0) {
       *abort_flag = 0;
@@ -216,7 +220,7 @@ struct Tiles {
   }
   // Fetches the group's next tile into the stage that was read last.
   __device__ __forceinline__ void fetch() {
-    if (next < tiles && leader()) {
+    if (next < tiles && leader() && !gave_up) {
       uintptr_t at[ARRAYS];
       uint32_t bytes[ARRAYS], all = 0;
 #pragma unroll
@@ -236,8 +240,8 @@ struct Tiles {
     next += step;
     fetch_stage = fetch_stage + 1 == a.stages ? 0 : fetch_stage + 1;
   }
-  // Waits for the present tile and returns its rows. (Should the wait run out,
-  // which raises the error, they are wrong but every barrier is still met.)
+  // Waits for the present tile and returns its rows. Should the wait run out,
+  // which raises the error, they are wrong, but every barrier is still met.
   __device__ __forceinline__ int wait() {
 #pragma unroll
     for (int i = 0; i < ARRAYS; ++i) {
@@ -251,7 +255,13 @@ struct Tiles {
         offset[i] += static_cast<uint32_t>(begin - at);
       }
     }
-    mbar_wait(bars + 8 * stage, phase, ctx, true);
+    if (!mbar_wait(bars + 8 * stage, phase, ctx, true) && !gave_up) {
+      gave_up = true;
+      lost = tile;
+      lost_end = next < tiles ? next : tiles;
+      lost_stage = stage;
+      lost_phase = phase;
+    }
     return M == LANES ? rows_of(tile) : 1;
   }
   __device__ __forceinline__ bool more() const { return tile < tiles; }
@@ -259,6 +269,16 @@ struct Tiles {
     tile += step;
     stage = stage + 1 == a.stages ? 0 : stage + 1;
     if (stage == 0) phase ^= 1;
+  }
+  // After a wait that ran out: the copies still under way end, or are given
+  // as long again, before the block does.
+  __device__ __forceinline__ void drain() {
+    if (!gave_up || !leader()) return;
+    for (; lost < lost_end; lost += step) {
+      mbar_wait(bars + 8 * lost_stage, lost_phase, ctx, false);
+      lost_stage = lost_stage + 1 == a.stages ? 0 : lost_stage + 1;
+      if (lost_stage == 0) lost_phase ^= 1;
+    }
   }
   // Chunk k of row r of the present tile's slice (array 0: x, 1: dy).
   __device__ __forceinline__ Chunk<T, V> chunk(int i, int r, int k) const {
@@ -400,6 +420,7 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
       tiles.fetch();
     }
   }
+  tiles.drain();
   if (M == CLUSTER) cluster_sync();  // no block ends before its sums are read
 }
 
@@ -514,6 +535,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
       tiles.fetch();
     }
   }
+  tiles.drain();
   if (M == CLUSTER) cluster_sync();  // no block ends before its sums are read
   if (!a.part) return;
   const int slab = M == CLUSTER ? blockIdx.x / a.cluster : blockIdx.x;
