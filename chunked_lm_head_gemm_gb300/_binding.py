@@ -1043,11 +1043,13 @@ def _call(name, device, *args):
     device's current stream (the last argument)."""
     index = device.index
     fn = getattr(_lib or load(), name)
-    if index is None or index == torch._C._cuda_getDevice():
+    if index is None:
         st = fn(*args, _stream_ptr(device))
+    elif index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, _stream_ptr(device))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st:
         _check(st, name)
 
@@ -1108,10 +1110,12 @@ def _norm_forward(kind, x, weight, bias, eps, y_out, save_stats):
     if save_stats:
         rstd = torch.empty(L, dtype=torch.float32, device=dev)
         if kind == LAYER_NORM:
-            mean = torch.empty(L, dtype=torch.float32, device=dev)
-    _call("lce_norm_forward", dev, kind, x.data_ptr(), code, _ptr(weight),
-          _ptr(bias), param, L, H, float(eps), y.data_ptr(), _ptr(mean),
-          _ptr(rstd))
+            mean = torch.empty_like(rstd)
+    _call("lce_norm_forward", dev, kind, x.data_ptr(), code,
+          None if weight is None else weight.data_ptr(),
+          None if bias is None else bias.data_ptr(), param, L, H, eps,
+          y.data_ptr(), None if mean is None else mean.data_ptr(),
+          None if rstd is None else rstd.data_ptr())
     return y, mean, rstd
 
 
@@ -1122,7 +1126,8 @@ def _norm_backward(kind, x, weight, mean, rstd, dy, grad_dtype, workspace,
     _check_rows("rstd", rstd, (L,), torch.float32, dev)
     if kind == LAYER_NORM:
         _check_rows("mean", mean, (L,), torch.float32, dev)
-    if grad_dtype not in (torch.float32, torch.bfloat16):
+    grad_code = _TYPE_CODES.get(grad_dtype)
+    if grad_code is None:
         raise TypeError("grad_dtype must be float32 or bfloat16")
     dx = dw = db = None
     if compute_dx:
@@ -1134,17 +1139,21 @@ def _norm_backward(kind, x, weight, mean, rstd, dy, grad_dtype, workspace,
         dw = torch.empty(H, dtype=grad_dtype, device=dev)
     if compute_dbias:
         db = torch.empty(H, dtype=grad_dtype, device=dev)
-    bytes_ = 0
+    size = 0
     if workspace is not None:
         _check_workspace(workspace, dev)
-        bytes_ = workspace.numel() * workspace.element_size()
+        size = workspace.numel() * workspace.element_size()
     elif compute_dweight or compute_dbias:
-        bytes_ = norm_workspace_size(L, H)
-        workspace = torch.empty(bytes_, dtype=torch.uint8, device=dev)
-    _call("lce_norm_backward", dev, kind, x.data_ptr(), code, _ptr(weight),
-          param, _ptr(mean), rstd.data_ptr(), dy.data_ptr(), L, H,
-          LCE_F32 if grad_dtype == torch.float32 else LCE_BF16, _ptr(dx),
-          _ptr(dw), _ptr(db), _ptr(workspace), bytes_)
+        size = norm_workspace_size(L, H)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    _call("lce_norm_backward", dev, kind, x.data_ptr(), code,
+          None if weight is None else weight.data_ptr(), param,
+          None if mean is None else mean.data_ptr(), rstd.data_ptr(),
+          dy.data_ptr(), L, H, grad_code,
+          None if dx is None else dx.data_ptr(),
+          None if dw is None else dw.data_ptr(),
+          None if db is None else db.data_ptr(),
+          None if workspace is None else workspace.data_ptr(), size)
     return dx, dw, db
 
 
@@ -1237,7 +1246,8 @@ def balance_forward(logits, experts, scoring: str = "softmax",
     counts = torch.empty(E, dtype=torch.int32, device=dev)
     slopes = torch.empty(E, dtype=torch.float32, device=dev)
     _call("lce_balance_forward", dev, logits.data_ptr(), code,
-          experts.data_ptr(), _ptr(mask), L, E, K, score, float(coef),
+          experts.data_ptr(), None if mask is None else mask.data_ptr(), L, E,
+          K, score, float(coef),
           loss.data_ptr(), counts.data_ptr(), slopes.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return loss, counts, slopes
@@ -1255,14 +1265,16 @@ def balance_backward(logits, slopes, dloss, scoring: str = "softmax",
     score = _scoring_code(scoring)
     if dloss.numel() != 1:
         raise ValueError("dloss must be one value")
-    dloss = dloss.reshape(1).to(device=dev, dtype=torch.float32)
+    if dloss.dtype is not torch.float32 or dloss.device != dev:
+        dloss = dloss.to(device=dev, dtype=torch.float32)
     if dlogits_out is not None:
         out = _check_out("dlogits_out", dlogits_out, logits.shape,
                          logits.dtype, dev)
     else:
         out = torch.empty_like(logits)
-    _call("lce_balance_backward", dev, logits.data_ptr(), code, _ptr(mask), L,
-          E, score, slopes.data_ptr(), dloss.data_ptr(), out.data_ptr())
+    _call("lce_balance_backward", dev, logits.data_ptr(), code,
+          None if mask is None else mask.data_ptr(), L, E, score,
+          slopes.data_ptr(), dloss.data_ptr(), out.data_ptr())
     return out
 
 
@@ -1278,7 +1290,8 @@ def expert_counts(experts, num_experts: int, mask=None, counts_out=None):
         counts = _check_out("counts_out", counts_out, (E,), torch.int32, dev)
     else:
         counts = torch.empty(max(E, 0), dtype=torch.int32, device=dev)
-    _call("lce_expert_counts", dev, experts.data_ptr(), _ptr(mask), L, E, K,
+    _call("lce_expert_counts", dev, experts.data_ptr(),
+          None if mask is None else mask.data_ptr(), L, E, K,
           counts.data_ptr())
     return counts
 

@@ -207,7 +207,8 @@ def test_a_call_runs_with_its_tensors_device_current(monkeypatch):
             return 0
 
     monkeypatch.setattr(B, "_lib", Lib)
-    monkeypatch.setattr(B, "_stream_ptr", lambda d: 100 + d.index)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream",
+                        lambda i: 100 + i, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0,
                         raising=False)
     monkeypatch.setattr(torch.cuda, "device", Guard)
