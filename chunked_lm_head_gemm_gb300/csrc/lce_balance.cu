@@ -156,7 +156,8 @@ __device__ __forceinline__ float scores(uint64_t (&z)[P], uint64_t (&slope)[P],
 }
 
 // The rows of a lane: its row's elements, runs of V, a row every `step`; the
-// next is under way while one is computed. Rows that take no part are not read.
+// next is under way while one is computed. Rows that take no part are not read
+// and leave the last one's elements; elements beyond E are -inf throughout.
 template <typename T, int N, int V>
 struct Rows {
   const int id, team, E, L, step;
@@ -179,6 +180,11 @@ struct Rows {
         masks(a.mask ? a.mask + first : nullptr),
         row(first),
         leap(static_cast<int64_t>(step_) * a.E) {
+    float off[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) off[i] = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < N / V; ++c) q[c].pack(off);
     look();
     load();
   }
@@ -199,19 +205,9 @@ struct Rows {
     next += leap;
     look();
   }
-  // The row in pairs; -inf beyond E and for a row that takes no part.
   __device__ __forceinline__ void unpack(uint64_t (&z)[N / 2]) const {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      if constexpr (V > 1) {
-        const bool has = on && (id + team * (2 * i / V)) * V < E;
-        z[i] = has ? pair_of(q, i) : both(-INFINITY);
-      } else {
-        const int j = id + team * 2 * i;
-        z[i] = f2pack(on && j < E ? q[2 * i].at(0) : -INFINITY,
-                      on && j + team < E ? q[2 * i + 1].at(0) : -INFINITY);
-      }
-    }
+    for (int i = 0; i < N / 2; ++i) z[i] = pair_of(q, i);
   }
 };
 
@@ -226,7 +222,7 @@ __device__ __forceinline__ void count_slots(const int32_t* experts,
                                             const uint8_t* mask, int64_t t0,
                                             int64_t t1, int K, int E, int* hist,
                                             unsigned* err) {
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = 8;
   const int64_t end = t1 * K;
   for (int64_t i0 = t0 * K + threadIdx.x; i0 < end;
        i0 += AHEAD * static_cast<int64_t>(blockDim.x)) {
@@ -288,12 +284,15 @@ __global__ void __launch_bounds__(WARPS * 32, blocks_per_sm(N))
   for (int t0 = first; t0 < a.L; t0 += step) {
     uint64_t z[P], unused[P];
     rows.unpack(z);
-    tokens += rows.on;
+    const bool on = rows.on;
+    tokens += on;
     rows.load();
     const float t = scores<P, SIGMOID, false>(z, unused, a.team);
     const uint64_t inv = both(t == 0.f ? 0.f : reciprocal(t));
+    if (on) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) pairs[i] = fma2(z[i], inv, pairs[i]);
+      for (int i = 0; i < P; ++i) pairs[i] = fma2(z[i], inv, pairs[i]);
+    }
   }
   float acc[N];
 #pragma unroll

@@ -134,12 +134,13 @@ __device__ __forceinline__ void team_sum(float (&v)[N], const NormArgs& a,
 
 // A group (a warp of lane teams, or the block) and its ring of tiles. A tile
 // is tile_rows rows, one after the other in memory; the group takes tiles
-// first, first + step, ... Rows that are not on 16 bytes (V = 1): the 16-byte
-// units that cover the tile are copied; a tile whose units reach past the
+// first, first + step, ... Of rows that are not on 16 bytes (chunks of less) the
+// 16-byte units that cover the tile are copied; a tile whose units reach past the
 // array's ends (the first and last, of arrays that do not begin or end on 16
 // bytes) is read where it lies.
 template <typename T, int V, Mode M, int ARRAYS>
 struct Tiles {
+  static constexpr bool EXACT = V * sizeof(T) == 16;
   const NormArgs& a;
   int64_t tiles, step, tile, next;  // the present tile, the next to be fetched
   int rank, column, width;          // of the cluster's slice
@@ -211,7 +212,7 @@ struct Tiles {
                                              uintptr_t* at) const {
     const uint32_t bytes = ((rows_of(t) - 1) * a.H + width) * sizeof(T);
     *at = begin;
-    if (V > 1) return bytes;
+    if (EXACT) return bytes;
     *at = begin & ~static_cast<uintptr_t>(15);
     const uintptr_t to = (begin + bytes + 15) & ~static_cast<uintptr_t>(15);
     const uintptr_t base = reinterpret_cast<uintptr_t>(array(i));
@@ -231,7 +232,7 @@ struct Tiles {
       mbar_arrive_expect_tx(bar, all);
 #pragma unroll
       for (int i = 0; i < ARRAYS; ++i)
-        if (V > 1 || bytes[i])
+        if (EXACT || bytes[i])
           bulk_load(ring + (fetch_stage * ARRAYS + i) * a.array_bytes,
                     reinterpret_cast<const void*>(at[i]), bytes[i], bar);
     }
@@ -247,7 +248,7 @@ struct Tiles {
     for (int i = 0; i < ARRAYS; ++i) {
       offset[i] = ring + (stage * ARRAYS + i) * a.array_bytes;
       copied[i] = true;
-      if (V == 1) {
+      if (!EXACT) {
         const uintptr_t begin = reinterpret_cast<uintptr_t>(array(i)) +
                                 (first_row() * a.H + column) * sizeof(T);
         uintptr_t at;
@@ -280,32 +281,51 @@ struct Tiles {
       if (lost_stage == 0) lost_phase ^= 1;
     }
   }
-  // Chunk k of row r of the present tile's slice (array 0: x, 1: dy).
-  __device__ __forceinline__ Chunk<T, V> chunk(int i, int r, int k) const {
-    Chunk<T, V> c;
-    const uint32_t at =
-        offset[i] + (static_cast<uint32_t>(r) * a.H + k * V) * sizeof(T);
-    if constexpr (V > 1) {
+  // Chunks id, id + team, ... of row r of the present tile's slice (array 0: x,
+  // 1: dy), zeros past its end or without `on`.
+  __device__ __forceinline__ void row(int i, int r, bool on, int id, int team,
+                                      int chunks,
+                                      Chunk<T, V> (&q)[EPT / V]) const {
+    constexpr int C = EPT / V;
+    if (EXACT || copied[i]) {
+      const uint32_t at =
+          offset[i] + (static_cast<uint32_t>(r) * a.H + id * V) * sizeof(T);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        q[c] = no_chunk<T, V>();
+        if (on && id + team * c < chunks)
+          load_shared(at + team * c * V * sizeof(T), q[c]);
+      }
+    } else {
+      const T* p = reinterpret_cast<const T*>(array(i)) +
+                   (first_row() + r) * a.H + column + id * V;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        q[c] = on && id + team * c < chunks ? load_chunk<T, V>(p + team * c * V)
+                                            : no_chunk<T, V>();
+    }
+  }
+  static __device__ __forceinline__ void load_shared(uint32_t at,
+                                                     Chunk<T, V>& c) {
+    if constexpr (EXACT) {
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(c.q.x), "=r"(c.q.y), "=r"(c.q.z), "=r"(c.q.w)
                    : "r"(at)
                    : "memory");
+    } else if constexpr (V * sizeof(T) == 8) {
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(c.q.x), "=r"(c.q.y)
+                   : "r"(at)
+                   : "memory");
+    } else if constexpr (V == 2) {
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.q) : "r"(at) : "memory");
+    } else if constexpr (sizeof(T) == 4) {
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(c.q) : "r"(at) : "memory");
     } else {
-      if (!copied[i])
-        return load_chunk<T, V>(reinterpret_cast<const T*>(array(i)) +
-                                (first_row() + r) * a.H + column + k);
-      if constexpr (sizeof(T) == 4) {
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(c.q) : "r"(at) : "memory");
-      } else {
-        unsigned short bits;
-        asm volatile("ld.shared.u16 %0, [%1];"
-                     : "=h"(bits)
-                     : "r"(at)
-                     : "memory");
-        c.q = __ushort_as_bfloat16(bits);
-      }
+      unsigned short bits;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(at) : "memory");
+      c.q = __ushort_as_bfloat16(bits);
     }
-    return c;
   }
 };
 
@@ -355,11 +375,7 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
       const int r = m + sub;
       const bool on = r < rows;
       Chunk<T, V> x[C];
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int k = id + team * c;
-        x[c] = on && k < chunks ? tiles.chunk(0, r, k) : no_chunk<T, V>();
-      }
+      tiles.row(0, r, on, id, team, chunks, x);
       float mu = 0.f, s[1];
       uint64_t q = 0;  // a pair of zeros
       if (LAYER) {
@@ -477,13 +493,8 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd(const NormArgs a) {
       }
       const uint64_t rs2 = f2pack(rs, rs), minus = f2pack(-mu, -mu);
       Chunk<T, V> x[C], dy[C];
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int k = id + team * c;
-        const bool has = on && k < chunks;
-        x[c] = has ? tiles.chunk(0, r, k) : no_chunk<T, V>();
-        dy[c] = has ? tiles.chunk(1, r, k) : no_chunk<T, V>();
-      }
+      tiles.row(0, r, on, id, team, chunks, x);
+      tiles.row(1, r, on, id, team, chunks, dy);
       auto normed = [&](int i) {
         uint64_t n = pair_of(x, i);
         if (LAYER) n = add2(n, minus);
@@ -714,13 +725,14 @@ struct Geometry {
 
 // Team, tile and ring of rows of H elements, `arrays` of them read, `v` to a
 // chunk. Tiles of lane teams are about 2 KB, so that a copy is worth its
-// issue. A cluster's slices are 4096 columns at first, as blocks of 256 threads
+// issue, where there are rows enough for all warps. A cluster's slices are 4096 columns at first, as blocks of 256 threads
 // share an SM with others, then 8192.
-Geometry geometry(NormArgs& a, int v, int size, int arrays) {
+Geometry geometry(NormArgs& a, int v, int size, int arrays, int num_sms) {
   Geometry g{};
+  const bool exact = v * size == 16;
   a.cluster = 1;
   a.slice = a.H;
-  const bool big = arrays == 1 && v > 1 && a.H > BLOCK_H && a.H <= BIG_H;
+  const bool big = arrays == 1 && exact && a.H > BLOCK_H && a.H <= BIG_H;
   if (a.H > BLOCK_H && !big) {
     a.cluster = a.H <= 4 * 4096 ? 4 : MAX_CLUSTER;
     a.slice = static_cast<int>(round_up(ceil_div(a.H, a.cluster), 16));
@@ -742,13 +754,14 @@ Geometry geometry(NormArgs& a, int v, int size, int arrays) {
     while (a.team < need) a.team *= 2;
     const int at_once = 32 / a.team;
     a.tile_rows = at_once;
-    while (a.tile_rows * a.H * size < 2048 && a.tile_rows < 32)
+    while (a.tile_rows * a.H * size < 2048 && a.tile_rows < 32 &&
+           a.L > static_cast<int64_t>(num_sms) * TEAM_WARPS * a.tile_rows * 2)
       a.tile_rows += at_once;
   }
   // with room for the units at both ends
   const int64_t bytes = static_cast<int64_t>(a.tile_rows) * a.slice * size;
   a.array_bytes = static_cast<uint32_t>(
-      v > 1 ? bytes : round_up(bytes, 16) + 16);
+      exact ? bytes : round_up(bytes, 16) + 16);
   const int64_t stage = static_cast<int64_t>(g.mode == LANES ? TEAM_WARPS : 1) *
                         arrays * a.array_bytes;
   a.stages = static_cast<int>(RING_BYTES / stage);
@@ -817,11 +830,11 @@ cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
 
 template <typename T, int V, bool LAYER>
 cudaError_t rows_fwd(NormArgs& a, int num_sms, cudaStream_t s) {
-  const Geometry g = geometry(a, V, sizeof(T), 1);
+  const Geometry g = geometry(a, V, sizeof(T), 1, num_sms);
   auto kern = g.mode == LANES   ? k_norm_fwd<T, V, LANES, LAYER>
               : g.mode == BLOCK ? k_norm_fwd<T, V, BLOCK, LAYER>
                                 : k_norm_fwd<T, V, CLUSTER, LAYER>;
-  if constexpr (V > 1) {
+  if constexpr (V * sizeof(T) == 16) {
     if (g.mode == BIG) kern = k_norm_fwd<T, V, BIG, LAYER>;
   }
   int teams;
@@ -829,7 +842,7 @@ cudaError_t rows_fwd(NormArgs& a, int num_sms, cudaStream_t s) {
 }
 template <typename T, int V, bool LAYER>
 cudaError_t rows_bwd(NormArgs& a, int num_sms, cudaStream_t s) {
-  const Geometry g = geometry(a, V, sizeof(T), 2);
+  const Geometry g = geometry(a, V, sizeof(T), 2, num_sms);
   a.size = sizeof(T);
   auto kern = g.mode == LANES   ? k_norm_bwd<T, V, LANES, LAYER>
               : g.mode == BLOCK ? k_norm_bwd<T, V, BLOCK, LAYER>
@@ -837,13 +850,28 @@ cudaError_t rows_bwd(NormArgs& a, int num_sms, cudaStream_t s) {
   return launch_rows(kern, a, g, num_sms, s, &a.slabs);
 }
 
+// Elements to a chunk: 16 bytes, else two, as far as every row of every array
+// begins on them; else one.
+template <typename T>
+int chunk_of(int H, const void* p, const void* q, const void* r) {
+  for (int v : {static_cast<int>(16 / sizeof(T)), 2}) {
+    const uintptr_t n = v * sizeof(T);
+    if (H % v == 0 && aligned_to(p, n) && aligned_to(q, n) && aligned_to(r, n))
+      return v;
+  }
+  return 1;
+}
+
 template <typename T, bool LAYER>
 cudaError_t forward(NormArgs& a, int num_sms, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const bool wide = a.H % V == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16);
-  if (a.H <= CLUSTER_H)
-    return wide ? rows_fwd<T, V, LAYER>(a, num_sms, s)
-                : rows_fwd<T, 1, LAYER>(a, num_sms, s);
+  if (a.H <= CLUSTER_H) {
+    switch (chunk_of<T>(a.H, a.x, a.y, nullptr)) {
+      case V: return rows_fwd<T, V, LAYER>(a, num_sms, s);
+      case 2: return rows_fwd<T, 2, LAYER>(a, num_sms, s);
+      default: return rows_fwd<T, 1, LAYER>(a, num_sms, s);
+    }
+  }
   const int64_t most = num_sms * 8;
   k_norm_fwd_wide<T, LAYER>
       <<<static_cast<unsigned>(a.L < most ? a.L : most), 256, 0, s>>>(a);
@@ -853,11 +881,13 @@ cudaError_t forward(NormArgs& a, int num_sms, cudaStream_t s) {
 template <typename T, bool LAYER>
 cudaError_t backward(NormArgs& a, int num_sms, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const bool wide = a.H % V == 0 && aligned_to(a.x, 16) &&
-                    aligned_to(a.dy, 16) && aligned_to(a.y, 16);
-  if (a.H <= CLUSTER_H)
-    return wide ? rows_bwd<T, V, LAYER>(a, num_sms, s)
-                : rows_bwd<T, 1, LAYER>(a, num_sms, s);
+  if (a.H <= CLUSTER_H) {
+    switch (chunk_of<T>(a.H, a.x, a.dy, a.y)) {
+      case V: return rows_bwd<T, V, LAYER>(a, num_sms, s);
+      case 2: return rows_bwd<T, 2, LAYER>(a, num_sms, s);
+      default: return rows_bwd<T, 1, LAYER>(a, num_sms, s);
+    }
+  }
   if (a.part) {
     a.slabs = static_cast<int>(slabs_of(a.L));
     k_norm_dparams_wide<T, LAYER>

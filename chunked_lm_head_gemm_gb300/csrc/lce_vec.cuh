@@ -61,6 +61,26 @@ struct Chunk<__nv_bfloat16, 8> {
                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 };
+template <>
+struct Chunk<float, 2> {
+  uint2 q;
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i ? q.y : q.x);
+  }
+  __device__ __forceinline__ void pack(const float* v) {
+    q = make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1]));
+  }
+};
+template <>
+struct Chunk<__nv_bfloat16, 2> {
+  uint32_t q;
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i ? q & 0xffff0000u : q << 16);
+  }
+  __device__ __forceinline__ void pack(const float* v) {
+    q = pack_bf16x2(v[0], v[1]);
+  }
+};
 template <typename T>
 struct Chunk<T, 1> {
   T q;

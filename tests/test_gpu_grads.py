@@ -79,6 +79,24 @@ def test_large():
     check(make([((50_000_001,), BF), ((30_000_000,), F32), ((17,), F32)]), 1.0)
 
 
+def test_a_tensor_past_32_bits():
+    """2^31 + 1000 elements, clipped in place: the last ones too."""
+    import chunked_lm_head_gemm_gb300 as lce
+    require_gpu()
+    n = 2 ** 31 + 1000
+    g = torch.zeros(n, dtype=BF, device="cuda")
+    g[-700:] = 3.0
+    g[:300] = 4.0
+    norm = lce.clip_grad_norm([g], 1.0)
+    want = math.sqrt(700 * 9 + 300 * 16)
+    assert abs(float(norm) - want) <= want * NORM
+    scale = 1.0 / (float(norm) + 1e-6)
+    for part, v in ((g[-700:], 3.0), (g[:300], 4.0)):
+        off = (part.double() - v * scale).abs().max()
+        assert off <= v * scale * (2 * ref.U + ref.half(BF))
+    assert not g[300:-700:100003].any()
+
+
 @pytest.mark.parametrize("max_norm", [0.0, 1e-6, 1.0, 1e30, math.inf])
 def test_limits(max_norm):
     """From everything to nothing clipped; a factor of 1 leaves the bits."""
