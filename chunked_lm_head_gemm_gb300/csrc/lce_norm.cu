@@ -132,6 +132,66 @@ __device__ __forceinline__ void team_sum(float (&v)[N], const NormArgs& a,
   }
 }
 
+// A thread's columns of a row's slice: n chunks of V, the first at column
+// `first`, `stride` columns apart.
+//
+// Pairs (V = 2) of rows of odd width begin on a pair's address in every other
+// row only. A team has rows of one parity, for which the pairs are shifted: where
+// a row begins on an odd element, its first pair holds one element, else its last
+// one does, and then the pairs are counted from the row's end. So the pair with
+// one element is always the first chunk of thread 0.
+struct Share {
+  int first, stride, n;
+  int outside;  // of the first chunk: 0 none, 1 the first element, 2 the second
+
+  template <int V>
+  static __device__ __forceinline__ Share of(int width, int id, int team,
+                                             int odd_start) {
+    Share p;
+    if (V == 2 && (width & 1)) {
+      const int pairs = (width + 1) >> 1;
+      const int k = odd_start ? id : pairs - 1 - id;
+      p.first = 2 * k - odd_start;
+      p.stride = odd_start ? 2 * team : -2 * team;
+      p.n = max(0, (pairs - id + team - 1) / team);
+      p.outside = id ? 0 : odd_start ? 1 : 2;
+    } else {
+      p.first = id * V;
+      p.stride = team * V;
+      p.n = max(0, (width / V - id + team - 1) / team);
+      p.outside = 0;
+    }
+    return p;
+  }
+  // Column of the thread's element i of EPT, -1 where it has none.
+  template <int V>
+  __device__ __forceinline__ int column(int i, int width) const {
+    const int j = first + (i / V) * stride + i % V;
+    return i / V < n && j < width ? j : -1;
+  }
+  __device__ __forceinline__ void mask(Chunk<__nv_bfloat16, 2>& c) const {
+    c.q &= outside == 1 ? 0xffff0000u : outside == 2 ? 0xffffu : 0xffffffffu;
+  }
+  __device__ __forceinline__ void mask(Chunk<float, 2>& c) const {
+    if (outside == 1) c.q.x = 0;
+    if (outside == 2) c.q.y = 0;
+  }
+  template <typename T, int V>
+  __device__ __forceinline__ void store(T* row, const float (&o)[EPT]) const {
+#pragma unroll
+    for (int c = 0; c < EPT / V; ++c) {
+      if (c >= n) continue;
+      T* at = row + first + c * stride;
+      if (V == 2 && c == 0 && outside) {
+        const int k = outside == 1;
+        at[k] = from_float<T>(o[k]);
+      } else {
+        store_chunk<T, V>(at, &o[c * V]);
+      }
+    }
+  }
+};
+
 // A group (a warp of lane teams, or the block) and its ring of tiles. A tile
 // is tile_rows rows, one after the other in memory; the group takes tiles
 // first, first + step, ... Of rows that are not on 16 bytes (chunks of less) the
@@ -266,6 +326,14 @@ struct Tiles {
     return M == LANES ? rows_of(tile) : 1;
   }
   __device__ __forceinline__ bool more() const { return tile < tiles; }
+  // Whether the team's rows of odd width begin on an odd element: they are of
+  // the parity of the team's place in its warp, or of the group's first tile,
+  // its tiles being an even number of rows apart.
+  __device__ __forceinline__ int odd_start(int rows_at_once, int sub) const {
+    const int row = rows_at_once > 1 ? sub : static_cast<int>(tile & 1);
+    return static_cast<int>(
+        (reinterpret_cast<uintptr_t>(a.x) / sizeof(T) + row) & 1);
+  }
   __device__ __forceinline__ void advance() {
     tile += step;
     stage = stage + 1 == a.stages ? 0 : stage + 1;
@@ -281,26 +349,35 @@ struct Tiles {
       if (lost_stage == 0) lost_phase ^= 1;
     }
   }
-  // The first n of the chunks id, id + team, ... of row r of the present tile's
-  // slice (array 0: x, 1: dy), zeros for the others.
-  __device__ __forceinline__ void row(int i, int r, int id, int team, int n,
+  // The thread's chunks of row r of the present tile's slice (array 0: x, 1:
+  // dy), zeros where it has none.
+  __device__ __forceinline__ void row(int i, int r, const Share& p, bool on,
                                       Chunk<T, V> (&q)[EPT / V]) const {
     constexpr int C = EPT / V;
+    const int n = on ? p.n : 0;
     if (EXACT || copied[i]) {
-      const uint32_t at =
-          offset[i] + (static_cast<uint32_t>(r) * a.H + id * V) * sizeof(T);
+      const uint32_t at = offset[i] + (r * a.H + p.first) *
+                                          static_cast<int>(sizeof(T));
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         q[c] = no_chunk<T, V>();
         if (c < n)
-          load_shared(at + team * c * V * sizeof(T), q[c]);
+          load_shared(at + c * p.stride * static_cast<int>(sizeof(T)), q[c]);
       }
+      if constexpr (V == 2) p.mask(q[0]);
     } else {
-      const T* p = reinterpret_cast<const T*>(array(i)) +
-                   (first_row() + r) * a.H + column + id * V;
+      const T* from = reinterpret_cast<const T*>(array(i)) +
+                      (first_row() + r) * a.H + column;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        q[c] = c < n ? load_chunk<T, V>(p + team * c * V) : no_chunk<T, V>();
+      for (int c = 0; c < C; ++c) {
+        float v[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const int j = p.first + c * p.stride + k;
+          v[k] = c < n && j >= 0 && j < width ? to_float(from[j]) : 0.f;
+        }
+        q[c].pack(v);
+      }
     }
   }
   static __device__ __forceinline__ void load_shared(uint32_t at,
@@ -330,12 +407,12 @@ struct Tiles {
 // A thread's columns of weight or bias in pairs, `absent` where there is none.
 template <int V>
 __device__ __forceinline__ void load_params(const void* p, bool f32, int column,
-                                            int width, int id, int team,
+                                            int width, const Share& share,
                                             float absent,
                                             uint64_t (&w)[PAIRS]) {
   auto at = [&](int i) {
-    const int j = (id + team * (i / V)) * V + i % V;
-    return j >= width ? 0.f : p ? load_as_float(p, f32, column + j) : absent;
+    const int j = share.column<V>(i, width);
+    return j < 0 ? 0.f : p ? load_as_float(p, f32, column + j) : absent;
   };
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) w[i] = f2pack(at(2 * i), at(2 * i + 1));
@@ -356,25 +433,25 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
   const int id = M == LANES ? threadIdx.x & (team - 1) : threadIdx.x;
   const int rows_at_once = M == LANES ? 32 / team : 1;
   const int sub = M == LANES ? (threadIdx.x & 31) / team : 0;
-  // chunks of the thread: the first `mine` of id, id + team, ...
-  const int mine = max(0, (tiles.width / V - id + team - 1) / team);
+  const Share share = Share::of<V>(tiles.width, id, team,
+                                   tiles.odd_start(rows_at_once, sub));
   const float inv = 1.f / a.H;
   int turn = 0;
   uint64_t w[PAIRS], b[PAIRS];
-  load_params<V>(a.weight, a.param_f32, tiles.column, tiles.width, id,
-                 team, 1.f, w);
+  load_params<V>(a.weight, a.param_f32, tiles.column, tiles.width, share, 1.f,
+                 w);
   if (LAYER)
-    load_params<V>(a.bias, a.param_f32, tiles.column, tiles.width, id, team,
-                   0.f, b);
+    load_params<V>(a.bias, a.param_f32, tiles.column, tiles.width, share, 0.f,
+                   b);
   for (; tiles.more(); tiles.advance()) {
     const int rows = tiles.wait();
     const int64_t row0 = tiles.first_row();
-    T* out = static_cast<T*>(a.y) + row0 * a.H + tiles.column + id * V;
+    T* out = static_cast<T*>(a.y) + row0 * a.H + tiles.column;
     for (int m = 0; m < rows; m += rows_at_once) {
       const int r = m + sub;
       const bool on = r < rows;
       Chunk<T, V> x[C];
-      tiles.row(0, r, id, team, on ? mine : 0, x);
+      tiles.row(0, r, share, on, x);
       float mu = 0.f, s[1];
       uint64_t q = 0;  // a pair of zeros
       if (LAYER) {
@@ -391,14 +468,15 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
         uint64_t d = pair_of(x, i);
         if (LAYER) {
           d = add2(d, minus);
-          // columns past the row's end
-          if constexpr (V == 1) {
+          // elements outside the row
+          if (V == 1 || (V == 2 && i == 0)) {
             float lo, hi;
             f2unpack(d, lo, hi);
-            if (2 * i >= mine) lo = 0.f;
-            if (2 * i + 1 >= mine) hi = 0.f;
+            if (2 * i / V >= share.n || (V == 2 && share.outside == 1)) lo = 0.f;
+            if ((2 * i + 1) / V >= share.n || (V == 2 && share.outside == 2))
+              hi = 0.f;
             d = f2pack(lo, hi);
-          } else if (2 * i / V >= mine) {
+          } else if (2 * i / V >= share.n) {
             d = 0;
           }
         }
@@ -419,11 +497,7 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
           d = LAYER ? fma2(d, w[i], b[i]) : mul2(d, w[i]);
           f2unpack(d, o[2 * i], o[2 * i + 1]);
         }
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (c < mine)
-            store_chunk<T, V>(out + r * a.H + team * c * V, &o[c * V]);
-        }
+        share.store<T, V>(out + r * a.H, o);
         if (id == 0 && tiles.rank == 0) {
           if (LAYER && a.mean) a.mean[row0 + r] = mu;
           if (a.rstd) a.rstd[row0 + r] = rs;
@@ -463,13 +537,13 @@ __global__ void __launch_bounds__(BOUND, BOUND == PAIRED ? 2 : 1)
   const int id = M == LANES ? threadIdx.x & (team - 1) : threadIdx.x;
   const int rows_at_once = M == LANES ? 32 / team : 1;
   const int sub = M == LANES ? (threadIdx.x & 31) / team : 0;
-  // chunks of the thread: the first `mine` of id, id + team, ...
-  const int mine = max(0, (tiles.width / V - id + team - 1) / team);
+  const Share share = Share::of<V>(tiles.width, id, team,
+                                   tiles.odd_start(rows_at_once, sub));
   const float inv = 1.f / a.H;
   int turn = 0;
   uint64_t w[PAIRS], dw[PAIRS], db[PAIRS];
-  load_params<V>(a.weight, a.param_f32, tiles.column, tiles.width, id,
-                 team, 1.f, w);
+  load_params<V>(a.weight, a.param_f32, tiles.column, tiles.width, share, 1.f,
+                 w);
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) dw[i] = db[i] = 0;
   // the statistics of the next tile, a lane to a row, are under way while one
@@ -487,8 +561,7 @@ __global__ void __launch_bounds__(BOUND, BOUND == PAIRED ? 2 : 1)
     const int rows = tiles.wait();
     const float rs_tile = rs_next, mu_tile = mu_next;
     look_ahead(tiles.tile + tiles.step);
-    T* out =
-        static_cast<T*>(a.y) + tiles.first_row() * a.H + tiles.column + id * V;
+    T* out = static_cast<T*>(a.y) + tiles.first_row() * a.H + tiles.column;
     for (int m = 0; m < rows; m += rows_at_once) {
       const int r = m + sub;
       const bool on = r < rows;
@@ -499,8 +572,8 @@ __global__ void __launch_bounds__(BOUND, BOUND == PAIRED ? 2 : 1)
       }
       const uint64_t rs2 = f2pack(rs, rs), minus = f2pack(-mu, -mu);
       Chunk<T, V> x[C], dy[C];
-      tiles.row(0, r, id, team, on ? mine : 0, x);
-      tiles.row(1, r, id, team, on ? mine : 0, dy);
+      tiles.row(0, r, share, on, x);
+      tiles.row(1, r, share, on, dy);
       // d = x - mu, n = rs d: rs is applied to products and sums instead
       auto deviation = [&](int i) {
         const uint64_t d = pair_of(x, i);
@@ -541,11 +614,7 @@ __global__ void __launch_bounds__(BOUND, BOUND == PAIRED ? 2 : 1)
           g = LAYER ? fma2(g, rs2, c12) : mul2(g, rs2);
           f2unpack(fma2(deviation(i), c22, g), o[2 * i], o[2 * i + 1]);
         }
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (c < mine)
-            store_chunk<T, V>(out + r * a.H + team * c * V, &o[c * V]);
-        }
+        share.store<T, V>(out + r * a.H, o);
       }
     }
     if (M == LANES) {
@@ -567,26 +636,28 @@ __global__ void __launch_bounds__(BOUND, BOUND == PAIRED ? 2 : 1)
   if constexpr (M != LANES) {
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int j = (id + team * (i / V)) * V + i % V;
-      if (j >= tiles.width) continue;
+      const int j = share.column<V>(i, tiles.width);
+      if (j < 0) continue;
       p[j] = aw[i];
       if (LAYER) p[a.H + j] = ab[i];
     }
   } else {
-    // the warp's teams by shuffles, then the warps one after the other
+    // the warp's teams that have the same columns by shuffles (of rows of odd
+    // width in pairs every other team), then what is left one after the other
+    const int kinds = V == 2 && (a.H & 1) && rows_at_once > 1 ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      for (int o = team; o < 32; o <<= 1) {
+      for (int o = kinds * team; o < 32; o <<= 1) {
         aw[i] += __shfl_xor_sync(ALL_LANES, aw[i], o);
         if (LAYER) ab[i] += __shfl_xor_sync(ALL_LANES, ab[i], o);
       }
     }
-    for (int turn_of = 0; turn_of < TEAM_WARPS; ++turn_of) {
-      if ((threadIdx.x >> 5) == turn_of && sub == 0) {
+    for (int turn_of = 0; turn_of < TEAM_WARPS * kinds; ++turn_of) {
+      if ((threadIdx.x >> 5) == turn_of / kinds && sub == turn_of % kinds) {
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
-          const int j = (id + team * (i / V)) * V + i % V;
-          if (j >= a.H) continue;
+          const int j = share.column<V>(i, a.H);
+          if (j < 0) continue;
           sums[j] = turn_of ? sums[j] + aw[i] : aw[i];
           if (LAYER)
             sums[32 * EPT + j] = turn_of ? sums[32 * EPT + j] + ab[i] : ab[i];
@@ -732,8 +803,8 @@ struct Geometry {
 
 // Team, tile and ring of rows of H elements, `arrays` of them read, `v` to a
 // chunk. Tiles of lane teams are about 2 KB, so that a copy is worth its
-// issue, where there are rows enough for all warps. A cluster's slices are 4096 columns at first, as blocks of 256 threads
-// share an SM with others, then 8192.
+// issue, where there are rows enough for all warps. A cluster's slices are 4096
+// columns at first, as blocks of 256 threads share an SM with others, then 8192.
 Geometry geometry(NormArgs& a, int v, int size, int arrays, int num_sms) {
   Geometry g{};
   const bool exact = v * size == 16;
@@ -761,7 +832,8 @@ Geometry geometry(NormArgs& a, int v, int size, int arrays, int num_sms) {
     while (a.team < need) a.team *= 2;
     const int at_once = 32 / a.team;
     a.tile_rows = at_once;
-    while (a.tile_rows * a.H * size < 2048 && a.tile_rows < 32 &&
+    const bool alternate = v == 2 && a.H % 2 && at_once == 1;  // Share
+    while (!alternate && a.tile_rows * a.H * size < 2048 && a.tile_rows < 32 &&
            a.L > static_cast<int64_t>(num_sms) * TEAM_WARPS * a.tile_rows * 2)
       a.tile_rows += at_once;
   }
@@ -778,8 +850,8 @@ Geometry geometry(NormArgs& a, int v, int size, int arrays, int num_sms) {
 }
 
 // The most shared memory that any geometry asks for: two stages of two arrays,
-// of a row of BLOCK_H fp32 (or one of BIG_H), or for each warp of a tile that a step of at most
-// 2 KB brought to 2 KB; each with the units at its ends.
+// of a row of BLOCK_H fp32 (or one of BIG_H), or for each warp of a tile that a
+// step of at most 2 KB brought to 2 KB; each with the units at its ends.
 constexpr int MAX_NORM_SMEM = 2 * 2 * TEAM_WARPS * (4096 + 16);
 static_assert(MAX_NORM_SMEM >= 2 * 2 * (BLOCK_H * 4 + 32), "a block's row");
 static_assert(32 * EPT * 4 <= 2048, "the step of a tile");
@@ -830,6 +902,8 @@ cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
     if (n > a.L) n = a.L;
     if (n > MAX_SLABS) n = MAX_SLABS;
   }
+  // rows of a block that has several are of one parity (Share)
+  if (g.mode == BLOCK && a.H % 2 && n < tiles) n = n < 2 ? 2 : n & ~1ll;
   *teams = static_cast<int>(n);
   cfg.gridDim = dim3(static_cast<unsigned>(n * a.cluster));
   return cudaLaunchKernelEx(&cfg, kern, a);
@@ -859,16 +933,21 @@ cudaError_t rows_bwd(NormArgs& a, int num_sms, cudaStream_t s) {
   return launch_rows(kern, a, g, num_sms, s, &a.slabs);
 }
 
-// Elements to a chunk: 16 bytes, else two, as far as every row of every array
-// begins on them; else one.
+// Elements to a chunk: 16 bytes where every row of every array begins on them;
+// else two where a row begins alike in all arrays, on a pair's address if it is
+// of even width; else one.
 template <typename T>
-int chunk_of(int H, const void* p, const void* q, const void* r) {
-  for (int v : {static_cast<int>(16 / sizeof(T)), 2}) {
-    const uintptr_t n = v * sizeof(T);
-    if (H % v == 0 && aligned_to(p, n) && aligned_to(q, n) && aligned_to(r, n))
-      return v;
-  }
-  return 1;
+int chunk_of(int H, const void* x, const void* p, const void* q) {
+  constexpr int V = 16 / sizeof(T);
+  if (H % V == 0 && aligned_to(x, 16) && aligned_to(p, 16) && aligned_to(q, 16))
+    return V;
+  auto element = [](const void* t) {
+    return reinterpret_cast<uintptr_t>(t) / sizeof(T) & 1;
+  };
+  const uintptr_t start = element(x);
+  if (element(p) != start || (q && element(q) != start)) return 1;
+  if (H % 2 == 0) return start == 0 ? 2 : 1;
+  return H <= BLOCK_H ? 2 : 1;
 }
 
 template <typename T, bool LAYER>
