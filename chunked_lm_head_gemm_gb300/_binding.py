@@ -1113,7 +1113,7 @@ def _norm_forward(kind, x, weight, bias, eps, y_out, save_stats):
             mean = torch.empty_like(rstd)
     _call("lce_norm_forward", dev, kind, x.data_ptr(), code,
           None if weight is None else weight.data_ptr(),
-          None if bias is None else bias.data_ptr(), param, L, H, eps,
+          None if bias is None else bias.data_ptr(), param, L, H, float(eps),
           y.data_ptr(), None if mean is None else mean.data_ptr(),
           None if rstd is None else rstd.data_ptr())
     return y, mean, rstd

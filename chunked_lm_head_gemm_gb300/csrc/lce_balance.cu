@@ -14,6 +14,10 @@
 // has several rows of few experts; a lane has the same experts in every row
 // and adds their scores in registers. Exponentials and reciprocals are the
 // approximate instructions (2^-22 of a score).
+//
+// Measured alone, 131072 x 256 fp32 sigmoid: forward 32 us (4.2 TB/s; 173
+// instructions a row and warp come first), joining 608 blocks' sums 11 us (a cold
+// L2), backward 44 us (6.1 TB/s).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -297,6 +301,7 @@ __global__ void __launch_bounds__(WARPS * 32, blocks_per_sm(N))
   float acc[N];
 #pragma unroll
   for (int i = 0; i < P; ++i) f2unpack(pairs[i], acc[2 * i], acc[2 * i + 1]);
+  let_next_begin();  // k_balance_join, which waits for this launch's end
   if (id == 0 && tokens) atomicAdd(&hist[a.E], tokens);
 #pragma unroll
   for (int i = 0; i < N; ++i) {

@@ -14,7 +14,8 @@
 //
 // Bound: the bytes of the gradients, read for the norm, read and written for
 // the clipping, which starts from the end, where the first pass has left them
-// in L2.
+// in L2. Measured alone on 3.0 GB: the squares 420 us (7.2 TB/s), the clipping
+// 908 us (6.6 TB/s).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -290,7 +291,9 @@ __device__ __forceinline__ void clip(const GradTable& t, int first, int step,
 __global__ void __launch_bounds__(GRAD_THREADS)
     k_grad_squares(const __grid_constant__ GradTable t, double* part) {
   __shared__ double warps[32];
-  const double sum = block_total(squares(t, blockIdx.x, gridDim.x), warps);
+  const double mine = squares(t, blockIdx.x, gridDim.x);
+  let_next_begin();  // what reads the parts, which waits for this launch's end
+  const double sum = block_total(mine, warps);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
@@ -473,8 +476,10 @@ cudaError_t each_table(const void* const* grads, void* const* outs,
   return cudaSuccess;
 }
 
-// Chunks up to which one cluster takes them all.
-constexpr int64_t SMALL_CHUNKS = 32;
+// Chunks up to which one cluster takes them all. On the GPU 8 chunks take 5.1 us
+// in one launch and 6.3 in two, 16 take 6.8 and 6.3, 32 take 9.7 and 6.3; a launch
+// less saves the host 2 us.
+constexpr int64_t SMALL_CHUNKS = 16;
 
 // Launches a kernel whose first argument is a table: `early` while the kernel
 // before it still runs (it waits for it itself), or its blocks as one cluster.

@@ -677,8 +677,9 @@ lce_status lce_norm_forward(lce_norm_kind kind, const void* x, lce_dtype dt,
  *   not all of them (RMS norm: dbias NULL).
  *   ws      device, 16-byte aligned, lce_norm_workspace_size() bytes; needed
  *           for dweight and dbias alone (else NULL)
- * The sums over rows are formed in fp32 over a few hundred runs of rows, and
- * the runs added in fp64 in a fixed order. L = 0: zero dweight and dbias.
+ * The sums over rows are formed in fp32 over up to a thousand runs of rows,
+ * and the runs added in a fixed order to twice fp32's precision. L = 0: zero
+ * dweight and dbias.
  */
 size_t lce_norm_workspace_size(int64_t L, int64_t H);
 lce_status lce_norm_backward(lce_norm_kind kind, const void* x, lce_dtype dt,
@@ -709,8 +710,8 @@ lce_status lce_norm_backward(lce_norm_kind kind, const void* x, lce_dtype dt,
  *            needs of the counts
  *   ws       device, 16-byte aligned, lce_balance_workspace_size() bytes
  * 1 <= E <= 1024, 1 <= top_k <= 32, L top_k <= 2^30, coef finite. The sum over
- * tokens is formed in fp32 over runs of tokens and the runs added in fp64 in a
- * fixed order.
+ * tokens is formed in fp32 over runs of tokens, and the runs added in a fixed
+ * order to twice fp32's precision.
  */
 size_t lce_balance_workspace_size(int64_t L, int64_t E);
 lce_status lce_balance_forward(const void* logits, lce_dtype dt,
