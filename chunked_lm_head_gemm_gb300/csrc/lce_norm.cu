@@ -776,6 +776,7 @@ __global__ void __launch_bounds__(128) k_norm_dparams_wide(const NormArgs a) {
 // slab of a column, then the runs in order. (By fp64 additions this took 23 us
 // for 456 slabs of 2 x 2560 columns.)
 constexpr int JOIN_RUNS = 32;
+constexpr int JOIN_AHEAD = 16;  // loads of a thread under way
 __global__ void __launch_bounds__(32 * JOIN_RUNS)
     k_norm_join(const float* __restrict__ part, int slabs, int H, void* dweight,
                 void* dbias, int grad_f32) {
@@ -787,15 +788,15 @@ __global__ void __launch_bounds__(32 * JOIN_RUNS)
   if (!out) return;
   LongSum t;
   const float* p = part + static_cast<int64_t>(blockIdx.y) * H + j;
-  for (int s0 = run; s0 < slabs; s0 += 8 * JOIN_RUNS) {
-    float v[8];
+  for (int s0 = run; s0 < slabs; s0 += JOIN_AHEAD * JOIN_RUNS) {
+    float v[JOIN_AHEAD];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < JOIN_AHEAD; ++u) {
       const int s = s0 + u * JOIN_RUNS;
       v[u] = j < H && s < slabs ? p[static_cast<int64_t>(s) * 2 * H] : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) t.add(v[u]);
+    for (int u = 0; u < JOIN_AHEAD; ++u) t.add(v[u]);
   }
   runs[run][col] = t;
   __syncthreads();
