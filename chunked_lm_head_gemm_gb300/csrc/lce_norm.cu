@@ -65,8 +65,7 @@ constexpr int BLOCK_H = EPT * MAX_THREADS;  // the widest row of a block
 constexpr int MAX_CLUSTER = 8;
 constexpr int CLUSTER_H = BLOCK_H * MAX_CLUSTER;
 // A row's team. BIG: a block of up to 1024 threads, where the registers allow it
-// (the forward pass of rows on 16 bytes): a block's barrier is a third of a
-// cluster's. 16384 rows of 16384 bf16, layer norm: 217 us against
+// (the forward pass): a block's barrier is a third of a cluster's. 16384 rows of 16384 bf16, layer norm: 217 us against
 // 585.
 enum Mode { LANES, BLOCK, CLUSTER, BIG };
 constexpr int BIG_H = 2 * BLOCK_H;
@@ -231,6 +230,14 @@ struct Tiles {
     rank = M == CLUSTER ? blockIdx.x % a.cluster : 0;
     column = M == CLUSTER ? rank * a.slice : 0;
     width = M == CLUSTER ? min(a.slice, a.H - column) : a.H;
+    if (M == CLUSTER && V == 2 && (a.H & 1)) {
+      // slices of whole pairs, in the order in which Share counts them
+      const int odd = (reinterpret_cast<uintptr_t>(a.x) / sizeof(T) + block) & 1;
+      const int pairs = (a.H + 1) / 2, first = rank * (a.slice / 2);
+      const int last = min(first + a.slice / 2, pairs);
+      column = max(0, odd ? 2 * first - 1 : 2 * (pairs - last));
+      width = min(a.H, odd ? 2 * last - 1 : 2 * (pairs - first)) - column;
+    }
     tiles = M == LANES ? (a.L + a.tile_rows - 1) / a.tile_rows : a.L;
     last_rows = static_cast<int>(a.L - (tiles - 1) * a.tile_rows);
     step = static_cast<int64_t>(M == CLUSTER ? gridDim.x / a.cluster
@@ -831,11 +838,12 @@ Geometry geometry(NormArgs& a, int v, int size, int arrays, int num_sms) {
   const bool exact = v * size == 16;
   a.cluster = 1;
   a.slice = a.H;
-  const bool big = arrays == 1 && exact && a.H > BLOCK_H && a.H <= BIG_H;
+  const bool big = arrays == 1 && v > 1 && a.H > BLOCK_H && a.H <= BIG_H;
   if (a.H > BLOCK_H && !big) {
+    const int64_t columns = v == 2 ? round_up(a.H, 2) : a.H;  // whole pairs
     a.cluster = a.H <= 4 * 4096 ? 4 : MAX_CLUSTER;
-    a.slice = static_cast<int>(round_up(ceil_div(a.H, a.cluster), 16));
-    a.cluster = static_cast<int>(ceil_div(a.H, a.slice));
+    a.slice = static_cast<int>(round_up(ceil_div(columns, a.cluster), 16));
+    a.cluster = static_cast<int>(ceil_div(columns, a.slice));
   }
   const int per = EPT / v, chunks = static_cast<int>(ceil_div(a.slice, v));
   const int need = static_cast<int>(ceil_div(chunks, per));
@@ -923,8 +931,8 @@ cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
     if (n > a.L) n = a.L;
     if (n > MAX_SLABS) n = MAX_SLABS;
   }
-  // rows of a block that has several are of one parity (Share)
-  if (g.mode == BLOCK && a.H % 2 && n < tiles) n = n < 2 ? 2 : n & ~1ll;
+  // rows of a team that has several are of one parity (Share)
+  if (g.mode != LANES && a.H % 2 && n < tiles) n = n < 2 ? 2 : n & ~1ll;
   *teams = static_cast<int>(n);
   cfg.gridDim = dim3(static_cast<unsigned>(n * a.cluster));
   return cudaLaunchKernelEx(&cfg, kern, a);
@@ -936,7 +944,7 @@ cudaError_t rows_fwd(NormArgs& a, int num_sms, cudaStream_t s) {
   auto kern = g.mode == LANES   ? k_norm_fwd<T, V, LANES, LAYER>
               : g.mode == BLOCK ? k_norm_fwd<T, V, BLOCK, LAYER>
                                 : k_norm_fwd<T, V, CLUSTER, LAYER>;
-  if constexpr (V * sizeof(T) == 16) {
+  if constexpr (V > 1) {
     if (g.mode == BIG) kern = k_norm_fwd<T, V, BIG, LAYER>;
   }
   int teams;
@@ -967,8 +975,7 @@ int chunk_of(int H, const void* x, const void* p, const void* q) {
   };
   const uintptr_t start = element(x);
   if (element(p) != start || (q && element(q) != start)) return 1;
-  if (H % 2 == 0) return start == 0 ? 2 : 1;
-  return H <= BLOCK_H ? 2 : 1;
+  return H % 2 == 0 && start != 0 ? 1 : 2;
 }
 
 template <typename T, bool LAYER>

@@ -87,7 +87,8 @@ def test_widths(H, dtype, pdtype, layer):
 
 
 @KINDS
-@pytest.mark.parametrize("H", [32768, 32776, 65537, 200000])
+@pytest.mark.parametrize("H", [9001, 12345, 16383, 32768, 32769, 32776, 40001,
+                               65535, 65536, 65537, 200000])
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf", "f32"])
 def test_wide_rows(H, dtype, layer):
     require_gpu()
@@ -107,7 +108,7 @@ def test_row_counts(L, H, dtype, layer):
 @pytest.mark.parametrize("L,H,dtype", [(200003, 128, BF), (100001, 64, F32),
                                        (40000, 1024, BF), (20000, 4096, BF),
                                        (70001, 33, BF), (3000, 16384, BF),
-                                       (2000, 9001, F32), (700, 40000, BF),
+                                       (2000, 9001, F32), (2001, 9003, BF), (700, 40000, BF),
                                        (600, 65536, F32)])
 def test_many_rows(L, H, dtype, layer):
     require_gpu()
@@ -166,7 +167,8 @@ def test_rows_that_are_not_finite_stay_apart(H, dtype, bad, layer):
 
 @KINDS
 @pytest.mark.parametrize("dtype,H", [(BF, 136), (BF, 2048), (F32, 132),
-                                     (F32, 4096), (BF, 999)])
+                                     (F32, 4096), (BF, 999), (BF, 9001),
+                                     (F32, 20001), (BF, 9002)])
 @pytest.mark.parametrize("shift", [1, 3, 4])
 def test_addresses(dtype, H, shift, layer):
     """Tensors that start on their element's alignment alone give the bits of
@@ -196,7 +198,8 @@ def test_addresses(dtype, H, shift, layer):
 
 @KINDS
 @pytest.mark.parametrize("L,H,dtype", [(50, 128, BF), (7, 1001, BF),
-                                       (600, 2048, BF), (9, 40000, F32)])
+                                       (600, 2048, BF), (9, 40000, F32),
+                                       (400, 9001, BF), (300, 9002, BF)])
 def test_in_place(L, H, dtype, layer):
     """y over x; dx over dy, and over x."""
     require_gpu()
