@@ -428,6 +428,19 @@ __device__ __forceinline__ void load_params(const void* p, bool f32, int column,
     const int j = share.column<V>(i, width);
     return j < 0 ? 0.f : p ? load_as_float(p, f32, column + j) : absent;
   };
+  // four at a time where a chunk has as many and they lie so
+  if (V >= 4 && p &&
+      (reinterpret_cast<uintptr_t>(p) & (f32 ? 15 : 7)) == 0) {
+#pragma unroll
+    for (int i = 0; i < PAIRS; i += 2) {
+      const int j = share.column<V>(2 * i, width);
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (j >= 0) load4(p, f32, column + j, v);
+      w[i] = f2pack(v[0], v[1]);
+      w[i + 1] = f2pack(v[2], v[3]);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) w[i] = f2pack(at(2 * i), at(2 * i + 1));
 }

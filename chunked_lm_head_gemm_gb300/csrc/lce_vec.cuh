@@ -28,6 +28,22 @@ __device__ __forceinline__ float load_as_float(const void* p, bool f32,
   return f32 ? static_cast<const float*>(p)[i]
              : to_float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
+// Elements i to i + 3, which begin on four elements.
+__device__ __forceinline__ void load4(const void* p, bool f32, int64_t i,
+                                      float (&v)[4]) {
+  if (f32) {
+    const float4 q =
+        *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else {
+    const uint2 q = *reinterpret_cast<const uint2*>(
+        static_cast<const __nv_bfloat16*>(p) + i);
+    v[0] = __uint_as_float(q.x << 16);
+    v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16);
+    v[3] = __uint_as_float(q.y & 0xffff0000u);
+  }
+}
 __device__ __forceinline__ void store_from_float(void* p, bool f32, int64_t i,
                                                  float v) {
   if (f32)
