@@ -16,8 +16,8 @@
 // approximate instructions (2^-22 of a score).
 //
 // Measured alone, 131072 x 256 fp32 sigmoid: forward 32 us (4.2 TB/s; 173
-// instructions a row and warp come first), joining 608 blocks' sums 11 us (a cold
-// L2), backward 44 us (6.1 TB/s).
+// instructions a row and warp come first), joining 608 blocks' sums 11 us (a
+// cold L2), backward 44 us (6.1 TB/s).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -216,8 +216,8 @@ struct Rows {
 };
 
 // Blocks of an SM that the registers leave room for. (131072 x 256 fp32, us of
-// a forward and a backward pass: 81 with 4 blocks of one row under way, 103 with
-// 5, 139 with 6, where registers spill; 87 with 3 blocks of two rows.)
+// a forward and a backward pass: 81 with 4 blocks of one row under way, 103
+// with 5, 139 with 6, where registers spill; 87 with 3 blocks of two rows.)
 constexpr int blocks_per_sm(int n) { return n <= 8 ? 4 : n <= 16 ? 2 : 1; }
 static_assert(SMS * 4 <= JOIN_THREADS, "a thread to a block's tokens");
 
@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(WARPS * 32, blocks_per_sm(N))
     return j < a.E ? a.slopes[j] * d : 0.f;
   };
 #pragma unroll
-  for (int i = 0; i < P; ++i) f[i] = f2pack(slope_of(2 * i), slope_of(2 * i + 1));
+  for (int i = 0; i < P; ++i)
+    f[i] = f2pack(slope_of(2 * i), slope_of(2 * i + 1));
   for (int t0 = first; t0 < a.L; t0 += step) {
     uint64_t z[P], slope[P], dots = 0;
     rows.unpack(z);
@@ -469,11 +470,11 @@ int team_of(int64_t E) {
   return team;
 }
 
-// Blocks of a forward pass. One alone, without a join, up to 8 rows to a team: 128
-// x 128 takes 6.8 us on the GPU so and 7.3 in several blocks, 256 x 128 (16 rows)
-// 9.8 and 7.5. Else two rows to a team as long as the SMs have no more than a
-// block, then four, since every block's sums have to be joined: 4099 x 60 takes
-// 8.4 us with two and 9.1 with four, 16384 x 128 11.7 and 10.2.
+// Blocks of a forward pass. One alone, without a join, up to 8 rows to a team:
+// 128 x 128 takes 6.8 us on the GPU so and 7.3 in several blocks, 256 x 128 (16
+// rows) 9.8 and 7.5. Else two rows to a team as long as the SMs have no more
+// than a block, then four, since every block's sums have to be joined: 4099 x
+// 60 takes 8.4 us with two and 9.1 with four, 16384 x 128 11.7 and 10.2.
 int blocks_of(int64_t L, int64_t E) {
   const int64_t rows = WARPS * 32 / team_of(E);  // of a block at a time
   if (L <= 8 * rows) return 1;

@@ -476,9 +476,9 @@ cudaError_t each_table(const void* const* grads, void* const* outs,
   return cudaSuccess;
 }
 
-// Chunks up to which one cluster takes them all. On the GPU 8 chunks take 5.1 us
-// in one launch and 6.3 in two, 16 take 6.8 and 6.3, 32 take 9.7 and 6.3; a launch
-// less saves the host 2 us.
+// Chunks up to which one cluster takes them all. On the GPU 8 chunks take 5.1
+// us in one launch and 6.3 in two, 16 take 6.8 and 6.3, 32 take 9.7 and 6.3; a
+// launch less saves the host 2 us.
 constexpr int64_t SMALL_CHUNKS = 16;
 
 // Launches a kernel whose first argument is a table: `early` while the kernel

@@ -8,20 +8,19 @@
 // Bound: the bytes of x and y, or of x, dy and dx, each moved once. Up to 65536
 // columns a row stays in the registers of its team, 16 elements to a thread: a
 // power of two of lanes for narrow rows (several rows to a warp), a block up to
-// 8192 columns, beyond that a larger block or a cluster, whose sums pass through
-// distributed shared memory. A thread has the same columns in every row, so it
-// keeps its weights and its sums for dw and db in registers, and the backward
-// needs no second pass over x and dy. Rows come through a ring of shared memory by
-// bulk copies, issued several rows ahead, so that enough bytes are under way
-// without registers to hold them. Wider rows are read again where a pass over
-// them needs it.
+// 8192 columns, beyond that a larger block or a cluster, whose sums pass
+// through distributed shared memory. A thread has the same columns in every
+// row, so it keeps its weights and its sums for dw and db in registers, and the
+// backward needs no second pass over x and dy. Rows come through a ring of
+// shared memory by bulk copies, issued several rows ahead, so that enough bytes
+// are under way without registers to hold them. Wider rows are read again where
+// a pass over them needs it.
 //
-// Measured alone, 65536 x 4096 bf16 RMS norm: forward 179 us (6.0 TB/s), backward
-// 233 us (6.9 TB/s) and 10 us for joining its blocks' sums; 1048576 x 128 bf16 88
-// and 128 us (6.1, 6.3 TB/s); 16384 x 2560 fp32 layer norm 52 and 71 us (6.4, 7.1
-// TB/s). Rows that are not on 16 bytes are bound by instructions: 65536 x 1001
-// bf16 RMS norm 53 and 121 us (4.9, 3.3 TB/s). The backward of a layer norm of
-// bf16 is too (5 more instructions a pair): 32768 x 4096 takes 125 us against 100.
+// Measured alone, 65536 x 4096 bf16 RMS norm: forward 179 us (6.0 TB/s),
+// backward 233 us (6.9 TB/s) and 10 us for joining its blocks' sums; 1048576 x
+// 128 bf16 88 and 128 us (6.1, 6.3 TB/s); 16384 x 2560 fp32 layer norm 52 and
+// 71 us (6.4, 7.1 TB/s). Rows that are not on 16 bytes are bound by
+// instructions: 65536 x 1001 bf16 RMS norm 53 and 121 us (4.9, 3.3 TB/s).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -64,10 +63,10 @@ constexpr int MAX_THREADS = 512;  // of a block that is a team
 constexpr int BLOCK_H = EPT * MAX_THREADS;  // the widest row of a block
 constexpr int MAX_CLUSTER = 8;
 constexpr int CLUSTER_H = BLOCK_H * MAX_CLUSTER;
-// A row's team. BIG: a block of up to 1024 threads, where the registers allow it
-// (the forward pass, and the backward of an RMS norm of bf16): a block's barrier
-// is a third of a cluster's. 16384 rows of 16384 bf16: layer norm forward 222 us
-// against 585, RMS norm backward 340 against 399.
+// A row's team. BIG: a block of up to 1024 threads, where the registers allow
+// it (the forward pass, and the backward of an RMS norm of bf16): a block's
+// barrier is a third of a cluster's. 16384 rows of 16384 bf16: layer norm
+// forward 222 us against 585, RMS norm backward 340 against 399.
 enum Mode { LANES, BLOCK, CLUSTER, BIG };
 constexpr int BIG_H = 2 * BLOCK_H;
 constexpr int threads_of(Mode m) { return m == BIG ? 1024 : MAX_THREADS; }
@@ -142,10 +141,10 @@ __device__ __forceinline__ void team_sum(float (&v)[N], const NormArgs& a,
 // `first`, `stride` columns apart.
 //
 // Pairs (V = 2) of rows of odd width begin on a pair's address in every other
-// row only. A team has rows of one parity, for which the pairs are shifted: where
-// a row begins on an odd element, its first pair holds one element, else its last
-// one does, and then the pairs are counted from the row's end. So the pair with
-// one element is always the first chunk of thread 0.
+// row only. A team has rows of one parity, for which the pairs are shifted:
+// where a row begins on an odd element, its first pair holds one element, else
+// its last one does, and then the pairs are counted from the row's end. So the
+// pair with one element is always the first chunk of thread 0.
 struct Share {
   int first, stride, n;
   int outside;  // of the first chunk: 0 none, 1 the first element, 2 the second
@@ -198,12 +197,12 @@ struct Share {
   }
 };
 
-// A group (a warp of lane teams, or the block) and its ring of tiles. A tile
-// is tile_rows rows, one after the other in memory; the group takes tiles
-// first, first + step, ... Of rows that are not on 16 bytes (chunks of less) the
-// 16-byte units that cover the tile are copied; a tile whose units reach past the
-// array's ends (the first and last, of arrays that do not begin or end on 16
-// bytes) is read where it lies.
+// A group (a warp of lane teams, or the block) and its ring of tiles. A tile is
+// tile_rows rows, one after the other in memory; the group takes tiles first,
+// first + step, ... Of rows that are not on 16 bytes (chunks of less) the
+// 16-byte units that cover the tile are copied; a tile whose units reach past
+// the array's ends (the first and last, of arrays that do not begin or end on
+// 16 bytes) is read where it lies.
 template <typename T, int V, Mode M, int ARRAYS>
 struct Tiles {
   static constexpr bool EXACT = V * sizeof(T) == 16;
@@ -233,7 +232,8 @@ struct Tiles {
     width = M == CLUSTER ? min(a.slice, a.H - column) : a.H;
     if (M == CLUSTER && V == 2 && (a.H & 1)) {
       // slices of whole pairs, in the order in which Share counts them
-      const int odd = (reinterpret_cast<uintptr_t>(a.x) / sizeof(T) + block) & 1;
+      const int odd =
+          (reinterpret_cast<uintptr_t>(a.x) / sizeof(T) + block) & 1;
       const int pairs = (a.H + 1) / 2, first = rank * (a.slice / 2);
       const int last = min(first + a.slice / 2, pairs);
       column = max(0, odd ? 2 * first - 1 : 2 * (pairs - last));
@@ -499,7 +499,8 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
           if (V == 1 || (V == 2 && i == 0)) {
             float lo, hi;
             f2unpack(d, lo, hi);
-            if (2 * i / V >= share.n || (V == 2 && share.outside == 1)) lo = 0.f;
+            if (2 * i / V >= share.n || (V == 2 && share.outside == 1))
+              lo = 0.f;
             if ((2 * i + 1) / V >= share.n || (V == 2 && share.outside == 2))
               hi = 0.f;
             d = f2pack(lo, hi);
@@ -844,9 +845,10 @@ struct Geometry {
 };
 
 // Team, tile and ring of rows of H elements, `arrays` of them read, `v` to a
-// chunk. Tiles of lane teams are about 2 KB, so that a copy is worth its
-// issue, where there are rows enough for all warps. A cluster's slices are 4096
-// columns at first, as blocks of 256 threads share an SM with others, then 8192.
+// chunk. Tiles of lane teams are about 2 KB, so that a copy is worth its issue,
+// where there are rows enough for all warps. A cluster's slices are 4096
+// columns at first, as blocks of 256 threads share an SM with others, then
+// 8192.
 Geometry geometry(NormArgs& a, int v, int size, int arrays, bool may_be_big,
                   int num_sms) {
   Geometry g{};
@@ -1113,7 +1115,8 @@ lce_status lce_norm_backward(lce_norm_kind kind, const void* x, lce_dtype dt,
                              void* stream) {
   LCE_TRY(check(kind, dt, x, weight, param_dt, L, H));
   if (grad_dt != LCE_BF16 && grad_dt != LCE_F32) return LCE_ERR_UNSUPPORTED;
-  const uintptr_t elt = dt == LCE_F32 ? 4 : 2, gelt = grad_dt == LCE_F32 ? 4 : 2;
+  const uintptr_t elt = dt == LCE_F32 ? 4 : 2;
+  const uintptr_t gelt = grad_dt == LCE_F32 ? 4 : 2;
   const bool layer = kind == LCE_LAYER_NORM, params = dweight || dbias;
   if ((!dx && !params) || (!layer && (mean || dbias)) || !aligned_to(dx, elt) ||
       !aligned_to(dy, elt) || !aligned_to(dweight, gelt) ||
