@@ -15,6 +15,7 @@ import os
 import threading
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import build as _build
@@ -1666,8 +1667,14 @@ class RMSNorm(torch.autograd.Function):
 
 
 def _wants_grad(*tensors):
-    return torch.is_grad_enabled() and any(
-        t is not None and t.requires_grad for t in tensors)
+    """Whether a call has to go through its autograd Function: for a gradient,
+    or for a tangent, which the Function refuses (it has no forward mode)."""
+    backward = torch.is_grad_enabled()
+    for t in tensors:
+        if t is not None and (backward and t.requires_grad or
+                              forward_ad.unpack_dual(t).tangent is not None):
+            return True
+    return False
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
