@@ -13,7 +13,9 @@
 // of lanes holds a row, 8 elements to a lane up to 256 experts, so that a warp
 // has several rows of few experts; a lane has the same experts in every row
 // and adds their scores in registers. Exponentials and reciprocals are the
-// approximate instructions (2^-22 of a score).
+// approximate instructions, the rounding of the exponential's argument put back
+// (2^-21 of a score, however far from zero or below the row's largest; 131072 x
+// 256: 1 to 3 us of a pass).
 //
 // Measured alone, 131072 x 256 fp32 sigmoid: forward 32 us (4.2 TB/s; 173
 // instructions a row and warp come first), joining 608 blocks' sums 11 us (a
@@ -80,6 +82,38 @@ __device__ __forceinline__ uint64_t ex2_of_pair(uint64_t v) {
   return f2pack(ex2(lo), ex2(hi));
 }
 
+// v (or -v) within [LEAST_EXP, MOST_EXP]; NaN stays. There e^v is 0 and 1 / (1
+// + e^v) is 0, what lies below 2^-126 being 0 to both instructions; beyond it
+// the correction below would meet infinities.
+constexpr float LEAST_EXP = -104.f, MOST_EXP = 88.5f;
+template <bool NEGATE>
+__device__ __forceinline__ float clamped(float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;"
+      : "=f"(r)
+      : "f"(NEGATE ? -v : v), "f"(LEAST_EXP));
+  if (NEGATE)
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(MOST_EXP));
+  return r;
+}
+
+// e^v of a pair of v <= 0, or e^-v of any pair, to 2^-22 of itself. The
+// argument h of 2^h is rounded, which alone is an error that grows with |v| (3e-6
+// at 60); v - h ln 2, exact but for its own last place, says by how much, and
+// e^(v - h ln 2) is 1 + (v - h ln 2) to 2^-35.
+constexpr float LN2_HIGH = 0.693147180559945309, LN2_LOW =
+    0.693147180559945309 - LN2_HIGH;
+template <bool NEGATE>
+__device__ __forceinline__ uint64_t exp_of_pair(uint64_t v) {
+  float lo, hi;
+  f2unpack(v, lo, hi);
+  v = f2pack(clamped<NEGATE>(lo), clamped<NEGATE>(hi));
+  const uint64_t h = mul2(v, both(LOG2E)), r = ex2_of_pair(h);
+  const uint64_t off =
+      fma2(h, both(-LN2_LOW), fma2(h, both(-LN2_HIGH), v));
+  return fma2(r, off, r);
+}
+
 // The largest of a row's logits, 0 for a row without one above -inf.
 template <int P>
 __device__ __forceinline__ float row_max(const uint64_t (&z)[P], int team) {
@@ -100,54 +134,44 @@ constexpr float LEAST_SUM = 1e-30f;
 // A row's scores in place of its logits, not yet divided by their sum, which
 // is returned; with SLOPE 1 - s of sigmoid scores (for softmax not written).
 // Two elements to an instruction where there is one. s = 1 / (1 + q), 1 - s = q
-// s with q = e^-z; where q is infinite, s is 0 and 1 - s, of no account, too.
-// Should all sigmoid scores be tiny, they are taken relative to the largest:
-// s e^-m = e^(z - m) / (1 + e^z).
+// s with q = e^-z; where s is 0, 1 - s is too, which is of no account.
+// Should all sigmoid scores be tiny, where s = e^z, they are taken relative to
+// the largest: e^(z - m), and 1 - s is 1.
 template <int P, bool SIGMOID, bool SLOPE>
 __device__ __forceinline__ float scores(uint64_t (&z)[P], uint64_t (&slope)[P],
                                         int team) {
   uint64_t t = 0;
   if (!SIGMOID) {
-    const uint64_t minus = both(-row_max(z, team)), log2e = both(LOG2E);
+    const uint64_t minus = both(-row_max(z, team));
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      z[i] = ex2_of_pair(mul2(add2(z[i], minus), log2e));
+      z[i] = exp_of_pair<false>(add2(z[i], minus));
       t = add2(t, z[i]);
     }
     return team_sum(sum_of_pair(t), team);
   }
-  const uint64_t minus_log2e = both(-LOG2E), one = both(1.f);
+  const uint64_t one = both(1.f);
   uint64_t s[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const uint64_t q = ex2_of_pair(mul2(z[i], minus_log2e));
+    const uint64_t q = exp_of_pair<true>(z[i]);
     float lo, hi;
     f2unpack(add2(q, one), lo, hi);
     s[i] = f2pack(reciprocal(lo), reciprocal(hi));
-    if (SLOPE) {
-      f2unpack(q, lo, hi);
-      slope[i] = mul2(f2pack(fminf(lo, 3e38f), fminf(hi, 3e38f)), s[i]);
-    }
+    if (SLOPE) slope[i] = mul2(q, s[i]);
     t = add2(t, s[i]);
   }
   float sum = team_sum(sum_of_pair(t), team);
   // the vote is the warp's: its teams take the shuffles together
   if (__any_sync(ALL_LANES, sum < LEAST_SUM)) {
-    const float m = row_max(z, team);
+    const uint64_t minus = both(-row_max(z, team));
     uint64_t far = 0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      float v[2], e[2], d[2];
-      f2unpack(z[i], v[0], v[1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        d[h] = reciprocal(1.f + ex2(v[h] * LOG2E));
-        e[h] = ex2((v[h] - m) * LOG2E) * d[h];
-      }
-      z[i] = f2pack(e[0], e[1]);
+      z[i] = exp_of_pair<false>(add2(z[i], minus));
       if (sum < LEAST_SUM) {
         s[i] = z[i];
-        if (SLOPE) slope[i] = f2pack(d[0], d[1]);
+        if (SLOPE) slope[i] = one;
       }
       far = add2(far, z[i]);
     }
