@@ -392,14 +392,21 @@ lce_status check(const void* const* grads, const lce_dtype* dts,
 }
 
 // What is written must not be read or written through another tensor: the
-// outputs are disjoint, a gradient is its own output or apart from all, and the
-// norm is apart from all.
+// outputs are disjoint, a gradient is its own output or apart from all, the
+// norm is apart from the outputs and, where it is written, from the gradients.
 lce_status check_disjoint(const void* const* grads, void* const* outs,
                           const lce_dtype* dts, const int64_t* sizes, int64_t n,
-                          const float* norm) {
+                          const float* norm, bool norm_written) {
   struct Range {
     uintptr_t a, b;
   };
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
+  for (int64_t i = 0; norm_written && i < n; ++i) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(grads[i]);
+    if (sizes[i] > 0 && a < at + sizeof(float) &&
+        at < a + bytes_of(dts[i], sizes[i]))
+      return LCE_ERR_INVALID_ARG;
+  }
   Range* r = new (std::nothrow) Range[n];
   if (!r) return cuda_fail(cudaErrorMemoryAllocation, "clip_grads (host)");
   int64_t m = 0;
@@ -427,7 +434,8 @@ lce_status check_disjoint(const void* const* grads, void* const* outs,
 
 lce_status check_outputs(const void* const* grads, void* const* outs,
                          const lce_dtype* dts, const int64_t* sizes, int64_t n,
-                         const float* norm, float max_norm) {
+                         const float* norm, bool norm_written,
+                         float max_norm) {
   if (n > 0 && !outs) return LCE_ERR_INVALID_ARG;
   if (!norm || !aligned_to(norm, 4) || !(max_norm >= 0.f))
     return LCE_ERR_INVALID_ARG;
@@ -435,7 +443,7 @@ lce_status check_outputs(const void* const* grads, void* const* outs,
     if (sizes[i] > 0 &&
         (!outs[i] || !aligned_to(outs[i], dts[i] == LCE_F32 ? 4 : 2)))
       return LCE_ERR_INVALID_ARG;
-  return check_disjoint(grads, outs, dts, sizes, n, norm);
+  return check_disjoint(grads, outs, dts, sizes, n, norm, norm_written);
 }
 
 // Chunks of a tensor, one at least.
@@ -564,7 +572,7 @@ lce_status lce_clip_grads(const void* const* grads, void* const* outs,
                           const lce_dtype* dts, const int64_t* sizes, int64_t n,
                           const float* norm, float max_norm, void* stream) {
   LCE_TRY(check(grads, dts, sizes, n));
-  LCE_TRY(check_outputs(grads, outs, dts, sizes, n, norm, max_norm));
+  LCE_TRY(check_outputs(grads, outs, dts, sizes, n, norm, false, max_norm));
   DeviceInfo* dev = nullptr;
   LCE_TRY(device_info(&dev));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -582,7 +590,7 @@ lce_status lce_clip_grad_norm(const void* const* grads, void* const* outs,
                               int64_t n, float max_norm, float* norm, void* ws,
                               size_t ws_bytes, void* stream) {
   LCE_TRY(check(grads, dts, sizes, n));
-  LCE_TRY(check_outputs(grads, outs, dts, sizes, n, norm, max_norm));
+  LCE_TRY(check_outputs(grads, outs, dts, sizes, n, norm, true, max_norm));
   if (!ws || !aligned_to(ws, 16)) return LCE_ERR_INVALID_ARG;
   if (ws_bytes < lce_grad_norm_workspace_size(n)) return LCE_ERR_WORKSPACE;
   DeviceInfo* dev = nullptr;

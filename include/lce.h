@@ -769,9 +769,10 @@ lce_status lce_clip_grads(const void* const* grads, void* const* outs,
                           const float* norm, float max_norm, void* stream);
 
 /*
- * lce_grad_norm and lce_clip_grads in one call (norm: device [1] float32 out):
- * fewer launches, one alone for few small gradients. The squares' fp64 sum may
- * be formed in another order than lce_grad_norm's.
+ * lce_grad_norm and lce_clip_grads in one call (norm: device [1] float32 out,
+ * apart from the gradients too): fewer launches, one alone for few small
+ * gradients. The squares' fp64 sum may be formed in another order than
+ * lce_grad_norm's.
  */
 lce_status lce_clip_grad_norm(const void* const* grads, void* const* outs,
                               const lce_dtype* dts, const int64_t* sizes,

@@ -1,0 +1,42 @@
+"""More of what the gradient clipping refuses and takes, without a GPU: the C ABI
+before it touches a device, the Python calls on host tensors that say they are
+on one."""
+import ctypes
+
+import pytest
+
+from chunked_lm_head_gemm_gb300 import _binding as B
+from tests.test_step_binding import NULL, P, c  # noqa: F401
+
+A, BB, CC = 0x10000, 0x20000, 0x30000
+
+
+def clip_grad_norm(c, rows, norm):  # noqa: F811
+    """lce_clip_grad_norm of (gradient, output, type, elements), with no
+    workspace, which is looked at behind the pointers that overlap."""
+    n = len(rows)
+    return c.lce_clip_grad_norm(
+        (ctypes.c_void_p * n)(*[r[0] for r in rows]),
+        (ctypes.c_void_p * n)(*[r[1] for r in rows]),
+        (ctypes.c_int * n)(*[r[2] for r in rows]),
+        (ctypes.c_int64 * n)(*[r[3] for r in rows]), n, 1.0,
+        ctypes.c_void_p(norm), P, 8, NULL)
+
+
+@pytest.mark.parametrize("norm", [A, A + 40, A + 396, BB, BB + 196])
+def test_the_norm_may_not_be_written_into_a_gradient(c, norm):  # noqa: F811
+    """Gradients with outputs of their own: blocks still read them while the
+    norm is written."""
+    rows = [(A, CC, 1, 100), (BB, CC + 400, 0, 100)]
+    assert clip_grad_norm(c, rows, norm) == B.LCE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("norm", [A - 4, A + 400, BB - 4, BB + 200])
+def test_the_norm_may_stand_beside_a_gradient(c, norm):  # noqa: F811
+    rows = [(A, CC, 1, 100), (BB, CC + 400, 0, 100)]
+    assert clip_grad_norm(c, rows, norm) == B.LCE_ERR_WORKSPACE
+
+
+def test_an_empty_gradient_holds_no_norm(c):  # noqa: F811
+    rows = [(A, CC, 1, 100), (BB, BB, 1, 0)]
+    assert clip_grad_norm(c, rows, BB) == B.LCE_ERR_WORKSPACE
