@@ -168,8 +168,10 @@ __device__ __forceinline__ double squares(const GradTable& t, int first,
   return sum;
 }
 
-// The factor of a norm: NaN for a norm that is NaN.
+// The factor of a norm: NaN for a norm that is NaN, whatever the limit; 1 for
+// any other under an infinite limit.
 __device__ __forceinline__ float factor(float norm, float max_norm) {
+  if (isnan(norm)) return norm;
   const double r =
       static_cast<double>(max_norm) / (static_cast<double>(norm) + 1e-6);
   return isinf(max_norm) || r >= 1.0 ? 1.f : static_cast<float>(r);

@@ -751,14 +751,16 @@ lce_status lce_expert_counts(const int32_t* experts, const uint8_t* mask,
  *   norm         device [1] float32, out of lce_grad_norm (or any other, such
  *                as the root of squares summed over processes), into
  *                lce_clip_grads
- *   max_norm     not negative; with infinity nothing is clipped
+ *   max_norm     not negative; with infinity nothing is clipped (but for a
+ *                norm that is NaN)
  *   ws           device, 16-byte aligned, lce_grad_norm_workspace_size(n)
  * The host arrays are read before the call returns. Outputs may not overlap
  * each other, norm, or a gradient other than their own (LCE_ERR_INVALID_ARG):
  * the same gradient given twice is refused. Squares are summed so that
  * neither tiny nor huge gradients are lost (fp32 groups, fp64 sums), in a
- * fixed order. A norm that is NaN makes every output NaN, an infinite one 0,
- * or NaN where the gradient is not finite. In place, factor 1 writes nothing.
+ * fixed order. A norm that is NaN makes every output NaN, whatever max_norm; an
+ * infinite one, under a finite max_norm, 0, or NaN where the gradient is not
+ * finite. In place, factor 1 writes nothing.
  */
 size_t lce_grad_norm_workspace_size(int64_t n);
 lce_status lce_grad_norm(const void* const* grads, const lce_dtype* dts,
