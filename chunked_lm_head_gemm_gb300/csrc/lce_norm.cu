@@ -50,6 +50,7 @@ struct NormArgs {
   uint32_t array_bytes;  // of a tile's place there
   float* part;    // [slabs][2][H] sums of dy n and dy
   int slabs;
+  int run;  // rows that a thread may add in registers, 64 at least
   int want_dx;
   int size;  // bytes of an element
   uint64_t timeout_ns;
@@ -574,6 +575,45 @@ __global__ void __launch_bounds__(BOUND, BOUND == PAIRED ? 2 : 1)
                  w);
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) dw[i] = db[i] = 0;
+  // the thread's sums into the slab: stored, or added to what is there
+  auto slab = [&] {
+    const int i = M == CLUSTER ? blockIdx.x / a.cluster : blockIdx.x;
+    return a.part + static_cast<int64_t>(i) * 2 * a.H + tiles.column;
+  };
+  auto to_slab = [&](bool add) {
+    float* p = slab();
+    float aw[EPT], ab[EPT];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      f2unpack(dw[i], aw[2 * i], aw[2 * i + 1]);
+      f2unpack(db[i], ab[2 * i], ab[2 * i + 1]);
+    }
+    if constexpr (V * sizeof(T) == 16) {  // H is a multiple of 4
+      auto put = [&](float* to, const float* v) {
+        float4 q = make_float4(v[0], v[1], v[2], v[3]);
+        if (add) {
+          const float4 o = *reinterpret_cast<const float4*>(to);
+          q = make_float4(o.x + q.x, o.y + q.y, o.z + q.z, o.w + q.w);
+        }
+        *reinterpret_cast<float4*>(to) = q;
+      };
+#pragma unroll
+      for (int i = 0; i < EPT; i += 4) {
+        const int j = share.column<V>(i, tiles.width);
+        if (j < 0) continue;
+        put(p + j, &aw[i]);
+        if (LAYER) put(p + a.H + j, &ab[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        const int j = share.column<V>(i, tiles.width);
+        if (j < 0) continue;
+        p[j] = add ? p[j] + aw[i] : aw[i];
+        if (LAYER) p[a.H + j] = add ? p[a.H + j] + ab[i] : ab[i];
+      }
+    }
+  };
   // the statistics of the next tile, a lane to a row, are under way while one
   // is computed
   const int lane = M == LANES ? threadIdx.x & 31 : 0;
@@ -585,7 +625,16 @@ __global__ void __launch_bounds__(BOUND, BOUND == PAIRED ? 2 : 1)
     if (LAYER) mu_next = on ? a.mean[row] : 0.f;
   };
   look_ahead(tiles.tile);
-  for (; tiles.more(); tiles.advance()) {
+  constexpr bool RUNS = M == CLUSTER && V * sizeof(T) == 16;  // MAX_RUN
+  bool again = false;
+  for (int left = a.run; tiles.more(); tiles.advance()) {
+    if (RUNS && left-- == 0) {
+      if (a.part) to_slab(again);
+      again = true;
+      left = a.run - 1;
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) dw[i] = db[i] = 0;
+    }
     const int rows = tiles.wait();
     const float rs_tile = rs_next, mu_tile = mu_next;
     look_ahead(tiles.tile + tiles.step);
@@ -654,36 +703,16 @@ __global__ void __launch_bounds__(BOUND, BOUND == PAIRED ? 2 : 1)
   let_next_begin();  // k_norm_join, which waits for this launch's end
   if (M == CLUSTER) cluster_sync();  // no block ends before its sums are read
   if (!a.part) return;
-  const int slab = M == CLUSTER ? blockIdx.x / a.cluster : blockIdx.x;
-  float* p = a.part + static_cast<int64_t>(slab) * 2 * a.H + tiles.column;
-  float aw[EPT], ab[EPT];
-#pragma unroll
-  for (int i = 0; i < PAIRS; ++i) {
-    f2unpack(dw[i], aw[2 * i], aw[2 * i + 1]);
-    f2unpack(db[i], ab[2 * i], ab[2 * i + 1]);
-  }
   if constexpr (M != LANES) {
-    if constexpr (V * sizeof(T) == 16) {  // H is a multiple of 4
-#pragma unroll
-      for (int i = 0; i < EPT; i += 4) {
-        const int j = share.column<V>(i, tiles.width);
-        if (j < 0) continue;
-        *reinterpret_cast<float4*>(p + j) =
-            make_float4(aw[i], aw[i + 1], aw[i + 2], aw[i + 3]);
-        if (LAYER)
-          *reinterpret_cast<float4*>(p + a.H + j) =
-              make_float4(ab[i], ab[i + 1], ab[i + 2], ab[i + 3]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        const int j = share.column<V>(i, tiles.width);
-        if (j < 0) continue;
-        p[j] = aw[i];
-        if (LAYER) p[a.H + j] = ab[i];
-      }
-    }
+    to_slab(again);
   } else {
+    float* p = slab();
+    float aw[EPT], ab[EPT];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      f2unpack(dw[i], aw[2 * i], aw[2 * i + 1]);
+      f2unpack(db[i], ab[2 * i], ab[2 * i + 1]);
+    }
     // the warp's teams that have the same columns by shuffles (of rows of odd
     // width in pairs every other team), then what is left one after the other
     const int kinds = V == 2 && (a.H & 1) && rows_at_once > 1 ? 2 : 1;
@@ -831,6 +860,14 @@ __global__ void __launch_bounds__(32 * JOIN_RUNS)
 
 constexpr int64_t MAX_H = 1 << 20;
 constexpr int64_t MAX_SLABS = 1024;
+// Rows that a thread adds in fp32, as far as the slabs go, and since clusters are
+// few (19 of eight blocks of 512 threads), no more than 64 and a 128th of all.
+// More blocks or clusters than are resident take longer runs in turns; clusters
+// whose rows are whole vectors add their registers to their slab instead. Either
+// costs the other dearly: 16384 x 32768 bf16, RMS norm, 905 us as one run, 1159
+// in turns, 920 so; 20000 x 12345, layer norm, 720 as one run, 726 in turns, 867
+// with the slab.
+constexpr int64_t MAX_RUN = 1024;
 
 int64_t slabs_of(int64_t L) {
   return L < MAX_SLABS ? (L > 0 ? L : 1) : MAX_SLABS;
@@ -840,6 +877,7 @@ constexpr int64_t RING_BYTES = 48 * 1024;  // of a block, as far as two stages
 
 struct Geometry {
   Mode mode;
+  bool exact;  // whole 16-byte vectors
   int threads;
   size_t smem;
 };
@@ -852,7 +890,7 @@ struct Geometry {
 Geometry geometry(NormArgs& a, int v, int size, int arrays, bool may_be_big,
                   int num_sms) {
   Geometry g{};
-  const bool exact = v * size == 16;
+  const bool exact = g.exact = v * size == 16;
   a.cluster = 1;
   a.slice = a.H;
   const bool big = may_be_big && v > 1 && a.H > BLOCK_H && a.H <= BIG_H;
@@ -903,10 +941,12 @@ static_assert(MAX_NORM_SMEM >= 2 * 2 * (BLOCK_H * 4 + 32), "a block's row");
 static_assert(32 * EPT * 4 <= 2048, "the step of a tile");
 
 // Launches a kernel over a.L rows; *teams: blocks, or clusters, of the launch,
-// as many as are resident at once.
+// as many as are resident at once, or a multiple of that.
 template <class K>
 cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
                         cudaStream_t s, int* teams) {
+  const int64_t slack = a.L / 128 + 64;
+  a.run = static_cast<int>(slack < MAX_RUN ? slack : MAX_RUN);
   cudaError_t e;
   if (g.smem > 40 * 1024) {  // with the static part, up to 5 KB
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -947,6 +987,11 @@ cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
     if (n > most) n = most > num_sms ? most : num_sms;
     if (n > a.L) n = a.L;
     if (n > MAX_SLABS) n = MAX_SLABS;
+    // longer runs of rows are taken in turns
+    const int64_t at_once = g.mode == LANES ? TEAM_WARPS * 32 / a.team : 1;
+    const int64_t turns = ceil_div(ceil_div(a.L, n * at_once), a.run);
+    if (g.mode != CLUSTER || !g.exact)
+      n *= turns < MAX_SLABS / n ? turns : MAX_SLABS / n;
   }
   // rows of a team that has several are of one parity (Share)
   if (g.mode != LANES && a.H % 2 && n < tiles) n = n < 2 ? 2 : n & ~1ll;

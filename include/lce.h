@@ -677,8 +677,9 @@ lce_status lce_norm_forward(lce_norm_kind kind, const void* x, lce_dtype dt,
  *   not all of them (RMS norm: dbias NULL).
  *   ws      device, 16-byte aligned, lce_norm_workspace_size() bytes; needed
  *           for dweight and dbias alone (else NULL)
- * The sums over rows are formed in fp32 over up to a thousand runs of rows,
- * and the runs added in a fixed order to twice fp32's precision. L = 0: zero
+ * The sums over rows are formed in fp32 in runs of at most 1024 rows or a
+ * 1024th of all, whichever is more; up to 1024 sums, of a run or a few of them,
+ * are added in a fixed order to twice fp32's precision. L = 0: zero
  * dweight and dbias.
  */
 size_t lce_norm_workspace_size(int64_t L, int64_t H);
