@@ -1300,6 +1300,8 @@ def expert_counts(experts, num_experts: int, mask=None, counts_out=None):
 def _dense(t):
     """Whether t's elements fill one run of memory without overlap, in any
     order of dimensions."""
+    if t.numel() == 0:
+        return True
     step = 1
     for stride, n in sorted((s, n) for s, n in zip(t.stride(), t.shape)
                             if n != 1):

@@ -4,9 +4,11 @@ on one."""
 import ctypes
 
 import pytest
+import torch
 
+import chunked_lm_head_gemm_gb300 as lce
 from chunked_lm_head_gemm_gb300 import _binding as B
-from tests.test_step_binding import NULL, P, c  # noqa: F401
+from tests.test_step_binding import BF, NULL, P, c, lib, t  # noqa: F401
 
 A, BB, CC = 0x10000, 0x20000, 0x30000
 
@@ -40,3 +42,14 @@ def test_the_norm_may_stand_beside_a_gradient(c, norm):  # noqa: F811
 def test_an_empty_gradient_holds_no_norm(c):  # noqa: F811
     rows = [(A, CC, 1, 100), (BB, BB, 1, 0)]
     assert clip_grad_norm(c, rows, BB) == B.LCE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("shape", [(3, 0), (0, 3), (2, 0, 4), (0,)])
+def test_empty_gradients_beside_transposed_ones(lib, shape):  # noqa: F811
+    """An empty tensor fills its memory whatever its strides."""
+    for empty in (t(*shape), t(*shape).permute(*range(len(shape))[::-1])):
+        lce.clip_grad_norm([t(4, 6).t(), empty], 1.0)
+        assert list(lib.calls[-1][1][3]) == [24, 0]
+        lce.grad_norm([empty, t(4, 6).t()])
+    with pytest.raises(ValueError, match="gaps"):
+        lce.grad_norm([t(6)[::2], t(*shape)])
