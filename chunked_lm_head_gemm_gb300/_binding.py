@@ -1324,7 +1324,8 @@ class _GradTable:
     hundreds of tensors: each property is asked of all of them at once."""
 
     def __init__(self, grads):
-        grads = self.grads = list(grads)
+        given = self.given = list(grads)
+        grads = self.grads = [g for g in given if g is not None]
         n = self.n = len(grads)
         if not n:
             self.device = torch.device("cuda", torch.cuda.current_device())
@@ -1355,8 +1356,13 @@ class _GradTable:
         if grads_out is None:
             return self.ptrs
         grads, outs = self.grads, list(grads_out)
-        if len(outs) != self.n:
-            raise ValueError(f"{len(outs)} outputs for {self.n} gradients")
+        if len(outs) != len(self.given):
+            raise ValueError(f"{len(outs)} outputs for {len(self.given)} "
+                             "gradients")
+        if any((o is None) != (g is None) for o, g in zip(outs, self.given)):
+            raise ValueError("an output must be None where its gradient is, "
+                             "and there alone")
+        outs = [o for o in outs if o is not None]
         codes = list(map(_TYPE_CODES.get, map(_dtype_of, outs)))
         same = (codes == self.code_list and
                 list(map(torch.Tensor.numel, outs)) == self.size_list and
@@ -1399,7 +1405,8 @@ def grad_norm_workspace_size(n: int) -> int:
 
 def grad_norm(grads, workspace=None):
     """sqrt of the sum of all squares of a list of gradients (bf16 or fp32
-    CUDA tensors of any shapes): a fp32 scalar on their device."""
+    CUDA tensors of any shapes; None, a parameter without one, is passed by):
+    a fp32 scalar on their device."""
     table = _GradTable(grads)
     dev = table.device
     ws = table.workspace(workspace)
@@ -1412,9 +1419,9 @@ def grad_norm(grads, workspace=None):
 def clip_grads(grads, norm, max_norm: float, grads_out=None):
     """Multiplies every gradient by min(1, max_norm / (norm + 1e-6)), in place
     or into grads_out (tensors laid out as the gradients; contiguous ones may
-    differ in shape, such as slices of a flat buffer). norm: one fp32 value
-    on the device, of grad_norm or of a sum over processes. Gradients or
-    outputs that overlap are refused."""
+    differ in shape, such as slices of a flat buffer; None where the gradient
+    is). norm: one fp32 value on the device, of grad_norm or of a sum over
+    processes. Gradients or outputs that overlap are refused."""
     max_norm = _max_norm(max_norm)
     table = _GradTable(grads)
     _check_rows("norm", norm.reshape(-1), (1,), torch.float32, table.device)

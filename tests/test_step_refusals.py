@@ -53,3 +53,25 @@ def test_empty_gradients_beside_transposed_ones(lib, shape):  # noqa: F811
         lce.grad_norm([empty, t(4, 6).t()])
     with pytest.raises(ValueError, match="gaps"):
         lce.grad_norm([t(6)[::2], t(*shape)])
+
+
+def test_parameters_without_a_gradient(lib):  # noqa: F811
+    """[p.grad for p in parameters] has None for a parameter that took no part:
+    it is passed by, and has no output."""
+    g = [t(3, 4), t(5, dtype=BF)]
+    outs = [t(3, 4), t(5, dtype=BF)]
+    mixed, mixed_outs = [None, g[0], None, g[1]], [None, outs[0], None, outs[1]]
+    lce.grad_norm(mixed)
+    lce.clip_grads(mixed, t(), 1.0)
+    lce.clip_grad_norm(mixed, 1.0)
+    lce.clip_grad_norm(mixed, 1.0, grads_out=mixed_outs)
+    for name, args in lib.calls:
+        n = args[args.index(2)]
+        assert n == 2 and list(args[0]) == [x.data_ptr() for x in g], name
+    assert list(lib.calls[-1][1][1]) == [x.data_ptr() for x in outs]
+    del lib.calls[:]
+    for bad in ([outs[0], outs[0], None, outs[1]], [None, outs[0], None, None],
+                outs):
+        with pytest.raises(ValueError, match="output"):
+            lce.clip_grad_norm(mixed, 1.0, grads_out=bad)
+    assert not lib.calls
