@@ -17,6 +17,7 @@ import threading
 import torch
 from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import build as _build
 
@@ -297,6 +298,13 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}; use bfloat16 or float32")
 
 
+def _written(*tensors):
+    """Tells autograd that a call has written tensors (None: not this one)
+    that may be the caller's, whose memory the library knows by address alone:
+    one that an operation has saved for its gradient is then an error there."""
+    increment_version([t for t in tensors if t is not None])
+
+
 def _check_inputs(h, W, labels):
     if not (h.is_cuda and W.is_cuda and labels.is_cuda):
         raise ValueError("h, W and labels must be CUDA tensors")
@@ -368,6 +376,7 @@ def forward(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
                                 workspace.data_ptr(), workspace.numel(),
                                 _stream_ptr(dev))
         _check(st, "lce_forward_ex")
+    _written(loss, lse)
     return loss, lse
 
 
@@ -407,6 +416,7 @@ def backward(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
                                  workspace.data_ptr(), workspace.numel(),
                                  _stream_ptr(dev))
         _check(st, "lce_backward_ex")
+    _written(dH, dW)
     return dH, dW
 
 
@@ -466,6 +476,7 @@ def forward_backward(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
                                          workspace.data_ptr(),
                                          workspace.numel(), _stream_ptr(dev))
         _check(st, "lce_forward_backward_ex")
+    _written(loss, lse, dH, dW)
     return loss, lse, dH, dW
 
 
@@ -483,6 +494,7 @@ def scale_gradients(dH, dW, dloss: torch.Tensor):
     st = load().lce_scale_gradients(_ptr(dH), code, L, H, _ptr(dW), V,
                                     dloss.data_ptr(), _stream_ptr(ref.device))
     _check(st, "lce_scale_gradients")
+    _written(dH, dW)
     return dH, dW
 
 
@@ -499,6 +511,7 @@ def count_valid(labels: torch.Tensor, V: int,
                                 ignore_index, out.data_ptr(),
                                 _stream_ptr(labels.device))
     _check(st, "lce_count_valid")
+    _written(out)
     return out
 
 
@@ -514,6 +527,7 @@ def shard_sums(loss_local: torch.Tensor, n_local: torch.Tensor,
     st = load().lce_shard_sums(loss_local.data_ptr(), n_local.data_ptr(),
                                out.data_ptr(), _stream_ptr(dev))
     _check(st, "lce_shard_sums")
+    _written(out)
     return out
 
 
@@ -585,6 +599,7 @@ def forward_slice(h: torch.Tensor, W_slice: torch.Tensor,
             rows[3].data_ptr() if len(rows) == 4 else None,
             workspace.data_ptr(), workspace.numel(), _stream_ptr(dev))
     _check(st, "lce_forward_slice")
+    _written(out)
     return rows
 
 
@@ -692,6 +707,7 @@ def forward_slice_exp(h, W_slice, labels, v0: int, V_total: int, workspace,
         rows[3].data_ptr() if len(rows) == 4 else None,
         workspace.data_ptr(), workspace.numel(), _stream_ptr(h.device))
     _check(st, "lce_forward_slice_exp")
+    _written(out)
     return rows
 
 
@@ -785,6 +801,7 @@ def mlp_forward(x, Wg, Wu, Wd, chunk_rows: int = 0, workspace=None,
                              workspace.data_ptr(), workspace.numel(),
                              _stream_ptr(x.device))
     _check(st, "lce_mlp_forward")
+    _written(y_out)
     return y
 
 
@@ -820,6 +837,7 @@ def mlp_backward(x, Wg, Wu, Wd, dy, chunk_rows: int = 0, workspace=None,
                               _ptr(dWd), workspace.data_ptr(),
                               workspace.numel(), _stream_ptr(dev))
     _check(st, "lce_mlp_backward")
+    _written(dx, dWg, dWu, dWd)
     return dx, dWg, dWu, dWd
 
 
@@ -899,6 +917,7 @@ def route_forward(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
                                opts, weights.data_ptr(),
                                experts.data_ptr(), _stream_ptr(dev))
     _check(st, "lce_route_forward")
+    _written(weights, experts)
     return weights, experts
 
 
@@ -928,6 +947,7 @@ def route_backward(logits: torch.Tensor, experts: torch.Tensor,
                                 dweights.data_ptr(), L, E, opts,
                                 out.data_ptr(), _stream_ptr(dev))
     _check(st, "lce_route_backward")
+    _written(dlogits_out)
     return out
 
 
@@ -996,6 +1016,8 @@ def experts_forward(x, Wg, Wu, Wd, weights, experts, workspace=None,
         _stream_ptr(dev))
     if st:
         _check(st, "lce_experts_forward")
+    if y_out is not None:
+        _written(y_out)
     return y
 
 
@@ -1117,6 +1139,8 @@ def _norm_forward(kind, x, weight, bias, eps, y_out, save_stats):
           None if bias is None else bias.data_ptr(), param, L, H, float(eps),
           y.data_ptr(), None if mean is None else mean.data_ptr(),
           None if rstd is None else rstd.data_ptr())
+    if y_out is not None:
+        _written(y_out)
     return y, mean, rstd
 
 
@@ -1155,6 +1179,8 @@ def _norm_backward(kind, x, weight, mean, rstd, dy, grad_dtype, workspace,
           None if dw is None else dw.data_ptr(),
           None if db is None else db.data_ptr(),
           None if workspace is None else workspace.data_ptr(), size)
+    if compute_dx and dx_out is not None:
+        _written(dx_out)
     return dx, dw, db
 
 
@@ -1276,6 +1302,8 @@ def balance_backward(logits, slopes, dloss, scoring: str = "softmax",
     _call("lce_balance_backward", dev, logits.data_ptr(), code,
           None if mask is None else mask.data_ptr(), L, E, score,
           slopes.data_ptr(), dloss.data_ptr(), out.data_ptr())
+    if dlogits_out is not None:
+        _written(dlogits_out)
     return out
 
 
@@ -1294,6 +1322,8 @@ def expert_counts(experts, num_experts: int, mask=None, counts_out=None):
     _call("lce_expert_counts", dev, experts.data_ptr(),
           None if mask is None else mask.data_ptr(), L, E, K,
           counts.data_ptr())
+    if counts_out is not None:
+        _written(counts_out)
     return counts
 
 
@@ -1354,6 +1384,7 @@ class _GradTable:
     def outputs(self, grads_out):
         """The outputs' pointers: the gradients' own without grads_out."""
         if grads_out is None:
+            self.outs = self.grads
             return self.ptrs
         grads, outs = self.grads, list(grads_out)
         if len(outs) != len(self.given):
@@ -1362,7 +1393,7 @@ class _GradTable:
         if any((o is None) != (g is None) for o, g in zip(outs, self.given)):
             raise ValueError("an output must be None where its gradient is, "
                              "and there alone")
-        outs = [o for o in outs if o is not None]
+        outs = self.outs = [o for o in outs if o is not None]
         codes = list(map(_TYPE_CODES.get, map(_dtype_of, outs)))
         same = (codes == self.code_list and
                 list(map(torch.Tensor.numel, outs)) == self.size_list and
@@ -1427,6 +1458,7 @@ def clip_grads(grads, norm, max_norm: float, grads_out=None):
     _check_rows("norm", norm.reshape(-1), (1,), torch.float32, table.device)
     _call("lce_clip_grads", table.device, table.ptrs, table.outputs(grads_out),
           table.codes, table.sizes, table.n, norm.data_ptr(), max_norm)
+    increment_version(table.outs)
 
 
 def clip_grad_norm(grads, max_norm: float, grads_out=None, workspace=None):
@@ -1441,6 +1473,7 @@ def clip_grad_norm(grads, max_norm: float, grads_out=None, workspace=None):
     _call("lce_clip_grad_norm", dev, table.ptrs, outs, table.codes,
           table.sizes, table.n, max_norm, norm.data_ptr(), ws.data_ptr(),
           ws.numel() * ws.element_size())
+    increment_version(table.outs)
     return norm
 
 
