@@ -869,8 +869,24 @@ constexpr int64_t MAX_SLABS = 1024;
 // with the slab.
 constexpr int64_t MAX_RUN = 1024;
 
-int64_t slabs_of(int64_t L) {
-  return L < MAX_SLABS ? (L > 0 ? L : 1) : MAX_SLABS;
+// Rows of a run (MAX_RUN).
+int64_t run_of(int64_t L) {
+  const int64_t slack = L / 128 + 64;
+  return slack < MAX_RUN ? slack : MAX_RUN;
+}
+
+// The most slabs of L rows. Blocks and clusters (H from 32 EPT to CLUSTER_H) are
+// no more than 1024 threads of EPT columns on each SM (64 registers a thread, of
+// the largest blocks), and the turns that their runs take: 65 MB for 16384 x
+// 65536, where MAX_SLABS are 537.
+int64_t slabs_of(int64_t L, int64_t H) {
+  int64_t n = MAX_SLABS;
+  if (H > 32 * EPT && H <= CLUSTER_H) {
+    const int64_t resident = 152 * 1024 * EPT / H;
+    const int64_t turns = resident + resident / 64 + 1 + L / run_of(L);
+    if (n > turns) n = turns;
+  }
+  return n < L ? n : L > 0 ? L : 1;
 }
 
 constexpr int64_t RING_BYTES = 48 * 1024;  // of a block, as far as two stages
@@ -945,8 +961,7 @@ static_assert(32 * EPT * 4 <= 2048, "the step of a tile");
 template <class K>
 cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
                         cudaStream_t s, int* teams) {
-  const int64_t slack = a.L / 128 + 64;
-  a.run = static_cast<int>(slack < MAX_RUN ? slack : MAX_RUN);
+  a.run = static_cast<int>(run_of(a.L));
   cudaError_t e;
   if (g.smem > 40 * 1024) {  // with the static part, up to 5 KB
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -986,12 +1001,13 @@ cudaError_t launch_rows(K kern, NormArgs& a, const Geometry& g, int num_sms,
     const int64_t most = a.L * a.size * 3 / 16;
     if (n > most) n = most > num_sms ? most : num_sms;
     if (n > a.L) n = a.L;
-    if (n > MAX_SLABS) n = MAX_SLABS;
+    const int64_t slabs = slabs_of(a.L, a.H);
+    if (n > slabs) n = slabs;
     // longer runs of rows are taken in turns
     const int64_t at_once = g.mode == LANES ? TEAM_WARPS * 32 / a.team : 1;
     const int64_t turns = ceil_div(ceil_div(a.L, n * at_once), a.run);
     if (g.mode != CLUSTER || !g.exact)
-      n *= turns < MAX_SLABS / n ? turns : MAX_SLABS / n;
+      n *= turns < slabs / n ? turns : slabs / n;
   }
   // rows of a team that has several are of one parity (Share)
   if (g.mode != LANES && a.H % 2 && n < tiles) n = n < 2 ? 2 : n & ~1ll;
@@ -1072,7 +1088,7 @@ cudaError_t backward(NormArgs& a, int num_sms, cudaStream_t s) {
     }
   }
   if (a.part) {
-    a.slabs = static_cast<int>(slabs_of(a.L));
+    a.slabs = static_cast<int>(slabs_of(a.L, a.H));
     k_norm_dparams_wide<T, LAYER>
         <<<dim3(static_cast<unsigned>(ceil_div(a.H, 128)),
                 static_cast<unsigned>(a.slabs)),
@@ -1110,7 +1126,7 @@ extern "C" {
 
 size_t lce_norm_workspace_size(int64_t L, int64_t H) {
   if (L < 0 || L > (1ll << 31) || H < 1 || H > MAX_H) return 0;
-  return static_cast<size_t>(slabs_of(L)) * 2 * H * sizeof(float);
+  return static_cast<size_t>(slabs_of(L, H)) * 2 * H * sizeof(float);
 }
 
 lce_status lce_norm_forward(lce_norm_kind kind, const void* x, lce_dtype dt,

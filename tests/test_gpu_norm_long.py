@@ -49,3 +49,26 @@ def test_several_runs_of_rows(H, layer):
     again = backward(x, w, mean, rstd, dy, layer)
     for a, c in zip(grads, again):
         assert (a is None and c is None) or torch.equal(a, c)
+
+
+@pytest.mark.parametrize("layer", [True, False], ids=["layer", "rms"])
+@pytest.mark.parametrize("L,H", [(3, 16400), (300, 513), (3001, 20001),
+                                 (40000, 8200), (2000, 65536), (1500, 65535),
+                                 (20000, 1001), (60000, 8192)])
+def test_the_workspace_holds_all_slabs(L, H, layer):
+    """A workspace of just the stated size, with a mark behind it."""
+    import chunked_lm_head_gemm_gb300 as lce
+    from tests.test_gpu_norm import BF, backward, make
+    require_gpu()
+    x, w, _, dy = make(L, H, BF, BF, seed=H)
+    rstd = torch.rand(L, device="cuda") + 0.5
+    mean = torch.zeros(L, device="cuda") if layer else None
+    size = lce.norm_workspace_size(L, H)
+    room = torch.full((size + 4096,), 171, dtype=torch.uint8, device="cuda")
+    got = backward(x, w, mean, rstd, dy, layer, workspace=room[:size])
+    assert (room[size:] == 171).all()
+    want = ref.norm_grad(x, w, mean, rstd, dy, layer)
+    tol = ref.norm_grad_tolerance(x, w, mean, rstd, dy, layer, BF,
+                                  torch.float32)
+    for g, v, t in zip(got, want, tol):
+        assert g is None or ((g.double() - v).abs() <= t).all()

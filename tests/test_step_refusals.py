@@ -75,3 +75,13 @@ def test_parameters_without_a_gradient(lib):  # noqa: F811
         with pytest.raises(ValueError, match="output"):
             lce.clip_grad_norm(mixed, 1.0, grads_out=bad)
     assert not lib.calls
+
+
+@pytest.mark.parametrize("L,H,slabs", [(16384, 65536, 125), (131072, 32768, 210),
+                                       (131072, 4096, 750), (5, 65536, 5),
+                                       (1 << 31, 8192, 1024)])
+def test_the_norms_workspace_is_near_its_use(c, L, H, slabs):  # noqa: F811
+    """Two sums of H columns for each of the blocks or clusters that a launch
+    may have: rows of many columns have few."""
+    size = c.lce_norm_workspace_size(L, H)
+    assert 0 < size <= slabs * 2 * H * 4
