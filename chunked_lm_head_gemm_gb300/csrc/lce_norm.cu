@@ -50,7 +50,7 @@ struct NormArgs {
   uint32_t array_bytes;  // of a tile's place there
   float* part;    // [slabs][2][H] sums of dy n and dy
   int slabs;
-  int run;  // rows that a thread may add in registers, 64 at least
+  int run;  // rows that a thread may add in registers, 48 at least
   int want_dx;
   int size;  // bytes of an element
   uint64_t timeout_ns;
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(32 * JOIN_RUNS)
 constexpr int64_t MAX_H = 1 << 20;
 constexpr int64_t MAX_SLABS = 1024;
 // Rows that a thread adds in fp32, as far as the slabs go, and since clusters are
-// few (19 of eight blocks of 512 threads), no more than 64 and a 128th of all.
+// few (19 of eight blocks of 512 threads), no more than 48 and a 128th of all.
 // More blocks or clusters than are resident take longer runs in turns; clusters
 // whose rows are whole vectors add their registers to their slab instead. Either
 // costs the other dearly: 16384 x 32768 bf16, RMS norm, 905 us as one run, 1159
@@ -871,7 +871,7 @@ constexpr int64_t MAX_RUN = 1024;
 
 // Rows of a run (MAX_RUN).
 int64_t run_of(int64_t L) {
-  const int64_t slack = L / 128 + 64;
+  const int64_t slack = L / 128 + 48;
   return slack < MAX_RUN ? slack : MAX_RUN;
 }
 
