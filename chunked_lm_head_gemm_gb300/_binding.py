@@ -1390,10 +1390,12 @@ class _GradTable:
         if len(outs) != len(self.given):
             raise ValueError(f"{len(outs)} outputs for {len(self.given)} "
                              "gradients")
-        if any((o is None) != (g is None) for o, g in zip(outs, self.given)):
+        kept = self.outs = [o for o in outs if o is not None]
+        if (len(kept) != self.n or self.n != len(outs) and any(
+                (o is None) != (g is None) for o, g in zip(outs, self.given))):
             raise ValueError("an output must be None where its gradient is, "
                              "and there alone")
-        outs = self.outs = [o for o in outs if o is not None]
+        outs = kept
         codes = list(map(_TYPE_CODES.get, map(_dtype_of, outs)))
         same = (codes == self.code_list and
                 list(map(torch.Tensor.numel, outs)) == self.size_list and
