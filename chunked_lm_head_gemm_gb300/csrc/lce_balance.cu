@@ -17,9 +17,10 @@
 // (2^-21 of a score, however far from zero or below the row's largest; 131072 x
 // 256: 1 to 3 us of a pass).
 //
-// Measured alone, 131072 x 256 fp32 sigmoid: forward 32 us (4.2 TB/s; 173
-// instructions a row and warp come first), joining 608 blocks' sums 11 us (a
-// cold L2), backward 44 us (6.1 TB/s).
+// Measured alone, 131072 x 256 fp32 sigmoid: forward 36 us (3.9 TB/s; 68% of
+// the issue slots at 46% of the warps: instructions and their latency
+// together), joining 608 blocks' sums 11 us (a cold L2), backward 46 us (5.9
+// TB/s).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -98,9 +99,9 @@ __device__ __forceinline__ float clamped(float v) {
 }
 
 // e^v of a pair of v <= 0, or e^-v of any pair, to 2^-22 of itself. The
-// argument h of 2^h is rounded, which alone is an error that grows with |v| (3e-6
-// at 60); v - h ln 2, exact but for its own last place, says by how much, and
-// e^(v - h ln 2) is 1 + (v - h ln 2) to 2^-35.
+// argument h of 2^h is rounded, which alone is an error that grows with |v|
+// (3e-6 at 60); v - h ln 2, exact but for its own last place, says by how much,
+// and e^(v - h ln 2) is 1 + (v - h ln 2) to 2^-35.
 constexpr float LN2_HIGH = 0.693147180559945309, LN2_LOW =
     0.693147180559945309 - LN2_HIGH;
 template <bool NEGATE>
@@ -240,8 +241,9 @@ struct Rows {
 };
 
 // Blocks of an SM that the registers leave room for. (131072 x 256 fp32, us of
-// a forward and a backward pass: 81 with 4 blocks of one row under way, 103
-// with 5, 139 with 6, where registers spill; 87 with 3 blocks of two rows.)
+// a forward and a backward pass: 85 with 4 blocks of one row under way, 90 with
+// 3, 121 with 5, 143 with 6, where registers spill; with 3 blocks of two rows
+// under way 6 more than with 4 of one.)
 constexpr int blocks_per_sm(int n) { return n <= 8 ? 4 : n <= 16 ? 2 : 1; }
 static_assert(SMS * 4 <= JOIN_THREADS, "a thread to a block's tokens");
 
@@ -495,10 +497,10 @@ int team_of(int64_t E) {
 }
 
 // Blocks of a forward pass. One alone, without a join, up to 8 rows to a team:
-// 128 x 128 takes 6.8 us on the GPU so and 7.3 in several blocks, 256 x 128 (16
-// rows) 9.8 and 7.5. Else two rows to a team as long as the SMs have no more
+// 128 x 128 takes 7.3 us on the GPU so and 7.6 in several blocks, 256 x 128 (16
+// rows) 10.4 and 7.8. Else two rows to a team as long as the SMs have no more
 // than a block, then four, since every block's sums have to be joined: 4099 x
-// 60 takes 8.4 us with two and 9.1 with four, 16384 x 128 11.7 and 10.2.
+// 60 takes 8.8 us with two and 9.6 with four, 16384 x 128 12.1 and 10.5.
 int blocks_of(int64_t L, int64_t E) {
   const int64_t rows = WARPS * 32 / team_of(E);  // of a block at a time
   if (L <= 8 * rows) return 1;

@@ -16,11 +16,11 @@
 // are under way without registers to hold them. Wider rows are read again where
 // a pass over them needs it.
 //
-// Measured alone, 65536 x 4096 bf16 RMS norm: forward 179 us (6.0 TB/s),
-// backward 233 us (6.9 TB/s) and 10 us for joining its blocks' sums; 1048576 x
-// 128 bf16 88 and 128 us (6.1, 6.3 TB/s); 16384 x 2560 fp32 layer norm 52 and
-// 71 us (6.4, 7.1 TB/s). Rows that are not on 16 bytes are bound by
-// instructions: 65536 x 1001 bf16 RMS norm 53 and 121 us (4.9, 3.3 TB/s).
+// Measured alone, 65536 x 4096 bf16 RMS norm: forward 170 us (6.3 TB/s),
+// backward 224 us (7.2 TB/s) and 7 us for joining its blocks' sums; 1048576 x
+// 128 bf16 89 and 127 us (6.0, 6.4 TB/s); 16384 x 2560 fp32 layer norm 54 and
+// 70 us (6.3, 7.2 TB/s). Rows that are not on 16 bytes are bound by
+// instructions: 65536 x 1001 bf16 RMS norm 53 and 117 us (4.9, 3.4 TB/s).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -64,10 +64,11 @@ constexpr int MAX_THREADS = 512;  // of a block that is a team
 constexpr int BLOCK_H = EPT * MAX_THREADS;  // the widest row of a block
 constexpr int MAX_CLUSTER = 8;
 constexpr int CLUSTER_H = BLOCK_H * MAX_CLUSTER;
-// A row's team. BIG: a block of up to 1024 threads, where the registers allow
-// it (the forward pass, and the backward of an RMS norm of bf16): a block's
-// barrier is a third of a cluster's. 16384 rows of 16384 bf16: layer norm
-// forward 222 us against 585, RMS norm backward 340 against 399.
+// A row's team. BIG: a block of up to 1024 threads, whose barrier is a third of
+// a cluster's, where that is faster at its 64 registers a thread: in the
+// forward pass, and in the backward of an RMS norm of bf16, although it spills
+// 168 to 180 bytes. 16384 rows of 16384 bf16: layer norm forward 222 us against
+// 585, RMS norm backward 340 against 399.
 enum Mode { LANES, BLOCK, CLUSTER, BIG };
 constexpr int BIG_H = 2 * BLOCK_H;
 constexpr int threads_of(Mode m) { return m == BIG ? 1024 : MAX_THREADS; }
@@ -543,8 +544,10 @@ __global__ void __launch_bounds__(threads_of(M)) k_norm_fwd(const NormArgs a) {
 }
 
 // The backward's blocks of 257 to 320 threads share an SM by two when they are
-// built for it (102 registers a thread): 32768 x 5120 bf16 RMS norm 165 -> 143
-// us, layer norm 267 -> 212. Capped for other sizes they spill and are slower.
+// built for it (at most 96 registers a thread): 32768 x 5120 bf16 RMS norm 165
+// -> 143 us, layer norm 267 -> 212, although the layer norm spills (32 bytes
+// there, to 96 in pairs; single elements spill 130 to 230 in either norm).
+// Capped so for other sizes the kernels were up to 1.6 times as slow.
 constexpr int PAIRED = 320;
 
 // dx, and a slab's sums for dw and db: slab = block, or cluster.
@@ -860,13 +863,13 @@ __global__ void __launch_bounds__(32 * JOIN_RUNS)
 
 constexpr int64_t MAX_H = 1 << 20;
 constexpr int64_t MAX_SLABS = 1024;
-// Rows that a thread adds in fp32, as far as the slabs go, and since clusters are
-// few (19 of eight blocks of 512 threads), no more than 48 and a 128th of all.
-// More blocks or clusters than are resident take longer runs in turns; clusters
-// whose rows are whole vectors add their registers to their slab instead. Either
-// costs the other dearly: 16384 x 32768 bf16, RMS norm, 905 us as one run, 1159
-// in turns, 920 so; 20000 x 12345, layer norm, 720 as one run, 726 in turns, 867
-// with the slab.
+// Rows that a thread adds in fp32, as far as the slabs go, and since clusters
+// are few (19 of eight blocks of 512 threads), no more than 48 and a 128th of
+// all. More blocks or clusters than are resident take longer runs in turns;
+// clusters whose rows are whole vectors add their registers to their slab
+// instead. Either costs the other dearly: 16384 x 32768 bf16, RMS norm, 905 us
+// as one run, 1159 in turns, 920 so; 20000 x 12345, layer norm, 720 as one run,
+// 726 in turns, 867 with the slab.
 constexpr int64_t MAX_RUN = 1024;
 
 // Rows of a run (MAX_RUN).
@@ -875,10 +878,10 @@ int64_t run_of(int64_t L) {
   return slack < MAX_RUN ? slack : MAX_RUN;
 }
 
-// The most slabs of L rows. Blocks and clusters (H from 32 EPT to CLUSTER_H) are
-// no more than 1024 threads of EPT columns on each SM (64 registers a thread, of
-// the largest blocks), and the turns that their runs take: 65 MB for 16384 x
-// 65536, where MAX_SLABS are 537.
+// The most slabs of L rows. Blocks and clusters (H from 32 EPT to CLUSTER_H)
+// are no more than 1024 threads of EPT columns on each SM (64 registers a
+// thread, of the largest blocks), and the turns that their runs take: 69 MB for
+// 16384 x 65536, where MAX_SLABS are 537.
 int64_t slabs_of(int64_t L, int64_t H) {
   int64_t n = MAX_SLABS;
   if (H > 32 * EPT && H <= CLUSTER_H) {

@@ -11,7 +11,8 @@ from tests.test_step_binding import I32, lib, t  # noqa: F401
 @pytest.mark.parametrize("no_grad", [False, True])
 @pytest.mark.parametrize("kind,which", [("layer", 0), ("layer", 1),
                                         ("layer", 2), ("rms", 0), ("rms", 1)])
-def test_a_tangent_is_refused_by_the_norms(lib, kind, which, no_grad):  # noqa: F811
+def test_a_tangent_is_refused_by_the_norms(lib, kind,  # noqa: F811
+                                           which, no_grad):
     """Forward mode has no formula here; a result without a tangent would stand
     for a derivative of zero."""
     with forward_ad.dual_level(), torch.set_grad_enabled(not no_grad):
@@ -41,7 +42,7 @@ BF, BOOL = torch.bfloat16, torch.bool
 
 
 def written(call, *tensors):
-    """Whether autograd counts `call` as a write of each tensor, once or more."""
+    """Whether autograd counts `call` as a write of each tensor."""
     before = [x._version for x in tensors]
     call()
     return all(x._version > b for x, b in zip(tensors, before))
