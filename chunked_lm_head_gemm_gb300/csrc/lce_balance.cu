@@ -14,8 +14,8 @@
 // has several rows of few experts; a lane has the same experts in every row
 // and adds their scores in registers. Exponentials and reciprocals are the
 // approximate instructions, the rounding of the exponential's argument put back
-// (2^-21 of a score, however far from zero or below the row's largest; 131072 x
-// 256: 1 to 3 us of a pass).
+// (2^-21 of a score, however far from zero or below the row's largest, but for
+// the rounding of z - max; 131072 x 256: 1 to 3 us of a pass).
 //
 // Measured alone, 131072 x 256 fp32 sigmoid: forward 36 us (3.9 TB/s; 68% of
 // the issue slots at 46% of the warps: instructions and their latency
@@ -129,15 +129,16 @@ __device__ __forceinline__ float row_max(const uint64_t (&z)[P], int team) {
   return m == -INFINITY ? 0.f : m;
 }
 
-// Below this a sum of sigmoid scores has lost terms to fp32's range.
-constexpr float LEAST_SUM = 1e-30f;
+// Below this a row's sigmoid scores are taken relative to the largest: s is e^z
+// and 1 - s is 1, both to less than half a step of fp32, and none is lost to
+// fp32's range that is more than 1e-30 of the sum.
+constexpr float LEAST_SUM = 1e-8f;
 
 // A row's scores in place of its logits, not yet divided by their sum, which
 // is returned; with SLOPE 1 - s of sigmoid scores (for softmax not written).
 // Two elements to an instruction where there is one. s = 1 / (1 + q), 1 - s = q
 // s with q = e^-z; where s is 0, 1 - s is too, which is of no account.
-// Should all sigmoid scores be tiny, where s = e^z, they are taken relative to
-// the largest: e^(z - m), and 1 - s is 1.
+// Should all sigmoid scores be small, s e^-m = e^(z - m) and 1 - s = 1.
 template <int P, bool SIGMOID, bool SLOPE>
 __device__ __forceinline__ float scores(uint64_t (&z)[P], uint64_t (&slope)[P],
                                         int team) {

@@ -67,6 +67,19 @@ def test_softmax_scores_far_below_the_largest(lo, hi):
     assert relative(z, "softmax", [1.0, 0.0]) <= 14
 
 
+@pytest.mark.parametrize("lo,hi,below", [(-18, -10, 65), (-30, -19, 60),
+                                         (-50, -40, 40), (-69, -60, 25)])
+def test_sigmoid_scores_far_below_a_small_one(lo, hi, below):
+    """Scores below fp32's range that are e^-25 and less of the row's sum. The
+    logits are multiples of 2^-10, whose differences are exact, so the bound is
+    that of scores far below zero (relative to the largest they are 5, not 8,
+    and half a step for s = e^z and 1 - s = 1)."""
+    require_gpu()
+    z = (uniform(lo, hi, 4) * 1024).round() / 1024
+    assert relative(torch.stack([z - below, z], 1), "sigmoid",
+                    [1.0, 0.0]) <= 34
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_logits_at_the_ends_of_the_range(scoring):
     """The lowest and highest values of fp32 and infinities: each row is what
