@@ -917,7 +917,8 @@ def route_forward(logits: torch.Tensor, top_k: int, scoring: str = "softmax",
                                opts, weights.data_ptr(),
                                experts.data_ptr(), _stream_ptr(dev))
     _check(st, "lce_route_forward")
-    _written(weights, experts)
+    if weights_out is not None or experts_out is not None:
+        _written(weights_out, experts_out)
     return weights, experts
 
 
@@ -947,7 +948,8 @@ def route_backward(logits: torch.Tensor, experts: torch.Tensor,
                                 dweights.data_ptr(), L, E, opts,
                                 out.data_ptr(), _stream_ptr(dev))
     _check(st, "lce_route_backward")
-    _written(dlogits_out)
+    if dlogits_out is not None:
+        _written(dlogits_out)
     return out
 
 
