@@ -20,7 +20,8 @@
 // backward 224 us (7.2 TB/s) and 7 us for joining its blocks' sums; 1048576 x
 // 128 bf16 89 and 127 us (6.0, 6.4 TB/s); 16384 x 2560 fp32 layer norm 54 and
 // 70 us (6.3, 7.2 TB/s). Rows that are not on 16 bytes are bound by
-// instructions: 65536 x 1001 bf16 RMS norm 53 and 117 us (4.9, 3.4 TB/s).
+// instructions: 65536 x 1001 bf16 RMS norm 53 and, with the join, 112 us (4.9,
+// 3.5 TB/s).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -869,7 +870,7 @@ constexpr int64_t MAX_SLABS = 1024;
 // clusters whose rows are whole vectors add their registers to their slab
 // instead. Either costs the other dearly: 16384 x 32768 bf16, RMS norm, 905 us
 // as one run, 1159 in turns, 920 so; 20000 x 12345, layer norm, 720 as one run,
-// 726 in turns, 867 with the slab.
+// 726 in turns, 867 with the slab (x and dy one tensor).
 constexpr int64_t MAX_RUN = 1024;
 
 // Rows of a run (MAX_RUN).
